@@ -129,7 +129,7 @@ def _prepare_tables(case, gen):
     cap = _token_bound(case)
     st = dict(lens=lens, counts=counts, held=held, rows=rows, ring=ring, state=state, shared=shared, blocks=blocks, cap=cap)
     st["outs"] = dict(context_lens=torch.empty_like(lens), cu_seqlens=torch.empty(S + 1, dtype=torch.int32, device=DEV),
-                      positions=torch.empty(cap, dtype=torch.int32, device=DEV), slots=torch.empty(cap, dtype=torch.int64, device=DEV),
+                      cu_blocks=torch.empty(S + 1, dtype=torch.int32, device=DEV), positions=torch.empty(cap, dtype=torch.int32, device=DEV), slots=torch.empty(cap, dtype=torch.int64, device=DEV),
                       held_out=torch.empty_like(held), ring_state_out=torch.empty_like(state),
                       totals=torch.empty(4, dtype=torch.int32, device=DEV))
     return st
@@ -282,7 +282,8 @@ def _plain_tables(st):
     page = rows[s, (pos.clamp(min=0) // K)].long()
     slots = torch.where(live, page * K + pos % K, -1)
     total = torch.stack([torch.zeros_like(cu[-1]), cu[-1], take.sum(), give.sum()])
-    return {"rows": rows, "ring": ring, "context_lens": ctx.int(), "cu_seqlens": cu.int(), "positions": pos.int(), "slots": slots,
+    return {"rows": rows, "ring": ring, "context_lens": ctx.int(), "cu_seqlens": cu.int(),
+            "cu_blocks": torch.cat([torch.zeros_like(n[:1]), torch.cumsum(take, 0)]).int(), "positions": pos.int(), "slots": slots,
             "held_out": torch.where(over, 0, torch.maximum(held, need)).int(), "ring_state_out": st["state"] + torch.stack([take.sum(), give.sum()]),
             "totals": total.int()}
 
@@ -407,7 +408,7 @@ def work(case):
         over = case["over"]
         tokens = S * (1 - over) * (case["new_lo"] + case["new_hi"]) / 2
         pages = tokens / K + S * over * (case["len_lo"] + case["len_hi"]) / 2 / K
-        return {"bytes": S * 4 * 7 + pages * 8 + _token_bound(case) * 12, "flops": 0}
+        return {"bytes": S * 4 * 8 + pages * 8 + _token_bound(case) * 12, "flops": 0}
     if case["op"] == "rope":
         T, H, J, D = case["tokens"], case["heads"], case["kv"], case["dim"]
         e = 4 if case["pool"] == "f32" else 2
