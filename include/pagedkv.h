@@ -71,7 +71,11 @@ enum {
   PKV_DEVERR_CONTEXT_LEN = 4,  /* context_lens[s] < 0, > max_context_len or beyond the
                                   table row (the length is clamped)                  */
   PKV_DEVERR_POSITION = 5,     /* position beyond the block-table row                */
-  PKV_DEVERR_TIMEOUT = 6       /* a pipeline wait gave up after about a second       */
+  PKV_DEVERR_TIMEOUT = 6,      /* a pipeline wait gave up after about a second       */
+  PKV_DEVERR_STEP = 7,         /* pkv_step_tables refused the step (totals[0] says why) */
+  PKV_DEVERR_DRAFT = 8         /* pkv_verify_draft_tokens: draft token outside the
+                                  vocabulary, inconsistent cu_seqlens, or a row of
+                                  probabilities without any positive value           */
 };
 
 /* Human-readable name of a status.  Never NULL. */
@@ -471,6 +475,178 @@ PKV_API pkv_status pkv_kv_append_varlen(const void* k, const void* v, const int3
                                         int64_t num_blocks, int32_t block_size,
                                         int32_t num_kv_heads, int32_t head_dim, pkv_dtype dtype,
                                         int64_t* slot_mapping_out, void* stream);
+
+/*
+ * Block tables and slot maps of one engine step, made on the GPU from the
+ * requests' lengths ("19.2 KV Cache 系统化管理" §19.2.2: a request gets a new
+ * block when its last one is full; "推理与 KV Cache 02", 从一个位置找到缓存块).
+ * A step whose lengths are only known on the device (accepted draft tokens)
+ * needs no host round trip, and the call can sit in a captured graph.
+ *   lens:    int32 [num_seqs], tokens of each request already in the cache.
+ *   counts:  int32 [num_seqs], new tokens n >= 0 of the step; -1: the request
+ *            is over, its blocks go back to the free ring.
+ *   block_tables: int32 [num_seqs, max_blocks_per_seq], updated in place:
+ *            entries held .. need - 1 are filled (need = ceil((lens + n) /
+ *            block_size)), all others stay as they are.
+ *   held:    int32 [num_seqs], blocks that the row lists now; lens must not
+ *            exceed held * block_size.
+ *   shared:  int32 [num_seqs] or NULL (0 for all): leading blocks of a row
+ *            that other rows list too; they are not given back with it.
+ *   ring:    int32 [ring_size], the free blocks in the order in which they
+ *            are taken: entry i (i = head .. tail - 1, a running count) is
+ *            ring[i mod ring_size].  Blocks are taken at head, in the order
+ *            of the requests and of their table entries, and given back at
+ *            tail in the same order; a block given back in this call is not
+ *            taken in it.  ring_size >= num_blocks holds every case.
+ *   ring_state: int64 [2] = {head, tail}, 0 <= tail - head <= ring_size.
+ * Outputs:
+ *   context_lens: int32 [num_seqs] = lens + n (0: over), as the attention
+ *            calls read them; may be `lens`.
+ *   cu_seqlens: int32 [num_seqs + 1], running sum of n.
+ *   cu_blocks: int32 [num_seqs + 1], running sum of the blocks taken.
+ *   positions: int32 [num_tokens], slots: int64 [num_tokens]: packed by
+ *            request; rows at and behind cu_seqlens[num_seqs] get -1 (padding
+ *            of a captured step).  num_tokens is the host's bound.
+ *   held_out: int32 [num_seqs] (may be `held`); ring_state_out: int64 [2]
+ *            (may be `ring_state`).
+ *   totals:  int32 [4] = {code, tokens, blocks taken, blocks given back}.
+ * All or nothing: code 0 = done.  Otherwise block_tables, ring, held_out and
+ * ring_state_out keep (repeat) the old state, context_lens repeats lens,
+ * cu_seqlens and cu_blocks are 0, positions and slots are -1, and totals
+ * holds what the step asked for: code 1 = not enough free blocks (an
+ * ordinary event: preempt a request); code 2 = more than num_tokens tokens;
+ * code 3 = an invalid length, count, held, shared or ring_state, or a ring
+ * too small for the blocks given back.  Codes 2 and 3 record PKV_DEVERR_STEP.
+ * A free block outside [0, num_blocks) is listed as it is, its tokens get
+ * slot -1 and PKV_DEVERR_BLOCK_ID is recorded.
+ */
+PKV_API pkv_status pkv_step_tables(const int32_t* lens, const int32_t* counts,
+                                   int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* held, const int32_t* shared, int32_t* ring,
+                                   int64_t ring_size, const int64_t* ring_state,
+                                   int32_t num_seqs, int32_t num_tokens, int32_t block_size,
+                                   int64_t num_blocks, int32_t* context_lens,
+                                   int32_t* cu_seqlens, int32_t* cu_blocks, int32_t* positions,
+                                   int64_t* slots, int32_t* held_out, int64_t* ring_state_out,
+                                   int32_t* totals, void* stream);
+
+/*
+ * Head norms, rotation by position and KV append of new tokens in one pass
+ * over the projection's output (§19.2.3 write_slot stores K as attention
+ * reads it, after its norm and rotation).
+ *   For token t and each query or key head row x of head_dim values:
+ *     y = x * rsqrt(mean(x^2) + eps) * weight        (weight not NULL)
+ *     y = x                                          (weight NULL)
+ *   then, with c = cos_sin[p][i], s = cos_sin[p][rot_dim / 2 + i], p =
+ *   positions[t], i = 0 .. rot_dim / 2 - 1, the pair
+ *     (a, b) = (y[i], y[i + rot_dim / 2])            (interleaved = 0)
+ *     (a, b) = (y[2 i], y[2 i + 1])                  (interleaved = 1)
+ *   becomes (a c - b s, b c + a s); values from rot_dim on stay.  Computed in
+ *   float32 and rounded once, to the type it is stored in.  q_out[t] receives
+ *   the query rows; the key rows and v[t] as it is go to slot slots[t] of the
+ *   pools, as pkv_kv_write (quant NULL) or, quantized per `quant`, as
+ *   pkv_kv_append_quant store them.
+ *   q: [num_tokens, num_q_heads, head_dim], k, v: [num_tokens, num_kv_heads,
+ *   head_dim], each with its own distance between tokens (elements; heads and
+ *   values contiguous), so that they can be cut out of one projection's
+ *   output.  q_out: the same with q_out_stride; it may be q itself (same
+ *   stride).  q_weight, k_weight: [head_dim] or NULL.  All of in_dtype.
+ *   positions: int32 [num_tokens], slots: int64 [num_tokens] (as
+ *   pkv_step_tables makes them).  cos_sin: float32 [max_position, rot_dim].
+ * A negative position marks padding: nothing of the token is read or written.
+ * Slot -1: q_out is written, the pools are not.  A position >= max_position
+ * skips the token and records PKV_DEVERR_POSITION; another slot outside the
+ * pool skips its write and records PKV_DEVERR_SLOT.  Duplicate slots: which
+ * token wins is unspecified.
+ * Supported: head_dim even, <= 512; rot_dim even, 0 <= rot_dim <= head_dim;
+ * num_kv_heads * head_dim <= 8192 for PKV_KV_INT8_TOKEN pools.
+ */
+PKV_API pkv_status pkv_qk_norm_rope_append(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
+    const int32_t* positions, const float* cos_sin, int32_t max_position, int32_t rot_dim,
+    int32_t interleaved, const int64_t* slots, int32_t num_tokens, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_stride, void* k_cache,
+    void* v_cache, int64_t num_blocks, int32_t block_size, pkv_dtype in_dtype,
+    const pkv_kv_quant* quant, void* stream);
+
+/*
+ * Decode attention for a batch whose requests share a long prefix, the
+ * prefix computed once for all ("推理与 KV Cache 02", 前缀索引与 Block Table:
+ * requests with one prompt list the same whole blocks).  The same result as
+ * pkv_attention_decode (cu_seqlens NULL: one query row a sequence) or
+ * pkv_attention_prefill (cu_seqlens: packed new tokens) over the full tables.
+ *   prefix_table: int32 [prefix_len / block_size], the blocks of tokens 0 ..
+ *            prefix_len - 1 of every sequence; prefix_len is a multiple of
+ *            block_size.
+ *   block_tables: the full rows; entries below prefix_len / block_size are
+ *            not read.  context_lens count all tokens.  A sequence shorter
+ *            than prefix_len reads that much of the prefix; one of length 0
+ *            gets zeros (cu_seqlens NULL).
+ *   num_tokens: rows of q and out ([num_tokens, num_q_heads, head_dim]);
+ *            num_seqs when cu_seqlens is NULL.  Rows behind the last sequence
+ *            (num_tokens > cu_seqlens[num_seqs]) are left as they are.
+ *   max_query_len: host bound on the new tokens of a sequence (1 when
+ *            cu_seqlens is NULL); max_context_len: host bound on context_lens.
+ *   workspace: pkv_attention_decode_prefix_workspace_bytes bytes, 256-byte
+ *            aligned; not shared with a call that overlaps on the GPU.
+ * Supported: PKV_BF16, head_dim 64 or 128, block_size 8 or a multiple of 16,
+ * max_query_len * num_q_heads / num_kv_heads <= 8, num_seqs <= 2048,
+ * 16-byte aligned pools, scale > 0.  Other shapes: pkv_attention_decode and
+ * pkv_attention_prefill read the prefix through each row.
+ * Inconsistent counts (n < 0, n > L, cu_seqlens past num_tokens) skip the
+ * sequence and record PKV_DEVERR_CONTEXT_LEN.
+ */
+PKV_API pkv_status pkv_attention_decode_prefix(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_table,
+    int32_t prefix_len, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* cu_seqlens, const int32_t* context_lens, int32_t num_seqs,
+    int32_t num_tokens, int32_t max_query_len, int32_t max_context_len, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks, float scale,
+    void* out, void* workspace, size_t workspace_bytes, pkv_dtype dtype, void* stream);
+
+/* Workspace bytes of pkv_attention_decode_prefix for these sizes. */
+PKV_API pkv_status pkv_attention_decode_prefix_workspace_bytes(
+    int32_t num_seqs, int32_t num_tokens, int32_t max_query_len, int32_t max_context_len,
+    int32_t prefix_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t block_size, pkv_dtype dtype, size_t* bytes);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from
+ * given random numbers (the step after pkv_attention_prefill over speculative
+ * candidate tokens, "企业官网建设流程全解析" §8.2).
+ * Sequence s ran r = cu_seqlens[s+1] - cu_seqlens[s] rows through the model:
+ * its last token and n = r - 1 drafted ones.  With c = cu_seqlens[s], d_i =
+ * tokens[c + 1 + i], p_i = target_probs[c + i], q_i = draft_probs[s][i] and
+ * u_i = uniforms[c + i]:
+ *   draft i is accepted while u_i * q_i[d_i] < p_i[d_i] (the product exact);
+ *   at the first refusal i = a the next token is drawn from the weights
+ *   max(p_a - q_a, 0) (float32 difference; from p_a where all are 0), with
+ *   all n accepted (a = n) from p_n.
+ *   The draw is exact: weight x counts floor(min(x, 1) * 2^40), sums are
+ *   64-bit integers, U = floor(u * 2^24) with u = uniforms[c + n]; the token is the
+ *   smallest one whose inclusive sum exceeds floor(total * U / 2^24).  Two
+ *   runs on any machine give the same tokens.
+ * draft_probs NULL: drafts without probabilities (q_i is 1 at d_i, else 0).
+ *   target_probs: [num_tokens, vocab], distance target_stride elements;
+ *   draft_probs: [num_seqs, max_query_len - 1, vocab] with draft_seq_stride
+ *   and draft_tok_stride elements; both of prob_dtype.  Negative values and
+ *   NaN count as 0, values above 1 as 1 in the draw.
+ *   tokens: int32 [num_tokens]; uniforms: float32 [num_tokens], in [0, 1).
+ * Outputs: out_tokens int32 [num_seqs, max_query_len] = the a accepted
+ * drafts, the drawn token, then -1; num_new int32 [num_seqs] = a + 1.  A
+ * sequence without rows (r = 0) gets -1 and 0.
+ * A draft outside [0, vocab) is refused (q is taken as 0) and recorded as
+ * PKV_DEVERR_DRAFT; so is inconsistent cu_seqlens (outputs -1 and 0) and a
+ * drawn row without positive weight (token -1).
+ * Supported: 1 <= vocab <= 2^22.
+ */
+PKV_API pkv_status pkv_verify_draft_tokens(
+    const void* target_probs, int64_t target_stride, const void* draft_probs,
+    int64_t draft_seq_stride, int64_t draft_tok_stride, const int32_t* tokens,
+    const float* uniforms, const int32_t* cu_seqlens, int32_t num_seqs, int32_t num_tokens,
+    int32_t max_query_len, int32_t vocab, int32_t* out_tokens, int32_t* num_new,
+    pkv_dtype prob_dtype, void* stream);
 
 /*
  * Synchronises `stream`, copies the current device's error word into *code

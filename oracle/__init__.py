@@ -20,9 +20,11 @@ section:
   (logical block, offset and token-slot formulas and the worked K=4 example).
 
 Submodules: ``oracle.quant`` (FP8 e4m3 / INT8 per-token KV formats, pinned in
-``tests/test_oracle_quant_pins.py``) and ``oracle.prefill`` (multi-query
+``tests/test_oracle_quant_pins.py``), ``oracle.prefill`` (multi-query
 attention of several new tokens per sequence, pinned in
-``tests/test_oracle_prefill_pins.py``).
+``tests/test_oracle_prefill_pins.py``) and ``oracle.step`` (block tables from
+lengths, head norms + rotation, draft verification, pinned in
+``tests/test_oracle_step_pins.py``).
 
 Pins (checks against things other than the oracle itself) live in
 ``tests/test_oracle_pins.py``.  No function here is "parity unpinned".

@@ -16,7 +16,11 @@
 #include "pkv_prefill.cuh"
 #include "pkv_prefill_tc05.cuh"
 #include "pkv_prefill_tc05x2.cuh"
+#include "pkv_prefix.cuh"
 #include "pkv_reduce.cuh"
+#include "pkv_rope.cuh"
+#include "pkv_step.cuh"
+#include "pkv_verify.cuh"
 #include "pkv_copy.cuh"
 #include "pkv_device.cuh"
 
@@ -736,6 +740,105 @@ pkv_status check_quant(const pkv_kv_quant* q, bool need_token_scales) {
   return PKV_OK;
 }
 
+// ---- norm + rotation + append dispatch -------------------------------------------
+template <typename T, int FMT>
+pkv_status launch_rope_fmt(const pkv::RopeParams& p, cudaStream_t st) {
+  const size_t smem = FMT == PKV_KV_INT8_TOKEN ? 2 * sizeof(float) * (size_t)p.H_kv * p.D : 0;
+  if (smem > 0) {
+    static std::once_flag flags[kMaxDevices];
+    static cudaError_t errs[kMaxDevices];
+    int dev, sms;
+    pkv_status s = device_facts(&dev, &sms);
+    if (s == PKV_OK)
+      s = set_smem_once(pkv::rope_any_kernel<T, FMT>, 2 * (int)sizeof(float) * pkv::kRopeMaxInt8Row,
+                        flags, errs, dev);
+    if (s != PKV_OK) return s;
+  }
+  PKV_CUDA(launch_pdl(pkv::rope_any_kernel<T, FMT>, dim3((unsigned)p.T), dim3(pkv::kRopeThreads),
+                      smem, st, p));
+  return PKV_OK;
+}
+
+template <typename T>
+pkv_status launch_rope(int fmt, const pkv::RopeParams& p, cudaStream_t st) {
+  switch (fmt) {
+    case PKV_KV_FP8_E4M3: return launch_rope_fmt<T, PKV_KV_FP8_E4M3>(p, st);
+    case PKV_KV_INT8_TOKEN: return launch_rope_fmt<T, PKV_KV_INT8_TOKEN>(p, st);
+    case PKV_KV_BF16K_FP8V: return launch_rope_fmt<T, PKV_KV_BF16K_FP8V>(p, st);
+    default: return launch_rope_fmt<T, PKV_KV_PLAIN>(p, st);
+  }
+}
+
+// ---- shared-prefix attention planning ---------------------------------------------
+struct PrefixPlan {
+  size_t ws_bytes = 0;
+};
+
+pkv_status plan_prefix(int S, int T, int max_q, int max_len, int prefix_len, int H_q, int H_kv,
+                       int D, int K, int64_t num_blocks, float scale, pkv_dtype dt,
+                       PrefixPlan* out) {
+  PKV_CHECK(S >= 0 && T >= 0 && max_q >= 0 && max_len >= 0 && prefix_len >= 0 && H_q > 0 &&
+                H_kv > 0 && D > 0 && K > 0 && dtype_ok(dt),
+            PKV_ERR_INVALID_ARGUMENT, "bad prefix attention sizes");
+  PKV_CHECK(H_q % H_kv == 0, PKV_ERR_INVALID_ARGUMENT, "num_q_heads %% num_kv_heads != 0");
+  PKV_CHECK(prefix_len % K == 0, PKV_ERR_INVALID_ARGUMENT,
+            "prefix_len must be a multiple of block_size (whole blocks are shared)");
+  PKV_CHECK(std::isfinite(scale) && scale > 0.f, PKV_ERR_INVALID_ARGUMENT,
+            "scale must be finite and > 0");
+  PKV_CHECK(tc_shape_ok(H_q / H_kv, D, K, num_blocks, dt) &&
+                (int64_t)max_q * (H_q / H_kv) <= 8 && K <= 1024,
+            PKV_ERR_UNSUPPORTED,
+            "shared-prefix attention needs bf16, head_dim 64 or 128, block_size 8 or a multiple "
+            "of 16, and at most 8 query rows per KV head (max_query_len x G)");
+  PKV_CHECK(S <= pkv::kTcMaxSeqs && H_kv <= 65535, PKV_ERR_UNSUPPORTED, "at most %d sequences",
+            pkv::kTcMaxSeqs);
+  *out = PrefixPlan{};
+  return PKV_OK;
+}
+
+// ---- draft verification dispatch ----------------------------------------------------
+template <typename T, int E>
+pkv_status launch_verify_e(const pkv::VerifyParams& p, int S, cudaStream_t st) {
+  int dev, sms;
+  pkv_status s = device_facts(&dev, &sms);
+  if (s != PKV_OK) return s;
+  // CTAs a sequence: enough to fill the GPU, at least 4 vector loads a lane
+  int C = 1;
+  while (C < 8 && S * C < 2 * sms && (int64_t)C * pkv::kVerifyThreads * E * 4 < p.vocab) C *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(S * C));
+  cfg.blockDim = dim3(pkv::kVerifyThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  PKV_CUDA(cudaLaunchKernelEx(&cfg, pkv::verify_kernel<T, E>, p));
+  return PKV_OK;
+}
+
+// Widest vector (up to 16 bytes) that every row's first value is aligned to.
+template <typename T>
+pkv_status launch_verify(const pkv::VerifyParams& p, int S, cudaStream_t st) {
+  const int64_t eb = sizeof(T);
+  int w = 16;
+  const uint64_t bits = reinterpret_cast<uintptr_t>(p.target) | (uint64_t)(p.target_stride * eb) |
+                        reinterpret_cast<uintptr_t>(p.draft) |
+                        (p.draft ? (uint64_t)((p.draft_seq_stride | p.draft_tok_stride) * eb) : 0);
+  while (bits & (uint64_t)(w - 1)) w /= 2;
+  switch (w / (int)eb) {
+    case 8: return launch_verify_e<T, 16 / sizeof(T)>(p, S, st);
+    case 4: return launch_verify_e<T, 4>(p, S, st);
+    case 2: return launch_verify_e<T, 2>(p, S, st);
+    default: return launch_verify_e<T, 1>(p, S, st);
+  }
+}
+
 // ---- fixed scratch for pkv_attention_decode_noalloc ---------------------------
 // In host code this name is only a host-side stand-in for the array; the
 // device address is looked up per device with cudaGetSymbolAddress.
@@ -1442,6 +1545,212 @@ pkv_status pkv_kv_append_varlen(const void* k, const void* v, const int32_t* cu_
   }
 #undef PKV_APPEND_VARLEN
   return PKV_OK;
+}
+
+pkv_status pkv_step_tables(const int32_t* lens, const int32_t* counts, int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* held, const int32_t* shared,
+                           int32_t* ring, int64_t ring_size, const int64_t* ring_state,
+                           int32_t num_seqs, int32_t num_tokens, int32_t block_size,
+                           int64_t num_blocks, int32_t* context_lens, int32_t* cu_seqlens,
+                           int32_t* cu_blocks, int32_t* positions, int64_t* slots,
+                           int32_t* held_out, int64_t* ring_state_out, int32_t* totals,
+                           void* stream) {
+  PKV_CHECK(num_seqs >= 0 && num_tokens >= 0 && max_blocks_per_seq >= 1 && block_size >= 1 &&
+                num_blocks >= 1 && ring_size >= 1,
+            PKV_ERR_INVALID_ARGUMENT, "bad step sizes");
+  PKV_CHECK((int64_t)max_blocks_per_seq * block_size <= 2147483647 &&
+                (int64_t)num_seqs * max_blocks_per_seq <= 2147483647,
+            PKV_ERR_UNSUPPORTED, "table too large");
+  PKV_CHECK(num_blocks <= INT64_MAX / block_size, PKV_ERR_INVALID_ARGUMENT, "pool too large");
+  PKV_CHECK(ring && ring_state && cu_seqlens && cu_blocks && ring_state_out && totals,
+            PKV_ERR_INVALID_ARGUMENT, "null pointer");
+  PKV_CHECK(num_seqs == 0 || (lens && counts && block_tables && held && context_lens && held_out),
+            PKV_ERR_INVALID_ARGUMENT, "null pointer");
+  PKV_CHECK(num_tokens == 0 || (positions && slots), PKV_ERR_INVALID_ARGUMENT, "null pointer");
+  PKV_CHECK(aligned(ring_state, 8) && aligned(ring_state_out, 8) && aligned(slots, 8) &&
+                aligned(positions, 4) && aligned(block_tables, 4) && aligned(ring, 4) &&
+                aligned(lens, 4) && aligned(counts, 4) && aligned(held, 4) && aligned(shared, 4) &&
+                aligned(context_lens, 4) && aligned(cu_seqlens, 4) && aligned(cu_blocks, 4) &&
+                aligned(held_out, 4) && aligned(totals, 4),
+            PKV_ERR_INVALID_ARGUMENT, "misaligned step buffers");
+  pkv::StepParams p = {lens, counts, block_tables, held, shared, ring, ring_state, context_lens,
+                       cu_seqlens, cu_blocks, positions, slots, held_out, ring_state_out, totals,
+                       ring_size, num_blocks, max_blocks_per_seq, num_seqs, num_tokens, block_size,
+                       log2_exact(block_size)};
+  cudaStream_t st = as_stream(stream);
+  if (num_tokens <= pkv::kStepFusedTokens) {
+    PKV_CUDA(launch_pdl(pkv::step_requests_kernel<true>, dim3(1), dim3(pkv::kStepThreads), 0, st, p));
+    return PKV_OK;
+  }
+  PKV_CUDA(launch_pdl(pkv::step_requests_kernel<false>, dim3(1), dim3(pkv::kStepThreads), 0, st, p));
+  PKV_CUDA(launch_pdl(pkv::step_tokens_kernel, dim3((unsigned)ceil_div(num_tokens, 256)), dim3(256),
+                      0, st, p));
+  return PKV_OK;
+}
+
+pkv_status pkv_qk_norm_rope_append(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
+    const int32_t* positions, const float* cos_sin, int32_t max_position, int32_t rot_dim,
+    int32_t interleaved, const int64_t* slots, int32_t num_tokens, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_stride, void* k_cache,
+    void* v_cache, int64_t num_blocks, int32_t block_size, pkv_dtype in_dtype,
+    const pkv_kv_quant* quant, void* stream) {
+  PKV_CHECK(num_tokens >= 0 && num_q_heads >= 1 && num_kv_heads >= 1 && head_dim >= 1 &&
+                num_blocks >= 1 && block_size >= 1 && max_position >= 1 && dtype_ok(in_dtype) &&
+                (interleaved == 0 || interleaved == 1),
+            PKV_ERR_INVALID_ARGUMENT, "bad rope sizes");
+  PKV_CHECK(rot_dim >= 0 && rot_dim <= head_dim && rot_dim % 2 == 0, PKV_ERR_INVALID_ARGUMENT,
+            "rot_dim must be even and at most head_dim");
+  PKV_CHECK(std::isfinite(eps) && eps >= 0.f, PKV_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+  PKV_CHECK(head_dim % 2 == 0 && head_dim <= pkv::kRopeMaxDim, PKV_ERR_UNSUPPORTED,
+            "head_dim must be even and at most %d", pkv::kRopeMaxDim);
+  const int64_t q_row = (int64_t)num_q_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+  PKV_CHECK(q_row <= 2147483647 && kv_row <= 2147483647, PKV_ERR_UNSUPPORTED, "token row too wide");
+  PKV_CHECK(num_blocks <= INT64_MAX / block_size / (4 * kv_row), PKV_ERR_INVALID_ARGUMENT,
+            "pool too large");
+  if (quant != nullptr) {
+    pkv_status s = check_quant(quant, true);
+    if (s != PKV_OK) return s;
+    PKV_CHECK(quant->format != PKV_KV_INT8_TOKEN || kv_row <= pkv::kRopeMaxInt8Row,
+              PKV_ERR_UNSUPPORTED, "INT8 pools: num_kv_heads * head_dim must be at most %d",
+              pkv::kRopeMaxInt8Row);
+  }
+  if (num_tokens == 0) return PKV_OK;
+  PKV_CHECK(q && k && v && positions && slots && q_out && k_cache && v_cache &&
+                (cos_sin || rot_dim == 0),
+            PKV_ERR_INVALID_ARGUMENT, "null pointer");
+  PKV_CHECK(num_tokens == 1 || (q_stride >= q_row && q_out_stride >= q_row && k_stride >= kv_row &&
+                                v_stride >= kv_row),
+            PKV_ERR_INVALID_ARGUMENT, "token rows overlap");
+  const size_t eb = elem_bytes(in_dtype);
+  const size_t pool_eb = quant ? 1 : eb;
+  const size_t k_eb = quant && quant->format == PKV_KV_BF16K_FP8V ? 2 : pool_eb;
+  PKV_CHECK(aligned(q, eb) && aligned(k, eb) && aligned(v, eb) && aligned(q_out, eb) &&
+                aligned(q_weight, eb) && aligned(k_weight, eb) && aligned(k_cache, k_eb) &&
+                aligned(v_cache, pool_eb) && aligned(positions, 4) && aligned(cos_sin, 4) &&
+                aligned(slots, 8),
+            PKV_ERR_INVALID_ARGUMENT, "misaligned rope buffers");
+  pkv::RopeParams p = {};
+  p.q = q; p.k = k; p.v = v; p.wq = q_weight; p.wk = k_weight;
+  p.positions = positions; p.cos_sin = cos_sin; p.slots = slots; p.q_out = q_out;
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  if (quant) {
+    p.k_ts = quant->k_token_scales; p.v_ts = quant->v_token_scales;
+    p.k_scale = quant->k_scale; p.v_scale = quant->v_scale;
+  }
+  p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride; p.qo_stride = q_out_stride;
+  p.num_slots = num_blocks * block_size;
+  p.eps = eps;
+  p.T = num_tokens; p.H_q = num_q_heads; p.H_kv = num_kv_heads; p.D = head_dim; p.rot = rot_dim;
+  p.max_pos = max_position; p.interleaved = interleaved;
+  const int fmt = quant ? quant->format : 0;
+  return in_dtype == PKV_BF16 ? launch_rope<__nv_bfloat16>(fmt, p, as_stream(stream))
+                              : launch_rope<float>(fmt, p, as_stream(stream));
+}
+
+pkv_status pkv_attention_decode_prefix_workspace_bytes(
+    int32_t num_seqs, int32_t num_tokens, int32_t max_query_len, int32_t max_context_len,
+    int32_t prefix_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t block_size, pkv_dtype dtype, size_t* bytes) {
+  PKV_CHECK(bytes != nullptr, PKV_ERR_INVALID_ARGUMENT, "null bytes pointer");
+  PrefixPlan plan;
+  pkv_status st = plan_prefix(num_seqs, num_tokens, max_query_len, max_context_len, prefix_len,
+                              num_q_heads, num_kv_heads, head_dim, block_size, 1, 1.f, dtype,
+                              &plan);
+  if (st != PKV_OK) return st;
+  *bytes = plan.ws_bytes;
+  return PKV_OK;
+}
+
+pkv_status pkv_attention_decode_prefix(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_table,
+    int32_t prefix_len, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* cu_seqlens, const int32_t* context_lens, int32_t num_seqs, int32_t num_tokens,
+    int32_t max_query_len, int32_t max_context_len, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int64_t num_blocks, float scale, void* out,
+    void* workspace, size_t workspace_bytes, pkv_dtype dtype, void* stream) {
+  PKV_CHECK(max_blocks_per_seq >= 1 && num_blocks >= 1, PKV_ERR_INVALID_ARGUMENT,
+            "bad prefix attention sizes");
+  PKV_CHECK(cu_seqlens != nullptr || (num_tokens == num_seqs && max_query_len == 1),
+            PKV_ERR_INVALID_ARGUMENT,
+            "without cu_seqlens every sequence has one query row (num_tokens = num_seqs, "
+            "max_query_len = 1)");
+  PrefixPlan plan;
+  pkv_status st = plan_prefix(num_seqs, num_tokens, max_query_len, max_context_len, prefix_len,
+                              num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                              dtype, &plan);
+  if (st != PKV_OK) return st;
+  PKV_CHECK((int64_t)max_blocks_per_seq * block_size <= 2147483647, PKV_ERR_UNSUPPORTED,
+            "table row too long");
+  if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+  PKV_CHECK(q && k_cache && v_cache && block_tables && context_lens && out &&
+                (prefix_table || prefix_len == 0) && (workspace || plan.ws_bytes == 0),
+            PKV_ERR_INVALID_ARGUMENT, "null pointer");
+  PKV_CHECK(workspace_bytes >= plan.ws_bytes, PKV_ERR_WORKSPACE_TOO_SMALL,
+            "workspace %zu bytes < %zu needed", workspace_bytes, plan.ws_bytes);
+  PKV_CHECK(aligned(workspace, 256), PKV_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
+  PKV_CHECK(aligned(q, 16) && aligned(out, 16) && aligned(k_cache, 16) && aligned(v_cache, 16),
+            PKV_ERR_INVALID_ARGUMENT, "q, out and the pools must be 16-byte aligned");
+  pkv::PrefixParams p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k_cache);
+  p.v = static_cast<const __nv_bfloat16*>(v_cache);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.prefix_table = prefix_table;
+  p.block_tables = block_tables;
+  p.cu = cu_seqlens;
+  p.lens = context_lens;
+  p.num_blocks = num_blocks;
+  p.prefix_len = prefix_len;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.S = num_seqs;
+  p.T = num_tokens;
+  p.max_len = max_context_len;
+  p.H_q = num_q_heads;
+  p.H_kv = num_kv_heads;
+  p.block_size = block_size;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  const dim3 grid((unsigned)num_tokens, (unsigned)num_kv_heads);
+  if (head_dim == 64)
+    PKV_CUDA(launch_pdl(pkv::prefix_simple_kernel<64>, grid, dim3(128), 0, as_stream(stream), p));
+  else
+    PKV_CUDA(launch_pdl(pkv::prefix_simple_kernel<128>, grid, dim3(128), 0, as_stream(stream), p));
+  return PKV_OK;
+}
+
+pkv_status pkv_verify_draft_tokens(const void* target_probs, int64_t target_stride,
+                                   const void* draft_probs, int64_t draft_seq_stride,
+                                   int64_t draft_tok_stride, const int32_t* tokens,
+                                   const float* uniforms, const int32_t* cu_seqlens,
+                                   int32_t num_seqs, int32_t num_tokens, int32_t max_query_len,
+                                   int32_t vocab, int32_t* out_tokens, int32_t* num_new,
+                                   pkv_dtype prob_dtype, void* stream) {
+  PKV_CHECK(num_seqs >= 0 && num_tokens >= 0 && max_query_len >= 1 && vocab >= 1 &&
+                dtype_ok(prob_dtype),
+            PKV_ERR_INVALID_ARGUMENT, "bad verification sizes");
+  PKV_CHECK(vocab <= (1 << 22), PKV_ERR_UNSUPPORTED, "vocab must be at most 2^22");
+  PKV_CHECK(num_seqs <= 2147483647 / pkv::kVerifyMaxCluster, PKV_ERR_UNSUPPORTED,
+            "too many sequences");
+  if (num_seqs == 0) return PKV_OK;
+  PKV_CHECK(cu_seqlens && out_tokens && num_new &&
+                (num_tokens == 0 || (target_probs && tokens && uniforms)),
+            PKV_ERR_INVALID_ARGUMENT, "null pointer");
+  PKV_CHECK(num_tokens <= 1 || target_stride >= vocab, PKV_ERR_INVALID_ARGUMENT,
+            "target rows overlap");
+  PKV_CHECK(draft_seq_stride >= 0 && draft_tok_stride >= 0, PKV_ERR_INVALID_ARGUMENT,
+            "negative draft strides");
+  const int eb = (int)elem_bytes(prob_dtype);
+  PKV_CHECK(aligned(target_probs, eb) && aligned(draft_probs, eb) && aligned(tokens, 4) &&
+                aligned(uniforms, 4) && aligned(cu_seqlens, 4) && aligned(out_tokens, 4) &&
+                aligned(num_new, 4),
+            PKV_ERR_INVALID_ARGUMENT, "misaligned verification buffers");
+  pkv::VerifyParams p = {target_probs, draft_probs, tokens, uniforms, cu_seqlens, out_tokens,
+                         num_new, target_stride, draft_seq_stride, draft_tok_stride, num_tokens,
+                         max_query_len, vocab};
+  return prob_dtype == PKV_BF16 ? launch_verify<__nv_bfloat16>(p, num_seqs, as_stream(stream))
+                                : launch_verify<float>(p, num_seqs, as_stream(stream));
 }
 
 pkv_status pkv_get_device_error(int32_t* code, void* stream) {

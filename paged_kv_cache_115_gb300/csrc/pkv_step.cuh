@@ -1,0 +1,258 @@
+// Block tables, positions and token slots of one engine step, made from the
+// requests' lengths; integer arithmetic throughout.
+//
+// For request s with lens[s] cached tokens, n new ones (counts[s], -1: over)
+// and held[s] listed blocks:
+//   ctx = lens + n (0 when over), need = ceil(ctx / K),
+//   take = max(0, need - held), give = max(0, held - shared) when over,
+//   cu[s] / cb[s] = sums of n / take over the requests before s.
+// Table entries held .. need - 1 of s become the free blocks head + cb[s] ..
+// of the ring, the blocks of a finished request go to the ring's tail.  lens
+// <= held * K, so every fresh block starts with a new token: the token at an
+// offset 0 writes the table entry, and every token of the block reads its id
+// from the ring.  The part of the ring that is taken from and the part that
+// is given to never overlap (checked: tail + given - head <= ring size).
+#pragma once
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+constexpr int kStepThreads = 1024;
+constexpr int kStepFusedTokens = 4096;   // up to here the one CTA does the token rows too
+
+struct StepParams {
+  const int32_t* lens;
+  const int32_t* counts;
+  int32_t* tables;
+  const int32_t* held;
+  const int32_t* shared;      // may be null
+  int32_t* ring;
+  const int64_t* state;       // {head, tail}
+  int32_t* ctx;               // may be lens
+  int32_t* cu;
+  int32_t* cb;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t* held_out;          // may be held
+  int64_t* state_out;         // may be state
+  int32_t* totals;
+  int64_t ring_size;
+  int64_t num_blocks;
+  int max_blocks;
+  int S;
+  int T;                      // rows of positions / slots
+  int K;
+  int log2_k;                 // >= 0: K is a power of two
+};
+
+struct StepRequest {
+  long long n;                // new tokens
+  int take, give, first;      // blocks taken, given back, first entry given back
+  int ctx, held;
+  bool bad;
+};
+
+__device__ __forceinline__ StepRequest step_request(const StepParams& p, int s) {
+  StepRequest r{};
+  if (s >= p.S) return r;
+  const int len = p.lens[s], cnt = p.counts[s], held = p.held[s];
+  const int sh = p.shared != nullptr ? p.shared[s] : 0;
+  r.held = held;
+  r.first = sh;
+  const long long cap = (long long)p.max_blocks * p.K;
+  const long long ctx = (long long)len + max(cnt, 0);
+  r.bad = len < 0 || cnt < -1 || held < 0 || held > p.max_blocks || sh < 0 ||
+          len > (long long)held * p.K || ctx > cap;
+  if (r.bad) return r;
+  if (cnt < 0) {
+    r.give = max(0, held - sh);
+    return r;
+  }
+  r.n = cnt;
+  r.ctx = (int)ctx;
+  r.take = max(0, (int)((ctx + p.K - 1) / p.K) - held);
+  return r;
+}
+
+// Exclusive sums of (n; take and give packed in one 64-bit word, both below
+// 2^31) over the block; totals returned through tn / tp.  s_a, s_b: 32 words.
+__device__ __forceinline__ void step_scan(long long& n, long long& pk, long long& tn,
+                                          long long& tp, long long* s_a, long long* s_b) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long n0 = n, p0 = pk;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, n, o), b = __shfl_up_sync(0xffffffffu, pk, o);
+    if (lane >= o) {
+      n += a;
+      pk += b;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) {
+    s_a[warp] = n;
+    s_b[warp] = pk;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long a = s_a[lane], b = s_b[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+      if (lane >= o) {
+        a += x;
+        b += y;
+      }
+    }
+    s_a[lane] = a;
+    s_b[lane] = b;
+  }
+  __syncthreads();
+  n += (warp ? s_a[warp - 1] : 0) - n0;
+  pk += (warp ? s_b[warp - 1] : 0) - p0;
+  tn = s_a[31];
+  tp = s_b[31];
+}
+
+// Token row t: its request by binary search in cu, its position, its block
+// (an old table entry or a fresh one from the ring) and slot.
+__device__ __forceinline__ void step_token(const StepParams& p, int t, int total, int64_t head,
+                                           const int32_t* cu, const int32_t* cb) {
+  int pos = -1;
+  int64_t slot = -1;
+  if (t < total) {
+    int lo = 0, hi = p.S;                 // cu[lo] <= t < cu[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cu[mid] <= t) lo = mid; else hi = mid;
+    }
+    const int c0 = cu[lo], c1 = cu[lo + 1], b0 = cb[lo], take = cb[lo + 1] - b0;
+    pos = p.ctx[lo] - (c1 - t);
+    const int held = p.held_out[lo] - take;
+    const int lb = p.log2_k >= 0 ? pos >> p.log2_k : pos / p.K;
+    const int off = pos - lb * p.K;
+    (void)c0;
+    int32_t* entry = p.tables + (int64_t)lo * p.max_blocks + lb;
+    int id;
+    if (lb < held) {
+      id = *entry;
+    } else {
+      id = p.ring[(head + b0 + (lb - held)) % p.ring_size];
+      if (off == 0) *entry = id;
+    }
+    if (id < 0 || id >= p.num_blocks) {
+      record_error(PKV_DEVERR_BLOCK_ID);
+    } else {
+      slot = (int64_t)id * p.K + off;
+    }
+  }
+  p.positions[t] = pos;
+  p.slots[t] = slot;
+}
+
+// One CTA: checks, sums, per-request outputs and the blocks given back.
+// WITH_TOKENS: the token rows too.
+template <bool WITH_TOKENS>
+__global__ void __launch_bounds__(kStepThreads)
+step_requests_kernel(const __grid_constant__ StepParams p) {
+  __shared__ long long s_a[32], s_b[32];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, lane = tid & 31;
+  pdl_wait_primary();
+  const int64_t head = p.state[0], tail = p.state[1];
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  // ---- what the step asks for
+  long long n = 0, pk = 0;
+  bool bad = false;
+  for (int s = tid; s < p.S; s += kStepThreads) {
+    const StepRequest r = step_request(p, s);
+    n += r.n;
+    pk += (long long)r.take << 32 | (unsigned)r.give;
+    bad |= r.bad;
+  }
+  if (bad) s_bad = 1;
+  long long tn, tp;
+  step_scan(n, pk, tn, tp, s_a, s_b);
+  const long long take = tp >> 32, give = tp & 0xffffffffLL;
+  int code = 0;
+  if (s_bad || head < 0 || tail < head || tail - head > p.ring_size ||
+      tail + give - head > p.ring_size)
+    code = 3;
+  else if (tn > p.T)
+    code = 2;
+  else if (take > tail - head)
+    code = 1;
+  __syncthreads();
+  if (tid == 0) {
+    p.totals[0] = code;
+    p.totals[1] = (int)min(tn, (long long)INT32_MAX);
+    p.totals[2] = (int)take;
+    p.totals[3] = (int)give;
+    p.state_out[0] = head + (code ? 0 : take);
+    p.state_out[1] = tail + (code ? 0 : give);
+    p.cu[0] = 0;
+    p.cb[0] = 0;
+    if (code >= 2) record_error(PKV_DEVERR_STEP);
+  }
+  // ---- per request
+  long long cn = 0, cp = 0;             // sums of the earlier tiles
+  for (int s0 = 0; s0 < p.S; s0 += kStepThreads) {
+    const int s = s0 + tid;
+    if (code) {
+      if (s < p.S) {
+        p.ctx[s] = p.lens[s];
+        p.held_out[s] = p.held[s];
+        p.cu[s + 1] = 0;
+        p.cb[s + 1] = 0;
+      }
+      continue;
+    }
+    const StepRequest r = step_request(p, s);
+    long long en = r.n, ep = (long long)r.take << 32 | (unsigned)r.give;
+    step_scan(en, ep, tn, tp, s_a, s_b);
+    en += cn;
+    ep += cp;
+    if (s < p.S) {
+      const bool over = p.counts[s] < 0;
+      p.ctx[s] = r.ctx;
+      p.held_out[s] = over ? 0 : r.held + r.take;
+      p.cu[s + 1] = (int)(en + r.n);
+      p.cb[s + 1] = (int)(ep >> 32) + r.take;
+    }
+    // a warp gives back the blocks of its 32 requests, one after the other
+    unsigned todo = __ballot_sync(0xffffffffu, r.give > 0);
+    while (todo) {
+      const int l = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int give_l = __shfl_sync(0xffffffffu, r.give, l);
+      const int first = __shfl_sync(0xffffffffu, r.first, l);
+      const int64_t to = tail + __shfl_sync(0xffffffffu, (int)(ep & 0xffffffffLL), l);
+      const int32_t* row = p.tables + (int64_t)(s - lane + l) * p.max_blocks + first;
+      for (int i = lane; i < give_l; i += 32) p.ring[(to + i) % p.ring_size] = row[i];
+    }
+    cn += tn;
+    cp += tp;
+  }
+  if constexpr (WITH_TOKENS) {
+    __syncthreads();
+    const int total = code ? 0 : p.cu[p.S];
+    for (int t = tid; t < p.T; t += kStepThreads) step_token(p, t, total, head, p.cu, p.cb);
+  }
+  // later kernels read the tables and lengths before they wait for the
+  // kernel in front of them: no early trigger here, and everything is
+  // visible before the block ends
+  __threadfence();
+}
+
+__global__ void __launch_bounds__(256) step_tokens_kernel(const __grid_constant__ StepParams p) {
+  pdl_wait_primary();
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t >= p.T) return;
+  const int64_t head = p.state_out[0] - (p.totals[0] ? 0 : p.totals[2]);
+  step_token(p, t, p.cu[p.S], head, p.cu, p.cb);
+  __threadfence();
+}
+
+}  // namespace pkv

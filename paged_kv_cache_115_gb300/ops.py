@@ -34,6 +34,7 @@ PKV_F32, PKV_BF16 = 0, 1
 DEVICE_ERRORS = {
     0: "none", 1: "block id out of range", 2: "slot out of range", 3: "copy pair out of range",
     4: "context length out of range", 5: "position beyond block-table row", 6: "pipeline timeout",
+    7: "step refused", 8: "draft token, cu_seqlens or probabilities out of range",
 }
 
 c_i32, c_i64, c_vp, c_sz, c_f = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
@@ -102,6 +103,19 @@ _ws_quant = _sig("pkv_attention_quant_workspace_bytes", c_i32, c_i32, c_i32, c_i
 _attention_quant = _sig("pkv_attention_decode_quant", c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp,
                         c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i64, c_f, c_vp, c_vp, c_sz,
                         c_i32, ctypes.POINTER(KvQuant), ctypes.POINTER(AttentionConfig), c_vp)
+_step_tables = _sig("pkv_step_tables", c_i32, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_i64, c_vp,
+                    c_i32, c_i32, c_i32, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                    c_vp)
+_rope_append = _sig("pkv_qk_norm_rope_append", c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp,
+                    c_vp, c_f, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_i32, c_i32,
+                    c_vp, c_i64, c_vp, c_vp, c_i64, c_i32, c_i32, ctypes.POINTER(KvQuant), c_vp)
+_prefix = _sig("pkv_attention_decode_prefix", c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_i32,
+               c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i64, c_f,
+               c_vp, c_vp, c_sz, c_i32, c_vp)
+_prefix_ws = _sig("pkv_attention_decode_prefix_workspace_bytes", c_i32, c_i32, c_i32, c_i32, c_i32,
+                  c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_sz))
+_verify = _sig("pkv_verify_draft_tokens", c_i32, c_vp, c_i64, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp,
+               c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_i32, c_vp)
 _dev_error = _sig("pkv_get_device_error", c_i32, ctypes.POINTER(c_i32), c_vp)
 
 # bytes of the library's fixed attention scratch (PKV_NOALLOC_SCRATCH_BYTES)
@@ -114,7 +128,9 @@ EXPORTED = ("pkv_status_string", "pkv_last_error_message", "pkv_version", "pkv_s
             "pkv_attention_decode_noalloc", "pkv_kv_append_quant", "pkv_kv_block_copy_quant",
             "pkv_attention_quant_workspace_bytes", "pkv_attention_decode_quant",
             "pkv_attention_prefill", "pkv_attention_prefill_workspace_bytes",
-            "pkv_kv_append_varlen", "pkv_get_device_error")
+            "pkv_kv_append_varlen", "pkv_step_tables", "pkv_qk_norm_rope_append",
+            "pkv_attention_decode_prefix", "pkv_attention_decode_prefix_workspace_bytes",
+            "pkv_verify_draft_tokens", "pkv_get_device_error")
 
 
 class PagedKVError(RuntimeError):
@@ -650,3 +666,283 @@ def prefill_workspace_bytes(num_seqs, num_tokens, max_query_len, max_context_len
                        ctypes.byref(_cfg(kernel, num_splits)), ctypes.byref(out)),
            "pkv_attention_prefill_workspace_bytes")
     return int(out.value)
+
+
+# ---------------------------------------------------------------------------
+# one engine step around the attention: tables from lengths, head norms +
+# rotation + append, attention behind a shared prefix, draft verification
+# ---------------------------------------------------------------------------
+
+def _same_device(named) -> int:
+    """Device index of the CUDA tensors in ``named`` ((name, tensor or None)
+    pairs); they must all live on one device."""
+    dev = -1
+    for name, t in named:
+        if t is None:
+            continue
+        d = t.get_device() if isinstance(t, torch.Tensor) else -1
+        if d < 0:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{name}: CUDA tensors on several devices")
+    return dev
+
+
+def _call_on(dev: int, fn, args, what: str) -> None:
+    """Calls the library with device ``dev`` current and its current stream as
+    the last argument."""
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != PKV_OK:
+        _check(st, what)
+
+
+def _vec(t: torch.Tensor, name: str, dtype, n: int) -> int:
+    """Address of a contiguous vector of ``n`` values."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous with {n} values, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def step_tables(lens: torch.Tensor, counts: torch.Tensor, block_tables: torch.Tensor,
+                held: torch.Tensor, ring: torch.Tensor, ring_state: torch.Tensor,
+                block_size: int, num_blocks: int, shared: Optional[torch.Tensor] = None,
+                num_tokens: Optional[int] = None, context_lens: Optional[torch.Tensor] = None,
+                cu_seqlens: Optional[torch.Tensor] = None,
+                cu_blocks: Optional[torch.Tensor] = None,
+                positions: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                held_out: Optional[torch.Tensor] = None,
+                ring_state_out: Optional[torch.Tensor] = None,
+                totals: Optional[torch.Tensor] = None) -> dict:
+    """Block tables, positions and slots of one step from the requests'
+    lengths, on the GPU.  ``lens`` int32 [S] cached tokens, ``counts`` int32
+    [S] new tokens (-1: the request is over and its blocks return to the free
+    ring), ``block_tables`` int32 [S, max_blocks] updated in place, ``held``
+    int32 [S] listed blocks, ``ring`` int32 [R] with ``ring_state`` int64 [2]
+    = {head, tail}: the free blocks; ``shared`` int32 [S]: leading blocks of a
+    row that are not given back.  ``num_tokens`` bounds the new tokens (rows
+    of ``positions`` / ``slots``; taken from them when given).  Returns a dict
+    of context_lens, cu_seqlens, cu_blocks, positions, slots, held_out,
+    ring_state_out and totals = {code, tokens, blocks taken, blocks given
+    back} (code 0: done, else nothing changed); outputs that are given are
+    written, ``context_lens`` may be ``lens``, ``held_out`` ``held`` and
+    ``ring_state_out`` ``ring_state``."""
+    given = (("lens", lens), ("counts", counts), ("block_tables", block_tables), ("held", held),
+             ("ring", ring), ("ring_state", ring_state), ("shared", shared),
+             ("context_lens", context_lens), ("cu_seqlens", cu_seqlens), ("cu_blocks", cu_blocks),
+             ("positions", positions), ("slots", slots), ("held_out", held_out),
+             ("ring_state_out", ring_state_out), ("totals", totals))
+    dev = _same_device(given)
+    i32, i64 = torch.int32, torch.int64
+    if num_tokens is None:
+        if positions is None and slots is None:
+            raise ValueError("num_tokens (or positions / slots) must be given")
+        num_tokens = (positions if positions is not None else slots).shape[0]
+    S, T = lens.shape[0], int(num_tokens)
+
+    def out(t, n, dtype):
+        return torch.empty(n, dtype=dtype, device=lens.device) if t is None else t
+    context_lens, held_out = out(context_lens, S, i32), out(held_out, S, i32)
+    cu_seqlens, cu_blocks = out(cu_seqlens, S + 1, i32), out(cu_blocks, S + 1, i32)
+    positions, slots = out(positions, T, i32), out(slots, T, i64)
+    ring_state_out, totals = out(ring_state_out, 2, i64), out(totals, 4, i32)
+    if block_tables.dtype != i32 or block_tables.dim() != 2 or block_tables.shape[0] != S or \
+            not block_tables.is_contiguous():
+        raise ValueError("block_tables must be contiguous int32 [num_seqs, max_blocks]")
+    _call_on(dev, _step_tables,
+             (_vec(lens, "lens", i32, S), _vec(counts, "counts", i32, S), block_tables.data_ptr(),
+              block_tables.shape[1], _vec(held, "held", i32, S),
+              None if shared is None else _vec(shared, "shared", i32, S),
+              _vec(ring, "ring", i32, ring.shape[0]), ring.shape[0],
+              _vec(ring_state, "ring_state", i64, 2), S, T, block_size, num_blocks,
+              _vec(context_lens, "context_lens", i32, S),
+              _vec(cu_seqlens, "cu_seqlens", i32, S + 1), _vec(cu_blocks, "cu_blocks", i32, S + 1),
+              _vec(positions, "positions", i32, T), _vec(slots, "slots", i64, T),
+              _vec(held_out, "held_out", i32, S),
+              _vec(ring_state_out, "ring_state_out", i64, 2), _vec(totals, "totals", i32, 4)),
+             "pkv_step_tables")
+    return dict(context_lens=context_lens, cu_seqlens=cu_seqlens, cu_blocks=cu_blocks,
+                positions=positions, slots=slots, held_out=held_out,
+                ring_state_out=ring_state_out, totals=totals)
+
+
+def _token_rows(t: torch.Tensor, name: str, dtype, T: int, H: int, D: int) -> int:
+    """Distance between the tokens of a [T, H, D] tensor whose heads and
+    values are contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[1] != H or t.shape[2] != D:
+        raise ValueError(f"{name} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
+    a, b, c = t.stride()
+    if (c != 1 and D > 1) or (b != D and H > 1):
+        raise ValueError(f"{name}: heads and values of a token must be contiguous")
+    return a if T > 1 else H * D
+
+
+def paged_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                              positions: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                              v_cache: torch.Tensor, cos_sin: torch.Tensor,
+                              q_weight: Optional[torch.Tensor] = None,
+                              k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                              interleaved: bool = False, quant: Optional[KvQuant] = None,
+                              q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """RMS norm of every query and key head (weights [D], None: no norm), the
+    rotation by ``positions`` (int32 [T], negative: padding) through
+    ``cos_sin`` (float32 [max_position, rot_dim]: cosines, then sines; pairs
+    (i, i + rot_dim / 2), or (2 i, 2 i + 1) when ``interleaved``), and the
+    write of K and V into the pages at ``slots`` (int64 [T], -1: none), in one
+    pass.  q [T, H_q, D], k and v [T, H_kv, D] may be cut out of one
+    projection's output (any distance between tokens).  Pools of the same
+    type, or one-byte pools described by ``quant``.  Returns ``q_out`` (new,
+    given, or ``q`` itself for in place)."""
+    T, H_q, D = q.shape
+    nb, K, H_kv, D2 = k_cache.shape
+    if q_out is None:
+        q_out = torch.empty((T, H_q, D), dtype=q.dtype, device=q.device)
+    dev = _same_device((("q", q), ("k", k), ("v", v), ("positions", positions), ("slots", slots),
+                        ("k_cache", k_cache), ("v_cache", v_cache), ("cos_sin", cos_sin),
+                        ("q_weight", q_weight), ("k_weight", k_weight), ("q_out", q_out)))
+    if D2 != D or v_cache.shape != k_cache.shape:
+        raise ValueError("pools must be [num_blocks, block_size, H_kv, D] of q's head size")
+    if quant is None:
+        if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or \
+                not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+            raise TypeError("plain pools must be contiguous and of q's dtype")
+    else:
+        _need_pool(k_cache, "k_cache", quant)
+        _need_pool(v_cache, "v_cache")
+        if quant.format == KV_INT8_TOKEN:
+            for t in getattr(quant, "_scale_tensors", ()):
+                if t.shape[0] != nb * K or t.get_device() != dev:
+                    raise ValueError("token scales must cover every slot of the pool, on its device")
+    if cos_sin.dtype != torch.float32:
+        raise TypeError(f"cos_sin must be float32, got {cos_sin.dtype}")
+    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be contiguous float32 [max_position, rot_dim]")
+    _call_on(dev, _rope_append,
+             (q.data_ptr(), _token_rows(q, "q", q.dtype, T, H_q, D),
+              k.data_ptr(), _token_rows(k, "k", q.dtype, T, H_kv, D),
+              v.data_ptr(), _token_rows(v, "v", q.dtype, T, H_kv, D),
+              None if q_weight is None else _vec(q_weight, "q_weight", q.dtype, D),
+              None if k_weight is None else _vec(k_weight, "k_weight", q.dtype, D), eps,
+              _vec(positions, "positions", torch.int32, T), cos_sin.data_ptr(), cos_sin.shape[0],
+              cos_sin.shape[1], 1 if interleaved else 0, _vec(slots, "slots", torch.int64, T), T,
+              H_q, H_kv, D, q_out.data_ptr(), _token_rows(q_out, "q_out", q.dtype, T, H_q, D),
+              k_cache.data_ptr(), v_cache.data_ptr(), nb, K, _dtype_code(q),
+              None if quant is None else ctypes.byref(quant)), "pkv_qk_norm_rope_append")
+    return q_out
+
+
+def prefix_workspace_bytes(num_seqs: int, num_tokens: int, max_query_len: int,
+                           max_context_len: int, prefix_len: int, num_q_heads: int,
+                           num_kv_heads: int, head_dim: int, block_size: int,
+                           dtype: torch.dtype) -> int:
+    """Workspace bytes of :func:`paged_attention_decode_prefix`."""
+    out = c_sz(0)
+    code = PKV_BF16 if dtype == torch.bfloat16 else PKV_F32
+    _check(_prefix_ws(num_seqs, num_tokens, max_query_len, max_context_len, prefix_len,
+                      num_q_heads, num_kv_heads, head_dim, block_size, code, ctypes.byref(out)),
+           "pkv_attention_decode_prefix_workspace_bytes")
+    return int(out.value)
+
+
+def paged_attention_decode_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  prefix_table: torch.Tensor, block_tables: torch.Tensor,
+                                  context_lens: torch.Tensor, scale: float, prefix_len: int,
+                                  max_context_len: int, cu_seqlens: Optional[torch.Tensor] = None,
+                                  max_query_len: int = 1, out: Optional[torch.Tensor] = None,
+                                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of new tokens for a batch whose sequences share their first
+    ``prefix_len`` tokens (whole blocks, listed in ``prefix_table`` int32),
+    the prefix computed once for all.  Same result as
+    :func:`paged_attention_decode` (``cu_seqlens`` None: one query row a
+    sequence) or :func:`paged_attention_prefill` (packed new tokens, at most 8
+    query rows per KV head) over the full ``block_tables``, whose prefix
+    entries are not read.  The host bounds ``max_query_len`` and
+    ``max_context_len`` size the launch; ``workspace``: uint8 of
+    :func:`prefix_workspace_bytes` bytes (allocated when None)."""
+    if out is None:
+        out = torch.empty_like(q)
+    dev = _same_device((("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
+                        ("prefix_table", prefix_table), ("block_tables", block_tables),
+                        ("context_lens", context_lens), ("cu_seqlens", cu_seqlens), ("out", out),
+                        ("workspace", workspace)))
+    T, H_q, D = q.shape
+    nb, K, H_kv, D2 = k_cache.shape
+    S = context_lens.shape[0]
+    if D2 != D or v_cache.shape != k_cache.shape or out.shape != q.shape:
+        raise ValueError("shape mismatch between q, pools and out")
+    for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("out", out)):
+        if t.dtype != q.dtype or not t.is_contiguous():
+            raise TypeError(f"{name} must be contiguous {q.dtype}")
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or \
+            block_tables.shape[0] != S or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be contiguous int32 [num_seqs, max_blocks]")
+    if prefix_table.shape[0] * K < prefix_len:
+        raise ValueError("prefix_table does not list prefix_len tokens")
+    if workspace is None:
+        workspace = torch.empty(
+            max(prefix_workspace_bytes(S, T, max_query_len, max_context_len, prefix_len, H_q,
+                                       H_kv, D, K, q.dtype), 256), dtype=torch.uint8,
+            device=q.device)
+    _call_on(dev, _prefix,
+             (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+              _vec(prefix_table, "prefix_table", torch.int32, prefix_table.shape[0]),
+              prefix_len, block_tables.data_ptr(), block_tables.shape[1],
+              None if cu_seqlens is None else _vec(cu_seqlens, "cu_seqlens", torch.int32, S + 1),
+              _vec(context_lens, "context_lens", torch.int32, S), S, T, max_query_len,
+              max_context_len, H_q, H_kv, D, K, nb, scale, out.data_ptr(),
+              _vec(workspace, "workspace", torch.uint8, workspace.shape[0]), workspace.shape[0],
+              _dtype_code(q)), "pkv_attention_decode_prefix")
+    return out
+
+
+def verify_draft_tokens(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor],
+                        tokens: torch.Tensor, uniforms: torch.Tensor, cu_seqlens: torch.Tensor,
+                        max_query_len: int, out_tokens: Optional[torch.Tensor] = None,
+                        num_new: Optional[torch.Tensor] = None):
+    """Verify drafted tokens from given random numbers.  Sequence s ran rows
+    cu_seqlens[s] .. cu_seqlens[s+1]-1 of ``tokens`` (int32 [T]: its last
+    token, then its drafts) through the target, ``target_probs`` [T, V];
+    ``draft_probs`` [S, max_query_len - 1, V] (any distances of the first two
+    axes; None: drafts without probabilities), ``uniforms`` float32 [T] in
+    [0, 1).  Returns (out_tokens int32 [S, max_query_len]: accepted drafts,
+    one drawn token, then -1; num_new int32 [S])."""
+    dev = _same_device((("target_probs", target_probs), ("draft_probs", draft_probs),
+                        ("tokens", tokens), ("uniforms", uniforms), ("cu_seqlens", cu_seqlens),
+                        ("out_tokens", out_tokens), ("num_new", num_new)))
+    T, V = target_probs.shape
+    S = cu_seqlens.shape[0] - 1
+    if out_tokens is None:
+        out_tokens = torch.empty((S, max_query_len), dtype=torch.int32, device=tokens.device)
+    if num_new is None:
+        num_new = torch.empty(S, dtype=torch.int32, device=tokens.device)
+    if T > 0 and V > 1 and target_probs.stride(1) != 1:
+        raise ValueError("target_probs: a row must be contiguous")
+    dp, ds, dt = None, 0, 0
+    if draft_probs is not None and max_query_len > 1:
+        if draft_probs.dtype != target_probs.dtype:
+            raise TypeError(f"draft_probs must be {target_probs.dtype}")
+        if draft_probs.dim() != 3 or draft_probs.shape[0] != S or \
+                draft_probs.shape[1] < max_query_len - 1 or draft_probs.shape[2] != V or \
+                (V > 1 and draft_probs.stride(2) != 1):
+            raise ValueError(f"draft_probs must be [{S}, {max_query_len - 1}, {V}] with "
+                             "contiguous rows")
+        dp, ds, dt = draft_probs.data_ptr(), draft_probs.stride(0), draft_probs.stride(1)
+    if out_tokens.dtype != torch.int32 or out_tokens.dim() != 2 or out_tokens.shape[0] != S or \
+            out_tokens.shape[1] != max_query_len or not out_tokens.is_contiguous():
+        raise ValueError(f"out_tokens must be contiguous int32 [{S}, {max_query_len}]")
+    _call_on(dev, _verify,
+             (target_probs.data_ptr(), target_probs.stride(0) if T > 1 else V, dp, ds, dt,
+              _vec(tokens, "tokens", torch.int32, T), _vec(uniforms, "uniforms", torch.float32, T),
+              _vec(cu_seqlens, "cu_seqlens", torch.int32, S + 1), S, T, max_query_len, V,
+              out_tokens.data_ptr(), _vec(num_new, "num_new", torch.int32, S),
+              _dtype_code(target_probs)), "pkv_verify_draft_tokens")
+    return out_tokens, num_new
