@@ -16,8 +16,8 @@
 #include "pkv_prefill.cuh"
 #include "pkv_prefill_tc05.cuh"
 #include "pkv_prefill_tc05x2.cuh"
-#include "pkv_prefix.cuh"
 #include "pkv_reduce.cuh"
+#include "pkv_prefix.cuh"
 #include "pkv_rope.cuh"
 #include "pkv_step.cuh"
 #include "pkv_verify.cuh"
@@ -293,7 +293,7 @@ int* carve_glen(void* ws, const AttnPlan& p, int H_q, int H_kv, int D) {
 }
 
 // ---- tensor-core kernel dispatch ------------------------------------------------
-template <int D, int HPC, int CT, bool B8, bool SH = false>
+template <int D, int HPC, int CT, bool B8, bool SH = false, bool PX = false>
 struct TcInst {
   // stages: as many as fit in ~192 KiB (bf16) / ~203 KiB (one-byte pools)
   // of shared memory, between 2 and 8
@@ -305,17 +305,17 @@ struct TcInst {
   static std::once_flag flags[kMaxDevices];
   static cudaError_t errs[kMaxDevices];
   static pkv_status launch(const pkv::TcParams& prm, int n, int groups, cudaStream_t st, int dev) {
-    auto k = pkv::attn_tc_kernel<D, HPC, NS, CT, B8, SH>;
+    auto k = pkv::attn_tc_kernel<D, HPC, NS, CT, B8, SH, PX>;
     pkv_status s = set_smem_once(k, C::SMEM, flags, errs, dev);
     if (s != PKV_OK) return s;
     PKV_CUDA(launch_pdl(k, dim3(n, groups), dim3(C::THREADS), (size_t)C::SMEM, st, prm));
     return PKV_OK;
   }
 };
-template <int D, int HPC, int CT, bool B8, bool SH>
-std::once_flag TcInst<D, HPC, CT, B8, SH>::flags[kMaxDevices];
-template <int D, int HPC, int CT, bool B8, bool SH>
-cudaError_t TcInst<D, HPC, CT, B8, SH>::errs[kMaxDevices];
+template <int D, int HPC, int CT, bool B8, bool SH, bool PX>
+std::once_flag TcInst<D, HPC, CT, B8, SH, PX>::flags[kMaxDevices];
+template <int D, int HPC, int CT, bool B8, bool SH, bool PX>
+cudaError_t TcInst<D, HPC, CT, B8, SH, PX>::errs[kMaxDevices];
 
 // ---- multi-query (prefill) kernel dispatch -----------------------------------------
 template <int D, int NW>
@@ -466,14 +466,14 @@ pkv_status plan_prefill(int num_seqs, int num_tokens, int max_query_len, int max
   return PKV_OK;
 }
 
-template <int D, int CT, bool B8, bool SH = false>
+template <int D, int CT, bool B8, bool SH = false, bool PX = false>
 pkv_status launch_tc_hpc(int hpc, const pkv::TcParams& prm, int n, int groups, cudaStream_t st,
                          int dev) {
   switch (hpc) {
-    case 8: return TcInst<D, 8, CT, B8, SH>::launch(prm, n, groups, st, dev);
-    case 4: return TcInst<D, 4, CT, B8, SH>::launch(prm, n, groups, st, dev);
-    case 2: return TcInst<D, 2, CT, B8, SH>::launch(prm, n, groups, st, dev);
-    default: return TcInst<D, 1, CT, B8, SH>::launch(prm, n, groups, st, dev);
+    case 8: return TcInst<D, 8, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
+    case 4: return TcInst<D, 4, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
+    case 2: return TcInst<D, 2, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
+    default: return TcInst<D, 1, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
   }
 }
 
@@ -769,14 +769,9 @@ pkv_status launch_rope(int fmt, const pkv::RopeParams& p, cudaStream_t st) {
   }
 }
 
-// ---- shared-prefix attention planning ---------------------------------------------
-struct PrefixPlan {
-  size_t ws_bytes = 0;
-};
-
-pkv_status plan_prefix(int S, int T, int max_q, int max_len, int prefix_len, int H_q, int H_kv,
-                       int D, int K, int64_t num_blocks, float scale, pkv_dtype dt,
-                       PrefixPlan* out) {
+// ---- shared-prefix attention planning and launch -------------------------------
+pkv_status check_prefix(int S, int T, int max_q, int max_len, int prefix_len, int H_q, int H_kv,
+                        int D, int K, int64_t num_blocks, float scale, pkv_dtype dt) {
   PKV_CHECK(S >= 0 && T >= 0 && max_q >= 0 && max_len >= 0 && prefix_len >= 0 && H_q > 0 &&
                 H_kv > 0 && D > 0 && K > 0 && dtype_ok(dt),
             PKV_ERR_INVALID_ARGUMENT, "bad prefix attention sizes");
@@ -790,9 +785,64 @@ pkv_status plan_prefix(int S, int T, int max_q, int max_len, int prefix_len, int
             PKV_ERR_UNSUPPORTED,
             "shared-prefix attention needs bf16, head_dim 64 or 128, block_size 8 or a multiple "
             "of 16, and at most 8 query rows per KV head (max_query_len x G)");
-  PKV_CHECK(S <= pkv::kTcMaxSeqs && H_kv <= 65535, PKV_ERR_UNSUPPORTED, "at most %d sequences",
-            pkv::kTcMaxSeqs);
-  *out = PrefixPlan{};
+  PKV_CHECK(S <= pkv::kTcMaxSeqs && H_kv <= 65535 && T <= S * 8, PKV_ERR_UNSUPPORTED,
+            "at most %d sequences and 8 rows for each", pkv::kTcMaxSeqs);
+  PKV_CHECK((int64_t)T * H_q < (int64_t(1) << 31), PKV_ERR_UNSUPPORTED, "too many query rows");
+  return PKV_OK;
+}
+
+// Workspace: the prefix kernel's CTA count, the first own slot of each token,
+// then partial (m, l) pairs and outputs of the own tokens (a slot per CTA +
+// sequence, max_q rows of H_q heads) and of the prefix (a slot per CTA + item,
+// the rows of the item's tiles).
+struct PrefixPlan {
+  int dev = 0;
+  pkv::PxSplit split = {};
+  int hpc = 1, n_per_group = 1;
+  int tile_rows = 128;        // rows of an item: one tile of 128, or two
+  int64_t own_slots = 0;
+  size_t meta = 0, own_ml = 0, own_o = 0, ml = 0, o = 0, ws_bytes = 0;
+};
+
+pkv_status plan_prefix(int S, int T, int max_q, int prefix_len, int H_q, int H_kv, int D,
+                       PrefixPlan* out) {
+  PrefixPlan p;
+  int sms;
+  pkv_status st = device_facts(&p.dev, &sms);
+  if (st != PKV_OK) return st;
+  p.hpc = tc_hpc(H_kv);
+  const int groups = H_kv / p.hpc, G = H_q / H_kv;
+  p.n_per_group = std::max(1, sms / groups);
+  p.tile_rows = (int64_t)T * G <= pkv::kT5Rows ? pkv::kT5Rows : 2 * pkv::kT5Rows;
+  p.split.prefix_len = prefix_len;
+  p.split.max_q = max_q;
+  p.split.sms = sms;
+  p.split.groups = groups;
+  // relative SM time of a prefix step (64 keys x one KV head) and of an own
+  // chunk (16 tokens x hpc KV heads)
+  p.split.w1 = (p.tile_rows == pkv::kT5Rows ? 7 : 10) * D / 64;
+  p.split.w2 = std::max(7 * p.hpc / 4, 4) * D / 64;
+  p.own_slots = ((int64_t)p.n_per_group + S) * max_q;
+  const int64_t items = ceil_div((int64_t)T * G, p.tile_rows) * H_kv;
+  const int64_t rows = prefix_len > 0 ? (sms + items) * p.tile_rows : 0;
+  p.meta = 256;
+  p.own_ml = p.meta + align256((size_t)T * sizeof(int4));
+  p.own_o = p.own_ml + align256((size_t)p.own_slots * H_q * sizeof(float2));
+  p.ml = p.own_o + align256((size_t)p.own_slots * H_q * (size_t)D * sizeof(float));
+  p.o = p.ml + align256((size_t)rows * sizeof(float2));
+  p.ws_bytes = p.o + align256((size_t)rows * (size_t)D * sizeof(float));
+  *out = p;
+  return PKV_OK;
+}
+
+template <int D, bool SOLO>
+pkv_status launch_prefix_part(const pkv::PxParams& prm, int sms, cudaStream_t st, int dev) {
+  static std::once_flag flags[kMaxDevices];
+  static cudaError_t errs[kMaxDevices];
+  auto k = pkv::prefix_tc05_kernel<D, SOLO>;
+  pkv_status s = set_smem_once(k, pkv::PxCfg<D>::SMEM, flags, errs, dev);
+  if (s != PKV_OK) return s;
+  PKV_CUDA(launch_pdl(k, dim3(sms), dim3(pkv::kPxThreads), (size_t)pkv::PxCfg<D>::SMEM, st, prm));
   return PKV_OK;
 }
 
@@ -1655,10 +1705,12 @@ pkv_status pkv_attention_decode_prefix_workspace_bytes(
     int32_t prefix_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
     int32_t block_size, pkv_dtype dtype, size_t* bytes) {
   PKV_CHECK(bytes != nullptr, PKV_ERR_INVALID_ARGUMENT, "null bytes pointer");
+  pkv_status st = check_prefix(num_seqs, num_tokens, max_query_len, max_context_len, prefix_len,
+                               num_q_heads, num_kv_heads, head_dim, block_size, 1, 1.f, dtype);
+  if (st != PKV_OK) return st;
   PrefixPlan plan;
-  pkv_status st = plan_prefix(num_seqs, num_tokens, max_query_len, max_context_len, prefix_len,
-                              num_q_heads, num_kv_heads, head_dim, block_size, 1, 1.f, dtype,
-                              &plan);
+  st = plan_prefix(num_seqs, num_tokens, max_query_len, prefix_len, num_q_heads, num_kv_heads,
+                   head_dim, &plan);
   if (st != PKV_OK) return st;
   *bytes = plan.ws_bytes;
   return PKV_OK;
@@ -1677,46 +1729,117 @@ pkv_status pkv_attention_decode_prefix(
             PKV_ERR_INVALID_ARGUMENT,
             "without cu_seqlens every sequence has one query row (num_tokens = num_seqs, "
             "max_query_len = 1)");
-  PrefixPlan plan;
-  pkv_status st = plan_prefix(num_seqs, num_tokens, max_query_len, max_context_len, prefix_len,
-                              num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
-                              dtype, &plan);
+  pkv_status st = check_prefix(num_seqs, num_tokens, max_query_len, max_context_len, prefix_len,
+                               num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                               dtype);
   if (st != PKV_OK) return st;
   PKV_CHECK((int64_t)max_blocks_per_seq * block_size <= 2147483647, PKV_ERR_UNSUPPORTED,
             "table row too long");
   if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
   PKV_CHECK(q && k_cache && v_cache && block_tables && context_lens && out &&
-                (prefix_table || prefix_len == 0) && (workspace || plan.ws_bytes == 0),
+                (prefix_table || prefix_len == 0) && workspace,
             PKV_ERR_INVALID_ARGUMENT, "null pointer");
+  PKV_CHECK(aligned(workspace, 256), PKV_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
+  PKV_CHECK(aligned(q, 16) && aligned(out, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) &&
+                aligned(prefix_table, 4) && aligned(block_tables, 4) && aligned(cu_seqlens, 4) &&
+                aligned(context_lens, 4),
+            PKV_ERR_INVALID_ARGUMENT, "q, out and the pools must be 16-byte aligned");
+  PrefixPlan plan;
+  st = plan_prefix(num_seqs, num_tokens, max_query_len, prefix_len, num_q_heads, num_kv_heads,
+                   head_dim, &plan);
+  if (st != PKV_OK) return st;
   PKV_CHECK(workspace_bytes >= plan.ws_bytes, PKV_ERR_WORKSPACE_TOO_SMALL,
             "workspace %zu bytes < %zu needed", workspace_bytes, plan.ws_bytes);
-  PKV_CHECK(aligned(workspace, 256), PKV_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
-  PKV_CHECK(aligned(q, 16) && aligned(out, 16) && aligned(k_cache, 16) && aligned(v_cache, 16),
-            PKV_ERR_INVALID_ARGUMENT, "q, out and the pools must be 16-byte aligned");
-  pkv::PrefixParams p = {};
+  const int D = head_dim, G = num_q_heads / num_kv_heads, sms = plan.split.sms;
+  cudaStream_t strm = as_stream(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const float sl = (float)((double)scale * 1.4426950408889634);
+
+  pkv::PxParams p;
+  memset(&p, 0, sizeof(p));
   p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k = static_cast<const __nv_bfloat16*>(k_cache);
-  p.v = static_cast<const __nv_bfloat16*>(v_cache);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.prefix_table = prefix_table;
-  p.block_tables = block_tables;
   p.cu = cu_seqlens;
   p.lens = context_lens;
+  p.split = plan.split;
+  p.n1 = reinterpret_cast<int*>(ws);
+  p.meta = reinterpret_cast<const int4*>(ws + plan.meta);
+  p.own_ml = reinterpret_cast<const float2*>(ws + plan.own_ml);
+  p.own_o = reinterpret_cast<const float*>(ws + plan.own_o);
+  p.ml = reinterpret_cast<float2*>(ws + plan.ml);
+  p.o = reinterpret_cast<float*>(ws + plan.o);
   p.num_blocks = num_blocks;
-  p.prefix_len = prefix_len;
-  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.own_slots = plan.own_slots;
+  p.own_stride = max_query_len;
+  p.max_len = max_context_len;
+  p.row_tokens = max_blocks_per_seq * block_size;
   p.S = num_seqs;
   p.T = num_tokens;
-  p.max_len = max_context_len;
   p.H_q = num_q_heads;
   p.H_kv = num_kv_heads;
+  p.G = G;
   p.block_size = block_size;
-  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  const dim3 grid((unsigned)num_tokens, (unsigned)num_kv_heads);
-  if (head_dim == 64)
-    PKV_CUDA(launch_pdl(pkv::prefix_simple_kernel<64>, grid, dim3(128), 0, as_stream(stream), p));
+  p.scale_log2 = sl;
+
+  pkv::TcParams t;
+  memset(&t, 0, sizeof(t));
+  t.q = p.q;
+  t.out = p.out;
+  t.block_tables = block_tables;
+  t.context_lens = context_lens;
+  t.ws.meta = reinterpret_cast<int4*>(ws + plan.meta);
+  t.ws.ml = reinterpret_cast<float2*>(ws + plan.own_ml);
+  t.ws.o = reinterpret_cast<float*>(ws + plan.own_o);
+  t.ws.pmax = 1;
+  t.num_blocks = num_blocks;
+  t.max_blocks_per_seq = max_blocks_per_seq;
+  t.num_seqs = num_seqs;
+  t.max_len = max_context_len;
+  t.H_q = num_q_heads;
+  t.G = G;
+  t.block_size = block_size;
+  t.scale_log2 = sl;
+  t.cu_seqlens = cu_seqlens;
+  t.share_m = 1;
+  t.px = plan.split;
+  t.px_heads = num_kv_heads;
+  t.num_tokens = num_tokens;
+  st = encode_pool_map_heads(&t.tmap_k, k_cache, num_blocks, block_size, num_kv_heads, D, plan.hpc,
+                             false);
+  if (st == PKV_OK)
+    st = encode_pool_map_heads(&t.tmap_v, v_cache, num_blocks, block_size, num_kv_heads, D,
+                               plan.hpc, false);
+  if (st == PKV_OK && prefix_len > 0) {
+    st = encode_pool_map(&p.tmap_k, k_cache, num_blocks, block_size, num_kv_heads, D);
+    if (st == PKV_OK)
+      st = encode_pool_map(&p.tmap_v, v_cache, num_blocks, block_size, num_kv_heads, D);
+    if (st == PKV_OK) {
+      const bool solo = plan.tile_rows == pkv::kT5Rows;
+      if (D == 64)
+        st = solo ? launch_prefix_part<64, true>(p, sms, strm, plan.dev)
+                  : launch_prefix_part<64, false>(p, sms, strm, plan.dev);
+      else
+        st = solo ? launch_prefix_part<128, true>(p, sms, strm, plan.dev)
+                  : launch_prefix_part<128, false>(p, sms, strm, plan.dev);
+    }
+  }
+  if (st != PKV_OK) return st;
+  const bool b8 = block_size < pkv::kTile;
+  if (D == 64)
+    st = b8 ? launch_tc_hpc<64, 0, true, false, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev)
+            : launch_tc_hpc<64, 0, false, false, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev);
   else
-    PKV_CUDA(launch_pdl(pkv::prefix_simple_kernel<128>, grid, dim3(128), 0, as_stream(stream), p));
+    st = b8 ? launch_tc_hpc<128, 0, true, false, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev)
+            : launch_tc_hpc<128, 0, false, false, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev);
+  if (st != PKV_OK) return st;
+  const dim3 grid((unsigned)ceil_div((int64_t)num_tokens * num_q_heads, pkv::kPxMergeWarps));
+  if (D == 64)
+    PKV_CUDA(launch_pdl(pkv::prefix_merge_kernel<64>, grid, dim3(pkv::kPxMergeWarps * 32), 0, strm, p,
+                        plan.tile_rows));
+  else
+    PKV_CUDA(launch_pdl(pkv::prefix_merge_kernel<128>, grid, dim3(pkv::kPxMergeWarps * 32), 0, strm, p,
+                        plan.tile_rows));
   return PKV_OK;
 }
 

@@ -45,6 +45,40 @@ constexpr int kBoxBytes = kTile * 128;
 // 3 bf16 K with FP8 V)
 constexpr int tc_chunk_tokens(int ct) { return ct == 1 || ct == 2 ? 2 * kTile : kTile; }
 
+// Attention behind a shared prefix (pkv_prefix.cuh): the prefix kernel and
+// this kernel (instantiated with PX, on the tokens from prefix_len on) share
+// the SMs.  Both derive the shares from the same counts: `steps` of the prefix
+// kernel weigh w1, chunks of this one w2.
+struct PxSplit {
+  int prefix_len;
+  int max_q;       // bound on the new tokens of a sequence
+  int sms;         // CTAs of both kernels together
+  int groups;      // KV-head groups of this kernel
+  int w1, w2;
+};
+
+// 16-token chunks of sequence s's own tokens (L: its clamped length; 0 for an
+// inconsistent sequence, or one without query rows).
+__device__ __forceinline__ int px_own_chunks(const PxSplit& x, const int32_t* cu, int T, int s,
+                                             int L) {
+  if (cu != nullptr) {
+    const int c0 = cu[s], c1 = cu[s + 1], n = c1 - c0;
+    if (n <= 0 || c0 < 0 || c1 > T || n > x.max_q || n > L) return 0;
+  }
+  return L > x.prefix_len ? (L - x.prefix_len + kTile - 1) / kTile : 0;
+}
+
+// CTAs of the prefix kernel (0 without prefix steps).
+__host__ __device__ __forceinline__ int px_ctas(const PxSplit& x, long long steps,
+                                                long long chunks) {
+  if (steps == 0) return 0;
+  const long long a = steps * x.w1, b = chunks * x.groups * x.w2;
+  long long n = b == 0 ? x.sms : (x.sms * a + (a + b) / 2) / (a + b);
+  if (b > 0 && n > x.sms - x.groups) n = x.sms - x.groups;
+  if (n > steps) n = steps;
+  return n < 1 ? 1 : (int)n;
+}
+
 struct TcParams {
   CUtensorMap tmap_k;
   CUtensorMap tmap_v;
@@ -80,6 +114,12 @@ struct TcParams {
   // decode: slot distance between the member regions of a shared unit (CTAs
   // + units of the launch; 0 without shared-prefix groups)
   int slot_stride;
+  // behind a shared prefix (kernel instantiated with PX): every partition
+  // writes a partial state, of query row i of the sequence in slot (CTA + unit)
+  // * max_q + i; meta[row] = {first slot, partials, 0, 0}
+  PxSplit px;
+  int num_tokens;           // rows of q / out
+  int px_heads;             // KV heads
 };
 
 // Pool formats of the kernel: CT 0 = bf16, 1 = FP8 e4m3 (per-tensor scale),
@@ -241,7 +281,7 @@ __host__ __device__ __forceinline__ int4 tc_seq_meta(const int* cstart, int s, i
   return r;
 }
 
-template <int D, int HPC, int NS, int CT = 0, bool B8 = false, bool SH = false>
+template <int D, int HPC, int NS, int CT = 0, bool B8 = false, bool SH = false, bool PX = false>
 __global__ void __launch_bounds__(TcCfg<D, HPC, NS, CT, B8>::THREADS, 1)
 attn_tc_kernel(const __grid_constant__ TcParams p) {
   using C = TcCfg<D, HPC, NS, CT, B8>;
@@ -250,6 +290,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   // heads of a group's members side by side), one otherwise
   constexpr int NB = SH ? 2 : 1;
   static_assert(!SH || CT == 0, "shared-prefix groups need bf16 pools");
+  static_assert(!PX || (CT == 0 && !SH), "shared-prefix attention needs bf16 pools");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -272,7 +313,12 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   // unit u: first sequence s0 (its table row and first query row), sequences
   // it serves (0: none), tokens [t0, end) of the sequence
   auto unit = [&](int u, int& s0, int& rows, int& t0, int& end) {
-    if constexpr (!SH) {
+    if constexpr (PX) {
+      s0 = u;
+      rows = 1;
+      t0 = p.px.prefix_len;
+      end = max(seq_len(u), t0);
+    } else if constexpr (!SH) {
       s0 = u;
       rows = 1;
       t0 = 0;
@@ -295,6 +341,15 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   };
   // chunks of unit u (none for a sequence without query rows)
   auto nchunks = [&](int u) -> int {
+    if constexpr (PX) {
+      const int L = seq_len(u);
+      if (cu != nullptr) {
+        const int c0 = cu[u], c1 = cu[u + 1];
+        if (c1 - c0 < 0 || c0 < 0 || c1 > p.num_tokens || c1 - c0 > p.px.max_q || c1 - c0 > L)
+          record_error(PKV_DEVERR_CONTEXT_LEN);
+      }
+      return px_own_chunks(p.px, cu, p.num_tokens, u, L);
+    }
     int s0, rows, t0, end;
     unit(u, s0, rows, t0, end);
     if (rows == 0) return 0;
@@ -360,7 +415,16 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   // Split over at most T CTAs so that every working CTA owns >= 1 chunk and a
   // unit's partial index (CTA - first CTA of the unit) stays below min(n,
   // chunks of the unit).  CTAs past n only do bookkeeping.
-  const int n = (int)(T < (long long)gridDim.x ? (T > 0 ? T : 1) : (long long)gridDim.x);
+  long long most = gridDim.x;
+  if constexpr (PX) {
+    // the SMs that the prefix kernel leaves
+    const int nt = cu == nullptr ? S : max(0, min(cu[S], p.num_tokens));
+    const int tile = p.num_tokens * p.G <= 128 ? 128 : 256;
+    const long long steps = (long long)((nt * p.G + tile - 1) / tile) * p.px_heads *
+                            ((p.px.prefix_len + 63) / 64);
+    most = max(1, min((int)gridDim.x, (p.px.sms - px_ctas(p.px, steps, T)) / p.px.groups));
+  }
+  const int n = (int)(T < most ? (T > 0 ? T : 1) : most);
   const int cta = blockIdx.x, group = blockIdx.y;
   const int head0 = group * HPC;
   const int G = p.G, H_q = p.H_q;
@@ -380,7 +444,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       const int u = seq_of_chunk(cstart, NU, c);
       int s0, rows, t0, end;
       unit(u, s0, rows, t0, end);
-      const int L = (TL > 1 || sbl || SH) ? end : 1 << 30;
+      const int L = (TL > 1 || sbl || SH || PX) ? end : 1 << 30;
 #pragma unroll
       for (int t = 0; t < TL; ++t) {
 #pragma unroll
@@ -403,13 +467,30 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   // writes the tables) before waiting for the previous kernel
   int row[TL][2];
   if (warp == HPC && cb < ce) tile_rows(cb, row);
-  if constexpr (!SH) pdl_wait_primary();
+  if constexpr (!SH && !PX) pdl_wait_primary();
+  // behind a shared prefix: the kernel in front (the prefix part) released
+  // this one after its own wait, so what earlier kernels wrote is there; this
+  // kernel ends after it (the merge waits for this one), by its first CTA
+  if constexpr (PX) {
+    if (p.px.prefix_len == 0) pdl_wait_primary();
+  }
+  auto px_leave = [&]() {
+    if constexpr (PX) {
+      if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait_primary();
+    }
+  };
 
   // ---- bookkeeping (sequence s by CTA s mod grid): partial slots of each
   // output row, and zero outputs of empty sequences
   for (int s = cta + tid * (int)gridDim.x; s < S; s += C::THREADS * (int)gridDim.x) {
     const int4 mt = tc_seq_meta(cstart, s, M, T, n, p.slot_stride);
-    if (mt.y + mt.w == 0) {
+    if constexpr (PX) {
+      if (group != 0) continue;
+      const int c0 = cu == nullptr ? s : cu[s], c1 = cu == nullptr ? s + 1 : cu[s + 1];
+      if (c0 < 0 || c1 > p.num_tokens || c1 - c0 > p.px.max_q) continue;
+      for (int r = c0; r < c1; ++r)
+        p.ws.meta[r] = make_int4(mt.x * p.px.max_q + r - c0, mt.y, 0, 0);
+    } else if (mt.y + mt.w == 0) {
       // empty context: zero output (decode); a sequence without query rows
       // has no output
       if (cu == nullptr) {
@@ -426,7 +507,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       }
     }
   }
-  if (cb >= ce) return;
+  if (cb >= ce) {
+    px_leave();
+    return;
+  }
 
   if (warp == HPC) {
     // =================== producer ===================
@@ -505,6 +589,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       for (int kk = max(0, k - NS); kk < k; ++kk)
         mbar_wait_bounded(bar_full + 8 * (kk % NS), (kk / NS) & 1);
     }
+    px_leave();
     return;
   }
 
@@ -964,7 +1049,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           // row * Pmax + the partition's index within the sequence for several
           // query tokens
           int np, slot;
-          if (cu == nullptr) {
+          if constexpr (PX) {
+            np = 2;                              // merged with the prefix part
+            slot = (cta + u) * p.px.max_q + cc / G;
+          } else if (cu == nullptr) {
             const int4 mt = tc_seq_meta(cstart, row / H_q, M, T, n, p.slot_stride);
             np = mt.y + mt.w;
             slot = (row / H_q - qr0) * p.slot_stride + cta + u;
@@ -1003,6 +1091,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       }
     }
   }
+  px_leave();
 }
 
 // ===========================================================================
