@@ -103,6 +103,14 @@ __device__ __forceinline__ bool px_row(const PxParams& p, int t, int& s, int& i,
   return p.cu == nullptr || n <= L;
 }
 
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
 // 64 consecutive fp32 columns of this thread's TMEM lane, landed.
 __device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, float (&v)[64]) {
   uint32_t a[32], b[32];
@@ -275,28 +283,30 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p) {
     }
   } else if (warp == 9 || warp == 11) {
     // =================== MMA issue: warp 9 S = Q K^T, warp 11 O += P V ===================
-    if (lane == 0) {
-      bool ok = true;
-      int kt = (int)(g0 % nkt), seg = 0;
-      for (int g = 0; g < ng && ok; ++g) {
-        const bool first = g == 0 || kt == 0;              // of a segment
-        if (warp == 9) {
-          const int stage = g % kPxKStages, b = g & 1;
-          if (first) {
-            for (int x = 0; x < NT && ok; ++x) ok = mbar_wait_bounded(q_full(x), seg & 1);
-            ++seg;
-          }
-          ok = ok && mbar_wait_bounded(k_full + 8 * stage, (g / kPxKStages) & 1);
-          const uint32_t kb = sbase + C::K_OFF + stage * C::KBYTES;
-          for (int x = 0; x < NT && ok; ++x) {
-            // S buffer b of tile x holds P(g - 2) until O += P(g - 2) V is done
-            if (g >= 2 && !mbar_wait_bounded(p_free(x, b), ((g >> 1) - 1) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t qb = sbase + C::Q_OFF + x * C::QBYTES;
-            const uint32_t sd = tmem + x * 256 + b * kPxBN;
+    // The whole warp walks the loop and one elected lane issues: under a lane
+    // test the compiler cannot tell that the descriptors are uniform, and an
+    // MMA took 80 to 90 cycles to issue.
+    bool ok = true;
+    int kt = (int)(g0 % nkt), seg = 0;
+    for (int g = 0; g < ng && ok; ++g) {
+      const bool first = g == 0 || kt == 0;                // of a segment
+      if (warp == 9) {
+        const int stage = g % kPxKStages, b = g & 1;
+        if (first) {
+          for (int x = 0; x < NT && ok; ++x) ok = mbar_wait_bounded(q_full(x), seg & 1);
+          ++seg;
+        }
+        ok = ok && mbar_wait_bounded(k_full + 8 * stage, (g / kPxKStages) & 1);
+        const uint32_t kb = sbase + C::K_OFF + stage * C::KBYTES;
+        for (int x = 0; x < NT && ok; ++x) {
+          // S buffer b of tile x holds P(g - 2) until O += P(g - 2) V is done
+          ok = __all_sync(0xffffffffu,
+                          g < 2 || mbar_wait_bounded(p_free(x, b), ((g >> 1) - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t qb = sbase + C::Q_OFF + x * C::QBYTES;
+          const uint32_t sd = tmem + x * 256 + b * kPxBN;
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint64_t ad = umma_desc_sw128(qb + (kk >> 2) * C::QHALF + (kk & 3) * 32, 16, 1024);
@@ -306,33 +316,36 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p) {
             umma_commit(s_full(x, b));
             umma_commit(k_empty + 8 * stage);
           }
-        } else {
-          const int stage = g % kPxVStages;
-          ok = mbar_wait_bounded(v_full + 8 * stage, (g / kPxVStages) & 1);
-          const uint32_t vb = sbase + C::V_OFF + stage * C::KBYTES;
-          for (int x = 0; x < NT && ok; ++x) {
-            if (!mbar_wait_bounded(p_full(x, g & 1), (g >> 1) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t pt = tmem + x * 256 + (g & 1) * kPxBN;
-            const uint32_t od = tmem + x * 256 + 128;
+          __syncwarp();
+        }
+      } else {
+        const int stage = g % kPxVStages;
+        ok = mbar_wait_bounded(v_full + 8 * stage, (g / kPxVStages) & 1);
+        const uint32_t vb = sbase + C::V_OFF + stage * C::KBYTES;
+        for (int x = 0; x < NT && ok; ++x) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(p_full(x, g & 1), (g >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t pt = tmem + x * 256 + (g & 1) * kPxBN;
+          const uint32_t od = tmem + x * 256 + 128;
+          if (elect_one()) {
 #pragma unroll
             for (int k16 = 0; k16 < kPxBN / 16; ++k16)
               umma_ts(od, pt + k16 * 8, umma_desc_sw128(vb + k16 * 2048, C::KVHALF, 1024),
                       C::IDESC_PV, (!first || k16 > 0) ? 1u : 0u);
             umma_commit(o_done(x));
             umma_commit(p_free(x, g & 1));
+            if (x == NT - 1) umma_commit(v_empty + 8 * stage);
           }
-          if (ok) umma_commit(v_empty + 8 * stage);
+          __syncwarp();
         }
-        kt = kt + 1 == nkt ? 0 : kt + 1;
       }
-      if (!ok) record_error(PKV_DEVERR_TIMEOUT);
-      umma_commit(mma_idle);
-      mbar_wait_bounded(mma_idle, 0);
+      kt = kt + 1 == nkt ? 0 : kt + 1;
     }
+    if (!ok && lane == 0) record_error(PKV_DEVERR_TIMEOUT);
+    if (elect_one()) umma_commit(mma_idle);
+    __syncwarp();
+    mbar_wait_bounded(mma_idle, 0);
   } else if ((warp >> 2) < NT) {
     // =================== softmax warps: warps 0-3 tile A, 4-7 tile B ===================
     const int x = warp >> 2;
