@@ -741,22 +741,55 @@ pkv_status check_quant(const pkv_kv_quant* q, bool need_token_scales) {
 }
 
 // ---- norm + rotation + append dispatch -------------------------------------------
-template <typename T, int FMT>
-pkv_status launch_rope_fmt(const pkv::RopeParams& p, cudaStream_t st) {
-  const size_t smem = FMT == PKV_KV_INT8_TOKEN ? 2 * sizeof(float) * (size_t)p.H_kv * p.D : 0;
-  if (smem > 0) {
-    static std::once_flag flags[kMaxDevices];
-    static cudaError_t errs[kMaxDevices];
+template <typename Kernel>
+pkv_status launch_rope_kernel(Kernel k, int fmt, const pkv::RopeParams& p, cudaStream_t st,
+                              std::once_flag (&flags)[kMaxDevices],
+                              cudaError_t (&errs)[kMaxDevices]) {
+  size_t smem = 0;
+  if (fmt == PKV_KV_INT8_TOKEN) {
+    smem = 2 * sizeof(float) * (size_t)p.H_kv * p.D;
     int dev, sms;
     pkv_status s = device_facts(&dev, &sms);
     if (s == PKV_OK)
-      s = set_smem_once(pkv::rope_any_kernel<T, FMT>, 2 * (int)sizeof(float) * pkv::kRopeMaxInt8Row,
-                        flags, errs, dev);
+      s = set_smem_once(k, 2 * (int)sizeof(float) * pkv::kRopeMaxInt8Row, flags, errs, dev);
     if (s != PKV_OK) return s;
   }
-  PKV_CUDA(launch_pdl(pkv::rope_any_kernel<T, FMT>, dim3((unsigned)p.T), dim3(pkv::kRopeThreads),
-                      smem, st, p));
+  PKV_CUDA(launch_pdl(k, dim3((unsigned)p.T), dim3(pkv::kRopeThreads), smem, st, p));
   return PKV_OK;
+}
+
+template <typename T, int FMT, int D>
+pkv_status launch_rope_vec(const pkv::RopeParams& p, cudaStream_t st) {
+  static std::once_flag flags[2][kMaxDevices];
+  static cudaError_t errs[2][kMaxDevices];
+  if (p.interleaved)
+    return launch_rope_kernel(pkv::rope_vec_kernel<T, FMT, D, true>, FMT, p, st, flags[1], errs[1]);
+  return launch_rope_kernel(pkv::rope_vec_kernel<T, FMT, D, false>, FMT, p, st, flags[0], errs[0]);
+}
+
+// The vectorised kernel needs every row on a 16-byte boundary (pools: 16
+// bytes too) and the rotation in whole lanes of V values.
+template <typename T>
+bool rope_vec_ok(const pkv::RopeParams& p) {
+  constexpr int V = 16 / sizeof(T);
+  const bool dim = p.D == 64 || p.D == 128 || (p.D == 256 && sizeof(T) == 2);
+  return dim && p.rot % (p.interleaved ? V : 2 * V) == 0 && p.q_stride % V == 0 &&
+         p.k_stride % V == 0 && p.v_stride % V == 0 && p.qo_stride % V == 0 && aligned(p.q, 16) &&
+         aligned(p.k, 16) && aligned(p.v, 16) && aligned(p.q_out, 16) && aligned(p.wq, 16) &&
+         aligned(p.wk, 16) && aligned(p.cos_sin, 16) && aligned(p.k_cache, 16) &&
+         aligned(p.v_cache, 16);
+}
+
+template <typename T, int FMT>
+pkv_status launch_rope_fmt(const pkv::RopeParams& p, cudaStream_t st) {
+  if (rope_vec_ok<T>(p)) {
+    if (p.D == 64) return launch_rope_vec<T, FMT, 64>(p, st);
+    if (p.D == 128) return launch_rope_vec<T, FMT, 128>(p, st);
+    if constexpr (sizeof(T) == 2) return launch_rope_vec<T, FMT, 256>(p, st);
+  }
+  static std::once_flag flags[kMaxDevices];
+  static cudaError_t errs[kMaxDevices];
+  return launch_rope_kernel(pkv::rope_any_kernel<T, FMT>, FMT, p, st, flags, errs);
 }
 
 template <typename T>
@@ -791,8 +824,8 @@ pkv_status check_prefix(int S, int T, int max_q, int max_len, int prefix_len, in
   return PKV_OK;
 }
 
-// Workspace: the prefix kernel's CTA count, the first own slot of each token,
-// then partial (m, l) pairs and outputs of the own tokens (a slot per CTA +
+// Workspace: the CTAs of each item, the first own slot of each token, then
+// partial (m, l) pairs and outputs of the own tokens (a slot per CTA +
 // sequence, max_q rows of H_q heads) and of the prefix (a slot per CTA + item,
 // the rows of the item's tiles).
 struct PrefixPlan {
@@ -801,6 +834,7 @@ struct PrefixPlan {
   int hpc = 1, n_per_group = 1;
   int tile_rows = 128;        // rows of an item: one tile of 128, or two
   int64_t own_slots = 0;
+  int merge_wpr = 1;          // merge: warps per (token, head) row
   size_t meta = 0, own_ml = 0, own_o = 0, ml = 0, o = 0, ws_bytes = 0;
 };
 
@@ -819,13 +853,21 @@ pkv_status plan_prefix(int S, int T, int max_q, int prefix_len, int H_q, int H_k
   p.split.sms = sms;
   p.split.groups = groups;
   // relative SM time of a prefix step (64 keys x one KV head) and of an own
-  // chunk (16 tokens x hpc KV heads)
-  p.split.w1 = (p.tile_rows == pkv::kT5Rows ? 7 : 10) * D / 64;
-  p.split.w2 = std::max(7 * p.hpc / 4, 4) * D / 64;
+  // chunk (16 tokens x hpc KV heads), from sweeps of the quotient: with two
+  // query tiles an item (1024 sequences over 2048 + ~520 tokens) 10 / 24 gives
+  // 924 us, 20 / 24 453, 40 / 24 363, 80 / 24 364, and (61 x ~2.5 rows over
+  // 4112 + ~350) 62, 46, 41, 46; with one (8 sequences over 131072 + ~1000)
+  // 8 / 24 gives 116 us, 22 / 24 108, 32 / 24 120
+  p.split.w1 = p.tile_rows == pkv::kT5Rows ? 22 : 40;
+  p.split.w2 = std::max(3 * p.hpc, 6);
   p.own_slots = ((int64_t)p.n_per_group + S) * max_q;
   const int64_t items = ceil_div((int64_t)T * G, p.tile_rows) * H_kv;
   const int64_t rows = prefix_len > 0 ? (sms + items) * p.tile_rows : 0;
-  p.meta = 256;
+  // partials of a row: CTAs per item, one more where shares cross items, and
+  // one or two of its own tokens; eight to a warp
+  const int64_t parts = prefix_len > 0 ? sms / std::max<int64_t>(items, 1) + 3 : 2;
+  while (p.merge_wpr < 8 && 8 * p.merge_wpr < parts) p.merge_wpr *= 2;
+  p.meta = align256((size_t)items * sizeof(int2));
   p.own_ml = p.meta + align256((size_t)T * sizeof(int4));
   p.own_o = p.own_ml + align256((size_t)p.own_slots * H_q * sizeof(float2));
   p.ml = p.own_o + align256((size_t)p.own_slots * H_q * (size_t)D * sizeof(float));
@@ -844,6 +886,25 @@ pkv_status launch_prefix_part(const pkv::PxParams& prm, int sms, cudaStream_t st
   if (s != PKV_OK) return s;
   PKV_CUDA(launch_pdl(k, dim3(sms), dim3(pkv::kPxThreads), (size_t)pkv::PxCfg<D>::SMEM, st, prm));
   return PKV_OK;
+}
+
+template <int D, int WPR>
+pkv_status launch_prefix_merge_w(const pkv::PxParams& prm, int tile_rows, cudaStream_t st) {
+  const int64_t rows = (int64_t)prm.T * prm.H_q;
+  PKV_CUDA(launch_pdl(pkv::prefix_merge_kernel<D, WPR>,
+                      dim3((unsigned)ceil_div(rows * WPR, pkv::kPxMergeWarps)),
+                      dim3(pkv::kPxMergeWarps * 32), 0, st, prm, tile_rows));
+  return PKV_OK;
+}
+
+template <int D>
+pkv_status launch_prefix_merge(const pkv::PxParams& prm, const PrefixPlan& plan, cudaStream_t st) {
+  switch (plan.merge_wpr) {
+    case 1: return launch_prefix_merge_w<D, 1>(prm, plan.tile_rows, st);
+    case 2: return launch_prefix_merge_w<D, 2>(prm, plan.tile_rows, st);
+    case 4: return launch_prefix_merge_w<D, 4>(prm, plan.tile_rows, st);
+    default: return launch_prefix_merge_w<D, 8>(prm, plan.tile_rows, st);
+  }
 }
 
 // ---- draft verification dispatch ----------------------------------------------------
@@ -1763,7 +1824,7 @@ pkv_status pkv_attention_decode_prefix(
   p.cu = cu_seqlens;
   p.lens = context_lens;
   p.split = plan.split;
-  p.n1 = reinterpret_cast<int*>(ws);
+  p.items = reinterpret_cast<int2*>(ws);
   p.meta = reinterpret_cast<const int4*>(ws + plan.meta);
   p.own_ml = reinterpret_cast<const float2*>(ws + plan.own_ml);
   p.own_o = reinterpret_cast<const float*>(ws + plan.own_o);
@@ -1833,14 +1894,7 @@ pkv_status pkv_attention_decode_prefix(
     st = b8 ? launch_tc_hpc<128, 0, true, false, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev)
             : launch_tc_hpc<128, 0, false, false, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev);
   if (st != PKV_OK) return st;
-  const dim3 grid((unsigned)ceil_div((int64_t)num_tokens * num_q_heads, pkv::kPxMergeWarps));
-  if (D == 64)
-    PKV_CUDA(launch_pdl(pkv::prefix_merge_kernel<64>, grid, dim3(pkv::kPxMergeWarps * 32), 0, strm, p,
-                        plan.tile_rows));
-  else
-    PKV_CUDA(launch_pdl(pkv::prefix_merge_kernel<128>, grid, dim3(pkv::kPxMergeWarps * 32), 0, strm, p,
-                        plan.tile_rows));
-  return PKV_OK;
+  return D == 64 ? launch_prefix_merge<64>(p, plan, strm) : launch_prefix_merge<128>(p, plan, strm);
 }
 
 pkv_status pkv_verify_draft_tokens(const void* target_probs, int64_t target_stride,

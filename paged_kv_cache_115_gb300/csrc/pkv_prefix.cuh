@@ -35,7 +35,7 @@ struct PxParams {
   const int32_t* cu;                  // null: one query row per sequence
   const int32_t* lens;
   PxSplit split;                      // how the SMs are shared with the decode kernel
-  int* n1;                            // CTAs that took prefix steps, for the merge
+  int2* items;                        // {first CTA, CTAs} of each item, for the merge
   const int4* meta;                   // own part: {first slot, partials, 0, 0} of each token
   const float2* own_ml;               // own part: [slot][H_q]
   const float* own_o;
@@ -186,8 +186,13 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p) {
   const int nkt = (P + kPxBN - 1) / kPxBN;
   const long long steps = (long long)npairs * p.H_kv * nkt;
   const int n1 = px_ctas(p.split, steps, chunks);
-  if (cta == 0 && tid == 0) *p.n1 = n1;
   if (cta >= n1) return;
+  if (cta == n1 - 1) {                                     // which CTAs hold steps of each item
+    for (int x = tid; x < npairs * p.H_kv; x += kPxThreads) {
+      const int a = cta_of_chunk((long long)x * nkt, steps, n1);
+      p.items[x] = make_int2(a, cta_of_chunk((long long)(x + 1) * nkt - 1, steps, n1) - a + 1);
+    }
+  }
   const long long g0 = cta * steps / n1;
   const int ng = (int)((cta + 1) * steps / n1 - g0);       // steps of this CTA
 
@@ -489,79 +494,109 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p) {
 }
 
 // ===========================================================================
-// Merge: one warp per (token, query head) over the partial states of its own
-// tokens and of the prefix.
+// Merge of the partial states of a (token, query head) row: its own tokens'
+// (slots of meta[t]) and the prefix's (items[item] = {first CTA, CTAs}).  WPR
+// warps per row take eight partials at a time, all of them in flight at once;
+// a row's time is that of its loads, and with few rows (a small batch over a
+// long prefix) several warps share one.
 // ===========================================================================
 constexpr int kPxMergeWarps = 8;
+constexpr int kPxMergeBatch = 8;
 
-template <int D>
+template <int D, int WPR>
 __global__ void __launch_bounds__(kPxMergeWarps * 32)
 prefix_merge_kernel(const __grid_constant__ PxParams p, int tile_rows) {
-  constexpr int V = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long pair = (long long)blockIdx.x * kPxMergeWarps + warp;
-  const int t = (int)(pair / p.H_q), h = (int)(pair - (long long)t * p.H_q);
+  constexpr int V = D / 32, RPC = kPxMergeWarps / WPR;
+  __shared__ float s_acc[WPR > 1 ? kPxMergeWarps : 1][D];
+  __shared__ float s_m[kPxMergeWarps], s_l[kPxMergeWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
+  const int pair = blockIdx.x * RPC + warp / WPR;
+  const int t = pair / p.H_q, h = pair - t * p.H_q;
   pdl_wait_primary();
   pdl_launch_dependents();
   const int tokens = px_tokens(p.cu, p.S, p.T);
-  if (t >= tokens) return;
   int s, i, n, L;
-  if (!px_row(p, t, s, i, n, L)) return;       // skipped (the decode kernel reports it)
-  // own part
-  const int4 mt = p.meta[t];
-  int np_own = mt.y;
-  if (np_own < 0 || mt.x < 0 || mt.x + (long long)max(np_own - 1, 0) * p.own_stride >= p.own_slots)
-    return;
-  // prefix part: the CTAs that held steps of this row's item
-  const int R = tokens * p.G, j = h / p.G, r = t * p.G + h - j * p.G;
-  const int npairs = (R + tile_rows - 1) / tile_rows;
-  const int nkt = (p.split.prefix_len + kPxBN - 1) / kPxBN;
-  const int item = j * npairs + r / tile_rows;
-  int first = 0, np = np_own;
-  if (nkt > 0) {
-    const long long steps = (long long)npairs * p.H_kv * nkt, a = (long long)item * nkt;
-    const int n1 = *p.n1;
-    first = cta_of_chunk(a, steps, n1);
-    np += cta_of_chunk(a + nkt - 1, steps, n1) - first + 1;
-  }
-  // partial x -> its (m, l) and its output row
-  auto ml_at = [&](int x) -> float2 {
-    return x < np_own ? p.own_ml[((int64_t)mt.x + (int64_t)x * p.own_stride) * p.H_q + h]
-                      : p.ml[(int64_t)(first + x - np_own + item) * tile_rows + r % tile_rows];
-  };
-  auto o_at = [&](int x) -> const float* {
-    return (x < np_own ? p.own_o + (((int64_t)mt.x + (int64_t)x * p.own_stride) * p.H_q + h) * D
-                       : p.o + ((int64_t)(first + x - np_own + item) * tile_rows + r % tile_rows) * D) +
-           lane * V;
-  };
-  float M = -INFINITY;
-  for (int x = lane; x < np; x += 32) M = fmaxf(M, ml_at(x).x);
-  M = warp_max(M);
-  if (M == -INFINITY) M = 0.f;                 // nothing visible: zeros
-  float acc[V] = {}, lsum = 0.f;
-  for (int x0 = 0; x0 < np; x0 += 32) {
-    float w = 0.f;
-    if (x0 + lane < np) {
-      const float2 ml = ml_at(x0 + lane);
-      w = exp2f(ml.x - M);
-      lsum += ml.y * w;
+  // rows of an inconsistent sequence are left as they are (the decode kernel reports it)
+  bool live = t < tokens && px_row(p, t, s, i, n, L);
+  int own = 0, np = 0, item = 0, first = 0, base = 0;
+  const int j = h / p.G, r = t * p.G + h - j * p.G;
+  if (live) {
+    const int4 mt = p.meta[t];
+    if (p.split.prefix_len > 0) {
+      const int npairs = (tokens * p.G + tile_rows - 1) / tile_rows;
+      item = j * npairs + r / tile_rows;
+      const int2 it = p.items[item];
+      first = it.x;
+      np = it.y;
     }
-    const int cnt = min(32, np - x0);
-#pragma unroll 4
-    for (int x = 0; x < cnt; ++x) {
-      const float wx = __shfl_sync(0xffffffffu, w, x);
-      float v[V];
-      load_f<V>(o_at(x0 + x), v);
+    own = mt.y;
+    base = mt.x;
+    live = own >= 0 && base >= 0 && base + (long long)max(own - 1, 0) * p.own_stride < p.own_slots;
+    np += own;
+  }
+  float M = -INFINITY, lsum = 0.f, acc[V] = {};
+  if (live) {
+    for (int x0 = sub * kPxMergeBatch; x0 < np; x0 += WPR * kPxMergeBatch) {
+      auto index = [&](int x) -> int64_t {
+        return x < own ? ((int64_t)base + (int64_t)x * p.own_stride) * p.H_q + h
+                       : (int64_t)(first + x - own + item) * tile_rows + r % tile_rows;
+      };
+      const int cnt = min(kPxMergeBatch, np - x0);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < cnt) ml = (x0 + lane < own ? p.own_ml : p.ml)[index(x0 + lane)];
+      float v[kPxMergeBatch][V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(wx, v[e], acc[e]);
+      for (int x = 0; x < kPxMergeBatch; ++x)
+        if (x < cnt) load_f<V>((x0 + x < own ? p.own_o : p.o) + index(x0 + x) * D + lane * V, v[x]);
+      const float m2 = fmaxf(M, warp_max(ml.x));
+      const float mu = m2 == -INFINITY ? 0.f : m2;          // nothing visible so far: weights 0
+      const float w = exp2f(ml.x - mu), a = exp2f(M - mu);
+      M = m2;
+      lsum = lsum * a + warp_sum(ml.y * w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] *= a;
+#pragma unroll
+      for (int x = 0; x < kPxMergeBatch; ++x) {
+        const float wx = __shfl_sync(0xffffffffu, w, x);
+        if (x < cnt) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[e] = fmaf(wx, v[x][e], acc[e]);
+        }
+      }
     }
   }
-  lsum = warp_sum(lsum);
-  const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
-  __nv_bfloat16* dst = p.out + ((int64_t)t * p.H_q + h) * D + lane * V;
+  if constexpr (WPR > 1) {
 #pragma unroll
-  for (int e = 0; e < V; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    for (int e = 0; e < V; ++e) s_acc[warp][lane * V + e] = acc[e];
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = lsum;
+    }
+    __syncthreads();
+    if (sub != 0 || !live) return;
+    float mu = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < WPR; ++x) mu = fmaxf(mu, s_m[warp + x]);
+    if (mu == -INFINITY) mu = 0.f;
+    lsum = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < WPR; ++x) {
+      const float w = exp2f(s_m[warp + x] - mu);
+      lsum += s_l[warp + x] * w;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(w, s_acc[warp + x][lane * V + e], acc[e]);
+    }
+  }
+  if (!live) return;
+  const float inv = lsum > 0.f ? 1.f / lsum : 0.f;          // nothing visible: zeros
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (int64_t)pair * D + lane * V);
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *dst = pack_bf16x2(acc[0] * inv, acc[1] * inv);
 }
 
 }  // namespace pkv

@@ -8,8 +8,9 @@
 //
 // One cluster of CTAs per sequence.  Each warp sums a contiguous segment of
 // the vocabulary; the CTAs exchange their sums through distributed shared
-// memory, and the warp whose segment holds the threshold reads it again (from
-// L1 / L2) to find the token.
+// memory, and the warps of the CTA whose sums hold the threshold share the
+// one segment that holds it (read again, from L1 / L2) to find the token.
+// Bound by HBM: one row of p, and one of q where a draft was refused.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -34,8 +35,22 @@ struct VerifyParams {
   int num_tokens, max_query, vocab;
 };
 
+// floor(min(max(w, 0), 1) 2^40) as (high, low) halves of 20 bits, by two sums
+// that truncate: 8 + x keeps floor(x 2^20) in the low mantissa bits (a
+// conversion to 64-bit integers runs at a fraction of the rate of these).
+// NaN counts 0.  The halves stand above the bits of 8.0f, which callers take
+// off once per sum.
+constexpr uint32_t kVerifyBias = 0x41000000u;   // bits of 8.0f
+__device__ __forceinline__ void verify_halves(float w, uint32_t& hi, uint32_t& lo) {
+  w = fminf(fmaxf(w, 0.f), 1.f);
+  const float t = __fadd_rz(w, 8.f);
+  hi = __float_as_uint(t);
+  lo = __float_as_uint(__fmaf_rz(w - (t - 8.f), 1048576.f, 8.f));
+}
 __device__ __forceinline__ long long verify_weight(float w) {
-  return __float2ll_rz(fminf(fmaxf(w, 0.f), 1.f) * 1099511627776.f);   // NaN counts 0
+  uint32_t hi, lo;
+  verify_halves(w, hi, lo);
+  return ((long long)(hi - kVerifyBias) << 20) + (lo - kVerifyBias);
 }
 
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
@@ -67,8 +82,9 @@ __global__ void __launch_bounds__(kVerifyThreads)
 verify_kernel(const __grid_constant__ VerifyParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ long long s_warp[2][kVerifyWarps];   // [p - q, p] sums of each warp's segment
-  __shared__ long long s_tot[2];
+  __shared__ long long s_warp[kVerifyWarps];      // sums of the warps' segments
+  __shared__ long long s_part[kVerifyWarps];      // sums of the parts of the threshold's segment
+  __shared__ long long s_tot;
   __shared__ int s_accepted, s_bad_draft;
   const int C = cluster.num_blocks(), rank = cluster.block_rank();
   const int s = blockIdx.x / C;
@@ -139,12 +155,14 @@ verify_kernel(const __grid_constant__ VerifyParams p) {
     }
   }
 
-  // ---- sums of this warp's segment
+  // ---- sums of this warp's segment, from p - q, and from p alone where
+  // nothing of that is left (a second pass, the same for the whole cluster)
   const int step = 32 * E;
   const int seg = ((V + C * kVerifyWarps - 1) / (C * kVerifyWarps) + step - 1) / step * step;
   const long long lo64 = (long long)(rank * kVerifyWarps + warp) * seg;
   const int lo = (int)min(lo64, (long long)V), hi = (int)min(lo64 + seg, (long long)V);
-  auto weights = [&](int x, bool minus, float (&w)[E]) {
+  bool minus = refused;
+  auto weights = [&](int x, float (&w)[E]) {
     verify_load<T, E>(prow, x, V, w);
     if (!minus) return;
     if (qrow != nullptr) {
@@ -157,51 +175,48 @@ verify_kernel(const __grid_constant__ VerifyParams p) {
     for (int e = 0; e < E; ++e)
       if (x + e == without) w[e] = 0.f;
   };
-  long long sum_w = 0, sum_p = 0;
-#pragma unroll 2
-  for (int x = lo + lane * E; x < hi; x += step) {
-    float v[E];
-    verify_load<T, E>(prow, x, V, v);
+  // sum of the weights of tiles [a, b) of this warp
+  auto sum_of = [&](int a, int b) -> long long {
+    long long sum = 0;
+    int x = a + lane * E;
+    while (x < b) {
+      // at most 2048 values to a 32-bit sum of halves below 2^20 + 1
+      const int stop = (int)min((long long)b, x + (long long)(2048 / E) * step);
+      uint32_t h = 0, l = 0, n = 0;
+#pragma unroll 4
+      for (; x < stop; x += step) {
+        float w[E];
+        weights(x, w);
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum_p += verify_weight(v[e]);
-    if (refused) {
-      float w[E];
-      weights(x, true, w);
-#pragma unroll
-      for (int e = 0; e < E; ++e) sum_w += verify_weight(w[e]);
+        for (int e = 0; e < E; ++e) {
+          uint32_t wh, wl;
+          verify_halves(w[e], wh, wl);
+          h += wh;
+          l += wl;
+        }
+        n += E;
+      }
+      sum += ((long long)(h - n * kVerifyBias) << 20) + (l - n * kVerifyBias);
     }
-  }
-  sum_w = warp_sum_ll(sum_w);
-  sum_p = warp_sum_ll(sum_p);
-  if (lane == 0) {
-    s_warp[0][warp] = sum_w;
-    s_warp[1][warp] = sum_p;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    const long long w = warp_sum_ll(lane < kVerifyWarps ? s_warp[0][lane] : 0);
-    const long long q = warp_sum_ll(lane < kVerifyWarps ? s_warp[1][lane] : 0);
-    if (lane == 0) {
-      s_tot[0] = w;
-      s_tot[1] = q;
+    return warp_sum_ll(sum);
+  };
+  long long total, before;
+  for (;;) {
+    const long long sum = sum_of(lo, hi);
+    if (lane == 0) s_warp[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      const long long w = warp_sum_ll(lane < kVerifyWarps ? s_warp[lane] : 0);
+      if (lane == 0) s_tot = w;
     }
+    cluster.sync();
+    const long long mine = lane < C ? *cluster.map_shared_rank(&s_tot, lane) : 0;
+    total = warp_sum_ll(mine);
+    before = warp_sum_ll(lane < rank ? mine : 0);
+    if (total > 0 || !minus) break;
+    minus = false;
+    cluster.sync();
   }
-  cluster.sync();
-  // ---- threshold among all segments
-  long long mine[2] = {0, 0}, before[2] = {0, 0};
-  if (lane < C) {
-    const long long* other = cluster.map_shared_rank(&s_tot[0], lane);
-    mine[0] = other[0];
-    mine[1] = other[1];
-  }
-  long long tot[2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    tot[m] = warp_sum_ll(mine[m]);
-    before[m] = warp_sum_ll(lane < rank ? mine[m] : 0);
-  }
-  const int m = refused && tot[0] > 0 ? 0 : 1;
-  const long long total = tot[m];
   if (total == 0) {
     if (rank == 0 && tid == 0) {
       out[a] = -1;
@@ -211,39 +226,51 @@ verify_kernel(const __grid_constant__ VerifyParams p) {
     const float uf = fminf(fmaxf(p.uniforms[c1 - 1], 0.f), 0.99999994f);
     const long long u = (long long)(uf * 16777216.f);
     const long long r = (total >> 24) * u + (((total & 0xffffffLL) * u) >> 24);
-    long long run = before[m];
-    for (int w = 0; w < warp; ++w) run += s_warp[m][w];
-    if (r >= run && r < run + s_warp[m][warp]) {          // this warp's segment (one warp of the cluster)
-      for (int base = lo; base < hi; base += step) {
-        const int x = base + lane * E;
-        float w[E];
+    if (r >= before && r < before + s_tot) {
+      // the threshold is in this CTA: its warps share the one segment that
+      // holds it, and the warp whose part holds it finds the token
+      long long run = before;
+      int w = 0;
+      while (r >= run + s_warp[w]) run += s_warp[w++];
+      const int from = (rank * kVerifyWarps + w) * seg, to = min(from + seg, V);
+      const int part = ((to - from + kVerifyWarps - 1) / kVerifyWarps + step - 1) / step * step;
+      const int pa = min(from + warp * part, to), pb = min(pa + part, to);
+      const long long psum = sum_of(pa, pb);
+      if (lane == 0) s_part[warp] = psum;
+      __syncthreads();
+      for (int x = 0; x < warp; ++x) run += s_part[x];
+      if (r >= run && r < run + psum) {
+        for (int base = pa; base < pb; base += step) {
+          const int x = base + lane * E;
+          float wt[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) w[e] = 0.f;
-        if (x < V) weights(x, m == 0, w);
-        long long own = 0;
+          for (int e = 0; e < E; ++e) wt[e] = 0.f;
+          if (x < pb) weights(x, wt);
+          long long own = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) own += verify_weight(w[e]);
-        long long incl = own;
+          for (int e = 0; e < E; ++e) own += verify_weight(wt[e]);
+          long long incl = own;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += up;
-        }
-        const unsigned over = __ballot_sync(0xffffffffu, run + incl > r);
-        if (over) {
-          if (lane == __ffs(over) - 1) {
-            long long at = run + incl - own;
-            int found = x;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              if (at <= r) found = x + e;
-              at += verify_weight(w[e]);
-            }
-            out[a] = found;
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
           }
-          break;
+          const unsigned over = __ballot_sync(0xffffffffu, run + incl > r);
+          if (over) {
+            if (lane == __ffs(over) - 1) {
+              long long at = run + incl - own;
+              int found = x;
+#pragma unroll
+              for (int e = 0; e < E; ++e) {
+                if (at <= r) found = x + e;
+                at += verify_weight(wt[e]);
+              }
+              out[a] = found;
+            }
+            break;
+          }
+          run += __shfl_sync(0xffffffffu, incl, 31);
         }
-        run += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
   }
