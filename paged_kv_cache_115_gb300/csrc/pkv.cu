@@ -741,55 +741,85 @@ pkv_status check_quant(const pkv_kv_quant* q, bool need_token_scales) {
 }
 
 // ---- norm + rotation + append dispatch -------------------------------------------
-template <typename Kernel>
-pkv_status launch_rope_kernel(Kernel k, int fmt, const pkv::RopeParams& p, cudaStream_t st,
-                              std::once_flag (&flags)[kMaxDevices],
-                              cudaError_t (&errs)[kMaxDevices]) {
-  size_t smem = 0;
-  if (fmt == PKV_KV_INT8_TOKEN) {
-    smem = 2 * sizeof(float) * (size_t)p.H_kv * p.D;
-    int dev, sms;
-    pkv_status s = device_facts(&dev, &sms);
-    if (s == PKV_OK)
-      s = set_smem_once(k, 2 * (int)sizeof(float) * pkv::kRopeMaxInt8Row, flags, errs, dev);
-    if (s != PKV_OK) return s;
-  }
-  PKV_CUDA(launch_pdl(k, dim3((unsigned)p.T), dim3(pkv::kRopeThreads), smem, st, p));
+constexpr int kRopeSmemPerSm = 220 * 1024;
+
+// Ring of token stages: two at least, up to four while four CTAs fit an SM.
+struct RopeRing {
+  int stages = 0, stage_bytes = 0, smem = 0, ctas = 0;   // stages 0: does not fit
+};
+template <typename T>
+RopeRing rope_ring(const pkv::RopeParams& p, int fmt) {
+  RopeRing r;
+  const int64_t stage =
+      ((int64_t)(p.H_q + 2 * p.H_kv) * p.D * (int64_t)sizeof(T) + 4 * (int64_t)p.rot + 127) / 128 * 128;
+  const int64_t extra = fmt == PKV_KV_INT8_TOKEN ? 8 * (int64_t)p.H_kv * p.D : 0;
+  if (2 * stage + extra > kRopeSmemPerSm) return r;
+  int64_t n = 2;
+  while (n < pkv::kRopeMaxStages && (n + 1) * stage + extra <= kRopeSmemPerSm / pkv::kRopeCtas - 1024) ++n;
+  r.stages = (int)n;
+  r.stage_bytes = (int)stage;
+  r.smem = (int)(n * stage + extra);
+  r.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(pkv::kRopeCtas, kRopeSmemPerSm / (r.smem + 1024)));
+  return r;
+}
+
+template <typename T, int FMT, int D, bool PAIRS>
+pkv_status launch_rope_ring(const pkv::RopeParams& p, const RopeRing& r, cudaStream_t st) {
+  static std::once_flag flags[kMaxDevices];
+  static cudaError_t errs[kMaxDevices];
+  int dev, sms;
+  pkv_status s = device_facts(&dev, &sms);
+  auto k = pkv::rope_ring_kernel<T, FMT, D, PAIRS>;
+  if (s == PKV_OK) s = set_smem_once(k, kRopeSmemPerSm, flags, errs, dev);
+  if (s != PKV_OK) return s;
+  PKV_CUDA(launch_pdl(k, dim3((unsigned)std::min(p.T, sms * r.ctas)), dim3(pkv::kRopeRingThreads),
+                      (size_t)r.smem, st, p, r.stages, r.stage_bytes));
   return PKV_OK;
 }
 
 template <typename T, int FMT, int D>
-pkv_status launch_rope_vec(const pkv::RopeParams& p, cudaStream_t st) {
-  static std::once_flag flags[2][kMaxDevices];
-  static cudaError_t errs[2][kMaxDevices];
-  if (p.interleaved)
-    return launch_rope_kernel(pkv::rope_vec_kernel<T, FMT, D, true>, FMT, p, st, flags[1], errs[1]);
-  return launch_rope_kernel(pkv::rope_vec_kernel<T, FMT, D, false>, FMT, p, st, flags[0], errs[0]);
+pkv_status launch_rope_dim(const pkv::RopeParams& p, const RopeRing& r, cudaStream_t st) {
+  return p.interleaved ? launch_rope_ring<T, FMT, D, true>(p, r, st)
+                       : launch_rope_ring<T, FMT, D, false>(p, r, st);
 }
 
-// The vectorised kernel needs every row on a 16-byte boundary (pools: 16
-// bytes too) and the rotation in whole lanes of V values.
+// The ring kernel needs every row on a 16-byte boundary (pools: 16 bytes too)
+// and the rotation in whole lanes of V values.
 template <typename T>
-bool rope_vec_ok(const pkv::RopeParams& p) {
+bool rope_ring_ok(const pkv::RopeParams& p) {
   constexpr int V = 16 / sizeof(T);
   const bool dim = p.D == 64 || p.D == 128 || (p.D == 256 && sizeof(T) == 2);
-  return dim && p.rot % (p.interleaved ? V : 2 * V) == 0 && p.q_stride % V == 0 &&
-         p.k_stride % V == 0 && p.v_stride % V == 0 && p.qo_stride % V == 0 && aligned(p.q, 16) &&
-         aligned(p.k, 16) && aligned(p.v, 16) && aligned(p.q_out, 16) && aligned(p.wq, 16) &&
-         aligned(p.wk, 16) && aligned(p.cos_sin, 16) && aligned(p.k_cache, 16) &&
-         aligned(p.v_cache, 16);
+  return dim && p.rot % V == 0 && p.q_stride % V == 0 && p.k_stride % V == 0 &&
+         p.v_stride % V == 0 && p.qo_stride % V == 0 && aligned(p.q, 16) && aligned(p.k, 16) &&
+         aligned(p.v, 16) && aligned(p.q_out, 16) && aligned(p.wq, 16) && aligned(p.wk, 16) &&
+         aligned(p.cos_sin, 16) && aligned(p.k_cache, 16) && aligned(p.v_cache, 16);
 }
 
 template <typename T, int FMT>
 pkv_status launch_rope_fmt(const pkv::RopeParams& p, cudaStream_t st) {
-  if (rope_vec_ok<T>(p)) {
-    if (p.D == 64) return launch_rope_vec<T, FMT, 64>(p, st);
-    if (p.D == 128) return launch_rope_vec<T, FMT, 128>(p, st);
-    if constexpr (sizeof(T) == 2) return launch_rope_vec<T, FMT, 256>(p, st);
+  if (rope_ring_ok<T>(p)) {
+    const RopeRing r = rope_ring<T>(p, FMT);
+    if (r.stages > 0) {
+      if (p.D == 64) return launch_rope_dim<T, FMT, 64>(p, r, st);
+      if (p.D == 128) return launch_rope_dim<T, FMT, 128>(p, r, st);
+      if constexpr (sizeof(T) == 2) return launch_rope_dim<T, FMT, 256>(p, r, st);
+    }
   }
-  static std::once_flag flags[kMaxDevices];
-  static cudaError_t errs[kMaxDevices];
-  return launch_rope_kernel(pkv::rope_any_kernel<T, FMT>, FMT, p, st, flags, errs);
+  size_t smem = 0;
+  if (FMT == PKV_KV_INT8_TOKEN) {
+    static std::once_flag flags[kMaxDevices];
+    static cudaError_t errs[kMaxDevices];
+    smem = 2 * sizeof(float) * (size_t)p.H_kv * p.D;
+    int dev, sms;
+    pkv_status s = device_facts(&dev, &sms);
+    if (s == PKV_OK)
+      s = set_smem_once(pkv::rope_any_kernel<T, FMT>, 2 * (int)sizeof(float) * pkv::kRopeMaxInt8Row,
+                        flags, errs, dev);
+    if (s != PKV_OK) return s;
+  }
+  PKV_CUDA(launch_pdl(pkv::rope_any_kernel<T, FMT>, dim3((unsigned)p.T), dim3(pkv::kRopeThreads),
+                      smem, st, p));
+  return PKV_OK;
 }
 
 template <typename T>
@@ -908,14 +938,19 @@ pkv_status launch_prefix_merge(const pkv::PxParams& prm, const PrefixPlan& plan,
 }
 
 // ---- draft verification dispatch ----------------------------------------------------
-template <typename T, int E>
-pkv_status launch_verify_e(const pkv::VerifyParams& p, int S, cudaStream_t st) {
+template <typename T>
+pkv_status launch_verify(const pkv::VerifyParams& p, int S, cudaStream_t st) {
   int dev, sms;
   pkv_status s = device_facts(&dev, &sms);
   if (s != PKV_OK) return s;
-  // CTAs a sequence: enough to fill the GPU, at least 4 vector loads a lane
+  // CTAs a sequence: as many as are resident together, each warp with three
+  // 512-byte tiles or more.  More cost their own start and exchange: 64
+  // sequences over 131072 float32 take 19.4 us with 1 CTA each, 13.7 with 2,
+  // 12.8 with 4, 18.5 with 8; 200 over 32000 take 12.2 with 1 and 17.1 with 2;
+  // one over 32000 takes 8.6 with 1, 6.3 with 4, 6.2 with 8.
+  const int64_t tiles = p.vocab * (int64_t)sizeof(T) / 512;
   int C = 1;
-  while (C < 8 && S * C < 2 * sms && (int64_t)C * pkv::kVerifyThreads * E * 4 < p.vocab) C *= 2;
+  while (C < 8 && 2 * S * C <= pkv::kVerifyCtas * sms && tiles >= 2 * C * 3 * pkv::kVerifyWarps) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(S * C));
   cfg.blockDim = dim3(pkv::kVerifyThreads);
@@ -929,25 +964,8 @@ pkv_status launch_verify_e(const pkv::VerifyParams& p, int S, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  PKV_CUDA(cudaLaunchKernelEx(&cfg, pkv::verify_kernel<T, E>, p));
+  PKV_CUDA(cudaLaunchKernelEx(&cfg, pkv::verify_kernel<T>, p));
   return PKV_OK;
-}
-
-// Widest vector (up to 16 bytes) that every row's first value is aligned to.
-template <typename T>
-pkv_status launch_verify(const pkv::VerifyParams& p, int S, cudaStream_t st) {
-  const int64_t eb = sizeof(T);
-  int w = 16;
-  const uint64_t bits = reinterpret_cast<uintptr_t>(p.target) | (uint64_t)(p.target_stride * eb) |
-                        reinterpret_cast<uintptr_t>(p.draft) |
-                        (p.draft ? (uint64_t)((p.draft_seq_stride | p.draft_tok_stride) * eb) : 0);
-  while (bits & (uint64_t)(w - 1)) w /= 2;
-  switch (w / (int)eb) {
-    case 8: return launch_verify_e<T, 16 / sizeof(T)>(p, S, st);
-    case 4: return launch_verify_e<T, 4>(p, S, st);
-    case 2: return launch_verify_e<T, 2>(p, S, st);
-    default: return launch_verify_e<T, 1>(p, S, st);
-  }
 }
 
 // ---- fixed scratch for pkv_attention_decode_noalloc ---------------------------

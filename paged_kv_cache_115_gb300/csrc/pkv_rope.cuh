@@ -53,11 +53,12 @@ __device__ __forceinline__ void rope_store(const RopeParams& p, int z, int64_t a
 
 // INT8 pools: the token's K and V rows stand in s_all; each gets its scale
 // max|x| / 127 and codes rint(x / scale), as kv_append_quant_kernel makes them.
-// Called by the whole CTA of W warps.
-template <int W>
+// Called by W warps that `sync` makes wait for one another.
+template <int W, typename Sync>
 __device__ __forceinline__ void rope_int8_rows(const RopeParams& p, int64_t slot,
                                                int64_t pool_row, const float (&amax)[2],
-                                               const float* s_all, float (*s_amax)[W]) {
+                                               const float* s_all, float (*s_amax)[W],
+                                               Sync&& sync) {
   if (slot < 0) return;
   const int n = p.H_kv * p.D;
 #pragma unroll
@@ -65,7 +66,7 @@ __device__ __forceinline__ void rope_int8_rows(const RopeParams& p, int64_t slot
     const float m = warp_max(amax[z]);
     if ((threadIdx.x & 31) == 0) s_amax[z][threadIdx.x >> 5] = m;
   }
-  __syncthreads();
+  sync();
 #pragma unroll
   for (int z = 0; z < 2; ++z) {
     float m = s_amax[z][0];
@@ -149,18 +150,19 @@ rope_any_kernel(const __grid_constant__ RopeParams p) {
     __syncwarp();
   }
   const float amax[2] = {amax_k, amax_v};
-  if constexpr (FMT == 2) rope_int8_rows<W>(p, slot, pool_row, amax, s_all, s_amax);
+  if constexpr (FMT == 2) rope_int8_rows<W>(p, slot, pool_row, amax, s_all, s_amax, [] { __syncthreads(); });
 }
 
-// Vectorised form: head_dim 64 or 128 (256 for bf16), rows and strides on
-// 16-byte boundaries, the rotation in whole lanes.  A lane holds V = 16 /
-// sizeof(TIN) values of a row, so a row takes D / V lanes and a CTA 256 V / D
-// rows at once (16 for bf16 at head_dim 128).  One CTA per token: its rows
-// (query heads, key heads, value heads) are loaded four to a thread before
-// any is used, the cosines and sines of a lane once per token.  A rotated
-// pair sits in one lane (interleaved) or in two lanes half a rotation apart
-// (a shuffle per value).
-// Bound by HBM: 2 (H_q + H_kv) D e + (2 H_kv D) e bytes a token.
+// Ring form: head_dim 64 or 128 (256 for bf16), rows and strides on 16-byte
+// boundaries, the rotation a multiple of 8 values (4 for float32).  Persistent
+// CTAs; a producer warp brings whole tokens (query, key and value heads, and
+// the position's cosines and sines) into a ring of shared-memory stages by
+// bulk copies, so that the bytes in flight do not hang on registers; eight
+// warps compute.  A lane holds V = 16 / sizeof(TIN) values of a row, V / 2
+// from either half of the rotation (interleaved: neighbours; behind the
+// rotation: as they come), so that a rotated pair sits in one lane and needs
+// no shuffle; a row takes D / V lanes, a CTA 256 V / D rows at once.
+// Bound by HBM: 2 (H_q + 2 H_kv) D e bytes a token.
 template <typename TIN>
 __device__ __forceinline__ void rope_unpack(const uint4& r, float (&x)[16 / sizeof(TIN)]) {
   if constexpr (sizeof(TIN) == 4) {
@@ -186,161 +188,277 @@ __device__ __forceinline__ uint4 rope_pack(const float (&x)[16 / sizeof(TIN)]) {
                       pack_bf16x2(x[6], x[7]));
 }
 
-// V values as e4m3 codes of x / scale, V bytes.
-template <int V>
-__device__ __forceinline__ void rope_store_fp8(uint8_t* dst, const float (&x)[V], float scale) {
-  uint32_t w[V / 4];
-#pragma unroll
-  for (int i = 0; i < V / 4; ++i) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)), __NV_SATFINITE, __NV_E4M3);
-    w[i] = lo | (hi << 16);
+// N values (half of a lane's) as T, and as e4m3 codes of x / scale.
+template <typename T, int N>
+__device__ __forceinline__ void rope_store_half(T* dst, const float* x) {
+  if constexpr (sizeof(T) == 4) {
+    static_assert(N == 2, "8 bytes");
+    *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[1]);
+  } else if constexpr (N == 4) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  } else {
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(x[0], x[1]);
   }
-  if constexpr (V == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+}
+template <int N>
+__device__ __forceinline__ void rope_store_codes(uint8_t* dst, const float* x, float scale) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale)), __NV_SATFINITE,
+        __NV_E4M3);
+  if constexpr (N == 4) *reinterpret_cast<uint32_t*>(dst) = w[0] | (w[1] << 16);
+  else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w[0];
+}
+template <typename TIN, int FMT>
+struct RopeKType { using T = TIN; };
+template <typename TIN>
+struct RopeKType<TIN, 3> { using T = __nv_bfloat16; };
+
+// 1-D bulk copy with an L2 hint for data that is read once.
+__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void* src, uint32_t bytes,
+                                               uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+constexpr int kRopeRingThreads = kRopeThreads + 32;
+constexpr int kRopeMaxStages = 4;
+constexpr int kRopeCtas = 4;                    // resident on an SM (at most)
+
+// V / 2 values (8 bytes) at a time.
+template <typename TIN>
+__device__ __forceinline__ void rope_unpack2(uint2 a, uint2 b, float (&x)[16 / sizeof(TIN)]) {
+  rope_unpack<TIN>(make_uint4(a.x, a.y, b.x, b.y), x);
 }
 
 template <typename TIN, int FMT, int D, bool PAIRS>
-__global__ void __launch_bounds__(kRopeThreads)
-rope_vec_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int V = 16 / sizeof(TIN), LANES = D / V, RPI = kRopeThreads / LANES, BATCH = 4;
+__global__ void __launch_bounds__(kRopeRingThreads, kRopeCtas)
+rope_ring_kernel(const __grid_constant__ RopeParams p, int stages, int stage_bytes) {
+  constexpr int V = 16 / sizeof(TIN), HV = V / 2, LANES = D / V, RPI = kRopeThreads / LANES;
   static_assert(LANES <= 32, "a row must fit a warp");
   constexpr int W = kRopeThreads / 32;
+  extern __shared__ __align__(128) uint8_t s_ring[];
+  __shared__ __align__(8) uint64_t s_full[kRopeMaxStages], s_empty[kRopeMaxStages];
+  __shared__ long long s_slot[kRopeMaxStages];
+  __shared__ int s_token[kRopeMaxStages];
   __shared__ float s_amax[2][W];
-  extern __shared__ float s_all[];              // INT8: the token's K, then V row
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int e0 = (tid % LANES) * V, rg = tid / LANES;
-  const int t = blockIdx.x;
+  float* const s_all = reinterpret_cast<float*>(s_ring + (size_t)stages * stage_bytes);   // INT8
+  // the consumers among themselves
+  auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kRopeThreads) : "memory"); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int HK = p.H_q + p.H_kv, rows = HK + p.H_kv;
+  const int q_bytes = p.H_q * D * (int)sizeof(TIN), kv_bytes = p.H_kv * D * (int)sizeof(TIN);
+  if (tid == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&s_empty[i]), W);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int pos = p.positions[t];
-  int64_t slot = p.slots[t];
-  const int HK = p.H_q + p.H_kv, rows = HK + p.H_kv;
-  const TIN* q = static_cast<const TIN*>(p.q) + t * p.q_stride;
-  const TIN* k = static_cast<const TIN*>(p.k) + t * p.k_stride;
-  const TIN* v = static_cast<const TIN*>(p.v) + t * p.v_stride;
-  TIN* qo = static_cast<TIN*>(p.q_out) + t * p.qo_stride;
-  auto source = [&](int r) -> const TIN* {
-    return (r < p.H_q ? q + r * D : (r < HK ? k + (r - p.H_q) * D : v + (r - HK) * D)) + e0;
-  };
-  if (pos < 0) return;                          // padding
-  if (pos >= p.max_pos) {
-    if (tid == 0) record_error(PKV_DEVERR_POSITION);
+
+  if (warp == W) {
+    // =================== producer ===================
+    const uint64_t policy = l2_policy_evict_first();
+    int n = 0;                                          // stages filled
+    bool ok = true;
+    for (int t0 = blockIdx.x; t0 < p.T && ok; t0 += 32 * gridDim.x) {
+      // positions and slots of the CTA's next 32 tokens
+      const int tl = t0 + lane * (int)gridDim.x;
+      int pos = -1;
+      long long slot = -1;
+      if (tl < p.T) {
+        pos = p.positions[tl];
+        slot = p.slots[tl];
+        if (pos >= p.max_pos) {
+          record_error(PKV_DEVERR_POSITION);
+          pos = -1;
+        } else if (pos >= 0 && (slot < 0 || slot >= p.num_slots)) {
+          if (slot != -1) record_error(PKV_DEVERR_SLOT);
+          slot = -1;
+        }
+      }
+      unsigned todo = __ballot_sync(0xffffffffu, pos >= 0);           // the others are skipped
+      while (todo) {
+        const int l = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int t = t0 + l * (int)gridDim.x;
+        const int pt = __shfl_sync(0xffffffffu, pos, l);
+        const long long st = __shfl_sync(0xffffffffu, slot, l);
+        const int stage = n % stages;
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_bounded(smem_u32(&s_empty[stage]), ((n / stages) & 1) ^ 1));
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t full = smem_u32(&s_full[stage]);
+          const uint32_t dst = smem_u32(s_ring + (size_t)stage * stage_bytes);
+          s_slot[stage] = st;
+          s_token[stage] = t;
+          mbar_arrive_expect_tx(full, q_bytes + 2 * kv_bytes + 4 * p.rot);
+          bulk_load_hint(dst, static_cast<const TIN*>(p.q) + t * p.q_stride, q_bytes, full, policy);
+          bulk_load_hint(dst + q_bytes, static_cast<const TIN*>(p.k) + t * p.k_stride, kv_bytes, full, policy);
+          bulk_load_hint(dst + q_bytes + kv_bytes, static_cast<const TIN*>(p.v) + t * p.v_stride, kv_bytes, full, policy);
+          if (p.rot > 0)
+            bulk_load(dst + q_bytes + 2 * kv_bytes, p.cos_sin + (int64_t)pt * p.rot, 4 * p.rot, full);
+        }
+        __syncwarp();
+        ++n;
+      }
+    }
+    // the consumers' end: a stage without a token
+    const int end = n % stages;
+    ok = ok && __all_sync(0xffffffffu,
+                          mbar_wait_bounded(smem_u32(&s_empty[end]), ((n / stages) & 1) ^ 1));
+    if (ok) {
+      if (lane == 0) {
+        s_slot[end] = -2;
+        mbar_arrive(smem_u32(&s_full[end]));
+      }
+    } else {
+      if (lane == 0) record_error(PKV_DEVERR_TIMEOUT);
+      // do not leave the CTA while our own copies may still land
+      for (int i = max(0, n - stages); i < n; ++i)
+        mbar_wait_bounded(smem_u32(&s_full[i % stages]), (i / stages) & 1);
+    }
     return;
   }
-  if (slot < 0 || slot >= p.num_slots) {
-    if (slot != -1 && tid == 0) record_error(PKV_DEVERR_SLOT);
-    slot = -1;
-  }
-  uint4 raw[BATCH];
-#pragma unroll
-  for (int b = 0; b < BATCH; ++b)
-    if (b * RPI + rg < rows) raw[b] = __ldcs(reinterpret_cast<const uint4*>(source(b * RPI + rg)));
-  // cosines and sines of this lane's values (1, 0 behind the rotation)
-  const int half = p.rot >> 1;
-  constexpr int NC = PAIRS ? V / 2 : V;
-  float c[NC], s[NC];
-  const bool turned = e0 < p.rot, second = !PAIRS && e0 >= half;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    c[i] = 1.f;
-    s[i] = 0.f;
-  }
-  if (turned) {
-    const float* cs = p.cos_sin + (int64_t)pos * p.rot + (PAIRS ? e0 >> 1 : (second ? e0 - half : e0));
-#pragma unroll
-    for (int i = 0; i < NC; i += 2) {
-      const float2 a = __ldg(reinterpret_cast<const float2*>(cs + i));
-      const float2 b = __ldg(reinterpret_cast<const float2*>(cs + half + i));
-      c[i] = a.x; c[i + 1] = a.y;
-      s[i] = b.x; s[i + 1] = b.y;
-    }
-    if (!PAIRS && !second) {                    // the first of a pair takes off
-#pragma unroll
-      for (int i = 0; i < NC; ++i) s[i] = -s[i];
-    }
-  }
-  // lane that holds the other value of this lane's pairs
-  const int mate = PAIRS || !turned ? lane : (second ? lane - half / V : lane + half / V);
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (p.wq != nullptr) wq = __ldg(reinterpret_cast<const uint4*>(static_cast<const TIN*>(p.wq) + e0));
-  if (p.wk != nullptr) wk = __ldg(reinterpret_cast<const uint4*>(static_cast<const TIN*>(p.wk) + e0));
-  const int64_t pool_row = slot * p.H_kv * D;
-  float amax[2] = {0.f, 0.f};
 
-  for (int r0 = 0; r0 < rows; r0 += RPI * BATCH) {
-    if (r0 > 0) {
-#pragma unroll
-      for (int b = 0; b < BATCH; ++b)
-        if (r0 + b * RPI + rg < rows)
-          raw[b] = __ldcs(reinterpret_cast<const uint4*>(source(r0 + b * RPI + rg)));
+  // =================== consumers ===================
+  const int li = tid % LANES, rg = tid / LANES;
+  const int half = p.rot >> 1;
+  // this lane's values: HV from ea on, HV from eb on
+  const bool turned = li * V < p.rot;
+  const int ea = PAIRS || !turned ? li * V : li * HV;
+  const int eb = PAIRS || !turned ? ea + HV : half + li * HV;
+  uint2 wqa = make_uint2(0, 0), wqb = wqa, wka = wqa, wkb = wqa;
+  if (p.wq != nullptr) {
+    wqa = __ldg(reinterpret_cast<const uint2*>(static_cast<const TIN*>(p.wq) + ea));
+    wqb = __ldg(reinterpret_cast<const uint2*>(static_cast<const TIN*>(p.wq) + eb));
+  }
+  if (p.wk != nullptr) {
+    wka = __ldg(reinterpret_cast<const uint2*>(static_cast<const TIN*>(p.wk) + ea));
+    wkb = __ldg(reinterpret_cast<const uint2*>(static_cast<const TIN*>(p.wk) + eb));
+  }
+  const int row0 = tid / 32 * (32 / LANES);             // first row of this warp in a group of RPI
+  int stage = 0, round = 0;
+  for (;;) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&s_full[stage]), round & 1));
+    if (!ok) {
+      if (lane == 0) record_error(PKV_DEVERR_TIMEOUT);
+      return;
     }
+    uint8_t* sb = s_ring + (size_t)stage * stage_bytes;
+    const long long slot = s_slot[stage];
+    if (slot == -2) return;
+    const int t = s_token[stage];
+    float c[HV], s[HV];
 #pragma unroll
-    for (int b = 0; b < BATCH; ++b) {
-      if (r0 + b * RPI >= rows) break;          // the same for the whole CTA: shuffles stay whole
-      const int r = r0 + b * RPI + rg;
-      const int z = r < p.H_q ? 0 : (r < HK ? 1 : 2);               // q, k, v (or past the end)
-      float x[V];
-      rope_unpack<TIN>(raw[b], x);
-      float ss = 0.f;
+    for (int i = 0; i < HV; ++i) {
+      c[i] = 1.f;
+      s[i] = 0.f;
+    }
+    if (turned) {
+      const float* cs = reinterpret_cast<const float*>(sb + q_bytes + 2 * kv_bytes) + li * HV;
 #pragma unroll
-      for (int i = 0; i < V; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (z < 2 && (z ? p.wk : p.wq) != nullptr) {
-        float w[V];
-        rope_unpack<TIN>(z ? wk : wq, w);
-        const float inv = rsqrtf(ss / D + p.eps);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] *= inv * w[i];
+      for (int i = 0; i < HV; ++i) {
+        c[i] = cs[i];
+        s[i] = cs[half + i];
       }
-      float y[V];
-      if constexpr (PAIRS) {
-#pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          y[i] = x[i] * c[i / 2] - x[i + 1] * s[i / 2];
-          y[i + 1] = x[i + 1] * c[i / 2] + x[i] * s[i / 2];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float o = __shfl_sync(0xffffffffu, x[i], mate);
-          y[i] = x[i] * c[i] + o * s[i];
-        }
-      }
-      if (r >= rows) continue;
-      if (z == 0) {
-        *reinterpret_cast<uint4*>(qo + r * D + e0) = rope_pack<TIN>(y);
+    }
+    TIN* qo = static_cast<TIN*>(p.q_out) + t * p.qo_stride;
+    const int64_t pool_row = slot * p.H_kv * D;
+    float amax[2] = {0.f, 0.f};
+    const int last = slot < 0 ? p.H_q : rows;           // without a slot the pools are left alone
+#pragma unroll 4
+    for (int r0 = 0; r0 + row0 < last; r0 += RPI) {     // the same for a whole warp: shuffles stay whole
+      const int r = r0 + rg;
+      const TIN* src = reinterpret_cast<const TIN*>(sb) + r * D;      // k and v follow q
+      if (FMT == 0 && r0 + row0 >= HK) {                // value rows only: copied as they are
+        if (r < last)
+          reinterpret_cast<uint4*>(p.v_cache)[(pool_row + (r - HK) * D) / V + li] =
+              *reinterpret_cast<const uint4*>(src + li * V);
         continue;
       }
-      if (slot < 0) continue;
-      const int at = (z == 1 ? r - p.H_q : r - HK) * D + e0;        // in the token's K or V row
-      if constexpr (FMT == 2) {
+      const bool live = r < last;
+      const int z = r < p.H_q ? 0 : (r < HK ? 1 : 2);                 // q, k, v
+      const uint2 xa = live ? *reinterpret_cast<const uint2*>(src + ea) : make_uint2(0, 0);
+      const uint2 xb = live ? *reinterpret_cast<const uint2*>(src + eb) : make_uint2(0, 0);
+      float x[V];
+      rope_unpack2<TIN>(xa, xb, x);
+      if (p.wq != nullptr || p.wk != nullptr) {
+        float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float val = z == 1 ? y[i] : x[i];
-          s_all[(z - 1) * p.H_kv * D + at + i] = val;
-          amax[z - 1] = fmaxf(amax[z - 1], fabsf(val));
+        for (int i = 0; i < V; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (z < 2 && (z ? p.wk : p.wq) != nullptr) {
+          float w[V];
+          rope_unpack2<TIN>(z ? wka : wqa, z ? wkb : wqb, w);
+          const float inv = rsqrtf(ss / D + p.eps);
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[i] *= inv * w[i];
+        }
+      }
+      if (!live) continue;
+      float y[V];
+#pragma unroll
+      for (int i = 0; i < HV; ++i) {
+        const int a = PAIRS ? 2 * i : i, b = PAIRS ? 2 * i + 1 : i + HV;
+        y[a] = x[a] * c[i] - x[b] * s[i];
+        y[b] = x[b] * c[i] + x[a] * s[i];
+      }
+      if (z == 0) {
+        const uint4 o = rope_pack<TIN>(y);
+        *reinterpret_cast<uint2*>(qo + r * D + ea) = make_uint2(o.x, o.y);
+        *reinterpret_cast<uint2*>(qo + r * D + eb) = make_uint2(o.z, o.w);
+        continue;
+      }
+      const int at = (z == 1 ? r - p.H_q : r - HK) * D;               // in the token's K or V row
+      if constexpr (FMT == 2) {
+        const float* val = z == 1 ? y : x;
+        float* dst = s_all + (z - 1) * p.H_kv * D + at;
+#pragma unroll
+        for (int i = 0; i < HV; ++i) {
+          dst[ea + i] = val[i];
+          dst[eb + i] = val[i + HV];
+          amax[z - 1] = fmaxf(amax[z - 1], fmaxf(fabsf(val[i]), fabsf(val[i + HV])));
         }
       } else if (z == 1) {
-        if constexpr (FMT == 0) {
-          reinterpret_cast<uint4*>(p.k_cache)[(pool_row + at) / V] = rope_pack<TIN>(y);
-        } else if constexpr (FMT == 3) {
-          uint32_t* dst = reinterpret_cast<uint32_t*>(p.k_cache + 2 * (pool_row + at));
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) dst[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+        if constexpr (FMT == 0 || FMT == 3) {
+          using TK = typename RopeKType<TIN, FMT>::T;
+          rope_store_half<TK, HV>(reinterpret_cast<TK*>(p.k_cache) + pool_row + at + ea, y);
+          rope_store_half<TK, HV>(reinterpret_cast<TK*>(p.k_cache) + pool_row + at + eb, y + HV);
         } else {
-          rope_store_fp8<V>(p.k_cache + pool_row + at, y, p.k_scale);
+          rope_store_codes<HV>(p.k_cache + pool_row + at + ea, y, p.k_scale);
+          rope_store_codes<HV>(p.k_cache + pool_row + at + eb, y + HV, p.k_scale);
         }
+      } else if constexpr (FMT == 0) {
+        TIN* dst = reinterpret_cast<TIN*>(p.v_cache) + pool_row + at;
+        *reinterpret_cast<uint2*>(dst + ea) = xa;
+        *reinterpret_cast<uint2*>(dst + eb) = xb;
       } else {
-        if constexpr (FMT == 0) reinterpret_cast<uint4*>(p.v_cache)[(pool_row + at) / V] = raw[b];
-        else rope_store_fp8<V>(p.v_cache + pool_row + at, x, p.v_scale);
+        rope_store_codes<HV>(p.v_cache + pool_row + at + ea, x, p.v_scale);
+        rope_store_codes<HV>(p.v_cache + pool_row + at + eb, x + HV, p.v_scale);
       }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&s_empty[stage]));
+    if (++stage == stages) {
+      stage = 0;
+      ++round;
+    }
+    if constexpr (FMT == 2) {
+      rope_int8_rows<W>(p, slot, pool_row, amax, s_all, s_amax, sync);
+      sync();                                           // s_all is free for the next token
+    }
   }
-  if constexpr (FMT == 2) rope_int8_rows<W>(p, slot, pool_row, amax, s_all, s_amax);
 }
 
 }  // namespace pkv

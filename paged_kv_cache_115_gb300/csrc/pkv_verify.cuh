@@ -10,7 +10,11 @@
 // the vocabulary; the CTAs exchange their sums through distributed shared
 // memory, and the warps of the CTA whose sums hold the threshold share the
 // one segment that holds it (read again, from L1 / L2) to find the token.
-// Bound by HBM: one row of p, and one of q where a draft was refused.
+// Bound by HBM: one row of p, and one of q where a draft was refused, behind
+// a chain of about 8 us (counts, tokens, their probabilities, sums, threshold,
+// the segment again).  256 sequences over 131072 float32, two in three
+// refused: 224 MB in 50 us, 4.5 TB/s; all of them are resident at once, two
+// on most SMs and one on the others, which leaves a sixth of the time.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -20,8 +24,10 @@
 namespace pkv {
 
 constexpr int kVerifyThreads = 512;
+constexpr int kVerifyCtas = 2;          // resident on an SM
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyMaxCluster = 16;
+constexpr int kVerifyBatch = 4;         // tiles whose loads are in flight together
 
 struct VerifyParams {
   const void* target;
@@ -59,26 +65,146 @@ __device__ __forceinline__ long long warp_sum_ll(long long v) {
   return v;
 }
 
-template <typename T, int E>
-struct alignas(sizeof(T) * E) VerifyVec {
-  T v[E];
+// The weights of one sequence's draw, read in 16-byte blocks that are aligned
+// on the row of p: block i holds values i E - sp .. of the vocabulary (E = 16
+// / sizeof(T); sp values of the first block lie in front of the row).  The row
+// of q may sit at another distance from a 16-byte boundary (an odd vocabulary
+// does that), so a block of it is cut out of two aligned ones.
+template <typename T>
+struct VerifyRow {
+  static constexpr int E = 16 / sizeof(T);
+  static constexpr int TILE = 32 * E;      // values of a tile: one block per lane
+  const T* p;
+  const T* q;                              // null: nothing comes off
+  const uint4* p_al;
+  const uint4* q_al;
+  int V, sp, without, word, half;          // q's shift: whole words, and 16 bits more
+  bool shifted;
+
+  __device__ __forceinline__ VerifyRow(const T* prow, const T* qrow, int vocab, int skip)
+      : p(prow), q(qrow), V(vocab), without(skip) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(prow);
+    sp = (int)(pa & 15) / (int)sizeof(T);
+    p_al = reinterpret_cast<const uint4*>(pa & ~uintptr_t(15));
+    const uintptr_t qa = reinterpret_cast<uintptr_t>(qrow) - (pa & 15);
+    const int o = (int)(qa & 15);
+    q_al = reinterpret_cast<const uint4*>(qa & ~uintptr_t(15));
+    shifted = o != 0;
+    word = o >> 2;
+    half = (o & 2) * 8;
+  }
+  __device__ __forceinline__ int tiles() const { return (V + sp + TILE - 1) / TILE; }
+  // tiles t .. t + n - 1 lie inside both rows and hold no refused draft
+  __device__ __forceinline__ bool inside(int t, int n) const {
+    const int a = t * TILE - sp, b = (t + n) * TILE - sp;
+    return a >= 0 && b <= V && (without < a || without >= b);
+  }
+  __device__ __forceinline__ static void unpack(const uint4& r, float (&x)[E]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        x[i] = __uint_as_float(w[i]);
+      } else {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+  // 16 bytes of (a, b) from byte word * 4 + half / 8 on
+  __device__ __forceinline__ uint4 cut(const uint4& a, const uint4& b) const {
+    uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, c[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const uint32_t lo = word & 1 ? v[i + 1] : v[i];
+      const uint32_t hi = i + 2 < 8 ? (word & 1 ? (i + 3 < 8 ? v[i + 3] : 0u) : v[i + 2]) : 0u;
+      c[i] = word & 2 ? hi : lo;
+    }
+    return make_uint4(__funnelshift_r(c[0], c[1], half), __funnelshift_r(c[1], c[2], half),
+                      __funnelshift_r(c[2], c[3], half), __funnelshift_r(c[3], c[4], half));
+  }
+  // this lane's block of n tiles that lie inside, all loads first
+  template <int N, typename F>
+  __device__ __forceinline__ void visit(int t, int lane, F&& f) const {
+    uint4 a[N], b[N], c[N];
+    const int64_t i0 = (int64_t)t * 32 + lane;
+#pragma unroll
+    for (int n = 0; n < N; ++n) a[n] = __ldg(p_al + i0 + 32 * n);
+    if (q != nullptr) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) b[n] = __ldg(q_al + i0 + 32 * n);
+      if (shifted) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) c[n] = __ldg(q_al + i0 + 32 * n + 1);
+#pragma unroll
+        for (int n = 0; n < N; ++n) b[n] = cut(b[n], c[n]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      float w[E];
+      unpack(a[n], w);
+      if (q != nullptr) {
+        float x[E];
+        unpack(b[n], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[e] -= x[e];
+      }
+      f(w);
+    }
+  }
+  // this lane's block of any tile (0 outside the row)
+  __device__ __forceinline__ void block(int t, int lane, float (&w)[E]) const {
+    const int x0 = (t * 32 + lane) * E - sp;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int x = x0 + e;
+      w[e] = 0.f;
+      if (x >= 0 && x < V && x != without) {
+        w[e] = to_f32(p[x]);
+        if (q != nullptr) w[e] -= to_f32(q[x]);
+      }
+    }
+  }
+  // sum of the weights of tiles [t0, t1), of the whole warp
+  __device__ __forceinline__ long long sum(int t0, int t1, int lane) const {
+    long long total = 0;
+    uint32_t h = 0, l = 0, n = 0;
+    auto add = [&](const float (&w)[E]) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        uint32_t wh, wl;
+        verify_halves(w[e], wh, wl);
+        h += wh;
+        l += wl;
+      }
+      n += E;
+    };
+    for (int t = t0; t < t1;) {
+      if (t + kVerifyBatch <= t1 && inside(t, kVerifyBatch)) {
+        visit<kVerifyBatch>(t, lane, add);
+        t += kVerifyBatch;
+      } else if (inside(t, 1)) {
+        visit<1>(t, lane, add);
+        ++t;
+      } else {
+        float w[E];
+        block(t, lane, w);
+        add(w);
+        ++t;
+      }
+      if (n >= 1024) {         // halves are at most 2^20: 32-bit sums of up to 2048 of them
+        total += ((long long)(h - n * kVerifyBias) << 20) + (l - n * kVerifyBias);
+        h = l = n = 0;
+      }
+    }
+    total += ((long long)(h - n * kVerifyBias) << 20) + (l - n * kVerifyBias);
+    return warp_sum_ll(total);
+  }
 };
 
-template <typename T, int E>
-__device__ __forceinline__ void verify_load(const T* row, int x, int V, float (&v)[E]) {
-  if (x + E <= V) {
-    const VerifyVec<T, E> r = *reinterpret_cast<const VerifyVec<T, E>*>(row + x);
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = to_f32(r.v[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = x + e < V ? to_f32(row[x + e]) : 0.f;
-  }
-}
-
-// E: values per vector load (rows and strides are aligned to it).
-template <typename T, int E>
-__global__ void __launch_bounds__(kVerifyThreads)
+template <typename T>
+__global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
 verify_kernel(const __grid_constant__ VerifyParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
@@ -155,54 +281,18 @@ verify_kernel(const __grid_constant__ VerifyParams p) {
     }
   }
 
-  // ---- sums of this warp's segment, from p - q, and from p alone where
-  // nothing of that is left (a second pass, the same for the whole cluster)
-  const int step = 32 * E;
-  const int seg = ((V + C * kVerifyWarps - 1) / (C * kVerifyWarps) + step - 1) / step * step;
-  const long long lo64 = (long long)(rank * kVerifyWarps + warp) * seg;
-  const int lo = (int)min(lo64, (long long)V), hi = (int)min(lo64 + seg, (long long)V);
+  // ---- sums of this warp's segment (whole tiles), from p - q, and from p
+  // alone where nothing of that is left (a second pass, the same for the
+  // whole cluster)
+  VerifyRow<T> row(prow, qrow, V, without);
+  constexpr int E = VerifyRow<T>::E;
+  const int tiles = row.tiles();
+  const int seg = (tiles + C * kVerifyWarps - 1) / (C * kVerifyWarps);
+  const int lo = min((rank * kVerifyWarps + warp) * seg, tiles), hi = min(lo + seg, tiles);
   bool minus = refused;
-  auto weights = [&](int x, float (&w)[E]) {
-    verify_load<T, E>(prow, x, V, w);
-    if (!minus) return;
-    if (qrow != nullptr) {
-      float q[E];
-      verify_load<T, E>(qrow, x, V, q);
-#pragma unroll
-      for (int e = 0; e < E; ++e) w[e] -= q[e];
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (x + e == without) w[e] = 0.f;
-  };
-  // sum of the weights of tiles [a, b) of this warp
-  auto sum_of = [&](int a, int b) -> long long {
-    long long sum = 0;
-    int x = a + lane * E;
-    while (x < b) {
-      // at most 2048 values to a 32-bit sum of halves below 2^20 + 1
-      const int stop = (int)min((long long)b, x + (long long)(2048 / E) * step);
-      uint32_t h = 0, l = 0, n = 0;
-#pragma unroll 4
-      for (; x < stop; x += step) {
-        float w[E];
-        weights(x, w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          uint32_t wh, wl;
-          verify_halves(w[e], wh, wl);
-          h += wh;
-          l += wl;
-        }
-        n += E;
-      }
-      sum += ((long long)(h - n * kVerifyBias) << 20) + (l - n * kVerifyBias);
-    }
-    return warp_sum_ll(sum);
-  };
   long long total, before;
   for (;;) {
-    const long long sum = sum_of(lo, hi);
+    const long long sum = row.sum(lo, hi, lane);
     if (lane == 0) s_warp[warp] = sum;
     __syncthreads();
     if (warp == 0) {
@@ -215,6 +305,7 @@ verify_kernel(const __grid_constant__ VerifyParams p) {
     before = warp_sum_ll(lane < rank ? mine : 0);
     if (total > 0 || !minus) break;
     minus = false;
+    row = VerifyRow<T>(prow, nullptr, V, -1);
     cluster.sync();
   }
   if (total == 0) {
@@ -232,20 +323,24 @@ verify_kernel(const __grid_constant__ VerifyParams p) {
       long long run = before;
       int w = 0;
       while (r >= run + s_warp[w]) run += s_warp[w++];
-      const int from = (rank * kVerifyWarps + w) * seg, to = min(from + seg, V);
-      const int part = ((to - from + kVerifyWarps - 1) / kVerifyWarps + step - 1) / step * step;
+      const int from = (rank * kVerifyWarps + w) * seg, to = min(from + seg, tiles);
+      const int part = (to - from + kVerifyWarps - 1) / kVerifyWarps;
       const int pa = min(from + warp * part, to), pb = min(pa + part, to);
-      const long long psum = sum_of(pa, pb);
+      const long long psum = row.sum(pa, pb, lane);
       if (lane == 0) s_part[warp] = psum;
       __syncthreads();
       for (int x = 0; x < warp; ++x) run += s_part[x];
       if (r >= run && r < run + psum) {
-        for (int base = pa; base < pb; base += step) {
-          const int x = base + lane * E;
+        for (int t = pa; t < pb; ++t) {
           float wt[E];
+          if (row.inside(t, 1)) {
+            row.template visit<1>(t, lane, [&](const float (&w)[E]) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) wt[e] = 0.f;
-          if (x < pb) weights(x, wt);
+              for (int e = 0; e < E; ++e) wt[e] = w[e];
+            });
+          } else {
+            row.block(t, lane, wt);
+          }
           long long own = 0;
 #pragma unroll
           for (int e = 0; e < E; ++e) own += verify_weight(wt[e]);
@@ -259,10 +354,10 @@ verify_kernel(const __grid_constant__ VerifyParams p) {
           if (over) {
             if (lane == __ffs(over) - 1) {
               long long at = run + incl - own;
-              int found = x;
+              int found = 0;
 #pragma unroll
               for (int e = 0; e < E; ++e) {
-                if (at <= r) found = x + e;
+                if (at <= r) found = (t * 32 + lane) * E - row.sp + e;
                 at += verify_weight(wt[e]);
               }
               out[a] = found;
