@@ -1705,15 +1705,16 @@ pkv_status pkv_step_tables(const int32_t* lens, const int32_t* counts, int32_t* 
   pkv::StepParams p = {lens, counts, block_tables, held, shared, ring, ring_state, context_lens,
                        cu_seqlens, cu_blocks, positions, slots, held_out, ring_state_out, totals,
                        ring_size, num_blocks, max_blocks_per_seq, num_seqs, num_tokens, block_size,
-                       log2_exact(block_size)};
+                       log2_exact(block_size), aligned(positions, 16) && aligned(slots, 16)};
   cudaStream_t st = as_stream(stream);
   if (num_tokens <= pkv::kStepFusedTokens) {
     PKV_CUDA(launch_pdl(pkv::step_requests_kernel<true>, dim3(1), dim3(pkv::kStepThreads), 0, st, p));
     return PKV_OK;
   }
   PKV_CUDA(launch_pdl(pkv::step_requests_kernel<false>, dim3(1), dim3(pkv::kStepThreads), 0, st, p));
-  PKV_CUDA(launch_pdl(pkv::step_tokens_kernel, dim3((unsigned)ceil_div(num_tokens, 256)), dim3(256),
-                      0, st, p));
+  PKV_CUDA(launch_pdl(pkv::step_tokens_kernel, 
+                      dim3((unsigned)ceil_div(num_tokens, pkv::kStepTokenRows)),
+                      dim3(pkv::kStepTokenThreads), 0, st, p));
   return PKV_OK;
 }
 

@@ -44,6 +44,7 @@ struct StepParams {
   int T;                      // rows of positions / slots
   int K;
   int log2_k;                 // >= 0: K is a power of two
+  int wide;                   // positions and slots are 16-byte aligned
 };
 
 struct StepRequest {
@@ -115,40 +116,50 @@ __device__ __forceinline__ void step_scan(long long& n, long long& pk, long long
   tp = s_b[31];
 }
 
-// Token row t: its request by binary search in cu, its position, its block
-// (an old table entry or a fresh one from the ring) and slot.
-__device__ __forceinline__ void step_token(const StepParams& p, int t, int total, int64_t head,
-                                           const int32_t* cu, const int32_t* cb) {
-  int pos = -1;
-  int64_t slot = -1;
-  if (t < total) {
-    int lo = 0, hi = p.S;                 // cu[lo] <= t < cu[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cu[mid] <= t) lo = mid; else hi = mid;
-    }
-    const int c0 = cu[lo], c1 = cu[lo + 1], b0 = cb[lo], take = cb[lo + 1] - b0;
-    pos = p.ctx[lo] - (c1 - t);
-    const int held = p.held_out[lo] - take;
-    const int lb = p.log2_k >= 0 ? pos >> p.log2_k : pos / p.K;
-    const int off = pos - lb * p.K;
-    (void)c0;
-    int32_t* entry = p.tables + (int64_t)lo * p.max_blocks + lb;
-    int id;
-    if (lb < held) {
-      id = *entry;
-    } else {
-      id = p.ring[(head + b0 + (lb - held)) % p.ring_size];
-      if (off == 0) *entry = id;
-    }
-    if (id < 0 || id >= p.num_blocks) {
-      record_error(PKV_DEVERR_BLOCK_ID);
-    } else {
-      slot = (int64_t)id * p.K + off;
-    }
+// What the token rows need of their requests, in global memory (the outputs
+// of the call) or, for a small step, in shared memory.
+struct StepView {
+  const int32_t* cu;
+  const int32_t* cb;
+  const int32_t* ctx;
+  const int32_t* held_out;
+  int total;                // tokens of the step
+  int64_t head;             // head of the ring, modulo its size
+};
+
+// The request that holds token t, among requests lo .. hi - 1 (cu[lo] <= t < cu[hi]).
+__device__ __forceinline__ int step_find(const int32_t* cu, int lo, int hi, int t) {
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid; else hi = mid;
   }
-  p.positions[t] = pos;
-  p.slots[t] = slot;
+  return lo;
+}
+
+// Position and slot of token t of request s: from an old table entry or a
+// fresh block of the ring, whose first token writes the entry.
+__device__ __forceinline__ void step_token(const StepParams& p, const StepView& v, int s, int t,
+                                           int& pos, int64_t& slot) {
+  const int b0 = v.cb[s], take = v.cb[s + 1] - b0;
+  pos = v.ctx[s] - (v.cu[s + 1] - t);
+  const int held = v.held_out[s] - take;
+  const int lb = p.log2_k >= 0 ? pos >> p.log2_k : pos / p.K;
+  const int off = pos - lb * p.K;
+  int32_t* entry = p.tables + (int64_t)s * p.max_blocks + lb;
+  int id;
+  if (lb < held) {
+    id = *entry;
+  } else {
+    int64_t at = v.head + b0 + (lb - held);       // below twice the ring
+    if (at >= p.ring_size) at -= p.ring_size;
+    id = p.ring[at];
+    if (off == 0) *entry = id;
+  }
+  slot = -1;
+  if (id < 0 || id >= p.num_blocks)
+    record_error(PKV_DEVERR_BLOCK_ID);
+  else
+    slot = (int64_t)id * p.K + off;
 }
 
 // One CTA: checks, sums, per-request outputs and the blocks given back.
@@ -158,8 +169,15 @@ __global__ void __launch_bounds__(kStepThreads)
 step_requests_kernel(const __grid_constant__ StepParams p) {
   __shared__ long long s_a[32], s_b[32];
   __shared__ int s_bad;
+  // small steps: the token rows find their requests in shared memory
+  __shared__ int32_t s_cu[WITH_TOKENS ? kStepThreads + 1 : 1], s_cb[WITH_TOKENS ? kStepThreads + 1 : 1];
+  __shared__ int32_t s_ctx[WITH_TOKENS ? kStepThreads : 1], s_held[WITH_TOKENS ? kStepThreads : 1];
   const int tid = threadIdx.x, lane = tid & 31;
+  const bool local = WITH_TOKENS && p.S <= kStepThreads;
   pdl_wait_primary();
+  // without the token rows the next kernel is step_tokens_kernel, which waits
+  // for this one before it reads anything
+  if (!WITH_TOKENS) pdl_launch_dependents();
   const int64_t head = p.state[0], tail = p.state[1];
   if (tid == 0) s_bad = 0;
   __syncthreads();
@@ -194,6 +212,7 @@ step_requests_kernel(const __grid_constant__ StepParams p) {
     p.state_out[1] = tail + (code ? 0 : give);
     p.cu[0] = 0;
     p.cb[0] = 0;
+    s_cu[0] = s_cb[0] = 0;
     if (code >= 2) record_error(PKV_DEVERR_STEP);
   }
   // ---- per request
@@ -220,6 +239,12 @@ step_requests_kernel(const __grid_constant__ StepParams p) {
       p.held_out[s] = over ? 0 : r.held + r.take;
       p.cu[s + 1] = (int)(en + r.n);
       p.cb[s + 1] = (int)(ep >> 32) + r.take;
+      if (local) {
+        s_ctx[s] = r.ctx;
+        s_held[s] = over ? 0 : r.held + r.take;
+        s_cu[s + 1] = (int)(en + r.n);
+        s_cb[s + 1] = (int)(ep >> 32) + r.take;
+      }
     }
     // a warp gives back the blocks of its 32 requests, one after the other
     unsigned todo = __ballot_sync(0xffffffffu, r.give > 0);
@@ -230,15 +255,33 @@ step_requests_kernel(const __grid_constant__ StepParams p) {
       const int first = __shfl_sync(0xffffffffu, r.first, l);
       const int64_t to = tail + __shfl_sync(0xffffffffu, (int)(ep & 0xffffffffLL), l);
       const int32_t* row = p.tables + (int64_t)(s - lane + l) * p.max_blocks + first;
-      for (int i = lane; i < give_l; i += 32) p.ring[(to + i) % p.ring_size] = row[i];
+      int64_t at = to % p.ring_size + lane;
+      for (int i = lane; i < give_l; i += 128) {          // four loads in flight
+        int32_t id[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (i + 32 * u < give_l) id[u] = row[i + 32 * u];
+#pragma unroll
+        for (int u = 0; u < 4; ++u, at += 32) {
+          if (at >= p.ring_size) at -= p.ring_size;
+          if (i + 32 * u < give_l) p.ring[at] = id[u];
+        }
+      }
     }
     cn += tn;
     cp += tp;
   }
   if constexpr (WITH_TOKENS) {
     __syncthreads();
-    const int total = code ? 0 : p.cu[p.S];
-    for (int t = tid; t < p.T; t += kStepThreads) step_token(p, t, total, head, p.cu, p.cb);
+    StepView v = {p.cu, p.cb, p.ctx, p.held_out, code ? 0 : (int)cn, head % p.ring_size};
+    if (local) v = {s_cu, s_cb, s_ctx, s_held, v.total, v.head};
+    for (int t = tid; t < p.T; t += kStepThreads) {
+      int pos = -1;
+      int64_t slot = -1;
+      if (t < v.total) step_token(p, v, step_find(v.cu, 0, p.S, t), t, pos, slot);
+      p.positions[t] = pos;
+      p.slots[t] = slot;
+    }
   }
   // later kernels read the tables and lengths before they wait for the
   // kernel in front of them: no early trigger here, and everything is
@@ -246,12 +289,64 @@ step_requests_kernel(const __grid_constant__ StepParams p) {
   __threadfence();
 }
 
-__global__ void __launch_bounds__(256) step_tokens_kernel(const __grid_constant__ StepParams p) {
+// Token rows of a large step: a warp takes 128 of them, four consecutive ones
+// a lane, and looks for the requests of its first and last row with 32 probes
+// at a time.  Bound by the 12 bytes written per row.
+constexpr int kStepTokenThreads = 256;
+constexpr int kStepTokenRows = 4 * kStepTokenThreads;
+
+__device__ __forceinline__ int step_find_warp(const int32_t* cu, int n, int t, int lane) {
+  int lo = 0, hi = n;                               // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < hi && cu[at] <= t);
+    lo += (31 - __clz(le)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kStepTokenThreads)
+step_tokens_kernel(const __grid_constant__ StepParams p) {
+  const int lane = threadIdx.x & 31;
+  const int w0 = blockIdx.x * kStepTokenRows + (threadIdx.x >> 5) * 128;
   pdl_wait_primary();
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t >= p.T) return;
-  const int64_t head = p.state_out[0] - (p.totals[0] ? 0 : p.totals[2]);
-  step_token(p, t, p.cu[p.S], head, p.cu, p.cb);
+  StepView v = {p.cu, p.cb, p.ctx, p.held_out, p.cu[p.S], 0};
+  int pos[4];
+  int64_t slot[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) pos[u] = -1, slot[u] = -1;
+  const int t0 = w0 + 4 * lane;
+  if (w0 < v.total) {
+    v.head = (p.state_out[0] - p.totals[2]) % p.ring_size;
+    const int first = step_find_warp(v.cu, p.S, w0, lane);
+    const int last = step_find_warp(v.cu, p.S, min(w0 + 127, v.total - 1), lane);
+    if (t0 < v.total) {
+      int s = step_find(v.cu, first, last + 1, t0);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int t = t0 + u;
+        if (t < v.total) {
+          while (t >= v.cu[s + 1]) ++s;
+          step_token(p, v, s, t, pos[u], slot[u]);
+        }
+      }
+    }
+  }
+  // (16-byte stores where the rows' ends and the arrays allow them)
+  if (t0 + 4 <= p.T && p.wide) {
+    *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    *reinterpret_cast<longlong2*>(p.slots + t0) = make_longlong2(slot[0], slot[1]);
+    *reinterpret_cast<longlong2*>(p.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (t0 + u < p.T) {
+        p.positions[t0 + u] = pos[u];
+        p.slots[t0 + u] = slot[u];
+      }
+    }
+  }
   __threadfence();
 }
 
