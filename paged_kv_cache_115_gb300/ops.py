@@ -673,41 +673,61 @@ def prefill_workspace_bytes(num_seqs, num_tokens, max_query_len, max_context_len
 # rotation + append, attention behind a shared prefix, draft verification
 # ---------------------------------------------------------------------------
 
-def _same_device(named) -> int:
-    """Device index of the CUDA tensors in ``named`` ((name, tensor or None)
-    pairs); they must all live on one device."""
-    dev = -1
-    for name, t in named:
-        if t is None:
-            continue
-        d = t.get_device() if isinstance(t, torch.Tensor) else -1
-        if d < 0:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if dev < 0:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"{name}: CUDA tensors on several devices")
-    return dev
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _call_on(dev: int, fn, args, what: str) -> None:
     """Calls the library with device ``dev`` current and its current stream as
     the last argument."""
     if torch.cuda.current_device() == dev:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, _raw_stream(dev))
     if st != PKV_OK:
         _check(st, what)
 
 
-def _vec(t: torch.Tensor, name: str, dtype, n: int) -> int:
-    """Address of a contiguous vector of ``n`` values."""
-    if t.dtype != dtype:
+def _device_of(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _refuse(t: torch.Tensor, name: str, dtype, dev: int, shape: str) -> None:
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: CUDA tensors on several devices")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and not t.is_contiguous()):
-        raise ValueError(f"{name} must be contiguous with {n} values, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _vec(t: torch.Tensor, name: str, dtype, n: int, dev: int) -> int:
+    """Address of a contiguous vector of ``n`` values on device ``dev``."""
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 1 or t.shape[0] != n or \
+            not t.is_contiguous():
+        _refuse(t, name, dtype, dev, f"contiguous [{n}]")
+    return t.data_ptr()
+
+
+def _table(t: torch.Tensor, name: str, dtype, n: int, dev: int) -> int:
+    """Address of a contiguous table of ``n`` rows on device ``dev``."""
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2 or t.shape[0] != n or \
+            not t.is_contiguous():
+        _refuse(t, name, dtype, dev, f"contiguous [{n}, ...]")
+    return t.data_ptr()
+
+
+def _whole(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of that shape on device ``dev``."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or \
+            not t.is_contiguous():
+        _refuse(t, name, dtype, dev, f"contiguous {tuple(shape)}")
     return t.data_ptr()
 
 
@@ -734,12 +754,7 @@ def step_tables(lens: torch.Tensor, counts: torch.Tensor, block_tables: torch.Te
     back} (code 0: done, else nothing changed); outputs that are given are
     written, ``context_lens`` may be ``lens``, ``held_out`` ``held`` and
     ``ring_state_out`` ``ring_state``."""
-    given = (("lens", lens), ("counts", counts), ("block_tables", block_tables), ("held", held),
-             ("ring", ring), ("ring_state", ring_state), ("shared", shared),
-             ("context_lens", context_lens), ("cu_seqlens", cu_seqlens), ("cu_blocks", cu_blocks),
-             ("positions", positions), ("slots", slots), ("held_out", held_out),
-             ("ring_state_out", ring_state_out), ("totals", totals))
-    dev = _same_device(given)
+    dev = _device_of(lens, "lens")
     i32, i64 = torch.int32, torch.int64
     if num_tokens is None:
         if positions is None and slots is None:
@@ -747,42 +762,52 @@ def step_tables(lens: torch.Tensor, counts: torch.Tensor, block_tables: torch.Te
         num_tokens = (positions if positions is not None else slots).shape[0]
     S, T = lens.shape[0], int(num_tokens)
 
-    def out(t, n, dtype):
-        return torch.empty(n, dtype=dtype, device=lens.device) if t is None else t
-    context_lens, held_out = out(context_lens, S, i32), out(held_out, S, i32)
-    cu_seqlens, cu_blocks = out(cu_seqlens, S + 1, i32), out(cu_blocks, S + 1, i32)
-    positions, slots = out(positions, T, i32), out(slots, T, i64)
-    ring_state_out, totals = out(ring_state_out, 2, i64), out(totals, 4, i32)
-    if block_tables.dtype != i32 or block_tables.dim() != 2 or block_tables.shape[0] != S or \
-            not block_tables.is_contiguous():
-        raise ValueError("block_tables must be contiguous int32 [num_seqs, max_blocks]")
+    def new(n, dtype):
+        return torch.empty(n, dtype=dtype, device=lens.device)
+    if context_lens is None:
+        context_lens = new(S, i32)
+    if cu_seqlens is None:
+        cu_seqlens = new(S + 1, i32)
+    if cu_blocks is None:
+        cu_blocks = new(S + 1, i32)
+    if positions is None:
+        positions = new(T, i32)
+    if slots is None:
+        slots = new(T, i64)
+    if held_out is None:
+        held_out = new(S, i32)
+    if ring_state_out is None:
+        ring_state_out = new(2, i64)
+    if totals is None:
+        totals = new(4, i32)
+    R = ring.shape[0]
     _call_on(dev, _step_tables,
-             (_vec(lens, "lens", i32, S), _vec(counts, "counts", i32, S), block_tables.data_ptr(),
-              block_tables.shape[1], _vec(held, "held", i32, S),
-              None if shared is None else _vec(shared, "shared", i32, S),
-              _vec(ring, "ring", i32, ring.shape[0]), ring.shape[0],
-              _vec(ring_state, "ring_state", i64, 2), S, T, block_size, num_blocks,
-              _vec(context_lens, "context_lens", i32, S),
-              _vec(cu_seqlens, "cu_seqlens", i32, S + 1), _vec(cu_blocks, "cu_blocks", i32, S + 1),
-              _vec(positions, "positions", i32, T), _vec(slots, "slots", i64, T),
-              _vec(held_out, "held_out", i32, S),
-              _vec(ring_state_out, "ring_state_out", i64, 2), _vec(totals, "totals", i32, 4)),
+             (_vec(lens, "lens", i32, S, dev), _vec(counts, "counts", i32, S, dev),
+              _table(block_tables, "block_tables", i32, S, dev), block_tables.shape[1],
+              _vec(held, "held", i32, S, dev),
+              None if shared is None else _vec(shared, "shared", i32, S, dev),
+              _vec(ring, "ring", i32, R, dev), R, _vec(ring_state, "ring_state", i64, 2, dev), S,
+              T, block_size, num_blocks, _vec(context_lens, "context_lens", i32, S, dev),
+              _vec(cu_seqlens, "cu_seqlens", i32, S + 1, dev),
+              _vec(cu_blocks, "cu_blocks", i32, S + 1, dev),
+              _vec(positions, "positions", i32, T, dev), _vec(slots, "slots", i64, T, dev),
+              _vec(held_out, "held_out", i32, S, dev),
+              _vec(ring_state_out, "ring_state_out", i64, 2, dev),
+              _vec(totals, "totals", i32, 4, dev)),
              "pkv_step_tables")
     return dict(context_lens=context_lens, cu_seqlens=cu_seqlens, cu_blocks=cu_blocks,
                 positions=positions, slots=slots, held_out=held_out,
                 ring_state_out=ring_state_out, totals=totals)
 
 
-def _token_rows(t: torch.Tensor, name: str, dtype, T: int, H: int, D: int) -> int:
+def _token_rows(t: torch.Tensor, name: str, dtype, T: int, H: int, D: int, dev: int) -> int:
     """Distance between the tokens of a [T, H, D] tensor whose heads and
     values are contiguous."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != T or t.shape[1] != H or t.shape[2] != D:
-        raise ValueError(f"{name} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (T, H, D):
+        _refuse(t, name, dtype, dev, f"[{T}, {H}, {D}]")
     a, b, c = t.stride()
     if (c != 1 and D > 1) or (b != D and H > 1):
-        raise ValueError(f"{name}: heads and values of a token must be contiguous")
+        _refuse(t, name, dtype, dev, f"[{T}, {H}, {D}], heads and values of a token contiguous,")
     return a if T > 1 else H * D
 
 
@@ -806,36 +831,33 @@ def paged_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     nb, K, H_kv, D2 = k_cache.shape
     if q_out is None:
         q_out = torch.empty((T, H_q, D), dtype=q.dtype, device=q.device)
-    dev = _same_device((("q", q), ("k", k), ("v", v), ("positions", positions), ("slots", slots),
-                        ("k_cache", k_cache), ("v_cache", v_cache), ("cos_sin", cos_sin),
-                        ("q_weight", q_weight), ("k_weight", k_weight), ("q_out", q_out)))
+    dev, dtype = _device_of(q, "q"), q.dtype
     if D2 != D or v_cache.shape != k_cache.shape:
         raise ValueError("pools must be [num_blocks, block_size, H_kv, D] of q's head size")
     if quant is None:
-        if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or \
-                not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-            raise TypeError("plain pools must be contiguous and of q's dtype")
+        kp = _whole(k_cache, "k_cache", dtype, k_cache.shape, dev)
+        vp = _whole(v_cache, "v_cache", dtype, k_cache.shape, dev)
     else:
         _need_pool(k_cache, "k_cache", quant)
         _need_pool(v_cache, "v_cache")
+        kp = _whole(k_cache, "k_cache", k_cache.dtype, k_cache.shape, dev)
+        vp = _whole(v_cache, "v_cache", v_cache.dtype, k_cache.shape, dev)
         if quant.format == KV_INT8_TOKEN:
             for t in getattr(quant, "_scale_tensors", ()):
                 if t.shape[0] != nb * K or t.get_device() != dev:
                     raise ValueError("token scales must cover every slot of the pool, on its device")
-    if cos_sin.dtype != torch.float32:
-        raise TypeError(f"cos_sin must be float32, got {cos_sin.dtype}")
-    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be contiguous float32 [max_position, rot_dim]")
+    far = cos_sin.shape[0]
     _call_on(dev, _rope_append,
-             (q.data_ptr(), _token_rows(q, "q", q.dtype, T, H_q, D),
-              k.data_ptr(), _token_rows(k, "k", q.dtype, T, H_kv, D),
-              v.data_ptr(), _token_rows(v, "v", q.dtype, T, H_kv, D),
-              None if q_weight is None else _vec(q_weight, "q_weight", q.dtype, D),
-              None if k_weight is None else _vec(k_weight, "k_weight", q.dtype, D), eps,
-              _vec(positions, "positions", torch.int32, T), cos_sin.data_ptr(), cos_sin.shape[0],
-              cos_sin.shape[1], 1 if interleaved else 0, _vec(slots, "slots", torch.int64, T), T,
-              H_q, H_kv, D, q_out.data_ptr(), _token_rows(q_out, "q_out", q.dtype, T, H_q, D),
-              k_cache.data_ptr(), v_cache.data_ptr(), nb, K, _dtype_code(q),
+             (q.data_ptr(), _token_rows(q, "q", dtype, T, H_q, D, dev),
+              k.data_ptr(), _token_rows(k, "k", dtype, T, H_kv, D, dev),
+              v.data_ptr(), _token_rows(v, "v", dtype, T, H_kv, D, dev),
+              None if q_weight is None else _vec(q_weight, "q_weight", dtype, D, dev),
+              None if k_weight is None else _vec(k_weight, "k_weight", dtype, D, dev), eps,
+              _vec(positions, "positions", torch.int32, T, dev),
+              _table(cos_sin, "cos_sin", torch.float32, far, dev), far, cos_sin.shape[1],
+              1 if interleaved else 0, _vec(slots, "slots", torch.int64, T, dev), T, H_q, H_kv, D,
+              q_out.data_ptr(), _token_rows(q_out, "q_out", dtype, T, H_q, D, dev), kp, vp, nb, K,
+              _dtype_code(q),
               None if quant is None else ctypes.byref(quant)), "pkv_qk_norm_rope_append")
     return q_out
 
@@ -870,36 +892,31 @@ def paged_attention_decode_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     :func:`prefix_workspace_bytes` bytes (allocated when None)."""
     if out is None:
         out = torch.empty_like(q)
-    dev = _same_device((("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
-                        ("prefix_table", prefix_table), ("block_tables", block_tables),
-                        ("context_lens", context_lens), ("cu_seqlens", cu_seqlens), ("out", out),
-                        ("workspace", workspace)))
+    dev, dtype, i32 = _device_of(q, "q"), q.dtype, torch.int32
     T, H_q, D = q.shape
     nb, K, H_kv, D2 = k_cache.shape
     S = context_lens.shape[0]
-    if D2 != D or v_cache.shape != k_cache.shape or out.shape != q.shape:
-        raise ValueError("shape mismatch between q, pools and out")
-    for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("out", out)):
-        if t.dtype != q.dtype or not t.is_contiguous():
-            raise TypeError(f"{name} must be contiguous {q.dtype}")
-    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or \
-            block_tables.shape[0] != S or not block_tables.is_contiguous():
-        raise ValueError("block_tables must be contiguous int32 [num_seqs, max_blocks]")
-    if prefix_table.shape[0] * K < prefix_len:
+    if D2 != D:
+        raise ValueError("shape mismatch between q and the pools")
+    listed = prefix_table.shape[0]
+    if listed * K < prefix_len:
         raise ValueError("prefix_table does not list prefix_len tokens")
+    kp = _whole(k_cache, "k_cache", dtype, k_cache.shape, dev)
+    vp = _whole(v_cache, "v_cache", dtype, k_cache.shape, dev)
     if workspace is None:
         workspace = torch.empty(
             max(prefix_workspace_bytes(S, T, max_query_len, max_context_len, prefix_len, H_q,
-                                       H_kv, D, K, q.dtype), 256), dtype=torch.uint8,
+                                       H_kv, D, K, dtype), 256), dtype=torch.uint8,
             device=q.device)
+    ws_bytes = workspace.shape[0]
     _call_on(dev, _prefix,
-             (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-              _vec(prefix_table, "prefix_table", torch.int32, prefix_table.shape[0]),
-              prefix_len, block_tables.data_ptr(), block_tables.shape[1],
-              None if cu_seqlens is None else _vec(cu_seqlens, "cu_seqlens", torch.int32, S + 1),
-              _vec(context_lens, "context_lens", torch.int32, S), S, T, max_query_len,
-              max_context_len, H_q, H_kv, D, K, nb, scale, out.data_ptr(),
-              _vec(workspace, "workspace", torch.uint8, workspace.shape[0]), workspace.shape[0],
+             (_whole(q, "q", dtype, q.shape, dev), kp, vp,
+              _vec(prefix_table, "prefix_table", i32, listed, dev), prefix_len,
+              _table(block_tables, "block_tables", i32, S, dev), block_tables.shape[1],
+              None if cu_seqlens is None else _vec(cu_seqlens, "cu_seqlens", i32, S + 1, dev),
+              _vec(context_lens, "context_lens", i32, S, dev), S, T, max_query_len,
+              max_context_len, H_q, H_kv, D, K, nb, scale, _whole(out, "out", dtype, q.shape, dev),
+              _vec(workspace, "workspace", torch.uint8, ws_bytes, dev), ws_bytes,
               _dtype_code(q)), "pkv_attention_decode_prefix")
     return out
 
@@ -915,34 +932,31 @@ def verify_draft_tokens(target_probs: torch.Tensor, draft_probs: Optional[torch.
     axes; None: drafts without probabilities), ``uniforms`` float32 [T] in
     [0, 1).  Returns (out_tokens int32 [S, max_query_len]: accepted drafts,
     one drawn token, then -1; num_new int32 [S])."""
-    dev = _same_device((("target_probs", target_probs), ("draft_probs", draft_probs),
-                        ("tokens", tokens), ("uniforms", uniforms), ("cu_seqlens", cu_seqlens),
-                        ("out_tokens", out_tokens), ("num_new", num_new)))
+    dev, dtype, i32 = _device_of(target_probs, "target_probs"), target_probs.dtype, torch.int32
     T, V = target_probs.shape
     S = cu_seqlens.shape[0] - 1
     if out_tokens is None:
-        out_tokens = torch.empty((S, max_query_len), dtype=torch.int32, device=tokens.device)
+        out_tokens = torch.empty((S, max_query_len), dtype=i32, device=tokens.device)
     if num_new is None:
-        num_new = torch.empty(S, dtype=torch.int32, device=tokens.device)
-    if T > 0 and V > 1 and target_probs.stride(1) != 1:
+        num_new = torch.empty(S, dtype=i32, device=tokens.device)
+    ts, one = target_probs.stride()
+    if one != 1 and V > 1:
         raise ValueError("target_probs: a row must be contiguous")
     dp, ds, dt = None, 0, 0
     if draft_probs is not None and max_query_len > 1:
-        if draft_probs.dtype != target_probs.dtype:
-            raise TypeError(f"draft_probs must be {target_probs.dtype}")
-        if draft_probs.dim() != 3 or draft_probs.shape[0] != S or \
-                draft_probs.shape[1] < max_query_len - 1 or draft_probs.shape[2] != V or \
-                (V > 1 and draft_probs.stride(2) != 1):
-            raise ValueError(f"draft_probs must be [{S}, {max_query_len - 1}, {V}] with "
-                             "contiguous rows")
-        dp, ds, dt = draft_probs.data_ptr(), draft_probs.stride(0), draft_probs.stride(1)
-    if out_tokens.dtype != torch.int32 or out_tokens.dim() != 2 or out_tokens.shape[0] != S or \
-            out_tokens.shape[1] != max_query_len or not out_tokens.is_contiguous():
-        raise ValueError(f"out_tokens must be contiguous int32 [{S}, {max_query_len}]")
+        if draft_probs.dtype is not dtype or draft_probs.get_device() != dev or \
+                draft_probs.dim() != 3 or draft_probs.shape[0] != S or \
+                draft_probs.shape[1] < max_query_len - 1 or draft_probs.shape[2] != V:
+            _refuse(draft_probs, "draft_probs", dtype, dev, f"[{S}, {max_query_len - 1}, {V}]")
+        ds, dt, one = draft_probs.stride()
+        if one != 1 and V > 1:
+            raise ValueError("draft_probs: a row must be contiguous")
+        dp = draft_probs.data_ptr()
     _call_on(dev, _verify,
-             (target_probs.data_ptr(), target_probs.stride(0) if T > 1 else V, dp, ds, dt,
-              _vec(tokens, "tokens", torch.int32, T), _vec(uniforms, "uniforms", torch.float32, T),
-              _vec(cu_seqlens, "cu_seqlens", torch.int32, S + 1), S, T, max_query_len, V,
-              out_tokens.data_ptr(), _vec(num_new, "num_new", torch.int32, S),
+             (target_probs.data_ptr(), ts if T > 1 else V, dp, ds, dt,
+              _vec(tokens, "tokens", i32, T, dev), _vec(uniforms, "uniforms", torch.float32, T, dev),
+              _vec(cu_seqlens, "cu_seqlens", i32, S + 1, dev), S, T, max_query_len, V,
+              _whole(out_tokens, "out_tokens", i32, (S, max_query_len), dev),
+              _vec(num_new, "num_new", i32, S, dev),
               _dtype_code(target_probs)), "pkv_verify_draft_tokens")
     return out_tokens, num_new
