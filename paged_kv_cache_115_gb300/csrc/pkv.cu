@@ -882,16 +882,13 @@ pkv_status plan_prefix(int S, int T, int max_q, int prefix_len, int H_q, int H_k
   p.split.max_q = max_q;
   p.split.sms = sms;
   p.split.groups = groups;
-  // relative SM time of a prefix step (64 keys x one KV head) and of an own
-  // chunk (16 tokens x hpc KV heads), from sweeps of the quotient: with two
-  // query tiles an item (1024 sequences over 2048 + ~520 tokens) 10 / 24 gives
-  // 924 us, 20 / 24 453, 40 / 24 363, 80 / 24 364, and (61 x ~2.5 rows over
-  // 4112 + ~350) 62, 46, 41, 46; with one (8 sequences over 131072 + ~1000)
-  // 8 / 24 gives 116 us, 22 / 24 108, 32 / 24 120
-  p.split.w1 = p.tile_rows == pkv::kT5Rows ? 22 : 40;
-  p.split.w2 = std::max(3 * p.hpc, 6);
+  // SM time, in 10 ns: a tile step of the prefix, a chunk of own tokens of hpc
+  // KV heads, a sequence's start and end
+  p.split.w1 = D == 64 ? 70 : 90;
+  p.split.w2 = 35 + 25 * p.hpc * D / 1024;
+  p.split.w3 = 180;
   p.own_slots = ((int64_t)p.n_per_group + S) * max_q;
-  const int64_t items = ceil_div((int64_t)T * G, p.tile_rows) * H_kv;
+  const int64_t items = ceil_div((int64_t)T * G, 2 * pkv::kT5Rows) * H_kv;
   const int64_t rows = prefix_len > 0 ? (sms + items) * p.tile_rows : 0;
   // partials of a row: CTAs per item, one more where shares cross items, and
   // one or two of its own tokens; eight to a warp
@@ -907,14 +904,15 @@ pkv_status plan_prefix(int S, int T, int max_q, int prefix_len, int H_q, int H_k
   return PKV_OK;
 }
 
-template <int D, bool SOLO>
-pkv_status launch_prefix_part(const pkv::PxParams& prm, int sms, cudaStream_t st, int dev) {
+template <int D>
+pkv_status launch_prefix_part(const pkv::PxParams& prm, const PrefixPlan& plan, cudaStream_t st) {
   static std::once_flag flags[kMaxDevices];
   static cudaError_t errs[kMaxDevices];
-  auto k = pkv::prefix_tc05_kernel<D, SOLO>;
-  pkv_status s = set_smem_once(k, pkv::PxCfg<D>::SMEM, flags, errs, dev);
+  auto k = pkv::prefix_tc05_kernel<D>;
+  pkv_status s = set_smem_once(k, pkv::PxCfg<D>::SMEM, flags, errs, plan.dev);
   if (s != PKV_OK) return s;
-  PKV_CUDA(launch_pdl(k, dim3(sms), dim3(pkv::kPxThreads), (size_t)pkv::PxCfg<D>::SMEM, st, prm));
+  PKV_CUDA(launch_pdl(k, dim3(plan.split.sms), dim3(pkv::kPxThreads), (size_t)pkv::PxCfg<D>::SMEM,
+                      st, prm, plan.tile_rows));
   return PKV_OK;
 }
 
@@ -1830,7 +1828,7 @@ pkv_status pkv_attention_decode_prefix(
   if (st != PKV_OK) return st;
   PKV_CHECK(workspace_bytes >= plan.ws_bytes, PKV_ERR_WORKSPACE_TOO_SMALL,
             "workspace %zu bytes < %zu needed", workspace_bytes, plan.ws_bytes);
-  const int D = head_dim, G = num_q_heads / num_kv_heads, sms = plan.split.sms;
+  const int D = head_dim, G = num_q_heads / num_kv_heads;
   cudaStream_t strm = as_stream(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const float sl = (float)((double)scale * 1.4426950408889634);
@@ -1894,15 +1892,8 @@ pkv_status pkv_attention_decode_prefix(
     st = encode_pool_map(&p.tmap_k, k_cache, num_blocks, block_size, num_kv_heads, D);
     if (st == PKV_OK)
       st = encode_pool_map(&p.tmap_v, v_cache, num_blocks, block_size, num_kv_heads, D);
-    if (st == PKV_OK) {
-      const bool solo = plan.tile_rows == pkv::kT5Rows;
-      if (D == 64)
-        st = solo ? launch_prefix_part<64, true>(p, sms, strm, plan.dev)
-                  : launch_prefix_part<64, false>(p, sms, strm, plan.dev);
-      else
-        st = solo ? launch_prefix_part<128, true>(p, sms, strm, plan.dev)
-                  : launch_prefix_part<128, false>(p, sms, strm, plan.dev);
-    }
+    if (st == PKV_OK)
+      st = D == 64 ? launch_prefix_part<64>(p, plan, strm) : launch_prefix_part<128>(p, plan, strm);
   }
   if (st != PKV_OK) return st;
   const bool b8 = block_size < pkv::kTile;

@@ -47,14 +47,20 @@ constexpr int tc_chunk_tokens(int ct) { return ct == 1 || ct == 2 ? 2 * kTile : 
 
 // Attention behind a shared prefix (pkv_prefix.cuh): the prefix kernel and
 // this kernel (instantiated with PX, on the tokens from prefix_len on) share
-// the SMs.  Both derive the shares from the same counts: `steps` of the prefix
-// kernel weigh w1, chunks of this one w2.
+// the SMs.  Both derive the shares from the same counts: tile steps of the
+// prefix kernel (128 query rows x 128 keys) weigh w1, chunks of this one w2
+// and its sequences w3 (the start and the partial state of each).
+constexpr int kPxKeys = 128;
+__host__ __device__ constexpr int px_tiles(int rows) { return (rows + 127) / 128; }
+__host__ __device__ constexpr int px_key_tiles(int prefix_len) {
+  return (prefix_len + kPxKeys - 1) / kPxKeys;
+}
 struct PxSplit {
   int prefix_len;
   int max_q;       // bound on the new tokens of a sequence
   int sms;         // CTAs of both kernels together
   int groups;      // KV-head groups of this kernel
-  int w1, w2;
+  int w1, w2, w3;
 };
 
 // 16-token chunks of sequence s's own tokens (L: its clamped length; 0 for an
@@ -68,14 +74,16 @@ __device__ __forceinline__ int px_own_chunks(const PxSplit& x, const int32_t* cu
   return L > x.prefix_len ? (L - x.prefix_len + kTile - 1) / kTile : 0;
 }
 
-// CTAs of the prefix kernel (0 without prefix steps).
-__host__ __device__ __forceinline__ int px_ctas(const PxSplit& x, long long steps,
-                                                long long chunks) {
-  if (steps == 0) return 0;
-  const long long a = steps * x.w1, b = chunks * x.groups * x.w2;
+// CTAs of the prefix kernel (0 without prefix work), each with two tile steps
+// or more: then every CTA begins a step.
+__host__ __device__ __forceinline__ int px_ctas(const PxSplit& x, long long work,
+                                                long long chunks, int seqs) {
+  if (work == 0) return 0;
+  const long long a = work * x.w1;
+  const long long b = chunks == 0 ? 0 : (chunks * x.w2 + (long long)seqs * x.w3) * x.groups;
   long long n = b == 0 ? x.sms : (x.sms * a + (a + b) / 2) / (a + b);
   if (b > 0 && n > x.sms - x.groups) n = x.sms - x.groups;
-  if (n > steps) n = steps;
+  if (n > work / 2) n = work / 2;
   return n < 1 ? 1 : (int)n;
 }
 
@@ -419,10 +427,8 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   if constexpr (PX) {
     // the SMs that the prefix kernel leaves
     const int nt = cu == nullptr ? S : max(0, min(cu[S], p.num_tokens));
-    const int tile = p.num_tokens * p.G <= 128 ? 128 : 256;
-    const long long steps = (long long)((nt * p.G + tile - 1) / tile) * p.px_heads *
-                            ((p.px.prefix_len + 63) / 64);
-    most = max(1, min((int)gridDim.x, (p.px.sms - px_ctas(p.px, steps, T)) / p.px.groups));
+    const long long work = (long long)p.px_heads * px_tiles(nt * p.G) * px_key_tiles(p.px.prefix_len);
+    most = max(1, min((int)gridDim.x, (p.px.sms - px_ctas(p.px, work, T, S)) / p.px.groups));
   }
   const int n = (int)(T < most ? (T > 0 ? T : 1) : most);
   const int cta = blockIdx.x, group = blockIdx.y;

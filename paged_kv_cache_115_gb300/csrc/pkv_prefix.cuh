@@ -21,9 +21,7 @@
 
 namespace pkv {
 
-constexpr int kPxBN = 64;             // keys per step
-constexpr int kPxKStages = 5;
-constexpr int kPxVStages = 5;
+constexpr int kPxBN = kPxKeys;        // keys per step
 constexpr int kPxThreads = 384;
 
 struct PxParams {
@@ -53,21 +51,22 @@ template <int D>
 struct PxCfg {
   static constexpr int NH = D / 64;
   static constexpr int QHALF = kT5Rows * 128;             // 16 KiB
-  static constexpr int QBYTES = NH * QHALF;               // one query tile
-  static constexpr int KVHALF = kPxBN * 128;              // 8 KiB
+  static constexpr int QBYTES = 2 * QHALF;                // one query tile (64 fp32 values of O too)
+  static constexpr int OROW = 256;
+  static constexpr int KVHALF = kPxBN * 128;              // 16 KiB
   static constexpr int KBYTES = NH * KVHALF;              // one K (or V) tile
   static constexpr int NBOX = NH * (kPxBN / 16);
+  static constexpr int NS = D == 128 ? 5 : 8;             // ring of K and V tiles in turn
   static constexpr int Q_OFF = 0;                         // [tile][half]
-  static constexpr int K_OFF = 2 * QBYTES;
-  static constexpr int V_OFF = K_OFF + kPxKStages * KBYTES;
-  static constexpr int BAR_OFF = V_OFF + kPxVStages * KBYTES;
-  // k_full/k_empty[KS], v_full/v_empty[VS], per tile: s_full[2], p_free[2],
-  // p_full[2], o_done, q_full; mma_idle
-  static constexpr int NBAR = 2 * (kPxKStages + kPxVStages) + 2 * 8 + 1;
+  static constexpr int KV_OFF = 2 * QBYTES;
+  static constexpr int BAR_OFF = KV_OFF + NS * KBYTES;
+  // full[NS], empty[NS]; per S buffer: p_free, p_full[2]; per query tile:
+  // s_full[2], o_done, q_full; mma_idle
+  static constexpr int NBAR = 2 * NS + 2 * 3 + 2 * 4 + 1;
   static constexpr int SLOT_OFF = BAR_OFF + 8 * NBAR;
   static constexpr int SMEM = SLOT_OFF + 16 + 1024;
-  // per tile: S buffers 0, 1 (64 columns each: fp32 S, then P as bf16 pairs
-  // in the lower 32), O (128)
+  // S buffers 0, 1 (128 columns each: fp32 S, then P as bf16 pairs in the
+  // upper 64), O of tile A, O of tile B (128 each)
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t IDESC_QK = umma_idesc_bf16(kT5Rows, kPxBN, 0, 0);
   static constexpr uint32_t IDESC_PV = umma_idesc_bf16(kT5Rows, D, 0, 1);
@@ -111,6 +110,24 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// The 128 softmax threads of a tile wait for one another.
+__device__ __forceinline__ void px_tile_sync(int x) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
+}
+
+// The same, and whether all of them say so: a warp that gave up on a wait
+// still gets here, so that no other one waits for it.
+__device__ __forceinline__ bool px_tile_all(int x, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.and.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(1 + x), "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+
 // 64 consecutive fp32 columns of this thread's TMEM lane, landed.
 __device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, float (&v)[64]) {
   uint32_t a[32], b[32];
@@ -125,16 +142,24 @@ __device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, float (&v)[64]) {
 }
 
 // ===========================================================================
-// Prefix part.  Item = (KV head, pair of 128-row tiles; SOLO: one tile); an
-// item takes ceil(prefix_len / 64) steps of 64 keys.  CTA c of n1 owns steps
-// [c S / n1, (c + 1) S / n1) of all S: a run of one item's steps is one
-// partial state, in slot c + item (distinct, as in the decode kernel).
+// Prefix part.  An item is a KV head and up to two tiles of 128 query rows;
+// it takes a step per 128 prefix keys.  The work of all items is counted in
+// tile steps, and CTA c of n1 takes the steps that begin in [c W / n1,
+// (c + 1) W / n1) of all W: a run of one item's steps is one partial state,
+// in slot c + item (distinct, as in the decode kernel).
 //
-// Warps 0-3: softmax of tile A, 4-7: of tile B (one thread per query row =
-// TMEM lane); warp 8: TMA producer of K tiles, warp 10: of V tiles; warp 9:
-// TMEM and, on one lane, S = Q K^T for both tiles (two S buffers each); warp
-// 11, one lane: O += P V.  P overwrites the S buffer it came from and is read
-// from TMEM as the A operand.
+// A job is one query tile's step: S = Q K^T into one of two S buffers (jobs
+// take them in turn), softmax, O += P V.  With two tiles an item the jobs of
+// the tiles alternate, so one tile's softmax runs under the other's products,
+// which share every K and V tile; with one tile the jobs of consecutive
+// steps do.  Warps 0-3: softmax of tile A, 4-7: of tile B (one thread per
+// query row = TMEM lane); warp 8: TMA producer of K tiles, warp 10: of V
+// tiles; warp 9: TMEM and the S products; warp 11: the O products.
+//
+// A thread reads S twice: both halves of 64 keys for the row maximum, the
+// upper one kept, then the lower one again, so that 64 scores are live at a
+// time.  P overwrites the upper half of its S buffer (read by then), and the
+// upper keys' product starts while the lower keys' weights are computed.
 // P is rounded to bf16 (to nearest): the tensor cores take both operands of
 // a product in one type, and V is bf16.  The relative error of a weight is at
 // most 2^-8 and independent from key to key, below the rounding of the
@@ -142,26 +167,45 @@ __device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, float (&v)[64]) {
 // The exponent base of a row is raised only when its maximum grows by more
 // than 2^8, so O is rescaled in TMEM rarely.  Every wait is bounded.
 // ===========================================================================
-template <int D, bool SOLO>
+
+// The steps of CTA c: [g0, g1) of item * nkt + step.
+__device__ __forceinline__ long long px_step_at(long long unit, int nkt, int ntiles) {
+  const int npairs = (ntiles + 1) >> 1;
+  const long long head = (long long)nkt * ntiles;
+  const int j = (int)(unit / head);
+  const long long rem = unit - j * head;
+  const int pair = (int)(rem / (2LL * nkt));
+  const int nt = 2 * pair + 2 <= ntiles ? 2 : 1;
+  const int in = (int)(rem - 2LL * pair * nkt);
+  return ((long long)j * npairs + pair) * nkt + (in + nt - 1) / nt;
+}
+// First tile step of step `step` of an item.
+__device__ __forceinline__ long long px_unit_of(int item, int step, int nkt, int ntiles) {
+  const int npairs = (ntiles + 1) >> 1, j = item / npairs, pair = item - j * npairs;
+  const int nt = 2 * pair + 2 <= ntiles ? 2 : 1;
+  return (long long)j * nkt * ntiles + 2LL * pair * nkt + (long long)step * nt;
+}
+
+template <int D>
 __global__ void __launch_bounds__(kPxThreads, 1)
-prefix_tc05_kernel(const __grid_constant__ PxParams p) {
+prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
   using C = PxCfg<D>;
-  constexpr int NT = SOLO ? 1 : 2;                        // query tiles per item
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ long long s_chunks[kPxThreads / 32];
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t bars = sbase + C::BAR_OFF;
-  const uint32_t k_full = bars, k_empty = k_full + 8 * kPxKStages;
-  const uint32_t v_full = k_empty + 8 * kPxKStages, v_empty = v_full + 8 * kPxVStages;
-  const uint32_t tb0 = v_empty + 8 * kPxVStages;          // per-tile barriers, 8 each
-  auto s_full = [&](int x, int b) { return tb0 + 64 * x + 8 * b; };
-  auto p_free = [&](int x, int b) { return tb0 + 64 * x + 16 + 8 * b; };
-  auto p_full = [&](int x, int b) { return tb0 + 64 * x + 32 + 8 * b; };
-  auto o_done = [&](int x) { return tb0 + 64 * x + 48; };
-  auto q_full = [&](int x) { return tb0 + 64 * x + 56; };
-  const uint32_t mma_idle = tb0 + 128;
+  const uint32_t full = sbase + C::BAR_OFF, empty = full + 8 * C::NS;
+  const uint32_t tb0 = empty + 8 * C::NS;
+  // s_full belongs to a tile and counts that tile's jobs: the other tile's
+  // softmax warps may be several items ahead (past items of one tile), and a
+  // parity names a phase only to who has seen every phase before it
+  auto s_full = [&](int x, int c) { return tb0 + 16 * x + 8 * (c & 1); };
+  auto p_free = [&](int b) { return tb0 + 32 + 8 * b; };
+  auto p_full = [&](int b, int half) { return tb0 + 48 + 16 * b + 8 * half; };
+  auto o_done = [&](int x) { return tb0 + 80 + 8 * x; };
+  auto q_full = [&](int x) { return tb0 + 96 + 8 * x; };
+  const uint32_t mma_idle = tb0 + 112;
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
@@ -181,36 +225,38 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p) {
 #pragma unroll
   for (int w = 0; w < kPxThreads / 32; ++w) chunks += s_chunks[w];
   const int R = px_tokens(p.cu, p.S, p.T) * p.G;           // query rows per KV head
-  const int npairs = (R + NT * kT5Rows - 1) / (NT * kT5Rows);
   const int P = p.split.prefix_len;
-  const int nkt = (P + kPxBN - 1) / kPxBN;
-  const long long steps = (long long)npairs * p.H_kv * nkt;
-  const int n1 = px_ctas(p.split, steps, chunks);
+  const int ntiles = px_tiles(R), npairs = (ntiles + 1) >> 1;
+  const int nkt = px_key_tiles(P);
+  const long long work = (long long)p.H_kv * nkt * ntiles;
+  const int n1 = px_ctas(p.split, work, chunks, p.S);
   if (cta >= n1) return;
   if (cta == n1 - 1) {                                     // which CTAs hold steps of each item
     for (int x = tid; x < npairs * p.H_kv; x += kPxThreads) {
-      const int a = cta_of_chunk((long long)x * nkt, steps, n1);
-      p.items[x] = make_int2(a, cta_of_chunk((long long)(x + 1) * nkt - 1, steps, n1) - a + 1);
+      const int a = cta_of_chunk(px_unit_of(x, 0, nkt, ntiles), work, n1);
+      p.items[x] =
+          make_int2(a, cta_of_chunk(px_unit_of(x, nkt - 1, nkt, ntiles), work, n1) - a + 1);
     }
   }
-  const long long g0 = cta * steps / n1;
-  const int ng = (int)((cta + 1) * steps / n1 - g0);       // steps of this CTA
+  const long long g0 = px_step_at(cta * work / n1, nkt, ntiles);
+  const long long g1 = cta + 1 == n1 ? (long long)npairs * p.H_kv * nkt
+                                     : px_step_at((cta + 1) * work / n1, nkt, ntiles);
+  const int ng = (int)(g1 - g0);                           // steps of this CTA
+  const int item0 = (int)(g0 / nkt), kt00 = (int)(g0 - (long long)item0 * nkt);
+  // query tiles of an item
+  auto tiles_of = [&](int item) -> int { return 2 * (item % npairs) + 2 <= ntiles ? 2 : 1; };
 
   if (tid == 0) {
-    for (int i = 0; i < kPxKStages; ++i) {
-      mbar_init(k_full + 8 * i, 1);
-      mbar_init(k_empty + 8 * i, NT);                      // every tile's S reads K
-    }
-    for (int i = 0; i < kPxVStages; ++i) {
-      mbar_init(v_full + 8 * i, 1);
-      mbar_init(v_empty + 8 * i, 1);
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
     }
     for (int x = 0; x < 2; ++x) {
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(s_full(x, b), 1);
-        mbar_init(p_free(x, b), 1);
-        mbar_init(p_full(x, b), kT5Rows);
-      }
+      mbar_init(s_full(x, 0), 1);
+      mbar_init(s_full(x, 1), 1);
+      mbar_init(p_free(x), 1);
+      mbar_init(p_full(x, 0), kT5Rows);
+      mbar_init(p_full(x, 1), kT5Rows);
       mbar_init(o_done(x), 1);
       mbar_init(q_full(x), kT5Rows);
     }
@@ -226,262 +272,293 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p) {
 
   if (warp == 8 || warp == 10) {
     // =================== TMA producers: warp 8 K tiles, warp 10 V tiles ===================
+    // Tile 2 g + kv of the ring.  A lane finds the pool row of a box of 16 (8)
+    // rows; one elected lane issues the copies of all of them (16 lanes with a
+    // copy each took 74 cycles a copy).
     const int kv = warp == 10;
     const CUtensorMap* map = kv ? &p.tmap_v : &p.tmap_k;
-    const int NS = kv ? kPxVStages : kPxKStages;
-    const uint32_t full = kv ? v_full : k_full, empty = kv ? v_empty : k_empty;
-    uint8_t* ring = smem + (kv ? C::V_OFF : C::K_OFF);
     if (lane == 0) prefetch_tensormap(map);
     // the prefix is read once per pair of tiles: kept in L2 when there are several
     const uint64_t policy = npairs > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
-    const int sbl = K < 16 ? 1 : 0;                       // 8-token blocks: 8-row boxes
-    const int ncopy = C::NBOX << sbl;                     // <= 16: one box per lane
-    const int bi = lane >> sbl, u = lane & sbl;
-    const int half = bi >> 2, rb = bi & 3;
-    const int tr = rb * 16 + (u << 3);
-    int kt = (int)(g0 % nkt), j = (int)(g0 / nkt / npairs);
-    int left = (int)(((long long)(j + 1) * npairs * nkt) - g0);     // steps left of KV head j
+    const bool small = K < 16;                            // 8-token blocks: 8-row boxes
+    const int nbox = small ? kPxBN / 8 : kPxBN / 16, box = small ? 8 : 16;
+    const int log2_k = (K & (K - 1)) == 0 ? __ffs(K) - 1 : -1;
+    auto block_of = [&](int tok) -> int { return log2_k >= 0 ? tok >> log2_k : tok / K; };
+    int kt = kt00, item = item0;
     // the table entry of this lane's box, loaded one step ahead
-    auto table_entry = [&](int g, int t) -> long long {
-      const int tok = t * kPxBN + tr;
-      if (lane >= ncopy || g >= ng || tok >= P) return -1;
-      return p.prefix_table[tok / K];
+    auto table_entry = [&](int g, int t) -> int {
+      const int tok = t * kPxBN + lane * box;
+      return lane < nbox && g < ng && tok < P ? p.prefix_table[block_of(tok)] : -1;
     };
-    long long phys_next = table_entry(0, kt);
-    int g = 0;
+    int id_next = table_entry(0, kt);
+    int n = kv;
     bool ok = true;
-    for (; g < ng; ++g) {
-      const int stage = g % NS;
-      const long long phys = phys_next;
+    for (int g = 0; g < ng; ++g, n += 2) {
+      const int id = id_next, stage = n % C::NS;
       const int ktn = kt + 1 == nkt ? 0 : kt + 1;
-      phys_next = table_entry(g + 1, ktn);
-      if (!mbar_wait_bounded(empty + 8 * stage, ((g / NS) & 1) ^ 1)) {
-        record_error(PKV_DEVERR_TIMEOUT);
-        ok = false;
-        break;
+      const int tok = kt * kPxBN + lane * box;
+      int row = -32;                                      // past the prefix: zero fill
+      if (lane < nbox && tok < P) {
+        if (id < 0 || id >= p.num_blocks)
+          record_error(PKV_DEVERR_BLOCK_ID);
+        else
+          row = id * K + (tok - block_of(tok) * K);
       }
-      if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, C::KBYTES);
-      __syncwarp();
-      if (lane < ncopy) {
-        const int tok = kt * kPxBN + tr;
-        int row = -32;                                    // past the prefix: zero fill
-        if (tok < P) {
-          if (phys < 0 || phys >= p.num_blocks) {
-            record_error(PKV_DEVERR_BLOCK_ID);
-          } else {
-            row = (int)(phys * K + (tok - (tok / K) * K));
+      id_next = table_entry(g + 1, ktn);
+      const int j = item / npairs;
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty + 8 * stage, ((n / C::NS) & 1) ^ 1));
+      if (!ok) break;
+      int rows[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) rows[i] = __shfl_sync(0xffffffffu, row, i);
+      if (elect_one()) {
+        const uint32_t dst = sbase + C::KV_OFF + stage * C::KBYTES, bar = full + 8 * stage;
+        mbar_arrive_expect_tx(bar, C::KBYTES);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (i < nbox) {
+#pragma unroll
+            for (int half = 0; half < C::NH; ++half)
+              tma_load_3d(dst + half * C::KVHALF + i * box * 128, map, bar, half * 64, j, rows[i],
+                          policy);
           }
         }
-        tma_load_3d(smem_u32(ring + stage * C::KBYTES + half * C::KVHALF + tr * 128), map,
-                    full + 8 * stage, half * 64, j, row, policy);
       }
       __syncwarp();
       kt = ktn;
-      if (--left == 0) {
-        ++j;
-        left = npairs * nkt;
-      }
+      if (kt == 0) ++item;
     }
     if (!ok) {
-      for (int kk = max(0, g - NS); kk < g; ++kk)
-        mbar_wait_bounded(full + 8 * (kk % NS), (kk / NS) & 1);
+      if (lane == 0) record_error(PKV_DEVERR_TIMEOUT);
+      // do not leave the CTA while our own copies may still land
+      for (int i = n - 2; i >= 0 && i >= n - 2 * C::NS; i -= 2)
+        mbar_wait_bounded(full + 8 * (i % C::NS), (i / C::NS) & 1);
     }
   } else if (warp == 9 || warp == 11) {
     // =================== MMA issue: warp 9 S = Q K^T, warp 11 O += P V ===================
-    // The whole warp walks the loop and one elected lane issues: under a lane
-    // test the compiler cannot tell that the descriptors are uniform, and an
-    // MMA took 80 to 90 cycles to issue.
+    // The whole warp walks the loop and one elected lane issues.
     bool ok = true;
-    int kt = (int)(g0 % nkt), seg = 0;
+    int kt = kt00, item = item0, job = 0, seg[2] = {0, 0}, jobs[2] = {0, 0};
+    int nt = tiles_of(item);
     for (int g = 0; g < ng && ok; ++g) {
       const bool first = g == 0 || kt == 0;                // of a segment
-      if (warp == 9) {
-        const int stage = g % kPxKStages, b = g & 1;
-        if (first) {
-          for (int x = 0; x < NT && ok; ++x) ok = mbar_wait_bounded(q_full(x), seg & 1);
-          ++seg;
-        }
-        ok = ok && mbar_wait_bounded(k_full + 8 * stage, (g / kPxKStages) & 1);
-        const uint32_t kb = sbase + C::K_OFF + stage * C::KBYTES;
-        for (int x = 0; x < NT && ok; ++x) {
-          // S buffer b of tile x holds P(g - 2) until O += P(g - 2) V is done
+      if (first) nt = tiles_of(item);
+      const int n = 2 * g + (warp == 11);                  // tile of the ring
+      const uint32_t kv = sbase + C::KV_OFF + (n % C::NS) * C::KBYTES;
+      if (warp == 9 && first) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (x < nt && ok) ok = mbar_wait_bounded(q_full(x), seg[x]++ & 1);
+      }
+      ok = __all_sync(0xffffffffu,
+                      ok && mbar_wait_bounded(full + 8 * (n % C::NS), (n / C::NS) & 1));
+      for (int x = 0; x < nt && ok; ++x, ++job) {
+        const int b = job & 1;
+        const uint32_t sd = tmem + b * kPxBN;
+        if (warp == 9) {
+          // S buffer b holds P of job - 2 until its O += P V is done
           ok = __all_sync(0xffffffffu,
-                          g < 2 || mbar_wait_bounded(p_free(x, b), ((g >> 1) - 1) & 1));
+                          job < 2 || mbar_wait_bounded(p_free(b), ((job >> 1) - 1) & 1));
           if (!ok) break;
           tc_fence_after();
           const uint32_t qb = sbase + C::Q_OFF + x * C::QBYTES;
-          const uint32_t sd = tmem + x * 256 + b * kPxBN;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint64_t ad = umma_desc_sw128(qb + (kk >> 2) * C::QHALF + (kk & 3) * 32, 16, 1024);
-              const uint64_t bd = umma_desc_sw128(kb + (kk >> 2) * C::KVHALF + (kk & 3) * 32, 16, 1024);
+              const uint64_t bd = umma_desc_sw128(kv + (kk >> 2) * C::KVHALF + (kk & 3) * 32, 16, 1024);
               umma_ss(sd, ad, bd, C::IDESC_QK, kk > 0 ? 1u : 0u);
             }
-            umma_commit(s_full(x, b));
-            umma_commit(k_empty + 8 * stage);
+            umma_commit(s_full(x, jobs[x]));
+            if (x == nt - 1) umma_commit(empty + 8 * (n % C::NS));
           }
           __syncwarp();
-        }
-      } else {
-        const int stage = g % kPxVStages;
-        ok = mbar_wait_bounded(v_full + 8 * stage, (g / kPxVStages) & 1);
-        const uint32_t vb = sbase + C::V_OFF + stage * C::KBYTES;
-        for (int x = 0; x < NT && ok; ++x) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(p_full(x, g & 1), (g >> 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t pt = tmem + x * 256 + (g & 1) * kPxBN;
-          const uint32_t od = tmem + x * 256 + 128;
-          if (elect_one()) {
+          ++jobs[x];
+        } else {
+          const uint32_t od = tmem + 256 + x * 128, pt = sd + 64;
 #pragma unroll
-            for (int k16 = 0; k16 < kPxBN / 16; ++k16)
-              umma_ts(od, pt + k16 * 8, umma_desc_sw128(vb + k16 * 2048, C::KVHALF, 1024),
-                      C::IDESC_PV, (!first || k16 > 0) ? 1u : 0u);
-            umma_commit(o_done(x));
-            umma_commit(p_free(x, g & 1));
-            if (x == NT - 1) umma_commit(v_empty + 8 * stage);
+          for (int h = 0; h < 2; ++h) {                    // upper keys first
+            ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(p_full(b, h), (job >> 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k4 = 0; k4 < 4; ++k4) {
+                const int k16 = (h ? 0 : 4) + k4;
+                umma_ts(od, pt + k16 * 8, umma_desc_sw128(kv + k16 * 2048, C::KVHALF, 1024),
+                        C::IDESC_PV, (!first || h > 0 || k4 > 0) ? 1u : 0u);
+              }
+              if (h == 1) {
+                umma_commit(o_done(x));
+                umma_commit(p_free(b));
+                if (x == nt - 1) umma_commit(empty + 8 * (n % C::NS));
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       kt = kt + 1 == nkt ? 0 : kt + 1;
+      if (kt == 0) ++item;
     }
     if (!ok && lane == 0) record_error(PKV_DEVERR_TIMEOUT);
     if (elect_one()) umma_commit(mma_idle);
     __syncwarp();
     mbar_wait_bounded(mma_idle, 0);
-  } else if ((warp >> 2) < NT) {
+  } else if (warp < 8) {
     // =================== softmax warps: warps 0-3 tile A, 4-7 tile B ===================
     const int x = warp >> 2;
     const int row = (warp & 3) * 32 + lane;      // TMEM lane = query row of tile x
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t scol = x * 256, ocol = x * 256 + 128;
+    const uint32_t ocol = tmem + lane_base + 256 + x * 128;
     const float sl = p.scale_log2;
     bool ok = true;
-    int g = 0;
-    long long at = g0;
-    while (g < ng && ok) {
-      // ---- one segment: steps kt0 .. kt1 - 1 of an item
-      const int item = (int)(at / nkt), kt0 = (int)(at - (long long)item * nkt);
-      const int kt1 = min(nkt, kt0 + ng - g);
-      const int j = item / npairs, pair = item - j * npairs;
-      const int r = (pair * NT + x) * kT5Rows + row;
-      bool valid = r < R;
-      const int t = valid ? r / p.G : 0;
-      const int h = j * p.G + (valid ? r - t * p.G : 0);
-      int last = P - 1;                          // last prefix key this row sees
-      if (valid) {
-        int s, i, n, L;
-        valid = px_row(p, t, s, i, n, L);
-        if (valid) last = min(last, L - n + i);
-      }
-      int lw = last;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) lw = min(lw, __shfl_xor_sync(0xffffffffu, lw, o));
-      {
-        // Q of the segment in front is free: its last S has been read
-        const uint4* qrow = reinterpret_cast<const uint4*>(p.q + ((int64_t)t * p.H_q + h) * D);
-        uint8_t* qt = smem + C::Q_OFF + x * C::QBYTES;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = valid ? __ldg(qrow + c) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(qt + (c >> 3) * C::QHALF + row * 128 +
-                                    (((c & 7) ^ (row & 7)) << 4)) = v;
+    int job0 = 0, done = 0;                      // jobs of earlier segments; jobs of this tile
+    int item = item0, kt0 = kt00;
+    for (int g = 0; g < ng && ok;) {
+      // ---- one segment: steps kt0 .. kt0 + nst - 1 of an item
+      const int nst = min(nkt - kt0, ng - g), nt = tiles_of(item);
+      if (x < nt) {
+        const int j = item / npairs, pair = item - j * npairs;
+        const int r = (2 * pair + x) * kT5Rows + row;
+        bool valid = r < R;
+        const int t = valid ? r / p.G : 0;
+        const int h = j * p.G + (valid ? r - t * p.G : 0);
+        int last = P - 1;                        // last prefix key this row sees
+        if (valid) {
+          int s, i, n, L;
+          valid = px_row(p, t, s, i, n, L);
+          if (valid) last = min(last, L - n + i);
         }
-        fence_proxy_async_smem();
-        mbar_arrive(q_full(x));
-      }
-      float m_used = 0.f, l = 0.f;
-      for (int kt = kt0; kt < kt1 && ok; ++kt, ++g) {
-        const int b = g & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(s_full(x, b), (g >> 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-        float xs[kPxBN];
-        tmem_ld64_wait(tmem + lane_base + scol + b * kPxBN, xs);
-        const int kbase = kt * kPxBN;
-        if (kbase + kPxBN - 1 > lw) {
-          const int lim = last - kbase;
+        int lw = last;
 #pragma unroll
-          for (int e = 0; e < kPxBN; ++e) xs[e] = e <= lim ? xs[e] : -INFINITY;
-        }
-        // row maximum: four chains of three-input max over the 64 scores
-        float m4[4] = {fmax3(xs[0], xs[1], xs[2]), fmax3(xs[3], xs[4], xs[5]),
-                       fmax3(xs[6], xs[7], xs[8]), fmax3(xs[9], xs[10], xs[11])};
+        for (int o = 16; o > 0; o >>= 1) lw = min(lw, __shfl_xor_sync(0xffffffffu, lw, o));
+        {
+          // Q of the segment in front is free: its last S has been read
+          const uint4* qrow = reinterpret_cast<const uint4*>(p.q + ((int64_t)t * p.H_q + h) * D);
+          uint8_t* qt = smem + C::Q_OFF + x * C::QBYTES;
 #pragma unroll
-        for (int e = 12; e + 1 < kPxBN; e += 2) m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], xs[e], xs[e + 1]);
-        const float mt = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl;
-        if (kt == kt0) {
-          m_used = mt == -INFINITY ? 0.f : mt;
-        } else {
-          const bool need = mt > m_used + kT5Slack;
-          if (__any_sync(0xffffffffu, need)) {
-            // O in TMEM is rescaled; O += P(g-1) V must have landed first.  S(g)
-            // full implies O += P(g-2) V done, so o_done is at most one phase
-            // behind and its parity names the phase unambiguously
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(o_done(x), (g - 1) & 1));
-            if (!ok) break;
-            tc_fence_after();
-            const float mn = need ? mt : m_used;
-            const float alpha = exp2f(m_used - mn);
-            l *= alpha;
-            m_used = mn;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tmem + lane_base + ocol + c * 32, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st32(tmem + lane_base + ocol + c * 32, o);
-            }
-            tmem_wait_st();
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = valid ? __ldg(qrow + c) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(qt + (c >> 3) * C::QHALF + row * 128 +
+                                      (((c & 7) ^ (row & 7)) << 4)) = v;
           }
+          fence_proxy_async_smem();
+          mbar_arrive(q_full(x));
         }
-        // p = 2^(s * scale * log2 e - m): the scale and shift as packed fp32x2 FMAs,
-        // the row sum as packed adds
-        float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(-m_used, -m_used);
-        uint32_t pk[kPxBN / 2];
+        float m_used = 0.f, l = 0.f;
+        for (int st = 0; st < nst; ++st) {
+          const int job = job0 + st * nt + x, b = job & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(s_full(x, done), (done >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sd = tmem + lane_base + b * kPxBN;
+          const int kbase = (kt0 + st) * kPxBN;
+          const bool masked = kbase + kPxBN - 1 > lw;
+          float xs[64];
+          // 64 scores from key kbase + 64 h on, keys the row does not see at -inf
+          auto load = [&](int h) {
+            tmem_ld64_wait(sd + 64 * h, xs);
+            if (masked) {
+              const int lim = last - kbase - 64 * h;
 #pragma unroll
-        for (int c = 0; c < kPxBN / 2; ++c) {
-          const float2 y = __ffma2_rn(make_float2(xs[2 * c], xs[2 * c + 1]), sl2, nm2);
-          const float2 e2 = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-          s2[c & 1] = __fadd2_rn(s2[c & 1], e2);
-          pk[c] = pack_bf16x2(e2.x, e2.y);
+              for (int e = 0; e < 64; ++e) xs[e] = e <= lim ? xs[e] : -INFINITY;
+            }
+          };
+          // row maximum: four chains of three-input max
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            load(h);
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], xs[e], xs[e + 1]);
+          }
+          const float mt = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl;
+          if (st == 0) {
+            m_used = mt == -INFINITY ? 0.f : mt;
+          } else {
+            const bool need = mt > m_used + kT5Slack;
+            if (__any_sync(0xffffffffu, need)) {
+              // O in TMEM is rescaled; the O product in front must have landed
+              // first (the next one waits for this job's P, so o_done is at
+              // most one phase ahead of `done`)
+              ok = __all_sync(0xffffffffu, mbar_wait_bounded(o_done(x), (done - 1) & 1));
+              if (!ok) break;
+              tc_fence_after();
+              const float mn = need ? mt : m_used;
+              const float alpha = exp2f(m_used - mn);
+              l *= alpha;
+              m_used = mn;
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(ocol + c * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st32(ocol + c * 32, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          // p = 2^(s * scale * log2 e - m): the scale and shift as packed fp32x2
+          // FMAs, the row sum as packed adds; the upper keys are live already
+          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(-m_used, -m_used);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1) load(0);
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float2 y = __ffma2_rn(make_float2(xs[2 * c], xs[2 * c + 1]), sl2, nm2);
+              const float2 e2 = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+              s2[c & 1] = __fadd2_rn(s2[c & 1], e2);
+              pk[c] = pack_bf16x2(e2.x, e2.y);
+            }
+            tmem_st32(sd + (h ? 64 : 96), pk);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(p_full(b, h));
+          }
+          l += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+          ++done;
         }
-        l += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-        tmem_st32(tmem + lane_base + scol + b * kPxBN, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(p_full(x, b));
-      }
-      // ---- the segment's partial state
-      if (ok) {
-        // the last O += P V of the segment
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(p_free(x, (g - 1) & 1), ((g - 1) >> 1) & 1));
+        // ---- the segment's partial state, after its last O product
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(o_done(x), (done - 1) & 1));
+        ok = px_tile_all(x, ok);
         if (ok) {
           tc_fence_after();
-          const int64_t pr = ((int64_t)(cta + item) * NT + x) * kT5Rows + row;
-          float4* orow = reinterpret_cast<float4*>(p.o + pr * D);
+          // rows of O to the workspace, 64 values of all rows at a time through
+          // this tile's Q (its last S is done): stored from the lanes, a row
+          // each, every 16 bytes would be a transaction of their own
+          const int64_t pr0 = (int64_t)(cta + item) * tile_rows + x * kT5Rows;
+          uint8_t* qt = smem + C::Q_OFF + x * C::QBYTES;
+          const int nrow = min(kT5Rows, R - (2 * pair + x) * kT5Rows);
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lane_base + ocol + c * 32, o);
-            tmem_wait_ld();
-            if (valid) {
+          for (int c = 0; c < D / 64; ++c) {
+            float o[64];
+            tmem_ld64_wait(ocol + c * 64, o);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                orow[c * 8 + e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                              __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+            for (int e = 0; e < 16; ++e)
+              *reinterpret_cast<float4*>(qt + row * C::OROW + ((e ^ (row & 7)) << 4)) =
+                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            px_tile_sync(x);
+            for (int i = row; i < nrow * 16; i += kT5Rows) {
+              const int rr = i >> 4, e = i & 15;
+              *reinterpret_cast<float4*>(p.o + (pr0 + rr) * D + c * 64 + e * 4) =
+                  *reinterpret_cast<const float4*>(qt + rr * C::OROW + ((e ^ (rr & 7)) << 4));
             }
+            px_tile_sync(x);
           }
-          if (valid) p.ml[pr] = make_float2(l > 0.f ? m_used : -INFINITY, l);
+          if (valid) p.ml[pr0 + row] = make_float2(l > 0.f ? m_used : -INFINITY, l);
           tc_fence_before();                     // O is read before the next segment's P V
         }
       }
-      at += kt1 - kt0;
+      job0 += nst * nt;
+      g += nst;
+      kt0 = 0;
+      ++item;
     }
     if (!ok) record_error(PKV_DEVERR_TIMEOUT);
   }
@@ -495,18 +572,19 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p) {
 
 // ===========================================================================
 // Merge of the partial states of a (token, query head) row: its own tokens'
-// (slots of meta[t]) and the prefix's (items[item] = {first CTA, CTAs}).  WPR
-// warps per row take eight partials at a time, all of them in flight at once;
-// a row's time is that of its loads, and with few rows (a small batch over a
-// long prefix) several warps share one.
+// (slots of meta[t]) and the prefix's (items[item] = {first CTA, CTAs}).  A
+// row costs a chain of loads (length, slots, states), so what counts is how
+// many warps are resident.  Many rows of few partials (WPR 1): two partials
+// at a time in 32 registers, eight CTAs an SM.  A small batch over a long
+// prefix has few rows of many partials: WPR warps share a row, eight partials
+// each at a time.
 // ===========================================================================
 constexpr int kPxMergeWarps = 8;
-constexpr int kPxMergeBatch = 8;
 
 template <int D, int WPR>
-__global__ void __launch_bounds__(kPxMergeWarps * 32)
+__global__ void __launch_bounds__(kPxMergeWarps * 32, WPR == 1 ? 8 : 2)
 prefix_merge_kernel(const __grid_constant__ PxParams p, int tile_rows) {
-  constexpr int V = D / 32, RPC = kPxMergeWarps / WPR;
+  constexpr int V = D / 32, RPC = kPxMergeWarps / WPR, B = WPR == 1 ? 2 : 8;
   __shared__ float s_acc[WPR > 1 ? kPxMergeWarps : 1][D];
   __shared__ float s_m[kPxMergeWarps], s_l[kPxMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
@@ -523,8 +601,8 @@ prefix_merge_kernel(const __grid_constant__ PxParams p, int tile_rows) {
   if (live) {
     const int4 mt = p.meta[t];
     if (p.split.prefix_len > 0) {
-      const int npairs = (tokens * p.G + tile_rows - 1) / tile_rows;
-      item = j * npairs + r / tile_rows;
+      const int npairs = (px_tiles(tokens * p.G) + 1) >> 1;
+      item = j * npairs + r / (2 * kT5Rows);
       const int2 it = p.items[item];
       first = it.x;
       np = it.y;
@@ -536,17 +614,17 @@ prefix_merge_kernel(const __grid_constant__ PxParams p, int tile_rows) {
   }
   float M = -INFINITY, lsum = 0.f, acc[V] = {};
   if (live) {
-    for (int x0 = sub * kPxMergeBatch; x0 < np; x0 += WPR * kPxMergeBatch) {
+    for (int x0 = sub * B; x0 < np; x0 += WPR * B) {
       auto index = [&](int x) -> int64_t {
         return x < own ? ((int64_t)base + (int64_t)x * p.own_stride) * p.H_q + h
-                       : (int64_t)(first + x - own + item) * tile_rows + r % tile_rows;
+                       : (int64_t)(first + x - own + item) * tile_rows + r % (2 * kT5Rows);
       };
-      const int cnt = min(kPxMergeBatch, np - x0);
+      const int cnt = min(B, np - x0);
       float2 ml = make_float2(-INFINITY, 0.f);
       if (lane < cnt) ml = (x0 + lane < own ? p.own_ml : p.ml)[index(x0 + lane)];
-      float v[kPxMergeBatch][V];
+      float v[B][V];
 #pragma unroll
-      for (int x = 0; x < kPxMergeBatch; ++x)
+      for (int x = 0; x < B; ++x)
         if (x < cnt) load_f<V>((x0 + x < own ? p.own_o : p.o) + index(x0 + x) * D + lane * V, v[x]);
       const float m2 = fmaxf(M, warp_max(ml.x));
       const float mu = m2 == -INFINITY ? 0.f : m2;          // nothing visible so far: weights 0
@@ -556,7 +634,7 @@ prefix_merge_kernel(const __grid_constant__ PxParams p, int tile_rows) {
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[e] *= a;
 #pragma unroll
-      for (int x = 0; x < kPxMergeBatch; ++x) {
+      for (int x = 0; x < B; ++x) {
         const float wx = __shfl_sync(0xffffffffu, w, x);
         if (x < cnt) {
 #pragma unroll
