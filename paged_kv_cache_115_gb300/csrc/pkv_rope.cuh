@@ -251,7 +251,6 @@ rope_ring_kernel(const __grid_constant__ RopeParams p, int stages, int stage_byt
   // the consumers among themselves
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kRopeThreads) : "memory"); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int HK = p.H_q + p.H_kv, rows = HK + p.H_kv;
   const int q_bytes = p.H_q * D * (int)sizeof(TIN), kv_bytes = p.H_kv * D * (int)sizeof(TIN);
   if (tid == 0) {
     for (int i = 0; i < stages; ++i) {
@@ -331,7 +330,7 @@ rope_ring_kernel(const __grid_constant__ RopeParams p, int stages, int stage_byt
   }
 
   // =================== consumers ===================
-  const int li = tid % LANES, rg = tid / LANES;
+  const int li = tid % LANES;
   const int half = p.rot >> 1;
   // this lane's values: HV from ea on, HV from eb on
   const bool turned = li * V < p.rot;
@@ -346,7 +345,8 @@ rope_ring_kernel(const __grid_constant__ RopeParams p, int stages, int stage_byt
     wka = __ldg(reinterpret_cast<const uint2*>(static_cast<const TIN*>(p.wk) + ea));
     wkb = __ldg(reinterpret_cast<const uint2*>(static_cast<const TIN*>(p.wk) + eb));
   }
-  const int row0 = tid / 32 * (32 / LANES);             // first row of this warp in a group of RPI
+  // rows of this warp in a group of RPI: row0 + sub
+  const int row0 = warp * (32 / LANES), sub = lane / LANES;
   int stage = 0, round = 0;
   for (;;) {
     const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&s_full[stage]), round & 1));
@@ -372,80 +372,104 @@ rope_ring_kernel(const __grid_constant__ RopeParams p, int stages, int stage_byt
         s[i] = cs[half + i];
       }
     }
-    TIN* qo = static_cast<TIN*>(p.q_out) + t * p.qo_stride;
+    const TIN* const src = reinterpret_cast<const TIN*>(sb);      // q, k and v rows one after the other
     const int64_t pool_row = slot * p.H_kv * D;
     float amax[2] = {0.f, 0.f};
-    const int last = slot < 0 ? p.H_q : rows;           // without a slot the pools are left alone
-#pragma unroll 4
-    for (int r0 = 0; r0 + row0 < last; r0 += RPI) {     // the same for a whole warp: shuffles stay whole
-      const int r = r0 + rg;
-      const TIN* src = reinterpret_cast<const TIN*>(sb) + r * D;      // k and v follow q
-      if (FMT == 0 && r0 + row0 >= HK) {                // value rows only: copied as they are
-        if (r < last)
-          reinterpret_cast<uint4*>(p.v_cache)[(pool_row + (r - HK) * D) / V + li] =
-              *reinterpret_cast<const uint4*>(src + li * V);
-        continue;
-      }
-      const bool live = r < last;
-      const int z = r < p.H_q ? 0 : (r < HK ? 1 : 2);                 // q, k, v
-      const uint2 xa = live ? *reinterpret_cast<const uint2*>(src + ea) : make_uint2(0, 0);
-      const uint2 xb = live ? *reinterpret_cast<const uint2*>(src + eb) : make_uint2(0, 0);
+    // a head row of this lane: norm (weights not null) and rotation
+    auto turn = [&](uint2 xa, uint2 xb, const void* weight, uint2 wa, uint2 wb, float (&y)[V]) {
       float x[V];
       rope_unpack2<TIN>(xa, xb, x);
-      if (p.wq != nullptr || p.wk != nullptr) {
+      if (weight != nullptr) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (z < 2 && (z ? p.wk : p.wq) != nullptr) {
-          float w[V];
-          rope_unpack2<TIN>(z ? wka : wqa, z ? wkb : wqb, w);
-          const float inv = rsqrtf(ss / D + p.eps);
+        float w[V];
+        rope_unpack2<TIN>(wa, wb, w);
+        const float inv = rsqrtf(ss / D + p.eps);
 #pragma unroll
-          for (int i = 0; i < V; ++i) x[i] *= inv * w[i];
-        }
+        for (int i = 0; i < V; ++i) x[i] *= inv * w[i];
       }
-      if (!live) continue;
-      float y[V];
-#pragma unroll
-      for (int i = 0; i < HV; ++i) {
-        const int a = PAIRS ? 2 * i : i, b = PAIRS ? 2 * i + 1 : i + HV;
-        y[a] = x[a] * c[i] - x[b] * s[i];
-        y[b] = x[b] * c[i] + x[a] * s[i];
-      }
-      if (z == 0) {
-        const uint4 o = rope_pack<TIN>(y);
-        *reinterpret_cast<uint2*>(qo + r * D + ea) = make_uint2(o.x, o.y);
-        *reinterpret_cast<uint2*>(qo + r * D + eb) = make_uint2(o.z, o.w);
-        continue;
-      }
-      const int at = (z == 1 ? r - p.H_q : r - HK) * D;               // in the token's K or V row
-      if constexpr (FMT == 2) {
-        const float* val = z == 1 ? y : x;
-        float* dst = s_all + (z - 1) * p.H_kv * D + at;
+      if constexpr (PAIRS) {
 #pragma unroll
         for (int i = 0; i < HV; ++i) {
-          dst[ea + i] = val[i];
-          dst[eb + i] = val[i + HV];
-          amax[z - 1] = fmaxf(amax[z - 1], fmaxf(fabsf(val[i]), fabsf(val[i + HV])));
+          y[2 * i] = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
+          y[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * s[i];
         }
-      } else if (z == 1) {
-        if constexpr (FMT == 0 || FMT == 3) {
-          using TK = typename RopeKType<TIN, FMT>::T;
-          rope_store_half<TK, HV>(reinterpret_cast<TK*>(p.k_cache) + pool_row + at + ea, y);
-          rope_store_half<TK, HV>(reinterpret_cast<TK*>(p.k_cache) + pool_row + at + eb, y + HV);
-        } else {
-          rope_store_codes<HV>(p.k_cache + pool_row + at + ea, y, p.k_scale);
-          rope_store_codes<HV>(p.k_cache + pool_row + at + eb, y + HV, p.k_scale);
-        }
-      } else if constexpr (FMT == 0) {
-        TIN* dst = reinterpret_cast<TIN*>(p.v_cache) + pool_row + at;
-        *reinterpret_cast<uint2*>(dst + ea) = xa;
-        *reinterpret_cast<uint2*>(dst + eb) = xb;
       } else {
-        rope_store_codes<HV>(p.v_cache + pool_row + at + ea, x, p.v_scale);
-        rope_store_codes<HV>(p.v_cache + pool_row + at + eb, x + HV, p.v_scale);
+        // two pairs at a time as packed float32 operations
+#pragma unroll
+        for (int i = 0; i < HV; i += 2) {
+          const float2 a = make_float2(x[i], x[i + 1]), b = make_float2(x[HV + i], x[HV + i + 1]);
+          const float2 c2 = make_float2(c[i], c[i + 1]), s2 = make_float2(s[i], s[i + 1]);
+          const float2 lo = __ffma2_rn(b, make_float2(-s2.x, -s2.y), __fmul2_rn(a, c2));
+          const float2 hi = __ffma2_rn(a, s2, __fmul2_rn(b, c2));
+          y[i] = lo.x; y[i + 1] = lo.y;
+          y[HV + i] = hi.x; y[HV + i + 1] = hi.y;
+        }
+      }
+    };
+    // rows of a kind for this warp: `row0` is the same for a whole warp, so
+    // that shuffles stay whole; lanes of a row past the last one repeat it
+    TIN* qo = static_cast<TIN*>(p.q_out) + t * p.qo_stride;
+#pragma unroll 4
+    for (int r0 = row0; r0 < p.H_q; r0 += RPI) {
+      const int r = min(r0 + sub, p.H_q - 1) * D;
+      float y[V];
+      turn(*reinterpret_cast<const uint2*>(src + r + ea), *reinterpret_cast<const uint2*>(src + r + eb),
+           p.wq, wqa, wqb, y);
+      const uint4 o = rope_pack<TIN>(y);
+      *reinterpret_cast<uint2*>(qo + r + ea) = make_uint2(o.x, o.y);
+      *reinterpret_cast<uint2*>(qo + r + eb) = make_uint2(o.z, o.w);
+    }
+    if (slot >= 0) {                                      // else the pools are left alone
+      const TIN* const ks = src + p.H_q * D;
+      const TIN* const vs = ks + p.H_kv * D;
+      for (int r0 = row0; r0 < p.H_kv; r0 += RPI) {
+        const int r = min(r0 + sub, p.H_kv - 1) * D;
+        float y[V];
+        turn(*reinterpret_cast<const uint2*>(ks + r + ea), *reinterpret_cast<const uint2*>(ks + r + eb),
+             p.wk, wka, wkb, y);
+        if constexpr (FMT == 2) {
+          float* dst = s_all + r;
+#pragma unroll
+          for (int i = 0; i < HV; ++i) {
+            dst[ea + i] = y[i];
+            dst[eb + i] = y[i + HV];
+            amax[0] = fmaxf(amax[0], fmaxf(fabsf(y[i]), fabsf(y[i + HV])));
+          }
+        } else if constexpr (FMT == 1) {
+          rope_store_codes<HV>(p.k_cache + pool_row + r + ea, y, p.k_scale);
+          rope_store_codes<HV>(p.k_cache + pool_row + r + eb, y + HV, p.k_scale);
+        } else {
+          using TK = typename RopeKType<TIN, FMT>::T;
+          TK* dst = reinterpret_cast<TK*>(p.k_cache) + pool_row + r;
+          rope_store_half<TK, HV>(dst + ea, y);
+          rope_store_half<TK, HV>(dst + eb, y + HV);
+        }
+      }
+      // value rows on the other half of the warps first
+      for (int r0 = (row0 + RPI / 2) % RPI; r0 < p.H_kv; r0 += RPI) {
+        const int r = min(r0 + sub, p.H_kv - 1) * D;
+        const uint4 raw = *reinterpret_cast<const uint4*>(vs + r + li * V);
+        if constexpr (FMT == 0) {
+          *reinterpret_cast<uint4*>(reinterpret_cast<TIN*>(p.v_cache) + pool_row + r + li * V) = raw;
+        } else {
+          float x[V];
+          rope_unpack<TIN>(raw, x);
+          if constexpr (FMT == 2) {
+            float* dst = s_all + p.H_kv * D + r + li * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              dst[i] = x[i];
+              amax[1] = fmaxf(amax[1], fabsf(x[i]));
+            }
+          } else {
+            rope_store_codes<HV>(p.v_cache + pool_row + r + li * V, x, p.v_scale);
+            rope_store_codes<HV>(p.v_cache + pool_row + r + li * V + HV, x + HV, p.v_scale);
+          }
+        }
       }
     }
     __syncwarp();
