@@ -743,23 +743,21 @@ pkv_status check_quant(const pkv_kv_quant* q, bool need_token_scales) {
 // ---- norm + rotation + append dispatch -------------------------------------------
 constexpr int kRopeSmemPerSm = 220 * 1024;
 
-// Ring of token stages: two at least, up to four while four CTAs fit an SM.
+// Ring of token stages in shared memory.
 struct RopeRing {
-  int stages = 0, stage_bytes = 0, smem = 0, ctas = 0;   // stages 0: does not fit
+  int stage_bytes = 0, smem = 0, ctas = 0;   // ctas 0: does not fit
 };
 template <typename T>
 RopeRing rope_ring(const pkv::RopeParams& p, int fmt) {
   RopeRing r;
   const int64_t stage =
       ((int64_t)(p.H_q + 2 * p.H_kv) * p.D * (int64_t)sizeof(T) + 4 * (int64_t)p.rot + 127) / 128 * 128;
-  const int64_t extra = fmt == PKV_KV_INT8_TOKEN ? 8 * (int64_t)p.H_kv * p.D : 0;
-  if (2 * stage + extra > kRopeSmemPerSm) return r;
-  int64_t n = 2;
-  while (n < pkv::kRopeMaxStages && (n + 1) * stage + extra <= kRopeSmemPerSm / pkv::kRopeCtas - 1024) ++n;
-  r.stages = (int)n;
+  const int64_t smem = pkv::kRopeStages * stage +
+                       (fmt == PKV_KV_INT8_TOKEN ? 8 * (int64_t)p.H_kv * p.D : 0);
+  if (smem > kRopeSmemPerSm) return r;
   r.stage_bytes = (int)stage;
-  r.smem = (int)(n * stage + extra);
-  r.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(pkv::kRopeCtas, kRopeSmemPerSm / (r.smem + 1024)));
+  r.smem = (int)smem;
+  r.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(pkv::kRopeCtas, kRopeSmemPerSm / (smem + 1024)));
   return r;
 }
 
@@ -773,7 +771,7 @@ pkv_status launch_rope_ring(const pkv::RopeParams& p, const RopeRing& r, cudaStr
   if (s == PKV_OK) s = set_smem_once(k, kRopeSmemPerSm, flags, errs, dev);
   if (s != PKV_OK) return s;
   PKV_CUDA(launch_pdl(k, dim3((unsigned)std::min(p.T, sms * r.ctas)), dim3(pkv::kRopeRingThreads),
-                      (size_t)r.smem, st, p, r.stages, r.stage_bytes));
+                      (size_t)r.smem, st, p, r.stage_bytes));
   return PKV_OK;
 }
 
@@ -799,7 +797,7 @@ template <typename T, int FMT>
 pkv_status launch_rope_fmt(const pkv::RopeParams& p, cudaStream_t st) {
   if (rope_ring_ok<T>(p)) {
     const RopeRing r = rope_ring<T>(p, FMT);
-    if (r.stages > 0) {
+    if (r.ctas > 0) {
       if (p.D == 64) return launch_rope_dim<T, FMT, 64>(p, r, st);
       if (p.D == 128) return launch_rope_dim<T, FMT, 128>(p, r, st);
       if constexpr (sizeof(T) == 2) return launch_rope_dim<T, FMT, 256>(p, r, st);

@@ -227,8 +227,12 @@ __device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void* src, ui
 }
 
 constexpr int kRopeRingThreads = kRopeThreads + 32;
-constexpr int kRopeMaxStages = 4;
-constexpr int kRopeCtas = 4;                    // resident on an SM (at most)
+// Two stages in each of three CTAs an SM: more bytes in flight make reads and
+// writes worse neighbours in HBM.  16381 tokens of 32 + 2 x 8 heads of 128,
+// 411 MB: 65.4 us (6.3 TB/s); three and four stages 69.7 and 71.5, four CTAs
+// with two to four stages 70.4, 73.3, 72.9, two CTAs with four 74.1.
+constexpr int kRopeStages = 2;
+constexpr int kRopeCtas = 3;
 
 // V / 2 values (8 bytes) at a time.
 template <typename TIN>
@@ -238,14 +242,15 @@ __device__ __forceinline__ void rope_unpack2(uint2 a, uint2 b, float (&x)[16 / s
 
 template <typename TIN, int FMT, int D, bool PAIRS>
 __global__ void __launch_bounds__(kRopeRingThreads, kRopeCtas)
-rope_ring_kernel(const __grid_constant__ RopeParams p, int stages, int stage_bytes) {
+rope_ring_kernel(const __grid_constant__ RopeParams p, int stage_bytes) {
+  constexpr int stages = kRopeStages;
   constexpr int V = 16 / sizeof(TIN), HV = V / 2, LANES = D / V, RPI = kRopeThreads / LANES;
   static_assert(LANES <= 32, "a row must fit a warp");
   constexpr int W = kRopeThreads / 32;
   extern __shared__ __align__(128) uint8_t s_ring[];
-  __shared__ __align__(8) uint64_t s_full[kRopeMaxStages], s_empty[kRopeMaxStages];
-  __shared__ long long s_slot[kRopeMaxStages];
-  __shared__ int s_token[kRopeMaxStages];
+  __shared__ __align__(8) uint64_t s_full[kRopeStages], s_empty[kRopeStages];
+  __shared__ long long s_slot[kRopeStages];
+  __shared__ int s_token[kRopeStages];
   __shared__ float s_amax[2][W];
   float* const s_all = reinterpret_cast<float*>(s_ring + (size_t)stages * stage_bytes);   // INT8
   // the consumers among themselves
