@@ -524,8 +524,16 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
           l += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
           ++done;
         }
-        // ---- the segment's partial state, after its last O product
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(o_done(x), (done - 1) & 1));
+        // ---- the segment's partial state, after its last O product.  With two
+        // tiles the product in front of it is known to be done (this tile's
+        // last S waited for it), so o_done's parity names the last one.  With
+        // one tile it may be two behind; there p_free of the last job's buffer
+        // does (the product two jobs before is done, and any later one on
+        // that buffer needs this tile's warps)
+        const int job1 = job0 + (nst - 1) * nt + x;
+        ok = ok && __all_sync(0xffffffffu,
+                              nt == 2 ? mbar_wait_bounded(o_done(x), (done - 1) & 1)
+                                      : mbar_wait_bounded(p_free(job1 & 1), (job1 >> 1) & 1));
         ok = px_tile_all(x, ok);
         if (ok) {
           tc_fence_after();

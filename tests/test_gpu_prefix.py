@@ -217,6 +217,36 @@ def test_repeats_bit_for_bit_and_on_another_stream(ops):
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("S,H,prefix", [(8, 64, 65536), (3, 8, 65536), (20, 64, 16384), (40, 64, 8192)])
+def test_long_prefix_repeats_bit_for_bit(ops, S, H, prefix):
+    """A prefix far larger than the caches, one to three tiles of query rows a
+    KV head: waits for memory in every step, the same bits every time, and the
+    framework's decode call over the full rows."""
+    J, D, K = 8, 128, 32
+    g = torch.Generator(device=DEV).manual_seed(prefix + S)
+    own = 64
+    shared, nb = prefix // K, prefix // K + S * 3
+    kc, vc = (torch.empty((nb, K, J, D), dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+              for _ in range(2))
+    order = torch.randperm(nb, generator=g, device=DEV).to(torch.int32)
+    rows = torch.cat([order[:shared][None].expand(S, -1), order[shared:].view(S, 3)], 1).contiguous()
+    lens = prefix + torch.randint(1, own, (S,), generator=g, device=DEV, dtype=torch.int32)
+    q = torch.randn((S, H, D), generator=g, device=DEV).to(torch.bfloat16)
+    call = lambda: ops.paged_attention_decode_prefix(  # noqa: E731
+        q, kc, vc, order[:shared].contiguous(), rows, lens, D ** -0.5, prefix_len=prefix,
+        max_context_len=prefix + own)
+    first = call()
+    for _ in range(30):
+        assert torch.equal(call().view(torch.int16), first.view(torch.int16))
+    ref = ops.paged_attention_decode(q, kc, vc, rows, lens, D ** -0.5, max_context_len=prefix + own)
+    a = ops.paged_attention_decode(q, kc, vc.abs(), rows, lens, D ** -0.5, max_context_len=prefix + own)
+    assert ops.get_device_error() == 0
+    err = (first.double() - ref.double()).abs()
+    assert bool((err <= (2.0**-7 + 2.0**-8) * a.double() * (1 + 2.0**-8) + 2.0**-7 * ref.double().abs()).all())
+    # the weights' roundings are independent: they add up like noise, not like the bound
+    assert float(err.norm() / ref.double().norm()) < 4 * 2.0**-8
+
+
 def test_captured_and_replayed(ops):
     pb = problem([400 + 3 * i for i in range(9)], [1] * 9, 8, 2, 128, 16, 384, seed=1)
     t = {k: pb[k].to(DEV) for k in ("q", "kc", "vc")}
