@@ -18,6 +18,7 @@
 
 #include "pkv_attention_tc.cuh"
 #include "pkv_prefill_tc05.cuh"
+#include "pkv_reduce.cuh"
 
 namespace pkv {
 
@@ -169,7 +170,7 @@ __device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, float (&v)[64]) {
 // ===========================================================================
 
 // The steps of CTA c: [g0, g1) of item * nkt + step.
-__device__ __forceinline__ long long px_step_at(long long unit, int nkt, int ntiles) {
+__host__ __device__ __forceinline__ long long px_step_at(long long unit, int nkt, int ntiles) {
   const int npairs = (ntiles + 1) >> 1;
   const long long head = (long long)nkt * ntiles;
   const int j = (int)(unit / head);
@@ -180,7 +181,7 @@ __device__ __forceinline__ long long px_step_at(long long unit, int nkt, int nti
   return ((long long)j * npairs + pair) * nkt + (in + nt - 1) / nt;
 }
 // First tile step of step `step` of an item.
-__device__ __forceinline__ long long px_unit_of(int item, int step, int nkt, int ntiles) {
+__host__ __device__ __forceinline__ long long px_unit_of(int item, int step, int nkt, int ntiles) {
   const int npairs = (ntiles + 1) >> 1, j = item / npairs, pair = item - j * npairs;
   const int nt = 2 * pair + 2 <= ntiles ? 2 : 1;
   return (long long)j * nkt * ntiles + 2LL * pair * nkt + (long long)step * nt;
