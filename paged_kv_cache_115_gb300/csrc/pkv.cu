@@ -846,8 +846,8 @@ pkv_status check_prefix(int S, int T, int max_q, int max_len, int prefix_len, in
             PKV_ERR_UNSUPPORTED,
             "shared-prefix attention needs bf16, head_dim 64 or 128, block_size 8 or a multiple "
             "of 16, and at most 8 query rows per KV head (max_query_len x G)");
-  PKV_CHECK(S <= pkv::kTcMaxSeqs && H_kv <= 65535 && T <= S * 8, PKV_ERR_UNSUPPORTED,
-            "at most %d sequences and 8 rows for each", pkv::kTcMaxSeqs);
+  PKV_CHECK(S <= pkv::kTcMaxSeqs && H_kv <= 65535, PKV_ERR_UNSUPPORTED, "at most %d sequences",
+            pkv::kTcMaxSeqs);
   PKV_CHECK((int64_t)T * H_q < (int64_t(1) << 31), PKV_ERR_UNSUPPORTED, "too many query rows");
   return PKV_OK;
 }

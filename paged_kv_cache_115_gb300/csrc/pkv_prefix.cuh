@@ -144,10 +144,9 @@ __device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, float (&v)[64]) {
 
 // ===========================================================================
 // Prefix part.  An item is a KV head and up to two tiles of 128 query rows;
-// it takes a step per 128 prefix keys.  The work of all items is counted in
-// tile steps, and CTA c of n1 takes the steps that begin in [c W / n1,
-// (c + 1) W / n1) of all W: a run of one item's steps is one partial state,
-// in slot c + item (distinct, as in the decode kernel).
+// it takes a step per 128 prefix keys.  A run of one item's steps in CTA c is
+// one partial state, in slot c + item (distinct, since the runs go through
+// CTAs and items in one order).
 //
 // A job is one query tile's step: S = Q K^T into one of two S buffers (jobs
 // take them in turn), softmax, O += P V.  With two tiles an item the jobs of
@@ -169,7 +168,39 @@ __device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, float (&v)[64]) {
 // than 2^8, so O is rescaled in TMEM rarely.  Every wait is bounded.
 // ===========================================================================
 
-// The steps of CTA c: [g0, g1) of item * nkt + step.
+// How the steps of all items are dealt to at most n1 CTAs.
+// Even: every CTA takes one run of one item, `duo` CTAs for an item of two
+// tiles and `solo` for the last item of an odd number of tiles (per_head of
+// them for a KV head), the steps of an item shared evenly.  Else (duo = solo =
+// 0) the tile steps are dealt out evenly and a CTA may go from one item to the
+// next, which costs it the start and end of a second run, about six tile
+// steps; taken when rounding to whole CTAs would cost more than that, and
+// with more items than CTAs.
+struct PxCut {
+  int n, duo, solo, per_head;
+};
+__host__ __device__ __forceinline__ PxCut px_cut(int n1, int heads, int nkt, int ntiles) {
+  const int npairs = (ntiles + 1) >> 1, share = n1 / heads;
+  const long long work = (long long)heads * nkt * ntiles;
+  PxCut c = {n1, 0, 0, 0};
+  if (share < npairs) return c;
+  const int odd = ntiles & 1, full = npairs - odd;
+  int duo = full ? 2 * share / ntiles : 0;
+  if (full && duo < 1) return c;
+  if (duo > nkt) duo = nkt;
+  int solo = odd ? share - full * duo : 0;
+  if (odd && solo < 1) return c;
+  if (solo > nkt) solo = nkt;
+  const int a = full ? 2 * ((nkt + duo - 1) / duo) : 0, b = odd ? (nkt + solo - 1) / solo : 0;
+  if ((a > b ? a : b) > work / n1 + 6) return c;
+  c.duo = duo;
+  c.solo = solo;
+  c.per_head = full * duo + solo;
+  c.n = c.per_head * heads;
+  return c;
+}
+
+// First step (item * nkt + step) that begins at or behind a tile step.
 __host__ __device__ __forceinline__ long long px_step_at(long long unit, int nkt, int ntiles) {
   const int npairs = (ntiles + 1) >> 1;
   const long long head = (long long)nkt * ntiles;
@@ -185,6 +216,35 @@ __host__ __device__ __forceinline__ long long px_unit_of(int item, int step, int
   const int npairs = (ntiles + 1) >> 1, j = item / npairs, pair = item - j * npairs;
   const int nt = 2 * pair + 2 <= ntiles ? 2 : 1;
   return (long long)j * nkt * ntiles + 2LL * pair * nkt + (long long)step * nt;
+}
+// Steps [g0, g1) of CTA x (item * nkt + step).
+__host__ __device__ __forceinline__ void px_cta_steps(const PxCut& c, int x, int heads, int nkt,
+                                                      int ntiles, long long& g0, long long& g1) {
+  const int npairs = (ntiles + 1) >> 1;
+  if (c.per_head > 0) {
+    const int j = x / c.per_head, r = x - j * c.per_head, full = npairs - (ntiles & 1);
+    const int pair = c.duo > 0 && r < full * c.duo ? r / c.duo : full;
+    const int part = r - pair * c.duo, parts = pair < full ? c.duo : c.solo;
+    const long long base = ((long long)j * npairs + pair) * nkt;
+    g0 = base + (long long)part * nkt / parts;
+    g1 = base + (long long)(part + 1) * nkt / parts;
+    return;
+  }
+  const long long work = (long long)heads * nkt * ntiles;
+  g0 = px_step_at(x * work / c.n, nkt, ntiles);
+  g1 = x + 1 == c.n ? (long long)npairs * heads * nkt : px_step_at((x + 1) * work / c.n, nkt, ntiles);
+}
+// {first CTA, CTAs} that hold steps of an item.
+__host__ __device__ __forceinline__ int2 px_item_ctas(const PxCut& c, int item, int heads, int nkt,
+                                                      int ntiles) {
+  if (c.per_head > 0) {
+    const int npairs = (ntiles + 1) >> 1, full = npairs - (ntiles & 1);
+    const int j = item / npairs, pair = item - j * npairs;
+    return make_int2(j * c.per_head + pair * c.duo, pair < full ? c.duo : c.solo);
+  }
+  const long long work = (long long)heads * nkt * ntiles;
+  const int a = cta_of_chunk(px_unit_of(item, 0, nkt, ntiles), work, c.n);
+  return make_int2(a, cta_of_chunk(px_unit_of(item, nkt - 1, nkt, ntiles), work, c.n) - a + 1);
 }
 
 template <int D>
@@ -230,18 +290,14 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
   const int ntiles = px_tiles(R), npairs = (ntiles + 1) >> 1;
   const int nkt = px_key_tiles(P);
   const long long work = (long long)p.H_kv * nkt * ntiles;
-  const int n1 = px_ctas(p.split, work, chunks, p.S);
-  if (cta >= n1) return;
-  if (cta == n1 - 1) {                                     // which CTAs hold steps of each item
-    for (int x = tid; x < npairs * p.H_kv; x += kPxThreads) {
-      const int a = cta_of_chunk(px_unit_of(x, 0, nkt, ntiles), work, n1);
-      p.items[x] =
-          make_int2(a, cta_of_chunk(px_unit_of(x, nkt - 1, nkt, ntiles), work, n1) - a + 1);
-    }
+  const PxCut cut = px_cut(px_ctas(p.split, work, chunks, p.S), p.H_kv, nkt, ntiles);
+  if (cta >= cut.n) return;
+  if (cta == cut.n - 1) {                                  // which CTAs hold steps of each item
+    for (int x = tid; x < npairs * p.H_kv; x += kPxThreads)
+      p.items[x] = px_item_ctas(cut, x, p.H_kv, nkt, ntiles);
   }
-  const long long g0 = px_step_at(cta * work / n1, nkt, ntiles);
-  const long long g1 = cta + 1 == n1 ? (long long)npairs * p.H_kv * nkt
-                                     : px_step_at((cta + 1) * work / n1, nkt, ntiles);
+  long long g0, g1;
+  px_cta_steps(cut, cta, p.H_kv, nkt, ntiles, g0, g1);
   const int ng = (int)(g1 - g0);                           // steps of this CTA
   const int item0 = (int)(g0 / nkt), kt00 = (int)(g0 - (long long)item0 * nkt);
   // query tiles of an item

@@ -21,6 +21,7 @@
 int main() {
   std::mt19937 rng(5);
   auto pick = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
+  int even = 0;
   for (int round = 0; round < 20000; ++round) {
     const int heads = pick(1, 9), nkt = round % 3 ? pick(1, 12) : pick(1, 300);
     const int ntiles = pick(1, 7), npairs = (ntiles + 1) / 2;
@@ -34,15 +35,18 @@ int main() {
     const long long work = (long long)heads * nkt * ntiles;
     const long long chunks = pick(0, 3) ? pick(1, 5000) : 0;
     const int n1 = pkv::px_ctas(x, work, chunks, pick(1, 200));
+    const pkv::PxCut cut = pkv::px_cut(n1, heads, nkt, ntiles);
+    even += cut.per_head > 0;
     CHECK(pkv::px_key_tiles(x.prefix_len) == nkt);
     CHECK(n1 >= 1 && n1 <= x.sms);
     if (chunks > 0) CHECK(n1 == 1 || n1 <= x.sms - x.groups);
     CHECK(pkv::px_ctas(x, 0, chunks, 3) == 0);
     const long long all = (long long)npairs * heads * nkt;
     std::vector<int> owner(all, -1);
-    for (int c = 0; c < n1; ++c) {
-      const long long g0 = pkv::px_step_at(c * work / n1, nkt, ntiles);
-      const long long g1 = c + 1 == n1 ? all : pkv::px_step_at((c + 1) * work / n1, nkt, ntiles);
+    CHECK(cut.n >= 1 && cut.n <= n1);
+    for (int c = 0; c < cut.n; ++c) {
+      long long g0, g1;
+      pkv::px_cta_steps(cut, c, heads, nkt, ntiles, g0, g1);
       CHECK(g0 < g1 && g0 >= 0 && g1 <= all);
       for (long long g = g0; g < g1; ++g) {
         CHECK(owner[g] == -1);
@@ -51,8 +55,8 @@ int main() {
     }
     std::set<int> slots;
     for (int item = 0; item < npairs * heads; ++item) {
-      const int a = pkv::cta_of_chunk(pkv::px_unit_of(item, 0, nkt, ntiles), work, n1);
-      const int b = pkv::cta_of_chunk(pkv::px_unit_of(item, nkt - 1, nkt, ntiles), work, n1);
+      const int2 at = pkv::px_item_ctas(cut, item, heads, nkt, ntiles);
+      const int a = at.x, b = at.x + at.y - 1;
       CHECK(owner[(long long)item * nkt] == a && owner[(long long)(item + 1) * nkt - 1] == b);
       for (int c = a; c <= b; ++c) {
         CHECK(slots.insert(c + item).second);                // a partial state each
@@ -63,6 +67,7 @@ int main() {
       }
     }
   }
+  if (even < 1000 || even > 19000) return printf("even %d\n", even), 1;
   printf("prefix work ok\n");
   return 0;
 }
