@@ -380,9 +380,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     fence_barrier_init();
   }
   // The prefix sums read only the lengths (and, with several query tokens,
-  // cu_seqlens), which no kernel of this library writes, so they overlap the
-  // previous kernel's tail; shared-prefix groups also need the group lengths
-  // the previous kernel (share_prefix_kernel) writes.
+  // cu_seqlens), so they overlap the previous kernel's tail: the kernels of
+  // this library that write them (the step tables) let no dependent start
+  // before they end.  Shared-prefix groups also need the group lengths the
+  // previous kernel (share_prefix_kernel) writes.
   if constexpr (SH) pdl_wait_primary();
 
   // ---- chunk prefix sums over the units: cstart[u] = sum_{u'<u} chunks(u')
@@ -469,8 +470,9 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       }
     }
   };
-  // the producer reads its first table entries (no kernel of this library
-  // writes the tables) before waiting for the previous kernel
+  // the producer reads its first table entries (written, like the lengths, by
+  // no kernel that lets this one start before it ends) before waiting for the
+  // previous kernel
   int row[TL][2];
   if (warp == HPC && cb < ce) tile_rows(cb, row);
   if constexpr (!SH && !PX) pdl_wait_primary();
@@ -1148,8 +1150,8 @@ share_prefix_kernel(const int32_t* __restrict__ block_tables, int max_blocks_per
       lg = min(run * K, lmin) / kTile * kTile;
     }
   }
-  // the tables and lengths are inputs no kernel of this library writes; the
-  // workspace may still be read by the previous launch
+  // the tables and lengths are written by no kernel that lets this one start
+  // before it ends; the workspace may still be read by the previous launch
   pdl_wait_primary();
   pdl_launch_dependents();
   if (g < ngroups && lane == 0) glen[g] = lg;
