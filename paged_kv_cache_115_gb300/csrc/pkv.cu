@@ -916,9 +916,8 @@ pkv_status launch_prefix_part(const pkv::PxParams& prm, const PrefixPlan& plan, 
 
 template <int D, int WPR>
 pkv_status launch_prefix_merge_w(const pkv::PxParams& prm, int tile_rows, cudaStream_t st) {
-  const int64_t rows = (int64_t)prm.T * prm.H_q;
-  PKV_CUDA(launch_pdl(pkv::prefix_merge_kernel<D, WPR>,
-                      dim3((unsigned)ceil_div(rows * WPR, pkv::kPxMergeWarps)),
+  const int64_t per_token = ceil_div(prm.H_q, pkv::kPxMergeWarps / WPR);
+  PKV_CUDA(launch_pdl(pkv::prefix_merge_kernel<D, WPR>, dim3((unsigned)(prm.T * per_token)),
                       dim3(pkv::kPxMergeWarps * 32), 0, st, prm, tile_rows));
   return PKV_OK;
 }

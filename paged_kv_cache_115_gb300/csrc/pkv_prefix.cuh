@@ -639,37 +639,41 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
 // Merge of the partial states of a (token, query head) row: its own tokens'
 // (slots of meta[t]) and the prefix's (items[item] = {first CTA, CTAs}).  A
 // row costs a chain of loads (length, slots, states), so what counts is how
-// many warps are resident.  Many rows of few partials (WPR 1): two partials
-// at a time in 32 registers, eight CTAs an SM.  A small batch over a long
+// many warps are resident and how few instructions each takes.  Many rows of
+// few partials (WPR 1): four partials at a time.  A small batch over a long
 // prefix has few rows of many partials: WPR warps share a row, eight partials
 // each at a time.
 // ===========================================================================
 constexpr int kPxMergeWarps = 8;
 
 template <int D, int WPR>
-__global__ void __launch_bounds__(kPxMergeWarps * 32, WPR == 1 ? 8 : 2)
+__global__ void __launch_bounds__(kPxMergeWarps * 32, WPR == 1 ? 5 : 2)
 prefix_merge_kernel(const __grid_constant__ PxParams p, int tile_rows) {
-  constexpr int V = D / 32, RPC = kPxMergeWarps / WPR, B = WPR == 1 ? 2 : 8;
+  constexpr int V = D / 32, RPC = kPxMergeWarps / WPR, B = WPR == 1 ? 4 : 8;
   __shared__ float s_acc[WPR > 1 ? kPxMergeWarps : 1][D];
   __shared__ float s_m[kPxMergeWarps], s_l[kPxMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
-  const int pair = blockIdx.x * RPC + warp / WPR;
-  const int t = pair / p.H_q, h = pair - t * p.H_q;
+  // a CTA takes RPC heads of one token
+  const int per_token = (p.H_q + RPC - 1) / RPC;
+  const int t = blockIdx.x / per_token;
+  const int h = (blockIdx.x - t * per_token) * RPC + warp / WPR;
+  const int j = h / p.G, r = t * p.G + h - j * p.G;
   pdl_wait_primary();
   pdl_launch_dependents();
   const int tokens = px_tokens(p.cu, p.S, p.T);
   int s, i, n, L;
   // rows of an inconsistent sequence are left as they are (the decode kernel reports it)
-  bool live = t < tokens && px_row(p, t, s, i, n, L);
-  int own = 0, np = 0, item = 0, first = 0, base = 0;
-  const int j = h / p.G, r = t * p.G + h - j * p.G;
+  bool live = h < p.H_q && t < tokens && px_row(p, t, s, i, n, L);
+  // partial x < own in slot base + x own_stride of its own tokens, the others
+  // in row `at` + (x - own) tile_rows of the prefix slots
+  int own = 0, np = 0, at = 0, base = 0;
   if (live) {
     const int4 mt = p.meta[t];
     if (p.split.prefix_len > 0) {
       const int npairs = (px_tiles(tokens * p.G) + 1) >> 1;
-      item = j * npairs + r / (2 * kT5Rows);
+      const int item = j * npairs + r / (2 * kT5Rows);
       const int2 it = p.items[item];
-      first = it.x;
+      at = (it.x + item) * tile_rows + r % (2 * kT5Rows);
       np = it.y;
     }
     own = mt.y;
@@ -680,30 +684,37 @@ prefix_merge_kernel(const __grid_constant__ PxParams p, int tile_rows) {
   float M = -INFINITY, lsum = 0.f, acc[V] = {};
   if (live) {
     for (int x0 = sub * B; x0 < np; x0 += WPR * B) {
-      auto index = [&](int x) -> int64_t {
-        return x < own ? ((int64_t)base + (int64_t)x * p.own_stride) * p.H_q + h
-                       : (int64_t)(first + x - own + item) * tile_rows + r % (2 * kT5Rows);
-      };
-      const int cnt = min(B, np - x0);
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < cnt) ml = (x0 + lane < own ? p.own_ml : p.ml)[index(x0 + lane)];
+      // (every lane reads the states of all partials: broadcasts cost less
+      // than the shuffles of one state per lane)
+      float2 ml[B];
       float v[B][V];
 #pragma unroll
-      for (int x = 0; x < B; ++x)
-        if (x < cnt) load_f<V>((x0 + x < own ? p.own_o : p.o) + index(x0 + x) * D + lane * V, v[x]);
-      const float m2 = fmaxf(M, warp_max(ml.x));
+      for (int x = 0; x < B; ++x) {
+        ml[x] = make_float2(-INFINITY, 0.f);
+        if (x0 + x < np) {
+          const bool mine = x0 + x < own;
+          const int row = mine ? (base + (x0 + x) * p.own_stride) * p.H_q + h
+                               : at + (x0 + x - own) * tile_rows;
+          ml[x] = (mine ? p.own_ml : p.ml)[row];
+          load_f<V>((mine ? p.own_o : p.o) + (int64_t)row * D + lane * V, v[x]);
+        }
+      }
+      float m2 = M;
+#pragma unroll
+      for (int x = 0; x < B; ++x) m2 = fmaxf(m2, ml[x].x);
       const float mu = m2 == -INFINITY ? 0.f : m2;          // nothing visible so far: weights 0
-      const float w = exp2f(ml.x - mu), a = exp2f(M - mu);
+      const float a = ex2_approx(M - mu);
       M = m2;
-      lsum = lsum * a + warp_sum(ml.y * w);
+      lsum *= a;
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[e] *= a;
 #pragma unroll
       for (int x = 0; x < B; ++x) {
-        const float wx = __shfl_sync(0xffffffffu, w, x);
-        if (x < cnt) {
+        if (x0 + x < np) {
+          const float w = ex2_approx(ml[x].x - mu);
+          lsum = fmaf(ml[x].y, w, lsum);
 #pragma unroll
-          for (int e = 0; e < V; ++e) acc[e] = fmaf(wx, v[x][e], acc[e]);
+          for (int e = 0; e < V; ++e) acc[e] = fmaf(w, v[x][e], acc[e]);
         }
       }
     }
@@ -734,7 +745,7 @@ prefix_merge_kernel(const __grid_constant__ PxParams p, int tile_rows) {
   }
   if (!live) return;
   const float inv = lsum > 0.f ? 1.f / lsum : 0.f;          // nothing visible: zeros
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (int64_t)pair * D + lane * V);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + ((int64_t)t * p.H_q + h) * D + lane * V);
   if constexpr (V == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
                                                 pack_bf16x2(acc[2] * inv, acc[3] * inv));

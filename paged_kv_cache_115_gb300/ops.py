@@ -673,6 +673,10 @@ def prefill_workspace_bytes(num_seqs, num_tokens, max_query_len, max_context_len
 # rotation + append, attention behind a shared prefix, draft verification
 # ---------------------------------------------------------------------------
 
+# types that hold one-byte codes
+_CODE_TYPES = frozenset(t for t in (torch.uint8, torch.int8, getattr(torch, "float8_e4m3fn", None))
+                        if t is not None)
+
 # the current stream's handle without a Stream object around it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -838,11 +842,14 @@ def paged_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         kp = _whole(k_cache, "k_cache", dtype, k_cache.shape, dev)
         vp = _whole(v_cache, "v_cache", dtype, k_cache.shape, dev)
     else:
-        _need_pool(k_cache, "k_cache", quant)
-        _need_pool(v_cache, "v_cache")
-        kp = _whole(k_cache, "k_cache", k_cache.dtype, k_cache.shape, dev)
-        vp = _whole(v_cache, "v_cache", v_cache.dtype, k_cache.shape, dev)
-        if quant.format == KV_INT8_TOKEN:
+        kt, vt, fmt = k_cache.dtype, v_cache.dtype, quant.format
+        if vt not in _CODE_TYPES or (kt is not torch.bfloat16 if fmt == KV_BF16K_FP8V
+                                     else kt not in _CODE_TYPES):
+            _need_pool(k_cache, "k_cache", quant)
+            _need_pool(v_cache, "v_cache")
+        kp = _whole(k_cache, "k_cache", kt, k_cache.shape, dev)
+        vp = _whole(v_cache, "v_cache", vt, k_cache.shape, dev)
+        if fmt == KV_INT8_TOKEN:
             for t in getattr(quant, "_scale_tensors", ()):
                 if t.shape[0] != nb * K or t.get_device() != dev:
                     raise ValueError("token scales must cover every slot of the pool, on its device")

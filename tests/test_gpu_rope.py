@@ -286,3 +286,15 @@ def test_refused_arguments(ops):
         f(q, k, v, pos, sl.cpu(), kc, kc, t)
     with pytest.raises(TypeError):
         f(q, k, v, pos, sl, kc, kc, t.double())
+    codes = torch.zeros(kc.shape, dtype=torch.uint8, device=DEV)
+    with pytest.raises(TypeError):
+        f(q, k, v, pos, sl, kc, codes, t, quant=ops.kv_quant("fp8"))
+    with pytest.raises(TypeError):
+        f(q, k, v, pos, sl, codes, codes, t, quant=ops.kv_quant("k16v8"))
+    with pytest.raises(TypeError):
+        f(q, k, v, pos, sl, kc, kc, t, quant=ops.kv_quant("k16v8"))
+    with pytest.raises(ValueError):
+        f(q, k, v, pos, sl, codes, codes[:-1], t, quant=ops.kv_quant("fp8"))
+    few = torch.zeros(3, device=DEV)
+    with pytest.raises(ValueError):
+        f(q, k, v, pos, sl, codes, codes, t, quant=ops.kv_quant("int8", 1.0, 1.0, few, few))
