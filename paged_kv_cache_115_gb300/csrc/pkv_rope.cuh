@@ -255,6 +255,16 @@ rope_ring_kernel(const __grid_constant__ RopeParams p, int stage_bytes) {
   float* const s_all = reinterpret_cast<float*>(s_ring + (size_t)stages * stage_bytes);   // INT8
   // the consumers among themselves
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kRopeThreads) : "memory"); };
+  auto all_of = [](bool ok) -> bool {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.and.pred q, 1, %1, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "n"(kRopeThreads), "r"((uint32_t)ok)
+        : "memory");
+    return all != 0;
+  };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q_bytes = p.H_q * D * (int)sizeof(TIN), kv_bytes = p.H_kv * D * (int)sizeof(TIN);
   if (tid == 0) {
@@ -354,7 +364,9 @@ rope_ring_kernel(const __grid_constant__ RopeParams p, int stage_bytes) {
   const int row0 = warp * (32 / LANES), sub = lane / LANES;
   int stage = 0, round = 0;
   for (;;) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&s_full[stage]), round & 1));
+    bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&s_full[stage]), round & 1));
+    // INT8: the warps wait for one another below, so they give up together
+    if constexpr (FMT == 2) ok = all_of(ok);
     if (!ok) {
       if (lane == 0) record_error(PKV_DEVERR_TIMEOUT);
       return;

@@ -139,6 +139,30 @@ def test_packed_new_tokens(ops, H, J, most):
     check(ops, problem(lens, news, H, J, 128, 16, 224, seed=H))
 
 
+@pytest.mark.parametrize("H,J,D,K", [(32, 16, 128, 16), (12, 12, 64, 8), (48, 24, 64, 32),
+                                     (10, 10, 128, 16)])
+def test_several_groups_of_kv_heads(ops, H, J, D, K):
+    """More KV heads than the decode kernel takes in one CTA."""
+    rng = np.random.default_rng(J)
+    lens = [6 * K + int(x) for x in rng.integers(1, 120, 9)]
+    check(ops, problem(lens, [1] * 9, H, J, D, K, 6 * K, seed=J))
+    news = [int(x) for x in rng.integers(1, 3, 9)]
+    check(ops, problem(lens, news, H, J, D, K, 6 * K, seed=J + 1))
+
+
+def test_the_largest_batch(ops):
+    """2048 sequences, the most of one call, most of them a token or two behind
+    the prefix."""
+    rng = np.random.default_rng(7)
+    lens = [int(x) for x in 64 + rng.integers(1, 4, 2048)]
+    lens[5], lens[2000] = 0, 40
+    pb = problem(lens, [1] * 2048, 2, 1, 64, 16, 64, seed=7)
+    check(ops, pb)
+    with pytest.raises(ops.PagedKVError):
+        call(ops, dict(pb, lens=lens + [1], q=torch.cat([pb["q"], pb["q"][:1]]),
+                       bt=np.concatenate([pb["bt"], pb["bt"][:1]])))
+
+
 def test_packed_new_tokens_inside_the_prefix(ops):
     """New tokens that sit in shared blocks see the keys up to their own."""
     news = [4, 4, 2, 1, 4]
