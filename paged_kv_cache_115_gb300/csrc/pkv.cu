@@ -940,9 +940,9 @@ pkv_status launch_verify(const pkv::VerifyParams& p, int S, cudaStream_t st) {
   if (s != PKV_OK) return s;
   // CTAs a sequence: as many as are resident together, each warp with three
   // 512-byte tiles or more.  More cost their own start and exchange: 64
-  // sequences over 131072 float32 take 19.4 us with 1 CTA each, 13.7 with 2,
-  // 12.8 with 4, 18.5 with 8; 200 over 32000 take 12.2 with 1 and 17.1 with 2;
-  // one over 32000 takes 8.6 with 1, 6.3 with 4, 6.2 with 8.
+  // sequences over 131072 float32 take 16.6 us with 1 CTA each, 11.1 with 2,
+  // 10.4 with 4; 256 take 41.3 with 1, 43.5 with 2; 200 over 32000 take 10.1
+  // with 1 and 14.6 with 2; one over 32000 takes 7.4 with 1, 5.7 with 4.
   const int64_t tiles = p.vocab * (int64_t)sizeof(T) / 512;
   int C = 1;
   while (C < 8 && 2 * S * C <= pkv::kVerifyCtas * sms && tiles >= 2 * C * 3 * pkv::kVerifyWarps) C *= 2;

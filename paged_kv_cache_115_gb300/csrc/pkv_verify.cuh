@@ -11,10 +11,11 @@
 // memory, and the warps of the CTA whose sums hold the threshold share the
 // one segment that holds it (read again, from L1 / L2) to find the token.
 // Bound by HBM: one row of p, and one of q where a draft was refused, behind
-// a chain of about 8 us (counts, tokens, their probabilities, sums, threshold,
+// a chain of about 6 us (counts, tokens, their probabilities, sums, threshold,
 // the segment again).  256 sequences over 131072 float32, two in three
-// refused: 224 MB in 50 us, 4.5 TB/s; all of them are resident at once, two
-// on most SMs and one on the others, which leaves a sixth of the time.
+// refused: 224 MB in 41.3 us, 5.4 TB/s.  Loops of their own for p, p - q and
+// shifted q, eight, four and two tiles in flight, keep two CTAs of 512 threads
+// on an SM without spills (one loop for all: 49.7 us).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -27,7 +28,7 @@ constexpr int kVerifyThreads = 512;
 constexpr int kVerifyCtas = 2;          // resident on an SM
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyMaxCluster = 16;
-constexpr int kVerifyBatch = 4;         // tiles whose loads are in flight together
+constexpr int kVerifyBatch = 4;         // tiles whose loads of p and q are in flight together
 
 struct VerifyParams {
   const void* target;
@@ -123,28 +124,29 @@ struct VerifyRow {
     return make_uint4(__funnelshift_r(c[0], c[1], half), __funnelshift_r(c[1], c[2], half),
                       __funnelshift_r(c[2], c[3], half), __funnelshift_r(c[3], c[4], half));
   }
-  // this lane's block of n tiles that lie inside, all loads first
-  template <int N, typename F>
+  // this lane's block of N tiles that lie inside, all loads first (MODE 0: p,
+  // 1: p - q, 2: p - q with q's blocks cut out of two)
+  template <int N, int MODE, typename F>
   __device__ __forceinline__ void visit(int t, int lane, F&& f) const {
     uint4 a[N], b[N], c[N];
     const int64_t i0 = (int64_t)t * 32 + lane;
 #pragma unroll
     for (int n = 0; n < N; ++n) a[n] = __ldg(p_al + i0 + 32 * n);
-    if (q != nullptr) {
+    if constexpr (MODE > 0) {
 #pragma unroll
       for (int n = 0; n < N; ++n) b[n] = __ldg(q_al + i0 + 32 * n);
-      if (shifted) {
+    }
+    if constexpr (MODE == 2) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) c[n] = __ldg(q_al + i0 + 32 * n + 1);
+      for (int n = 0; n < N; ++n) c[n] = __ldg(q_al + i0 + 32 * n + 1);
 #pragma unroll
-        for (int n = 0; n < N; ++n) b[n] = cut(b[n], c[n]);
-      }
+      for (int n = 0; n < N; ++n) b[n] = cut(b[n], c[n]);
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       float w[E];
       unpack(a[n], w);
-      if (q != nullptr) {
+      if constexpr (MODE > 0) {
         float x[E];
         unpack(b[n], x);
 #pragma unroll
@@ -166,8 +168,9 @@ struct VerifyRow {
       }
     }
   }
-  // sum of the weights of tiles [t0, t1), of the whole warp
-  __device__ __forceinline__ long long sum(int t0, int t1, int lane) const {
+  template <int MODE>
+  __device__ __forceinline__ long long sum_mode(int t0, int t1, int lane) const {
+    constexpr int N = MODE == 0 ? 2 * kVerifyBatch : (MODE == 1 ? kVerifyBatch : kVerifyBatch / 2);
     long long total = 0;
     uint32_t h = 0, l = 0, n = 0;
     auto add = [&](const float (&w)[E]) {
@@ -181,11 +184,11 @@ struct VerifyRow {
       n += E;
     };
     for (int t = t0; t < t1;) {
-      if (t + kVerifyBatch <= t1 && inside(t, kVerifyBatch)) {
-        visit<kVerifyBatch>(t, lane, add);
-        t += kVerifyBatch;
+      if (t + N <= t1 && inside(t, N)) {
+        visit<N, MODE>(t, lane, add);
+        t += N;
       } else if (inside(t, 1)) {
-        visit<1>(t, lane, add);
+        visit<1, MODE>(t, lane, add);
         ++t;
       } else {
         float w[E];
@@ -200,6 +203,11 @@ struct VerifyRow {
     }
     total += ((long long)(h - n * kVerifyBias) << 20) + (l - n * kVerifyBias);
     return warp_sum_ll(total);
+  }
+  // sum of the weights of tiles [t0, t1), of the whole warp
+  __device__ __forceinline__ long long sum(int t0, int t1, int lane) const {
+    if (q == nullptr) return sum_mode<0>(t0, t1, lane);
+    return shifted ? sum_mode<2>(t0, t1, lane) : sum_mode<1>(t0, t1, lane);
   }
 };
 
@@ -333,14 +341,7 @@ verify_kernel(const __grid_constant__ VerifyParams p) {
       if (r >= run && r < run + psum) {
         for (int t = pa; t < pb; ++t) {
           float wt[E];
-          if (row.inside(t, 1)) {
-            row.template visit<1>(t, lane, [&](const float (&w)[E]) {
-#pragma unroll
-              for (int e = 0; e < E; ++e) wt[e] = w[e];
-            });
-          } else {
-            row.block(t, lane, wt);
-          }
+          row.block(t, lane, wt);
           long long own = 0;
 #pragma unroll
           for (int e = 0; e < E; ++e) own += verify_weight(wt[e]);

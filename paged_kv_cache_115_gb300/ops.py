@@ -680,12 +680,13 @@ _CODE_TYPES = frozenset(t for t in (torch.uint8, torch.int8, getattr(torch, "flo
 # the current stream's handle without a Stream object around it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call_on(dev: int, fn, args, what: str) -> None:
     """Calls the library with device ``dev`` current and its current stream as
     the last argument."""
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -713,9 +714,8 @@ def _refuse(t: torch.Tensor, name: str, dtype, dev: int, shape: str) -> None:
 
 def _vec(t: torch.Tensor, name: str, dtype, n: int, dev: int) -> int:
     """Address of a contiguous vector of ``n`` values on device ``dev``."""
-    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 1 or t.shape[0] != n or \
-            not t.is_contiguous():
-        _refuse(t, name, dtype, dev, f"contiguous [{n}]")
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, dev, f"contiguous with {n} values")
     return t.data_ptr()
 
 
