@@ -183,7 +183,7 @@ __host__ __device__ __forceinline__ PxCut px_cut(int n1, int heads, int nkt, int
   const int npairs = (ntiles + 1) >> 1, share = n1 / heads;
   const long long work = (long long)heads * nkt * ntiles;
   PxCut c = {n1, 0, 0, 0};
-  if (share < npairs) return c;
+  if (n1 < 1 || share < npairs) return c;
   const int odd = ntiles & 1, full = npairs - odd;
   int duo = full ? 2 * share / ntiles : 0;
   if (full && duo < 1) return c;
@@ -271,38 +271,7 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
 
-  // ---- the SMs of this part: everything the kernel in front wrote is there
-  // after the wait, for the decode kernel too
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  long long chunks = 0;
-  for (int s = tid; s < p.S; s += kPxThreads)
-    chunks += px_own_chunks(p.split, p.cu, p.T, s, max(0, min(p.lens[s], min(p.max_len, p.row_tokens))));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) chunks += __shfl_xor_sync(0xffffffffu, chunks, o);
-  if (lane == 0) s_chunks[warp] = chunks;
-  __syncthreads();
-  chunks = 0;
-#pragma unroll
-  for (int w = 0; w < kPxThreads / 32; ++w) chunks += s_chunks[w];
-  const int R = px_tokens(p.cu, p.S, p.T) * p.G;           // query rows per KV head
-  const int P = p.split.prefix_len;
-  const int ntiles = px_tiles(R), npairs = (ntiles + 1) >> 1;
-  const int nkt = px_key_tiles(P);
-  const long long work = (long long)p.H_kv * nkt * ntiles;
-  const PxCut cut = px_cut(px_ctas(p.split, work, chunks, p.S), p.H_kv, nkt, ntiles);
-  if (cta >= cut.n) return;
-  if (cta == cut.n - 1) {                                  // which CTAs hold steps of each item
-    for (int x = tid; x < npairs * p.H_kv; x += kPxThreads)
-      p.items[x] = px_item_ctas(cut, x, p.H_kv, nkt, ntiles);
-  }
-  long long g0, g1;
-  px_cta_steps(cut, cta, p.H_kv, nkt, ntiles, g0, g1);
-  const int ng = (int)(g1 - g0);                           // steps of this CTA
-  const int item0 = (int)(g0 / nkt), kt00 = (int)(g0 - (long long)item0 * nkt);
-  // query tiles of an item
-  auto tiles_of = [&](int item) -> int { return 2 * (item % npairs) + 2 <= ntiles ? 2 : 1; };
-
+  // barriers and TMEM while the kernel in front still runs
   if (tid == 0) {
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(full + 8 * i, 1);
@@ -320,11 +289,51 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
     mbar_init(mma_idle, 2);
     fence_barrier_init();
   }
-  if (warp == 9) tmem_alloc(smem_u32(slot), C::TMEM_COLS);
+  if (warp == 9) {
+    tmem_alloc(smem_u32(slot), C::TMEM_COLS);
+    if (lane == 0) {
+      prefetch_tensormap(&p.tmap_k);
+      prefetch_tensormap(&p.tmap_v);
+    }
+  }
   tc_fence_before();
+  // ---- the SMs of this part: everything the kernel in front wrote is there
+  // after the wait, for the decode kernel too
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  long long chunks = 0;
+  for (int s = tid; s < p.S; s += kPxThreads)
+    chunks += px_own_chunks(p.split, p.cu, p.T, s, max(0, min(p.lens[s], min(p.max_len, p.row_tokens))));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) chunks += __shfl_xor_sync(0xffffffffu, chunks, o);
+  if (lane == 0) s_chunks[warp] = chunks;
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
+  chunks = 0;
+#pragma unroll
+  for (int w = 0; w < kPxThreads / 32; ++w) chunks += s_chunks[w];
+  const int R = px_tokens(p.cu, p.S, p.T) * p.G;           // query rows per KV head
+  const int P = p.split.prefix_len;
+  const int ntiles = px_tiles(R), npairs = (ntiles + 1) >> 1;
+  const int nkt = px_key_tiles(P);
+  const long long work = (long long)p.H_kv * nkt * ntiles;
+  const PxCut cut = px_cut(px_ctas(p.split, work, chunks, p.S), p.H_kv, nkt, ntiles);
+  if (cta >= cut.n) {
+    if (warp == 9) tmem_dealloc(tmem, C::TMEM_COLS);
+    return;
+  }
+  if (cta == cut.n - 1) {                                  // which CTAs hold steps of each item
+    for (int x = tid; x < npairs * p.H_kv; x += kPxThreads)
+      p.items[x] = px_item_ctas(cut, x, p.H_kv, nkt, ntiles);
+  }
+  long long g0, g1;
+  px_cta_steps(cut, cta, p.H_kv, nkt, ntiles, g0, g1);
+  const int ng = (int)(g1 - g0);                           // steps of this CTA
+  const int item0 = (int)(g0 / nkt), kt00 = (int)(g0 - (long long)item0 * nkt);
+  // query tiles of an item
+  auto tiles_of = [&](int item) -> int { return 2 * (item % npairs) + 2 <= ntiles ? 2 : 1; };
+
   const int K = p.block_size;
 
   if (warp == 8 || warp == 10) {
@@ -334,7 +343,6 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
     // copy each took 74 cycles a copy).
     const int kv = warp == 10;
     const CUtensorMap* map = kv ? &p.tmap_v : &p.tmap_k;
-    if (lane == 0) prefetch_tensormap(map);
     // the prefix is read once per pair of tiles: kept in L2 when there are several
     const uint64_t policy = npairs > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
     const bool small = K < 16;                            // 8-token blocks: 8-row boxes
