@@ -166,6 +166,11 @@ __device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, float (&v)[64]) {
 // output; the row sum l adds the unrounded weights in fp32.
 // The exponent base of a row is raised only when its maximum grows by more
 // than 2^8, so O is rescaled in TMEM rarely.  Every wait is bounded.
+//
+// On all SMs: 1024 x 32 rows over 16384 tokens (275 GFLOP) 208 us, 1320
+// TFLOP/s, bound by a tile's chain of softmax and products (3600 cycles for
+// two jobs against 3030 of tensor work) and by K and V from L2; 8 x 64 rows
+// over 131072 tokens (537 MB) 82.5 us, 6.5 TB/s, bound by HBM.
 // ===========================================================================
 
 // How the steps of all items are dealt to at most n1 CTAs.
@@ -651,6 +656,7 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
 // few partials (WPR 1): four partials at a time.  A small batch over a long
 // prefix has few rows of many partials: WPR warps share a row, eight partials
 // each at a time.
+// 32768 rows of two to four partials take about 14 us, 512 rows of twenty 4.
 // ===========================================================================
 constexpr int kPxMergeWarps = 8;
 
