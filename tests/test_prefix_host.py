@@ -78,7 +78,7 @@ class Cta:
         self.pipes = {"qk": [], "pv": [], "load": []}
 
     def issue(self, pipe, effects):
-        self.pipes[pipe].append([self.rng.randint(0, 6), effects])
+        self.pipes[pipe].append([self.rng.choice([0, 1, 3, 6, 30]), effects])
 
     def producer(self, kv):
         for g in range(len(self.steps)):
@@ -167,19 +167,20 @@ class Cta:
         idle = 0
         while any(a != "end" for a in at) or any(self.pipes.values()):
             moved = False
-            for ops in self.pipes.values():        # each pipe in order
+            for name, ops in self.pipes.items():   # products in order, loads in any
+                i = self.rng.randrange(len(ops)) if ops and name == "load" else 0
                 if ops:
                     moved = True
-                    if ops[0][0] <= 0:
-                        ops.pop(0)[1]()
+                    if ops[i][0] <= 0:
+                        ops.pop(i)[1]()
                     else:
-                        ops[0][0] -= 1
+                        ops[i][0] -= 1
             for i in self.rng.sample(range(6), self.rng.randint(1, 6)):
                 if at[i] != "end" and (at[i] is None or at[i][0].passes(at[i][1])):
                     at[i] = next(roles[i], "end")
                     moved = True
             idle = 0 if moved else idle + 1
-            assert idle < 200, "nobody can go on"
+            assert idle < 500, "nobody can go on"
 
 
 @pytest.mark.parametrize("ns", [5, 8])
