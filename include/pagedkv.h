@@ -578,11 +578,14 @@ PKV_API pkv_status pkv_qk_norm_rope_append(
  * pkv_attention_prefill (cu_seqlens: packed new tokens) over the full tables.
  *   prefix_table: int32 [prefix_len / block_size], the blocks of tokens 0 ..
  *            prefix_len - 1 of every sequence; prefix_len is a multiple of
- *            block_size.
+ *            block_size.  Entries behind the longest sequence are not read.
  *   block_tables: the full rows; entries below prefix_len / block_size are
  *            not read.  context_lens count all tokens.  A sequence shorter
- *            than prefix_len reads that much of the prefix; one of length 0
- *            gets zeros (cu_seqlens NULL).
+ *            than prefix_len, or with new tokens inside it, reads as much of
+ *            the prefix as it sees, on its own (the work is shared by the
+ *            sequences whose rows all see the whole prefix); one of length 0
+ *            gets zeros (cu_seqlens NULL).  Slots behind a sequence's end may
+ *            hold anything.
  *   num_tokens: rows of q and out ([num_tokens, num_q_heads, head_dim]);
  *            num_seqs when cu_seqlens is NULL.  Rows behind the last sequence
  *            (num_tokens > cu_seqlens[num_seqs]) are left as they are.

@@ -1883,6 +1883,7 @@ pkv_status pkv_attention_decode_prefix(
   t.cu_seqlens = cu_seqlens;
   t.share_m = 1;
   t.px = plan.split;
+  t.prefix_table = prefix_table;
   t.px_heads = num_kv_heads;
   t.num_tokens = num_tokens;
   st = encode_pool_map_heads(&t.tmap_k, k_cache, num_blocks, block_size, num_kv_heads, D, plan.hpc,

@@ -50,6 +50,14 @@ constexpr int tc_chunk_tokens(int ct) { return ct == 1 || ct == 2 ? 2 * kTile : 
 // the SMs.  Both derive the shares from the same counts: tile steps of the
 // prefix kernel (128 query rows x 128 keys) weigh w1, chunks of this one w2
 // and its sequences w3 (the start and the partial state of each).
+//
+// A product with a weight of 0 keeps a NaN, so a row takes part in the prefix
+// kernel's products only if it sees every key of the prefix.  A sequence with
+// a row that does not (one that ends inside the prefix, or has new tokens in
+// it) is left to this kernel as a whole, which gives V behind its end as
+// zeros; the blocks of its prefix tokens come from the prefix's table.  If
+// that is every sequence, the prefix kernel has no work, and reads neither
+// slots nor table entries that nobody has filled yet.
 constexpr int kPxKeys = 128;
 __host__ __device__ constexpr int px_tiles(int rows) { return (rows + 127) / 128; }
 __host__ __device__ constexpr int px_key_tiles(int prefix_len) {
@@ -63,15 +71,27 @@ struct PxSplit {
   int w1, w2, w3;
 };
 
-// 16-token chunks of sequence s's own tokens (L: its clamped length; 0 for an
-// inconsistent sequence, or one without query rows).
+// First token of the own part of a sequence of L tokens, n of them new: all n
+// rows see the prefix when the first one's position L - n is not in front of
+// its last token.
+__host__ __device__ __forceinline__ int px_first(int prefix_len, int n, int L) {
+  return L - n + 1 >= prefix_len ? prefix_len : 0;
+}
+
+// 16-token chunks of sequence s's own part (L: its clamped length; 0 for an
+// inconsistent sequence, or one without query rows).  `whole` is set if its
+// rows see the whole prefix.
 __device__ __forceinline__ int px_own_chunks(const PxSplit& x, const int32_t* cu, int T, int s,
-                                             int L) {
+                                             int L, bool& whole) {
+  int n = 1;
   if (cu != nullptr) {
-    const int c0 = cu[s], c1 = cu[s + 1], n = c1 - c0;
+    const int c0 = cu[s], c1 = cu[s + 1];
+    n = c1 - c0;
     if (n <= 0 || c0 < 0 || c1 > T || n > x.max_q || n > L) return 0;
   }
-  return L > x.prefix_len ? (L - x.prefix_len + kTile - 1) / kTile : 0;
+  const int t0 = px_first(x.prefix_len, n, L);
+  if (t0 == x.prefix_len) whole = true;
+  return L > t0 ? (L - t0 + kTile - 1) / kTile : 0;
 }
 
 // CTAs of the prefix kernel (0 without prefix work), each with two tile steps
@@ -126,6 +146,7 @@ struct TcParams {
   // writes a partial state, of query row i of the sequence in slot (CTA + unit)
   // * max_q + i; meta[row] = {first slot, partials, 0, 0}
   PxSplit px;
+  const int32_t* prefix_table;
   int num_tokens;           // rows of q / out
   int px_heads;             // KV heads
 };
@@ -324,8 +345,9 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     if constexpr (PX) {
       s0 = u;
       rows = 1;
-      t0 = p.px.prefix_len;
-      end = max(seq_len(u), t0);
+      const int L = seq_len(u);
+      t0 = px_first(p.px.prefix_len, cu == nullptr ? 1 : cu[u + 1] - cu[u], L);
+      end = max(L, t0);
     } else if constexpr (!SH) {
       s0 = u;
       rows = 1;
@@ -347,6 +369,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       }
     }
   };
+  bool whole = false;       // behind a shared prefix: a sequence sees all of it
   // chunks of unit u (none for a sequence without query rows)
   auto nchunks = [&](int u) -> int {
     if constexpr (PX) {
@@ -356,7 +379,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         if (c1 - c0 < 0 || c0 < 0 || c1 > p.num_tokens || c1 - c0 > p.px.max_q || c1 - c0 > L)
           record_error(PKV_DEVERR_CONTEXT_LEN);
       }
-      return px_own_chunks(p.px, cu, p.num_tokens, u, L);
+      return px_own_chunks(p.px, cu, p.num_tokens, u, L, whole);
     }
     int s0, rows, t0, end;
     unit(u, s0, rows, t0, end);
@@ -399,7 +422,8 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       if (lane >= o) incl += v;
     }
     if (lane == 31) s_wsum[warp] = incl;
-    __syncthreads();
+    if constexpr (PX) whole = __syncthreads_or(whole);
+    else __syncthreads();
     if (warp == 0) {
       int w = lane < (C::THREADS / 32) ? s_wsum[lane] : 0;
 #pragma unroll
@@ -428,7 +452,8 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   if constexpr (PX) {
     // the SMs that the prefix kernel leaves
     const int nt = cu == nullptr ? S : max(0, min(cu[S], p.num_tokens));
-    const long long work = (long long)p.px_heads * px_tiles(nt * p.G) * px_key_tiles(p.px.prefix_len);
+    const long long work =
+        whole ? (long long)p.px_heads * px_tiles(nt * p.G) * px_key_tiles(p.px.prefix_len) : 0;
     most = max(1, min((int)gridDim.x, (p.px.sms - px_ctas(p.px, work, T, S)) / p.px.groups));
   }
   const int n = (int)(T < most ? (T > 0 ? T : 1) : most);
@@ -459,7 +484,11 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           const int tok = t0 + (c - cstart[u]) * CH + t * kTile + uu * K;
           if (uu <= sbl && tok < L) {
             const int lb = tok / K;
-            const long long phys = p.block_tables[(int64_t)s0 * p.max_blocks_per_seq + lb];
+            const int32_t* entry = p.block_tables + (int64_t)s0 * p.max_blocks_per_seq + lb;
+            if constexpr (PX) {
+              if (tok < p.px.prefix_len) entry = p.prefix_table + lb;
+            }
+            const long long phys = *entry;
             if (phys < 0 || phys >= p.num_blocks) {
               record_error(PKV_DEVERR_BLOCK_ID);
             } else {

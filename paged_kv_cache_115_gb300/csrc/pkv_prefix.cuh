@@ -8,7 +8,8 @@
 // The prefix part is one matrix product over the query rows of the whole
 // batch: row r of KV head j is head j G + r % G of token r / G, and tiles of
 // 128 rows meet every prefix key once (tcgen05).  The own part is the
-// stream-K decode kernel on the tokens from prefix_len on.  The first is bound
+// stream-K decode kernel on the tokens from prefix_len on (on all tokens of a
+// sequence with a row that does not see the whole prefix: px_first).  The first is bound
 // by the tensor cores (or, with one tile of rows, by HBM), the second by HBM;
 // they run side by side on disjoint SMs: the prefix kernel releases its
 // dependent launch at once, the decode kernel does not wait for it, and both
@@ -80,12 +81,11 @@ __device__ __forceinline__ int px_tokens(const int32_t* cu, int S, int T) {
   return t < 0 ? 0 : min(t, T);
 }
 
-// Sequence of packed token t and whether it is consistent: cu[s] <= t <
-// cu[s+1] <= T and n <= its length; L its clamped length, i its index.
-__device__ __forceinline__ bool px_row(const PxParams& p, int t, int& s, int& i, int& n, int& L) {
-  s = t;
-  i = 0;
-  n = 1;
+// Whether packed token t belongs to a consistent sequence s: cu[s] <= t <
+// cu[s+1] <= T and n <= its length.  `whole`: its rows see the whole prefix.
+__device__ __forceinline__ bool px_row(const PxParams& p, int t, bool& whole) {
+  int s = t, n = 1;
+  whole = false;
   if (p.cu != nullptr) {
     int lo = 0, hi = p.S;
     while (hi - lo > 1) {
@@ -94,12 +94,12 @@ __device__ __forceinline__ bool px_row(const PxParams& p, int t, int& s, int& i,
     }
     s = lo;
     const int c0 = p.cu[s], c1 = p.cu[s + 1];
-    i = t - c0;
     n = c1 - c0;
-    if (i < 0 || t >= c1 || c0 < 0 || c1 > p.T || n > p.split.max_q) return false;
+    if (t < c0 || t >= c1 || c0 < 0 || c1 > p.T || n > p.split.max_q) return false;
   }
   const int cap = min(p.max_len, p.row_tokens);
-  L = max(0, min(p.lens[s], cap));
+  const int L = max(0, min(p.lens[s], cap));
+  whole = px_first(p.split.prefix_len, n, L) == p.split.prefix_len;
   return p.cu == nullptr || n <= L;
 }
 
@@ -307,12 +307,14 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
   pdl_wait_primary();
   pdl_launch_dependents();
   long long chunks = 0;
+  bool whole = false;
   for (int s = tid; s < p.S; s += kPxThreads)
-    chunks += px_own_chunks(p.split, p.cu, p.T, s, max(0, min(p.lens[s], min(p.max_len, p.row_tokens))));
+    chunks += px_own_chunks(p.split, p.cu, p.T, s,
+                            max(0, min(p.lens[s], min(p.max_len, p.row_tokens))), whole);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) chunks += __shfl_xor_sync(0xffffffffu, chunks, o);
   if (lane == 0) s_chunks[warp] = chunks;
-  __syncthreads();
+  whole = __syncthreads_or(whole);
   tc_fence_after();
   const uint32_t tmem = *slot;
   chunks = 0;
@@ -322,7 +324,7 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
   const int P = p.split.prefix_len;
   const int ntiles = px_tiles(R), npairs = (ntiles + 1) >> 1;
   const int nkt = px_key_tiles(P);
-  const long long work = (long long)p.H_kv * nkt * ntiles;
+  const long long work = whole ? (long long)p.H_kv * nkt * ntiles : 0;
   const PxCut cut = px_cut(px_ctas(p.split, work, chunks, p.S), p.H_kv, nkt, ntiles);
   if (cta >= cut.n) {
     if (warp == 9) tmem_dealloc(tmem, C::TMEM_COLS);
@@ -494,15 +496,10 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
         bool valid = r < R;
         const int t = valid ? r / p.G : 0;
         const int h = j * p.G + (valid ? r - t * p.G : 0);
-        int last = P - 1;                        // last prefix key this row sees
-        if (valid) {
-          int s, i, n, L;
-          valid = px_row(p, t, s, i, n, L);
-          if (valid) last = min(last, L - n + i);
+        if (valid) {                             // else zero queries, and a state that nobody reads
+          bool sees;
+          valid = px_row(p, t, sees) && sees;
         }
-        int lw = last;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) lw = min(lw, __shfl_xor_sync(0xffffffffu, lw, o));
         {
           // Q of the segment in front is free: its last S has been read
           const uint4* qrow = reinterpret_cast<const uint4*>(p.q + ((int64_t)t * p.H_q + h) * D);
@@ -524,15 +521,16 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
           tc_fence_after();
           const uint32_t sd = tmem + lane_base + b * kPxBN;
           const int kbase = (kt0 + st) * kPxBN;
-          const bool masked = kbase + kPxBN - 1 > lw;
+          const bool masked = kbase + kPxBN > P;
           float xs[64];
-          // 64 scores from key kbase + 64 h on, keys the row does not see at -inf
+          // 64 scores from key kbase + 64 h on, those past the prefix (their K
+          // and V are zeros) at -inf
           auto load = [&](int h) {
             tmem_ld64_wait(sd + 64 * h, xs);
             if (masked) {
-              const int lim = last - kbase - 64 * h;
+              const int end = P - kbase - 64 * h;
 #pragma unroll
-              for (int e = 0; e < 64; ++e) xs[e] = e <= lim ? xs[e] : -INFINITY;
+              for (int e = 0; e < 64; ++e) xs[e] = e < end ? xs[e] : -INFINITY;
             }
           };
           // row maximum: four chains of three-input max
@@ -675,15 +673,15 @@ prefix_merge_kernel(const __grid_constant__ PxParams p, int tile_rows) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int tokens = px_tokens(p.cu, p.S, p.T);
-  int s, i, n, L;
+  bool whole = false;
   // rows of an inconsistent sequence are left as they are (the decode kernel reports it)
-  bool live = h < p.H_q && t < tokens && px_row(p, t, s, i, n, L);
+  bool live = h < p.H_q && t < tokens && px_row(p, t, whole);
   // partial x < own in slot base + x own_stride of its own tokens, the others
   // in row `at` + (x - own) tile_rows of the prefix slots
   int own = 0, np = 0, at = 0, base = 0;
   if (live) {
     const int4 mt = p.meta[t];
-    if (p.split.prefix_len > 0) {
+    if (whole && p.split.prefix_len > 0) {
       const int npairs = (px_tiles(tokens * p.G) + 1) >> 1;
       const int item = j * npairs + r / (2 * kT5Rows);
       const int2 it = p.items[item];
@@ -724,7 +722,8 @@ prefix_merge_kernel(const __grid_constant__ PxParams p, int tile_rows) {
       for (int e = 0; e < V; ++e) acc[e] *= a;
 #pragma unroll
       for (int x = 0; x < B; ++x) {
-        if (x0 + x < np) {
+        // (not a partial of which the row sees no key: it may hold 0 x NaN)
+        if (ml[x].y != 0.f) {
           const float w = ex2_approx(ml[x].x - mu);
           lsum = fmaf(ml[x].y, w, lsum);
 #pragma unroll
