@@ -880,14 +880,17 @@ pkv_status plan_prefix(int S, int T, int max_q, int prefix_len, int H_q, int H_k
   p.split.max_q = max_q;
   p.split.sms = sms;
   p.split.groups = groups;
-  // SM time, in 10 ns: a tile step of the prefix (1830 cycles), a chunk of own
+  // SM time, in 10 ns: a tile step of the prefix (1.38 us), a chunk of own
   // tokens of hpc KV heads (33,800 of 8 heads of 128 take 304 us on 64 SMs), a
   // sequence's start and end (1024 of one chunk take 2 us each on 3 SMs).
-  // Halving or doubling the prefix's weight costs 2 to 25 %.  With one tile a
-  // KV head both parts wait for HBM: 70 is 3 % better than 90 (8 sequences over
-  // 131072 tokens 90.8 us), with more 90 than 70 (61 x ~2.5 rows over 4112 34.9
-  // us against 37.4).
-  p.split.w1 = D == 64 || p.tile_rows == pkv::kT5Rows ? 70 : 90;
+  // The prefix's weight, swept: with one tile a KV head both parts wait for
+  // HBM (8 x 64 rows over 131072 tokens 99, 97, 98, 103 us with 50, 70, 90,
+  // 110); with more, head_dim 128, 70, 90, 110, 130, 160 give 44.4, 40.9, 38.4,
+  // 37.8, 37.0 (61 x ~2.5 rows over 4112), 428, 364, 357, 357, 356 (1024 over
+  // 2048), 115, 106, 101.5, 98.3, 102.8 (300 over 8192) and 122, 117.5, 110.6,
+  // 111.6, 125.7 us (64 over 32768); head_dim 64 (512 over 8192) 130.7, 123.6,
+  // 119.7, 129.6, 143.8.
+  p.split.w1 = p.tile_rows == pkv::kT5Rows ? 70 : (D == 64 ? 110 : 130);
   p.split.w2 = 35 + 25 * p.hpc * D / 1024;
   p.split.w3 = 180;
   p.own_slots = ((int64_t)p.n_per_group + S) * max_q;

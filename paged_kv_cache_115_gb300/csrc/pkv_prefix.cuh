@@ -67,8 +67,9 @@ struct PxCfg {
   static constexpr int NBAR = 2 * NS + 2 * 3 + 2 * 4 + 1;
   static constexpr int SLOT_OFF = BAR_OFF + 8 * NBAR;
   static constexpr int SMEM = SLOT_OFF + 16 + 1024;
-  // S buffers 0, 1 (128 columns each: fp32 S, then P as bf16 pairs in the
-  // upper 64), O of tile A, O of tile B (128 each)
+  // S buffers 0, 1 (128 columns each: fp32 S, then P as bf16 pairs: of the
+  // lower 64 keys the lo terms, then the hi terms, then of the upper keys), O
+  // of tile A, O of tile B (128 each)
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t IDESC_QK = umma_idesc_bf16(kT5Rows, kPxBN, 0, 0);
   static constexpr uint32_t IDESC_PV = umma_idesc_bf16(kT5Rows, D, 0, 1);
@@ -129,6 +130,17 @@ __device__ __forceinline__ bool px_tile_all(int x, bool ok) {
   return all != 0;
 }
 
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+        "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 // 64 consecutive fp32 columns of this thread's TMEM lane, landed.
 __device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, float (&v)[64]) {
   uint32_t a[32], b[32];
@@ -158,19 +170,20 @@ __device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, float (&v)[64]) {
 //
 // A thread reads S twice: both halves of 64 keys for the row maximum, the
 // upper one kept, then the lower one again, so that 64 scores are live at a
-// time.  P overwrites the upper half of its S buffer (read by then), and the
-// upper keys' product starts while the lower keys' weights are computed.
-// P is rounded to bf16 (to nearest): the tensor cores take both operands of
-// a product in one type, and V is bf16.  The relative error of a weight is at
-// most 2^-8 and independent from key to key, below the rounding of the
-// output; the row sum l adds the unrounded weights in fp32.
+// time.  A half's P overwrites its part of the S buffer (read by then), and
+// the upper keys' product starts while the lower keys' weights are computed.
+// P enters as two bf16 terms, hi + lo (the tensor cores take both operands of
+// a product in one type, and V is bf16): a weight is off by less than 2^-14
+// of itself, where one bf16 term would be off by up to 2^-8, the same for all
+// keys of one weight, as much as the output's own rounding and more where
+// values cancel.  The row sum l adds the weights in fp32.
 // The exponent base of a row is raised only when its maximum grows by more
 // than 2^8, so O is rescaled in TMEM rarely.  Every wait is bounded.
 //
-// On all SMs: 1024 x 32 rows over 16384 tokens (275 GFLOP) 208 us, 1320
-// TFLOP/s, bound by a tile's chain of softmax and products (3600 cycles for
-// two jobs against 3030 of tensor work) and by K and V from L2; 8 x 64 rows
-// over 131072 tokens (537 MB) 82.5 us, 6.5 TB/s, bound by HBM.
+// On all SMs: 1024 x 32 rows over 16384 tokens (275 GFLOP, 412 with the lo
+// terms' products) 297 us, bound by the tensor cores (two jobs take 5150 cycles
+// for 4550 of products; with one term 3600 for 3030, 208 us); 8 x 64 rows over
+// 131072 tokens (537 MB) 84.6 us, 6.3 TB/s, bound by HBM (82.5 with one term).
 // ===========================================================================
 
 // How the steps of all items are dealt to at most n1 CTAs.
@@ -447,7 +460,7 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
           __syncwarp();
           ++jobs[x];
         } else {
-          const uint32_t od = tmem + 256 + x * 128, pt = sd + 64;
+          const uint32_t od = tmem + 256 + x * 128;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {                    // upper keys first
             ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(p_full(b, h), (job >> 1) & 1));
@@ -455,10 +468,11 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-              for (int k4 = 0; k4 < 4; ++k4) {
-                const int k16 = (h ? 0 : 4) + k4;
-                umma_ts(od, pt + k16 * 8, umma_desc_sw128(kv + k16 * 2048, C::KVHALF, 1024),
-                        C::IDESC_PV, (!first || h > 0 || k4 > 0) ? 1u : 0u);
+              for (int i = 0; i < 8; ++i) {                // hi terms, then lo terms
+                const int k4 = i & 3, k16 = (h ? 0 : 4) + k4;
+                umma_ts(od, sd + (h ? 0 : 64) + (i < 4 ? 32 : 0) + k4 * 8,
+                        umma_desc_sw128(kv + k16 * 2048, C::KVHALF, 1024), C::IDESC_PV,
+                        (!first || h > 0 || i > 0) ? 1u : 0u);
               }
               if (h == 1) {
                 umma_commit(o_done(x));
@@ -576,15 +590,20 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h == 1) load(0);
-            uint32_t pk[32];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float2 y = __ffma2_rn(make_float2(xs[2 * c], xs[2 * c + 1]), sl2, nm2);
-              const float2 e2 = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-              s2[c & 1] = __fadd2_rn(s2[c & 1], e2);
-              pk[c] = pack_bf16x2(e2.x, e2.y);
+            for (int d = 0; d < 2; ++d) {                  // 32 keys each
+              uint32_t hi[16], lo[16];
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const int e = 32 * d + 2 * c;
+                const float2 y = __ffma2_rn(make_float2(xs[e], xs[e + 1]), sl2, nm2);
+                const float2 e2 = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                s2[c & 1] = __fadd2_rn(s2[c & 1], e2);
+                split_bf16x2_trunc(e2.x, e2.y, hi[c], lo[c]);
+              }
+              tmem_st16(sd + (h ? 0 : 64) + 32 + 16 * d, hi);
+              tmem_st16(sd + (h ? 0 : 64) + 16 * d, lo);
             }
-            tmem_st32(sd + (h ? 64 : 96), pk);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(p_full(b, h));
