@@ -559,7 +559,9 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
           if (st == 0) {
             m_used = mt == -INFINITY ? 0.f : mt;
           } else {
-            const bool need = mt > m_used + kT5Slack;
+            // (no weight yet: every score so far was -inf, and 0 no base)
+            const bool none = l == 0.f;
+            const bool need = mt > m_used + kT5Slack || (none && mt > -INFINITY);
             if (__any_sync(0xffffffffu, need)) {
               // O in TMEM is rescaled; the O product in front must have landed
               // first (the next one waits for this job's P, so o_done is at
@@ -568,7 +570,7 @@ prefix_tc05_kernel(const __grid_constant__ PxParams p, int tile_rows) {
               if (!ok) break;
               tc_fence_after();
               const float mn = need ? mt : m_used;
-              const float alpha = exp2f(m_used - mn);
+              const float alpha = none ? 0.f : exp2f(m_used - mn);
               l *= alpha;
               m_used = mn;
 #pragma unroll
