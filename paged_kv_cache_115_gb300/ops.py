@@ -714,8 +714,8 @@ def _refuse(t: torch.Tensor, name: str, dtype, dev: int, shape: str) -> None:
 
 def _vec(t: torch.Tensor, name: str, dtype, n: int, dev: int) -> int:
     """Address of a contiguous vector of ``n`` values on device ``dev``."""
-    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, name, dtype, dev, f"contiguous with {n} values")
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, dev, f"contiguous [{n}]")
     return t.data_ptr()
 
 
