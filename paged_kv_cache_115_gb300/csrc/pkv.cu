@@ -953,7 +953,9 @@ pkv_status launch_verify(const pkv::VerifyParams& p, int S, cudaStream_t st) {
   // with 1 and 14.6 with 2; one over 32000 takes 7.4 with 1, 5.7 with 4.
   const int64_t tiles = p.vocab * (int64_t)sizeof(T) / 512;
   int C = 1;
-  while (C < 8 && 2 * S * C <= pkv::kVerifyCtas * sms && tiles >= 2 * C * 3 * pkv::kVerifyWarps) C *= 2;
+  while (C < pkv::kVerifyMaxCluster && 2 * S * C <= pkv::kVerifyCtas * sms &&
+         tiles >= 2 * C * 3 * pkv::kVerifyWarps)
+    C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(S * C));
   cfg.blockDim = dim3(pkv::kVerifyThreads);

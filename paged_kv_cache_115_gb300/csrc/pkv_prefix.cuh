@@ -57,7 +57,6 @@ struct PxCfg {
   static constexpr int OROW = 256;
   static constexpr int KVHALF = kPxBN * 128;              // 16 KiB
   static constexpr int KBYTES = NH * KVHALF;              // one K (or V) tile
-  static constexpr int NBOX = NH * (kPxBN / 16);
   static constexpr int NS = D == 128 ? 5 : 8;             // ring of K and V tiles in turn
   static constexpr int Q_OFF = 0;                         // [tile][half]
   static constexpr int KV_OFF = 2 * QBYTES;

@@ -27,7 +27,7 @@ namespace pkv {
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyCtas = 2;          // resident on an SM
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyMaxCluster = 16;
+constexpr int kVerifyMaxCluster = 8;
 constexpr int kVerifyBatch = 4;         // tiles whose loads of p and q are in flight together
 
 struct VerifyParams {
