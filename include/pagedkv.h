@@ -595,7 +595,7 @@ PKV_API pkv_status pkv_qk_norm_rope_append(
  *            aligned; not shared with a call that overlaps on the GPU.
  * Supported: PKV_BF16, head_dim 64 or 128, block_size 8 or a multiple of 16,
  * max_query_len * num_q_heads / num_kv_heads <= 8, num_seqs <= 2048,
- * 16-byte aligned pools, scale > 0.  Other shapes: pkv_attention_decode and
+ * num_seqs * max_context_len < 2^35, 16-byte aligned pools, scale > 0.  Other shapes: pkv_attention_decode and
  * pkv_attention_prefill read the prefix through each row.
  * Inconsistent counts (n < 0, n > L, cu_seqlens past num_tokens) skip the
  * sequence and record PKV_DEVERR_CONTEXT_LEN.

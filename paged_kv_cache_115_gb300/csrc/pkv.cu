@@ -849,6 +849,9 @@ pkv_status check_prefix(int S, int T, int max_q, int max_len, int prefix_len, in
   PKV_CHECK(S <= pkv::kTcMaxSeqs && H_kv <= 65535, PKV_ERR_UNSUPPORTED, "at most %d sequences",
             pkv::kTcMaxSeqs);
   PKV_CHECK((int64_t)T * H_q < (int64_t(1) << 31), PKV_ERR_UNSUPPORTED, "too many query rows");
+  // (the own parts' chunks are counted in 32 bits)
+  PKV_CHECK((int64_t)S * ceil_div(max_len, pkv::kTile) < (int64_t(1) << 31), PKV_ERR_UNSUPPORTED,
+            "num_seqs x max_context_len must be below 2^35");
   return PKV_OK;
 }
 
