@@ -576,6 +576,9 @@ PKV_API pkv_status pkv_qk_norm_rope_append(
  * requests with one prompt list the same whole blocks).  The same result as
  * pkv_attention_decode (cu_seqlens NULL: one query row a sequence) or
  * pkv_attention_prefill (cu_seqlens: packed new tokens) over the full tables.
+ * Three kernels: it pays from about 1,000 shared tokens on (4 sequences, 32
+ * query heads over 8 KV heads of 128: 14 us against 19 of pkv_attention_decode
+ * at 1024, 14 against 16 at 512, 17 against 9 at 64).
  *   prefix_table: int32 [prefix_len / block_size], the blocks of tokens 0 ..
  *            prefix_len - 1 of every sequence; prefix_len is a multiple of
  *            block_size.  Entries behind the longest sequence are not read.

@@ -953,7 +953,9 @@ pkv_status launch_verify(const pkv::VerifyParams& p, int S, cudaStream_t st) {
   // 512-byte tiles or more.  More cost their own start and exchange: 64
   // sequences over 131072 float32 take 16.6 us with 1 CTA each, 11.1 with 2,
   // 10.4 with 4; 256 take 41.3 with 1, 43.5 with 2; 200 over 32000 take 10.1
-  // with 1 and 14.6 with 2; one over 32000 takes 7.4 with 1, 5.7 with 4.
+  // with 1 and 14.6 with 2; one over 32000 takes 7.4 with 1, 5.7 with 4.  Tiles
+  // of bf16 hold twice the values, so that fewer CTAs may do as well: 61 over
+  // 50021 take 9.6 us with the 4 that this gives and 8.8 with 2 (10.5 with 1).
   const int64_t tiles = p.vocab * (int64_t)sizeof(T) / 512;
   int C = 1;
   while (C < pkv::kVerifyMaxCluster && 2 * S * C <= pkv::kVerifyCtas * sms &&

@@ -894,7 +894,9 @@ def paged_attention_decode_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     :func:`paged_attention_decode` (``cu_seqlens`` None: one query row a
     sequence) or :func:`paged_attention_prefill` (packed new tokens, at most 8
     query rows per KV head) over the full ``block_tables``, whose prefix
-    entries are not read.  The host bounds ``max_query_len`` and
+    entries are not read.  Pays from about 1,000 shared tokens on; sequences
+    that end inside the prefix are answered too, each on its own.  bf16 pools.
+    The host bounds ``max_query_len`` and
     ``max_context_len`` size the launch; ``workspace``: uint8 of
     :func:`prefix_workspace_bytes` bytes (allocated when None)."""
     if out is None:
