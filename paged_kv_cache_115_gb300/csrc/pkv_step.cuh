@@ -336,7 +336,7 @@ step_tokens_kernel(const __grid_constant__ StepParams p) {
     }
   }
   // (16-byte stores where the rows' ends and the arrays allow them)
-  if (t0 + 4 <= p.T && p.wide) {
+  if (t0 <= p.T - 4 && p.wide) {
     *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
     *reinterpret_cast<longlong2*>(p.slots + t0) = make_longlong2(slot[0], slot[1]);
     *reinterpret_cast<longlong2*>(p.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
