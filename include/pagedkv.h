@@ -519,6 +519,7 @@ PKV_API pkv_status pkv_kv_append_varlen(const void* k, const void* v, const int3
  * too small for the blocks given back.  Codes 2 and 3 record PKV_DEVERR_STEP.
  * A free block outside [0, num_blocks) is listed as it is, its tokens get
  * slot -1 and PKV_DEVERR_BLOCK_ID is recorded.
+ * Supported: num_seqs <= 2^30, num_seqs * max_blocks_per_seq < 2^31.
  */
 PKV_API pkv_status pkv_step_tables(const int32_t* lens, const int32_t* counts,
                                    int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -1700,6 +1700,8 @@ pkv_status pkv_step_tables(const int32_t* lens, const int32_t* counts, int32_t* 
   PKV_CHECK((int64_t)max_blocks_per_seq * block_size <= 2147483647 &&
                 (int64_t)num_seqs * max_blocks_per_seq <= 2147483647,
             PKV_ERR_UNSUPPORTED, "table too large");
+  // (the kernels step past the last request by less than that)
+  PKV_CHECK(num_seqs <= (1 << 30), PKV_ERR_UNSUPPORTED, "num_seqs must be at most 2^30");
   PKV_CHECK(num_blocks <= INT64_MAX / block_size, PKV_ERR_INVALID_ARGUMENT, "pool too large");
   PKV_CHECK(ring && ring_state && cu_seqlens && cu_blocks && ring_state_out && totals,
             PKV_ERR_INVALID_ARGUMENT, "null pointer");

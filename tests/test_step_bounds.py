@@ -1,0 +1,11 @@
+"""Sizes past which the step calls' kernels would count beyond 32 bits are
+refused on the host (no GPU is needed; the pointers are never followed)."""
+
+import pytest
+
+from tests.test_step_refusals import UNSUPPORTED, ops, prefix, rope, step, verify  # noqa: F401
+
+
+@pytest.mark.parametrize("S,refused", [(2**30 + 1, True), (2**31 - 1, True), (2**30, False)])
+def test_step_requests(ops, S, refused):  # noqa: F811
+    assert (step(ops, S=S, width=1, K=1, ring_size=0 if not refused else 8) == UNSUPPORTED) is refused
