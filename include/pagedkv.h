@@ -646,7 +646,7 @@ PKV_API pkv_status pkv_attention_decode_prefix_workspace_bytes(
  * A draft outside [0, vocab) is refused (q is taken as 0) and recorded as
  * PKV_DEVERR_DRAFT; so is inconsistent cu_seqlens (outputs -1 and 0) and a
  * drawn row without positive weight (token -1).
- * Supported: 1 <= vocab <= 2^22.
+ * Supported: 1 <= vocab <= 2^22, max_query_len <= 2^30.
  */
 PKV_API pkv_status pkv_verify_draft_tokens(
     const void* target_probs, int64_t target_stride, const void* draft_probs,

@@ -1933,6 +1933,7 @@ pkv_status pkv_verify_draft_tokens(const void* target_probs, int64_t target_stri
                 dtype_ok(prob_dtype),
             PKV_ERR_INVALID_ARGUMENT, "bad verification sizes");
   PKV_CHECK(vocab <= (1 << 22), PKV_ERR_UNSUPPORTED, "vocab must be at most 2^22");
+  PKV_CHECK(max_query_len <= (1 << 30), PKV_ERR_UNSUPPORTED, "max_query_len must be at most 2^30");
   PKV_CHECK(num_seqs <= 2147483647 / pkv::kVerifyMaxCluster, PKV_ERR_UNSUPPORTED,
             "too many sequences");
   if (num_seqs == 0) return PKV_OK;

@@ -9,3 +9,8 @@ from tests.test_step_refusals import UNSUPPORTED, ops, prefix, rope, step, verif
 @pytest.mark.parametrize("S,refused", [(2**30 + 1, True), (2**31 - 1, True), (2**30, False)])
 def test_step_requests(ops, S, refused):  # noqa: F811
     assert (step(ops, S=S, width=1, K=1, ring_size=0 if not refused else 8) == UNSUPPORTED) is refused
+
+
+@pytest.mark.parametrize("rows,refused", [(2**30 + 1, True), (2**31 - 1, True), (2**30, False)])
+def test_verification_rows(ops, rows, refused):  # noqa: F811
+    assert (verify(ops, mq=rows, cu=None) == UNSUPPORTED) is refused
