@@ -560,6 +560,7 @@ PKV_API pkv_status pkv_step_tables(const int32_t* lens, const int32_t* counts,
  * pool skips its write and records PKV_DEVERR_SLOT.  Duplicate slots: which
  * token wins is unspecified.
  * Supported: head_dim even, <= 512; rot_dim even, 0 <= rot_dim <= head_dim;
+ * (num_q_heads + 2 * num_kv_heads) * head_dim < 2^31;
  * num_kv_heads * head_dim <= 8192 for PKV_KV_INT8_TOKEN pools.
  */
 PKV_API pkv_status pkv_qk_norm_rope_append(

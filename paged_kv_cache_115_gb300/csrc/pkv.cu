@@ -1748,7 +1748,7 @@ pkv_status pkv_qk_norm_rope_append(
   PKV_CHECK(head_dim % 2 == 0 && head_dim <= pkv::kRopeMaxDim, PKV_ERR_UNSUPPORTED,
             "head_dim must be even and at most %d", pkv::kRopeMaxDim);
   const int64_t q_row = (int64_t)num_q_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
-  PKV_CHECK(q_row <= 2147483647 && kv_row <= 2147483647, PKV_ERR_UNSUPPORTED, "token row too wide");
+  PKV_CHECK(q_row + 2 * kv_row <= 2147483647, PKV_ERR_UNSUPPORTED, "token row too wide");
   PKV_CHECK(num_blocks <= INT64_MAX / block_size / (4 * kv_row), PKV_ERR_INVALID_ARGUMENT,
             "pool too large");
   if (quant != nullptr) {
