@@ -695,6 +695,13 @@ def _call_on(dev: int, fn, args, what: str) -> None:
         _check(st, what)
 
 
+def _in_32_bits(counts: int) -> None:
+    """Refuses counts (their bits or-ed) that the library's int32 arguments
+    would cut short."""
+    if counts >> 31 not in (0, -1):
+        raise ValueError("sizes must fit 32 bits")
+
+
 def _device_of(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
@@ -785,6 +792,7 @@ def step_tables(lens: torch.Tensor, counts: torch.Tensor, block_tables: torch.Te
     if totals is None:
         totals = new(4, i32)
     R = ring.shape[0]
+    _in_32_bits(S | T | block_size)
     _call_on(dev, _step_tables,
              (_vec(lens, "lens", i32, S, dev), _vec(counts, "counts", i32, S, dev),
               _table(block_tables, "block_tables", i32, S, dev), block_tables.shape[1],
@@ -854,6 +862,7 @@ def paged_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                 if t.shape[0] != nb * K or t.get_device() != dev:
                     raise ValueError("token scales must cover every slot of the pool, on its device")
     far = cos_sin.shape[0]
+    _in_32_bits(T | far)
     _call_on(dev, _rope_append,
              (q.data_ptr(), _token_rows(q, "q", dtype, T, H_q, D, dev),
               k.data_ptr(), _token_rows(k, "k", dtype, T, H_kv, D, dev),
@@ -874,6 +883,7 @@ def prefix_workspace_bytes(num_seqs: int, num_tokens: int, max_query_len: int,
                            num_kv_heads: int, head_dim: int, block_size: int,
                            dtype: torch.dtype) -> int:
     """Workspace bytes of :func:`paged_attention_decode_prefix`."""
+    _in_32_bits(num_seqs | num_tokens | max_query_len | max_context_len | prefix_len)
     out = c_sz(0)
     code = PKV_BF16 if dtype == torch.bfloat16 else PKV_F32
     _check(_prefix_ws(num_seqs, num_tokens, max_query_len, max_context_len, prefix_len,
@@ -918,6 +928,7 @@ def paged_attention_decode_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cach
                                        H_kv, D, K, dtype), 256), dtype=torch.uint8,
             device=q.device)
     ws_bytes = workspace.shape[0]
+    _in_32_bits(S | T | prefix_len | max_query_len | max_context_len)
     _call_on(dev, _prefix,
              (_whole(q, "q", dtype, q.shape, dev), kp, vp,
               _vec(prefix_table, "prefix_table", i32, listed, dev), prefix_len,
@@ -961,6 +972,7 @@ def verify_draft_tokens(target_probs: torch.Tensor, draft_probs: Optional[torch.
         if one != 1 and V > 1:
             raise ValueError("draft_probs: a row must be contiguous")
         dp = draft_probs.data_ptr()
+    _in_32_bits(S | T | max_query_len | V)
     _call_on(dev, _verify,
              (target_probs.data_ptr(), ts if T > 1 else V, dp, ds, dt,
               _vec(tokens, "tokens", i32, T, dev), _vec(uniforms, "uniforms", torch.float32, T, dev),
