@@ -20,7 +20,9 @@ section:
   (logical block, offset and token-slot formulas and the worked K=4 example).
 
 Submodules: ``oracle.quant`` (FP8 e4m3 / INT8 per-token KV formats, pinned in
-``tests/test_oracle_quant_pins.py``), ``oracle.prefill`` (multi-query
+``tests/test_oracle_quant_pins.py``; INT4 per token and head, pinned in
+``tests/test_oracle_beam_pins.py``), ``oracle.beam`` (beam selection, forks of
+block tables, pinned there too), ``oracle.prefill`` (multi-query
 attention of several new tokens per sequence, pinned in
 ``tests/test_oracle_prefill_pins.py``) and ``oracle.step`` (block tables from
 lengths, head norms + rotation, draft verification, pinned in

@@ -128,6 +128,45 @@ def bf16_encode(x: np.ndarray) -> np.ndarray:
     return np.where(nan, quiet, rounded).astype(np.uint16)
 
 
+def int4_quantize(rows: np.ndarray):
+    """Head rows (float32 values [..., D]) -> (4-bit codes uint8 [..., D], scale,
+    offset), the last two as bfloat16 bit patterns [...]: offset = min rounded
+    down, scale = (max - offset) / 15 rounded to nearest, code = (x - offset) *
+    (1 / scale) rounded half to even and clamped to 0 .. 15, float32 throughout;
+    NaN patterns and codes 0 for a row that is not finite."""
+    r = np.asarray(rows, dtype=np.float32)
+    with np.errstate(all="ignore"):
+        u = r.min(-1).view(np.uint32)
+        z16 = u >> np.uint32(16)
+        # a negative value is cut towards zero: one further down
+        z16 = z16 + (((u & np.uint32(0xFFFF)) != 0) & (u >> np.uint32(31) != 0)).astype(np.uint32)
+        z = (z16 << np.uint32(16)).view(np.float32)
+        s16 = bf16_encode((r.max(-1) - z) / np.float32(15)).astype(np.uint32)
+        s = (s16 << np.uint32(16)).view(np.float32)
+        inv = np.where(s >= np.float32(2.0 ** -126), np.float32(1) / s, np.float32(0))
+        c = np.clip(np.rint((r - z[..., None]) * inv[..., None]), 0, 15)
+        bad = ~np.isfinite(r).all(-1) | ~np.isfinite(z) | ~np.isfinite(s)
+        c = np.where(bad[..., None], 0, c).astype(np.uint8)
+    nan = np.uint16(0x7FFF)
+    return (c, np.where(bad, nan, s16).astype(np.uint16), np.where(bad, nan, z16).astype(np.uint16))
+
+
+def int4_pack(codes: np.ndarray) -> np.ndarray:
+    """Codes [..., D] -> bytes [..., D / 2], element 2 i in the low half."""
+    return (codes[..., 0::2] | (codes[..., 1::2] << 4)).astype(np.uint8)
+
+
+def int4_decode(pool: np.ndarray, scales: np.ndarray, slots, kv_head: int) -> np.ndarray:
+    """float64 values of the rows at ``slots`` of one KV head: ``pool`` bytes
+    [nb, K, H, D / 2], ``scales`` bfloat16 bit patterns [nb, H, K, 2]."""
+    slots = np.asarray(slots, np.int64)
+    K = pool.shape[1]
+    b = pool[slots // K, slots % K, kv_head]
+    codes = np.stack([b & 15, b >> 4], -1).reshape(len(slots), -1).astype(np.float64)
+    w = (scales[slots // K, kv_head, slots % K].astype(np.uint32) << np.uint32(16)).view(np.float32)
+    return w[:, 1:].astype(np.float64) + w[:, :1].astype(np.float64) * codes
+
+
 # --------------------------------------------------------------------------
 # quantized KV write and attention over a quantized pool
 # --------------------------------------------------------------------------
@@ -180,6 +219,40 @@ def kv_write_k16v8(k_pool, v_pool, k_rows, v_rows, slots, v_scale):
         kf[s] = bf16_encode(np.asarray(k_rows[i], np.float32))
         vf[s] = e4m3_encode(np.asarray(v_rows[i], np.float32) / vs)
     return kp, vp
+
+
+def kv_write_int4(k_pool, v_pool, k_scales, v_scales, k_rows, v_rows, slots):
+    """INT4 pools (bytes [nb, K, H, D / 2]) and scales (bfloat16 bit patterns
+    [nb, H, K, 2]) after storing token i's rows (float32 [T, H, D]) at slots[i]."""
+    out = [np.array(a) for a in (k_pool, v_pool, k_scales, v_scales)]
+    K = k_pool.shape[1]
+    slots = np.asarray(slots)
+    at = slots[slots >= 0]
+    for pool, scales, rows in ((out[0], out[2], k_rows), (out[1], out[3], v_rows)):
+        c, s, z = int4_quantize(rows[slots >= 0])
+        pool[at // K, at % K] = int4_pack(c)
+        scales[at // K, :, at % K, 0], scales[at // K, :, at % K, 1] = s, z
+    return tuple(out)
+
+
+def paged_attention_decode_int4(q, k_pool, v_pool, k_scales, v_scales, block_tables, context_lens,
+                                scale, q_dtype):
+    """Decode attention over a 4-bit pool: gather through the block table,
+    offset + code * scale in float64, then the dense definition."""
+    from .paged_attention import decode, dense_attention
+    S, H_q, D = q.shape
+    H_kv, K = k_pool.shape[2], k_pool.shape[1]
+    G = H_q // H_kv
+    q64 = decode(q, q_dtype)
+    out = np.zeros((S, H_q, D))
+    for s in range(S):
+        t = np.arange(int(context_lens[s]), dtype=np.int64)
+        slots = np.asarray(block_tables[s], np.int64)[t // K] * K + t % K
+        for j in range(H_kv):
+            Kj, Vj = (int4_decode(p, w, slots, j) for p, w in ((k_pool, k_scales), (v_pool, v_scales)))
+            for h in range(j * G, (j + 1) * G):
+                out[s, h] = dense_attention(q64[s, h], Kj, Vj, scale)
+    return out
 
 
 def dequantize_rows(pool, rows_slot, kv_head, fmt, tensor_scale=None, tok_scales=None):
