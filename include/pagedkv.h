@@ -72,10 +72,13 @@ enum {
                                   table row (the length is clamped)                  */
   PKV_DEVERR_POSITION = 5,     /* position beyond the block-table row                */
   PKV_DEVERR_TIMEOUT = 6,      /* a pipeline wait gave up after about a second       */
-  PKV_DEVERR_STEP = 7,         /* pkv_step_tables refused the step (totals[0] says why) */
-  PKV_DEVERR_DRAFT = 8         /* pkv_verify_draft_tokens: draft token outside the
+  PKV_DEVERR_STEP = 7,         /* pkv_step_tables or pkv_fork_tables refused the step
+                                  (totals[0] says why)                               */
+  PKV_DEVERR_DRAFT = 8,        /* pkv_verify_draft_tokens: draft token outside the
                                   vocabulary, inconsistent cu_seqlens, or a row of
                                   probabilities without any positive value           */
+  PKV_DEVERR_BEAM = 9          /* pkv_beam_select: a row of logits with a NaN or
+                                  +infinity                                          */
 };
 
 /* Human-readable name of a status.  Never NULL. */
@@ -272,7 +275,7 @@ PKV_API pkv_status pkv_attention_decode_noalloc(
 PKV_API pkv_status pkv_selftest_wait_timeout(int64_t limit_cycles, void* stream);
 
 /*
- * Quantized KV cache (one byte per element).
+ * Quantized KV cache (one byte per element, or half a byte).
  *
  * "学习大模型推理的显存优化", section KV Cache 量化: FP8 e4m3 (1 sign, 4
  * exponent, 3 mantissa bits, largest value 448); values are stored divided by
@@ -297,20 +300,32 @@ PKV_API pkv_status pkv_selftest_wait_timeout(int64_t limit_cycles, void* stream)
  *   the V pool e4m3 codes of x / v_scale as in PKV_KV_FP8_E4M3 (k_scale is
  *   not used).  The tensor-core kernel needs a block size that is a multiple
  *   of 16; other shapes use the CUDA-core kernel.
+ * PKV_KV_INT4_HEAD: pools hold two 4-bit codes a byte ([num_blocks,
+ *   block_size, num_kv_heads, head_dim / 2] bytes, element 2 i in the low half
+ *   of byte i); every token slot and KV head has its own bf16 scale s and bf16
+ *   offset z, over the head's head_dim values x: z = min x rounded down to
+ *   bf16, s = bf16((max x - z) / 15), code = clamp(round_half_even((x - z) *
+ *   (1 / s)), 0, 15), each step in float32 (1 / s taken as 0 for s < 2^-126);
+ *   read back as z + s * code, within 0.57 s of x.  A row with a NaN or an
+ *   infinity (or whose z or s overflows) gets s = z = NaN and reads as NaN.
+ *   head_dim 64 or 128.
  */
 typedef enum {
   PKV_KV_PLAIN = 0,
   PKV_KV_FP8_E4M3 = 1,
   PKV_KV_INT8_TOKEN = 2,
-  PKV_KV_BF16K_FP8V = 3
+  PKV_KV_BF16K_FP8V = 3,
+  PKV_KV_INT4_HEAD = 4
 } pkv_kv_format;
 
 typedef struct {
   int32_t format;          /* pkv_kv_format */
   float k_scale;           /* FP8: scale of the K pool (must be finite and > 0) */
   float v_scale;           /* FP8: scale of the V pool */
-  float* k_token_scales;   /* INT8: [num_blocks * block_size] device floats */
-  float* v_token_scales;   /* INT8: [num_blocks * block_size] device floats */
+  float* k_token_scales;   /* INT8: [num_blocks * block_size] device floats;
+                              INT4: [num_blocks, num_kv_heads, block_size] words,
+                              {bf16 scale, bf16 offset} each                    */
+  float* v_token_scales;   /* the same for V                                    */
 } pkv_kv_quant;
 
 /*
@@ -327,8 +342,24 @@ PKV_API pkv_status pkv_kv_append_quant(const void* k, const void* v, const int32
                                        int64_t* slot_mapping_out, void* stream);
 
 /*
- * a5 on a quantized pool: copies the byte blocks of K and V and, for INT8,
- * the blocks' per-token scales (so a copy is bit-exact in codes and scales).
+ * a2 into a quantized pool: as pkv_kv_append_quant, at given slots (int64
+ * [num_tokens], as pkv_step_tables makes them; -1 skips the token, another slot
+ * outside the pool skips it and records PKV_DEVERR_SLOT).  k, v: [num_tokens,
+ * num_kv_heads, head_dim] with their own distance between tokens (elements;
+ * heads and values contiguous), so that they can be cut out of one projection's
+ * output.  Duplicate slots: which token wins is unspecified.
+ * Supported for INT4: num_tokens * num_kv_heads < 2^30 - 256.
+ */
+PKV_API pkv_status pkv_kv_write_quant(const void* k, int64_t k_stride, const void* v,
+                                      int64_t v_stride, const int64_t* slots, int32_t num_tokens,
+                                      void* k_cache, void* v_cache, int64_t num_blocks,
+                                      int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                                      pkv_dtype in_dtype, const pkv_kv_quant* quant,
+                                      void* stream);
+
+/*
+ * a5 on a quantized pool: copies the byte blocks of K and V and, for INT8 and
+ * INT4, the blocks' scales (so a copy is bit-exact in codes and scales).
  */
 PKV_API pkv_status pkv_kv_block_copy_quant(void* k_cache, void* v_cache,
                                            const int64_t* src_dst_pairs, int64_t num_pairs,
@@ -655,6 +686,120 @@ PKV_API pkv_status pkv_verify_draft_tokens(
     const float* uniforms, const int32_t* cu_seqlens, int32_t num_seqs, int32_t num_tokens,
     int32_t max_query_len, int32_t vocab, int32_t* out_tokens, int32_t* num_new,
     pkv_dtype prob_dtype, void* stream);
+
+/*
+ * Selection of beam search: the best candidates over a request's beams and the
+ * vocabulary.  With row = r * num_beams + b of the logits,
+ *   candidate (b, v) = scores[r][b] + logits[row][v]
+ *                      - log sum_v' exp(logits[row][v']),
+ * in descending order; equal ones go to the lowest b * vocab + v.  Sums and
+ * candidates are joined in 64 bits (terms of the sum in float32).  A finished
+ * beam has one candidate: eos_token at its score as it is; its logits are not
+ * read.  Candidates of -infinity (a logit or score of -infinity) are none: a
+ * first step gives every beam but one the score -infinity, or num_beams = 1
+ * and num_select = the beams wanted; a mask is -infinity in the logits.
+ *   logits:   [num_requests * num_beams, vocab], logits_stride elements between
+ *             rows (any alignment); dtype.  Values at the type's lowest are
+ *             values.  A row with a NaN or +infinity has no candidates and
+ *             records PKV_DEVERR_BEAM.
+ *   scores:   float32 [num_requests, num_beams]; finished: one byte each, or
+ *             NULL.  A NaN or +infinity counts as -infinity.
+ *   eos_token: -1 (none) or a token; needed with `finished`.
+ * Outputs, [num_requests, num_select]: tokens, parents (int32: the beam within
+ * the request, as pkv_fork_tables reads it), scores_out (float32), finished_out
+ * (a byte, may be NULL): the parent was finished or the token is eos_token.
+ * Places without a candidate: token -1, parent -1, score -infinity, finished 1.
+ * num_select = 2 * num_beams serves schemes that put finished ones aside.
+ *   workspace: pkv_beam_select_workspace_bytes bytes, 256-byte aligned; not
+ *             shared with a call that overlaps on the GPU.
+ * Supported: num_beams <= 32, num_select <= 32, vocab <= 2^22.
+ */
+PKV_API pkv_status pkv_beam_select(const void* logits, int64_t logits_stride, const float* scores,
+                                   const uint8_t* finished, int32_t num_requests,
+                                   int32_t num_beams, int32_t vocab, int32_t num_select,
+                                   int32_t eos_token, int32_t* tokens, int32_t* parents,
+                                   float* scores_out, uint8_t* finished_out, void* workspace,
+                                   size_t workspace_bytes, pkv_dtype dtype, void* stream);
+
+/* Workspace bytes of pkv_beam_select for these sizes. */
+PKV_API pkv_status pkv_beam_select_workspace_bytes(int32_t num_requests, int32_t num_beams,
+                                                   int32_t vocab, int32_t num_select,
+                                                   size_t* bytes);
+
+/*
+ * Forks of block tables ("19.2 KV Cache 系统化管理" §19.2.2, 写时复制: samples of
+ * one request share its blocks until one of them writes): every row of a group
+ * (the beams of a request) continues a row of the same group, or none.
+ *   parents: int32 [num_groups, group_rows], the row of the group that is
+ *            continued, -1: the row is empty from now on.
+ *   lens:    int32 [num_groups * group_rows], cached tokens of each row.
+ *   held:    int32, listed blocks of each row; lens <= held * block_size.
+ *   shared:  int32 or NULL (0): leading entries of a row that rows outside the
+ *            group list too; they are passed on and never given back.
+ *   block_tables: int32 [num_groups * group_rows, max_blocks_per_seq].  Within
+ *            a group a block stands at the same entry of every row that lists
+ *            it, as it does in rows that came from one another by this call;
+ *            behind `shared` no other group lists it.  A partly filled block
+ *            and unused ones behind it belong to one row.
+ *   ring, ring_state: the free blocks, as in pkv_step_tables.
+ * The first row that continues a parent lists all its entries; the others list
+ * its full blocks and, where lens is not a multiple of block_size, a fresh block
+ * from the ring's head in place of the partly filled one (in the order of the
+ * rows).  Old blocks that no row of the group lists any more go to the ring's
+ * tail, each once, by group, then entry, then row.  A block given back in this
+ * call is not taken in it.
+ * Outputs:
+ *   block_tables_out: as block_tables, and may be it; entries of the new rows
+ *            are filled, all others stay as they are.
+ *   lens_out, held_out (may be lens, held): of the new rows, 0 for empty ones;
+ *            ring_state_out (may be ring_state).
+ *   pairs:   int64 [num_groups * group_rows, 2]: the block to copy and the
+ *            fresh block of each row, -1 -1: none (pkv_kv_fork_copy).
+ *   totals:  int32 [4] = {code, rows that are not empty, blocks taken, blocks
+ *            given back}.
+ * All or nothing, codes as pkv_step_tables: 0 = done; 1 = not enough free
+ * blocks; 3 = an invalid parent, length, held, shared or ring_state, or a ring
+ * too small for the blocks given back (records PKV_DEVERR_STEP; the blocks of
+ * groups with an invalid row are not counted).  With a code the tables, lens,
+ * held and ring_state stay (are repeated), pairs are -1.
+ * A finished request leaves by parents of -1 (pkv_step_tables would give its
+ * rows' shared blocks back once for each row).
+ *   workspace: pkv_fork_tables_workspace_bytes bytes, 256-byte aligned; not
+ *            shared with a call that overlaps on the GPU.
+ * Supported: group_rows <= 32, num_groups * group_rows * max_blocks_per_seq <
+ * 2^31.
+ */
+PKV_API pkv_status pkv_fork_tables(const int32_t* parents, const int32_t* lens,
+                                   const int32_t* held, const int32_t* shared,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   int32_t* ring, int64_t ring_size, const int64_t* ring_state,
+                                   int32_t num_groups, int32_t group_rows, int32_t block_size,
+                                   int32_t* block_tables_out, int32_t* lens_out,
+                                   int32_t* held_out, int64_t* ring_state_out, int64_t* pairs,
+                                   int32_t* totals, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* Workspace bytes of pkv_fork_tables for these sizes. */
+PKV_API pkv_status pkv_fork_tables_workspace_bytes(int32_t num_groups, int32_t group_rows,
+                                                   int32_t max_blocks_per_seq, size_t* bytes);
+
+/*
+ * The copies of a fork: for each row i with pairs[i] != (-1, -1) the leading
+ * lens[i] % block_size tokens of block pairs[i][0] to block pairs[i][1] (K and
+ * V, codes and scales alike), in every layer; the rest of the block stays.
+ * Takes pairs and lens as pkv_fork_tables leaves them (lens_out), so that no
+ * count goes through the host.
+ *   k_cache, v_cache: num_layers pools one behind the other ([num_layers,
+ *            num_blocks, ...]); the scale arrays of `quant` likewise.
+ *   dtype: type of plain pools (quant NULL).
+ * Pairs outside the pool are skipped and record PKV_DEVERR_COPY_PAIR.  A block
+ * that is a destination twice, or source and destination, is unspecified.
+ */
+PKV_API pkv_status pkv_kv_fork_copy(void* k_cache, void* v_cache, const int64_t* pairs,
+                                    const int32_t* lens, int32_t num_rows, int32_t num_layers,
+                                    int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                                    int32_t head_dim, pkv_dtype dtype, const pkv_kv_quant* quant,
+                                    void* stream);
 
 /*
  * Synchronises `stream`, copies the current device's error word into *code

@@ -162,7 +162,7 @@ def int4_decode(pool: np.ndarray, scales: np.ndarray, slots, kv_head: int) -> np
     slots = np.asarray(slots, np.int64)
     K = pool.shape[1]
     b = pool[slots // K, slots % K, kv_head]
-    codes = np.stack([b & 15, b >> 4], -1).reshape(len(slots), -1).astype(np.float64)
+    codes = np.stack([b & 15, b >> 4], -1).reshape(len(slots), 2 * pool.shape[3]).astype(np.float64)
     w = (scales[slots // K, kv_head, slots % K].astype(np.uint32) << np.uint32(16)).view(np.float32)
     return w[:, 1:].astype(np.float64) + w[:, :1].astype(np.float64) * codes
 

@@ -11,6 +11,7 @@
 #include <mutex>
 #include <string>
 
+#include "pkv_int4.cuh"
 #include "pkv_attention_simt.cuh"
 #include "pkv_attention_tc.cuh"
 #include "pkv_prefill.cuh"
@@ -21,6 +22,8 @@
 #include "pkv_rope.cuh"
 #include "pkv_step.cuh"
 #include "pkv_verify.cuh"
+#include "pkv_beam.cuh"
+#include "pkv_fork.cuh"
 #include "pkv_copy.cuh"
 #include "pkv_device.cuh"
 
@@ -255,7 +258,7 @@ pkv_status plan_attention_quant(int S, int H_q, int H_kv, int D, int K, int max_
   PKV_CHECK(D == 64 || D == 128, PKV_ERR_UNSUPPORTED, "quantized pools need head_dim 64 or 128");
   PKV_CHECK(H_q > 0 && H_kv > 0 && H_q % H_kv == 0, PKV_ERR_INVALID_ARGUMENT,
             "num_q_heads %% num_kv_heads != 0");
-  bool scales_ok = true;
+  bool scales_ok = quant->format != PKV_KV_INT4_HEAD;
   if (quant->format == PKV_KV_INT8_TOKEN && quant->k_token_scales && quant->v_token_scales)
     scales_ok = aligned(quant->k_token_scales, 16) && aligned(quant->v_token_scales, 16);
   const bool tc_ok = q_dt == PKV_BF16 && D == 128 && tc_shape_ok(H_q / H_kv, D, K, num_blocks,
@@ -611,6 +614,12 @@ pkv_status launch_simt_typed(const pkv_kv_quant* quant, int D, const void* q, co
     return launch_simt_q<T>(D, q, pkv::KvBf16Fp8{static_cast<const __nv_bfloat16*>(kc),
                                                   static_cast<const uint8_t*>(vc),
                                                   quant->v_scale}, out, a, st);
+  if (quant->format == PKV_KV_INT4_HEAD)
+    return launch_simt_q<T>(D, q, pkv::KvInt4{static_cast<const uint8_t*>(kc),
+                                               static_cast<const uint8_t*>(vc),
+                                               reinterpret_cast<const uint32_t*>(quant->k_token_scales),
+                                               reinterpret_cast<const uint32_t*>(quant->v_token_scales)},
+                            out, a, st);
   return launch_simt_q<T>(D, q, pkv::KvInt8{static_cast<const int8_t*>(kc),
                                              static_cast<const int8_t*>(vc),
                                              quant->k_token_scales, quant->v_token_scales},
@@ -718,12 +727,13 @@ pkv_status device_view(const void* p, const char* what, const void** out) {
   }
 }
 
-// Validates a quantized-pool description (token scales required for INT8).
+// Validates a quantized-pool description (scale arrays required for INT8 and INT4).
 pkv_status check_quant(const pkv_kv_quant* q, bool need_token_scales) {
   PKV_CHECK(q != nullptr, PKV_ERR_INVALID_ARGUMENT, "null quant description");
   PKV_CHECK(q->format == PKV_KV_FP8_E4M3 || q->format == PKV_KV_INT8_TOKEN ||
-                q->format == PKV_KV_BF16K_FP8V,
-            PKV_ERR_INVALID_ARGUMENT, "quant format must be FP8_E4M3, INT8_TOKEN or BF16K_FP8V");
+                q->format == PKV_KV_BF16K_FP8V || q->format == PKV_KV_INT4_HEAD,
+            PKV_ERR_INVALID_ARGUMENT,
+            "quant format must be FP8_E4M3, INT8_TOKEN, BF16K_FP8V or INT4_HEAD");
   if (q->format == PKV_KV_FP8_E4M3) {
     PKV_CHECK(std::isfinite(q->k_scale) && std::isfinite(q->v_scale) && q->k_scale > 0.f &&
                   q->v_scale > 0.f,
@@ -733,11 +743,169 @@ pkv_status check_quant(const pkv_kv_quant* q, bool need_token_scales) {
               "the FP8 V scale must be finite and > 0");
   } else if (need_token_scales) {
     PKV_CHECK(q->k_token_scales && q->v_token_scales, PKV_ERR_INVALID_ARGUMENT,
-              "INT8 pools need per-token scale arrays");
+              "INT8 and INT4 pools need scale arrays");
     PKV_CHECK(aligned(q->k_token_scales, 4) && aligned(q->v_token_scales, 4),
               PKV_ERR_INVALID_ARGUMENT, "misaligned token scales");
   }
   return PKV_OK;
+}
+
+// ---- quantizing writes ----------------------------------------------------------
+template <typename TIN, int D>
+pkv_status launch_write_int4(const pkv::Int4WriteParams& p, cudaStream_t st) {
+  constexpr int RPI = pkv::kInt4Threads / (D / (16 / (int)sizeof(TIN)));
+  const bool wide = aligned(p.k, 16) && aligned(p.v, 16) && p.k_stride % (16 / sizeof(TIN)) == 0 &&
+                    p.v_stride % (16 / sizeof(TIN)) == 0;
+  int dev, sms;
+  pkv_status s = device_facts(&dev, &sms);
+  if (s != PKV_OK) return s;
+  const int64_t rows = (int64_t)p.T * 2 * p.H;
+  const int64_t ctas = ceil_div(rows, RPI);
+  const dim3 block(pkv::kInt4Threads);
+  if (!wide) {
+    PKV_CUDA(launch_pdl(pkv::kv_write_int4_kernel<TIN, D, 1, false>, dim3((unsigned)ctas), block, 0,
+                        st, p));
+  } else if (ctas >= 8 * sms) {
+    PKV_CUDA(launch_pdl(pkv::kv_write_int4_kernel<TIN, D, 4, true>,
+                        dim3((unsigned)ceil_div(rows, 4 * RPI)), block, 0, st, p));
+  } else {
+    PKV_CUDA(launch_pdl(pkv::kv_write_int4_kernel<TIN, D, 1, true>, dim3((unsigned)ctas), block, 0,
+                        st, p));
+  }
+  return PKV_OK;
+}
+
+// What a 4-bit pool needs: head_dim, codes on 4-byte boundaries.
+pkv_status check_int4(const void* k_cache, const void* v_cache, int D) {
+  PKV_CHECK(D == 64 || D == 128, PKV_ERR_UNSUPPORTED, "INT4 pools need head_dim 64 or 128");
+  PKV_CHECK(aligned(k_cache, 4) && aligned(v_cache, 4), PKV_ERR_INVALID_ARGUMENT,
+            "INT4 pools must be 4-byte aligned");
+  return PKV_OK;
+}
+
+// New rows to the slots of positions and tables, or (slots not null) to slots.
+pkv_status write_quant(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                       const int64_t* slots, const int32_t* block_tables, int32_t max_blocks,
+                       const int32_t* positions, int32_t num_tokens, void* k_cache, void* v_cache,
+                       int64_t num_blocks, int32_t block_size, int32_t H, int32_t D,
+                       pkv_dtype in_dtype, const pkv_kv_quant* quant, int64_t* slots_out,
+                       cudaStream_t strm) {
+  PKV_CHECK(num_blocks <= INT64_MAX / block_size, PKV_ERR_INVALID_ARGUMENT, "pool too large");
+  PKV_CHECK(aligned(k, elem_bytes(in_dtype)) && aligned(v, elem_bytes(in_dtype)),
+            PKV_ERR_INVALID_ARGUMENT, "misaligned k/v");
+  const int l2 = log2_exact(block_size);
+  if (quant->format == PKV_KV_INT4_HEAD) {
+    pkv_status st = check_int4(k_cache, v_cache, D);
+    if (st != PKV_OK) return st;
+    PKV_CHECK((int64_t)num_tokens * H < (int64_t(1) << 30) - 256, PKV_ERR_UNSUPPORTED,
+              "num_tokens x num_kv_heads must be below 2^30 - 256");
+    PKV_CHECK(num_blocks <= INT64_MAX / block_size / ((int64_t)H * D), PKV_ERR_INVALID_ARGUMENT,
+              "pool too large");
+    pkv::Int4WriteParams p = {};
+    p.k = k; p.v = v; p.k_stride = k_stride; p.v_stride = v_stride;
+    p.slots = slots; p.positions = positions; p.block_tables = block_tables;
+    p.slots_out = slots_out;
+    p.k_cache = static_cast<uint8_t*>(k_cache);
+    p.v_cache = static_cast<uint8_t*>(v_cache);
+    p.k_words = reinterpret_cast<uint32_t*>(quant->k_token_scales);
+    p.v_words = reinterpret_cast<uint32_t*>(quant->v_token_scales);
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks; p.block_size = block_size; p.log2_bs = l2;
+    p.T = num_tokens; p.H = H;
+    if (in_dtype == PKV_BF16)
+      return D == 64 ? launch_write_int4<__nv_bfloat16, 64>(p, strm)
+                     : launch_write_int4<__nv_bfloat16, 128>(p, strm);
+    return D == 64 ? launch_write_int4<float, 64>(p, strm) : launch_write_int4<float, 128>(p, strm);
+  }
+  const int64_t row = (int64_t)H * D;
+  dim3 grid((unsigned)num_tokens, 2);
+  dim3 block(pkv::kQuantThreads);
+  auto* kc = static_cast<uint8_t*>(k_cache);
+  auto* vc = static_cast<uint8_t*>(v_cache);
+  const float ks = quant->k_scale, vs = quant->v_scale;
+  float* kts = quant->k_token_scales;
+  float* vts = quant->v_token_scales;
+#define PKV_LAUNCH_AQ(TIN, FMT)                                                               \
+  PKV_CUDA(launch_pdl(pkv::kv_append_quant_kernel<TIN, FMT>, grid, block, 0, strm,            \
+                      static_cast<const TIN*>(k), static_cast<const TIN*>(v), block_tables,   \
+                      max_blocks, positions, block_size, l2, num_blocks, kc, vc, row, ks, vs, \
+                      kts, vts, slots_out, slots, k_stride, v_stride))
+  if (quant->format == PKV_KV_FP8_E4M3) {
+    if (in_dtype == PKV_BF16) PKV_LAUNCH_AQ(__nv_bfloat16, 1); else PKV_LAUNCH_AQ(float, 1);
+  } else if (quant->format == PKV_KV_BF16K_FP8V) {
+    PKV_CHECK(aligned(k_cache, 2), PKV_ERR_INVALID_ARGUMENT, "misaligned bf16 K pool");
+    if (in_dtype == PKV_BF16) PKV_LAUNCH_AQ(__nv_bfloat16, 3); else PKV_LAUNCH_AQ(float, 3);
+  } else {
+    if (in_dtype == PKV_BF16) PKV_LAUNCH_AQ(__nv_bfloat16, 2); else PKV_LAUNCH_AQ(float, 2);
+  }
+#undef PKV_LAUNCH_AQ
+  return PKV_OK;
+}
+
+// ---- beam selection dispatch ------------------------------------------------------
+// Values a thread: 64 where that fills the SMs twice over, else 16, so that a few
+// rows still spread over the machine.
+constexpr int kBeamWide = 64, kBeamNarrow = 16;
+int beam_tiles(int64_t V, int ept) {
+  return (int)ceil_div(V + 7, (int64_t)pkv::kBeamThreads * ept);
+}
+int beam_ept(int64_t rows, int64_t V, int sms) {
+  return rows * beam_tiles(V, kBeamWide) >= 2 * sms ? kBeamWide : kBeamNarrow;
+}
+
+struct BeamWs {
+  size_t x, v, total;          // tile_ms first
+};
+BeamWs beam_ws(int64_t rows, int tiles, int N) {
+  BeamWs w;
+  w.x = align256((size_t)(rows * tiles) * sizeof(float2));
+  w.v = w.x + align256((size_t)(rows * tiles) * N * sizeof(float));
+  w.total = w.v + align256((size_t)(rows * tiles) * N * sizeof(int32_t));
+  return w;
+}
+
+pkv_status check_beam(int R, int B, int V, int N) {
+  PKV_CHECK(R >= 0 && B >= 1 && V >= 1 && N >= 1, PKV_ERR_INVALID_ARGUMENT, "bad beam sizes");
+  PKV_CHECK(B <= pkv::kBeamMax && N <= pkv::kBeamMax && V <= (1 << 22), PKV_ERR_UNSUPPORTED,
+            "beam selection takes at most %d beams, %d candidates and a vocabulary of 2^22",
+            pkv::kBeamMax, pkv::kBeamMax);
+  PKV_CHECK((int64_t)R * B * beam_tiles(V, kBeamNarrow) <= 2147483647, PKV_ERR_UNSUPPORTED,
+            "too many rows");
+  return PKV_OK;
+}
+
+template <typename T>
+pkv_status launch_beam(const pkv::BeamParams& p, int ept, cudaStream_t st) {
+  const dim3 grid((unsigned)((int64_t)p.R * p.B * p.tiles)), block(pkv::kBeamThreads);
+  if (ept == kBeamWide)
+    PKV_CUDA(launch_pdl(pkv::beam_tiles_kernel<T, kBeamWide>, grid, block, 0, st, p));
+  else
+    PKV_CUDA(launch_pdl(pkv::beam_tiles_kernel<T, kBeamNarrow>, grid, block, 0, st, p));
+  PKV_CUDA(launch_pdl(pkv::beam_pick_kernel, dim3((unsigned)p.R), block, 0, st, p));
+  return PKV_OK;
+}
+
+// ---- forks ----------------------------------------------------------------------
+pkv_status check_fork(int R, int B, int width) {
+  PKV_CHECK(R >= 0 && B >= 1 && width >= 1, PKV_ERR_INVALID_ARGUMENT, "bad fork sizes");
+  PKV_CHECK(B <= pkv::kForkMaxRows, PKV_ERR_UNSUPPORTED, "at most %d rows a group",
+            pkv::kForkMaxRows);
+  PKV_CHECK((int64_t)R * B <= 2147483647 && (int64_t)R * B * width <= 2147483647 &&
+                ceil_div(width, pkv::kForkThreads) <= 65535,
+            PKV_ERR_UNSUPPORTED, "table too large");
+  return PKV_OK;
+}
+
+struct ForkWs {
+  size_t group, row, give, total;        // the ring's state first
+};
+ForkWs fork_ws(int64_t R, int B, int chunks) {
+  ForkWs w;
+  w.group = 256;
+  w.row = w.group + align256((size_t)R * sizeof(int4));
+  w.give = w.row + align256((size_t)R * B * sizeof(int4));
+  w.total = w.give + align256((size_t)R * chunks * sizeof(int32_t));
+  return w;
 }
 
 // ---- norm + rotation + append dispatch -------------------------------------------
@@ -1178,34 +1346,31 @@ pkv_status pkv_kv_append_quant(const void* k, const void* v, const int32_t* bloc
   if (num_tokens == 0) return PKV_OK;
   PKV_CHECK(k && v && block_tables && positions && k_cache && v_cache, PKV_ERR_INVALID_ARGUMENT,
             "null pointer");
-  PKV_CHECK(num_blocks <= INT64_MAX / block_size, PKV_ERR_INVALID_ARGUMENT, "pool too large");
-  PKV_CHECK(aligned(k, elem_bytes(in_dtype)) && aligned(v, elem_bytes(in_dtype)),
-            PKV_ERR_INVALID_ARGUMENT, "misaligned k/v");
   const int64_t row = (int64_t)num_kv_heads * head_dim;
-  const int l2 = log2_exact(block_size);
-  dim3 grid((unsigned)num_tokens, 2);
-  dim3 block(pkv::kQuantThreads);
-  cudaStream_t strm = as_stream(stream);
-  auto* kc = static_cast<uint8_t*>(k_cache);
-  auto* vc = static_cast<uint8_t*>(v_cache);
-  const float ks = quant->k_scale, vs = quant->v_scale;
-  float* kts = quant->k_token_scales;
-  float* vts = quant->v_token_scales;
-#define PKV_LAUNCH_AQ(TIN, FMT)                                                               \
-  PKV_CUDA(launch_pdl(pkv::kv_append_quant_kernel<TIN, FMT>, grid, block, 0, strm,            \
-                      static_cast<const TIN*>(k), static_cast<const TIN*>(v), block_tables,   \
-                      max_blocks_per_seq, positions, block_size, l2, num_blocks, kc, vc, row, \
-                      ks, vs, kts, vts, slot_mapping_out))
-  if (quant->format == PKV_KV_FP8_E4M3) {
-    if (in_dtype == PKV_BF16) PKV_LAUNCH_AQ(__nv_bfloat16, 1); else PKV_LAUNCH_AQ(float, 1);
-  } else if (quant->format == PKV_KV_BF16K_FP8V) {
-    PKV_CHECK(aligned(k_cache, 2), PKV_ERR_INVALID_ARGUMENT, "misaligned bf16 K pool");
-    if (in_dtype == PKV_BF16) PKV_LAUNCH_AQ(__nv_bfloat16, 3); else PKV_LAUNCH_AQ(float, 3);
-  } else {
-    if (in_dtype == PKV_BF16) PKV_LAUNCH_AQ(__nv_bfloat16, 2); else PKV_LAUNCH_AQ(float, 2);
-  }
-#undef PKV_LAUNCH_AQ
-  return PKV_OK;
+  return write_quant(k, row, v, row, nullptr, block_tables, max_blocks_per_seq, positions,
+                     num_tokens, k_cache, v_cache, num_blocks, block_size, num_kv_heads, head_dim,
+                     in_dtype, quant, slot_mapping_out, as_stream(stream));
+}
+
+pkv_status pkv_kv_write_quant(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              const int64_t* slots, int32_t num_tokens, void* k_cache,
+                              void* v_cache, int64_t num_blocks, int32_t block_size,
+                              int32_t num_kv_heads, int32_t head_dim, pkv_dtype in_dtype,
+                              const pkv_kv_quant* quant, void* stream) {
+  PKV_CHECK(num_tokens >= 0 && num_blocks >= 1 && block_size >= 1 && num_kv_heads >= 1 &&
+                head_dim >= 1 && dtype_ok(in_dtype),
+            PKV_ERR_INVALID_ARGUMENT, "bad kv_write_quant sizes");
+  pkv_status st = check_quant(quant, true);
+  if (st != PKV_OK) return st;
+  if (num_tokens == 0) return PKV_OK;
+  PKV_CHECK(k && v && slots && k_cache && v_cache, PKV_ERR_INVALID_ARGUMENT, "null pointer");
+  PKV_CHECK(aligned(slots, 8), PKV_ERR_INVALID_ARGUMENT, "misaligned slots");
+  const int64_t row = (int64_t)num_kv_heads * head_dim;
+  PKV_CHECK(num_tokens == 1 || (k_stride >= row && v_stride >= row), PKV_ERR_INVALID_ARGUMENT,
+            "token rows overlap");
+  return write_quant(k, k_stride, v, v_stride, slots, nullptr, 1, nullptr, num_tokens, k_cache,
+                     v_cache, num_blocks, block_size, num_kv_heads, head_dim, in_dtype, quant,
+                     nullptr, as_stream(stream));
 }
 
 pkv_status pkv_kv_block_copy_quant(void* k_cache, void* v_cache, const int64_t* src_dst_pairs,
@@ -1221,6 +1386,15 @@ pkv_status pkv_kv_block_copy_quant(void* k_cache, void* v_cache, const int64_t* 
   PKV_CHECK(k_cache && v_cache && src_dst_pairs, PKV_ERR_INVALID_ARGUMENT, "null pointer");
   const int64_t blk = (int64_t)block_size * num_kv_heads * head_dim;
   cudaStream_t strm = as_stream(stream);
+  if (quant->format == PKV_KV_INT4_HEAD) {
+    // the codes, then the blocks' (scale, offset) words
+    st = check_int4(k_cache, v_cache, head_dim);
+    if (st != PKV_OK) return st;
+    st = copy_blocks(k_cache, v_cache, src_dst_pairs, num_pairs, num_blocks, blk / 2, strm);
+    if (st != PKV_OK) return st;
+    return copy_blocks(quant->k_token_scales, quant->v_token_scales, src_dst_pairs, num_pairs,
+                       num_blocks, (int64_t)block_size * num_kv_heads * 4, strm);
+  }
   if (quant->format == PKV_KV_BF16K_FP8V) {
     // two pools of different block sizes: K (2 bytes per element), then V
     st = move_blocks(k_cache, nullptr, num_blocks, k_cache, nullptr, num_blocks, src_dst_pairs,
@@ -1754,6 +1928,8 @@ pkv_status pkv_qk_norm_rope_append(
   if (quant != nullptr) {
     pkv_status s = check_quant(quant, true);
     if (s != PKV_OK) return s;
+    PKV_CHECK(quant->format != PKV_KV_INT4_HEAD, PKV_ERR_UNSUPPORTED,
+              "INT4 pools: pkv_kv_write_quant stores the rotated rows");
     PKV_CHECK(quant->format != PKV_KV_INT8_TOKEN || kv_row <= pkv::kRopeMaxInt8Row,
               PKV_ERR_UNSUPPORTED, "INT8 pools: num_kv_heads * head_dim must be at most %d",
               pkv::kRopeMaxInt8Row);
@@ -1954,6 +2130,168 @@ pkv_status pkv_verify_draft_tokens(const void* target_probs, int64_t target_stri
                          max_query_len, vocab};
   return prob_dtype == PKV_BF16 ? launch_verify<__nv_bfloat16>(p, num_seqs, as_stream(stream))
                                 : launch_verify<float>(p, num_seqs, as_stream(stream));
+}
+
+pkv_status pkv_beam_select_workspace_bytes(int32_t num_requests, int32_t num_beams, int32_t vocab,
+                                           int32_t num_select, size_t* bytes) {
+  PKV_CHECK(bytes != nullptr, PKV_ERR_INVALID_ARGUMENT, "null bytes pointer");
+  pkv_status st = check_beam(num_requests, num_beams, vocab, num_select);
+  if (st != PKV_OK) return st;
+  int dev, sms;
+  st = device_facts(&dev, &sms);
+  if (st != PKV_OK) return st;
+  const int64_t rows = (int64_t)num_requests * num_beams;
+  *bytes = beam_ws(rows, beam_tiles(vocab, beam_ept(rows, vocab, sms)), num_select).total;
+  return PKV_OK;
+}
+
+pkv_status pkv_beam_select(const void* logits, int64_t logits_stride, const float* scores,
+                           const uint8_t* finished, int32_t num_requests, int32_t num_beams,
+                           int32_t vocab, int32_t num_select, int32_t eos_token, int32_t* tokens,
+                           int32_t* parents, float* scores_out, uint8_t* finished_out,
+                           void* workspace, size_t workspace_bytes, pkv_dtype dtype,
+                           void* stream) {
+  pkv_status st = check_beam(num_requests, num_beams, vocab, num_select);
+  if (st != PKV_OK) return st;
+  PKV_CHECK(dtype_ok(dtype), PKV_ERR_INVALID_ARGUMENT, "bad dtype");
+  PKV_CHECK(eos_token >= -1 && eos_token < vocab && (finished == nullptr || eos_token >= 0),
+            PKV_ERR_INVALID_ARGUMENT,
+            "eos_token must be a token of the vocabulary (or -1 without finished beams)");
+  if (num_requests == 0) return PKV_OK;
+  const int64_t rows = (int64_t)num_requests * num_beams;
+  PKV_CHECK(logits && scores && tokens && parents && scores_out && workspace,
+            PKV_ERR_INVALID_ARGUMENT, "null pointer");
+  PKV_CHECK(rows == 1 || logits_stride >= vocab, PKV_ERR_INVALID_ARGUMENT, "logit rows overlap");
+  PKV_CHECK(aligned(logits, elem_bytes(dtype)) && aligned(scores, 4) && aligned(tokens, 4) &&
+                aligned(parents, 4) && aligned(scores_out, 4) && aligned(workspace, 256),
+            PKV_ERR_INVALID_ARGUMENT, "misaligned beam buffers");
+  int dev, sms;
+  st = device_facts(&dev, &sms);
+  if (st != PKV_OK) return st;
+  const int ept = beam_ept(rows, vocab, sms), tiles = beam_tiles(vocab, ept);
+  const BeamWs w = beam_ws(rows, tiles, num_select);
+  PKV_CHECK(workspace_bytes >= w.total, PKV_ERR_WORKSPACE_TOO_SMALL,
+            "workspace %zu bytes < %zu needed", workspace_bytes, w.total);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  pkv::BeamParams p = {logits, logits_stride, scores, finished, tokens, parents, scores_out,
+                       finished_out, reinterpret_cast<float2*>(ws),
+                       reinterpret_cast<float*>(ws + w.x), reinterpret_cast<int32_t*>(ws + w.v),
+                       num_requests, num_beams, vocab, num_select, tiles, eos_token};
+  return dtype == PKV_BF16 ? launch_beam<__nv_bfloat16>(p, ept, as_stream(stream))
+                           : launch_beam<float>(p, ept, as_stream(stream));
+}
+
+pkv_status pkv_fork_tables_workspace_bytes(int32_t num_groups, int32_t group_rows,
+                                           int32_t max_blocks_per_seq, size_t* bytes) {
+  PKV_CHECK(bytes != nullptr, PKV_ERR_INVALID_ARGUMENT, "null bytes pointer");
+  pkv_status st = check_fork(num_groups, group_rows, max_blocks_per_seq);
+  if (st != PKV_OK) return st;
+  *bytes = fork_ws(num_groups, group_rows,
+                   (int)ceil_div(max_blocks_per_seq, pkv::kForkThreads)).total;
+  return PKV_OK;
+}
+
+pkv_status pkv_fork_tables(const int32_t* parents, const int32_t* lens, const int32_t* held,
+                           const int32_t* shared, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, int32_t* ring, int64_t ring_size,
+                           const int64_t* ring_state, int32_t num_groups, int32_t group_rows,
+                           int32_t block_size, int32_t* block_tables_out, int32_t* lens_out,
+                           int32_t* held_out, int64_t* ring_state_out, int64_t* pairs,
+                           int32_t* totals, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  pkv_status st = check_fork(num_groups, group_rows, max_blocks_per_seq);
+  if (st != PKV_OK) return st;
+  PKV_CHECK(block_size >= 1 && ring_size >= 1, PKV_ERR_INVALID_ARGUMENT, "bad fork sizes");
+  PKV_CHECK((int64_t)max_blocks_per_seq * block_size <= 2147483647, PKV_ERR_UNSUPPORTED,
+            "table row too long");
+  if (num_groups == 0) return PKV_OK;
+  PKV_CHECK(parents && lens && held && block_tables && ring && ring_state && block_tables_out &&
+                lens_out && held_out && ring_state_out && pairs && totals && workspace,
+            PKV_ERR_INVALID_ARGUMENT, "null pointer");
+  PKV_CHECK(aligned(ring_state, 8) && aligned(ring_state_out, 8) && aligned(pairs, 8) &&
+                aligned(parents, 4) && aligned(lens, 4) && aligned(held, 4) && aligned(shared, 4) &&
+                aligned(block_tables, 4) && aligned(ring, 4) && aligned(block_tables_out, 4) &&
+                aligned(lens_out, 4) && aligned(held_out, 4) && aligned(totals, 4) &&
+                aligned(workspace, 256),
+            PKV_ERR_INVALID_ARGUMENT, "misaligned fork buffers");
+  const int chunks = (int)ceil_div(max_blocks_per_seq, pkv::kForkThreads);
+  const ForkWs w = fork_ws(num_groups, group_rows, chunks);
+  PKV_CHECK(workspace_bytes >= w.total, PKV_ERR_WORKSPACE_TOO_SMALL,
+            "workspace %zu bytes < %zu needed", workspace_bytes, w.total);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  pkv::ForkParams p = {};
+  p.parents = parents; p.lens = lens; p.held = held; p.shared = shared;
+  p.tables = block_tables; p.tables_out = block_tables_out;
+  p.ring = ring; p.state = ring_state;
+  p.lens_out = lens_out; p.held_out = held_out; p.state_out = ring_state_out;
+  p.pairs = pairs; p.totals = totals;
+  p.w_state = reinterpret_cast<int64_t*>(ws);
+  p.w_group = reinterpret_cast<int4*>(ws + w.group);
+  p.w_row = reinterpret_cast<int4*>(ws + w.row);
+  p.w_give = reinterpret_cast<int32_t*>(ws + w.give);
+  p.ring_size = ring_size;
+  p.R = num_groups; p.B = group_rows; p.width = max_blocks_per_seq; p.chunks = chunks;
+  p.K = block_size;
+  const dim3 grid((unsigned)num_groups, (unsigned)chunks), block(pkv::kForkThreads);
+  const size_t smem = sizeof(int32_t) * pkv::kForkThreads * (size_t)group_rows;
+  cudaStream_t strm = as_stream(stream);
+  PKV_CUDA(launch_pdl(pkv::fork_count_kernel, grid, block, smem, strm, p));
+  PKV_CUDA(launch_pdl(pkv::fork_apply_kernel, grid, block, smem, strm, p));
+  return PKV_OK;
+}
+
+pkv_status pkv_kv_fork_copy(void* k_cache, void* v_cache, const int64_t* pairs,
+                            const int32_t* lens, int32_t num_rows, int32_t num_layers,
+                            int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                            int32_t head_dim, pkv_dtype dtype, const pkv_kv_quant* quant,
+                            void* stream) {
+  PKV_CHECK(num_rows >= 0 && num_layers >= 1 && num_blocks >= 1 && block_size >= 1 &&
+                num_kv_heads >= 1 && head_dim >= 1 && dtype_ok(dtype),
+            PKV_ERR_INVALID_ARGUMENT, "bad fork-copy sizes");
+  const int fmt = quant ? quant->format : PKV_KV_PLAIN;
+  if (quant != nullptr) {
+    pkv_status st = check_quant(quant, true);
+    if (st == PKV_OK && fmt == PKV_KV_INT4_HEAD) st = check_int4(k_cache, v_cache, head_dim);
+    if (st != PKV_OK) return st;
+  }
+  PKV_CHECK(num_layers <= 32767, PKV_ERR_UNSUPPORTED, "at most 32767 layers");
+  const int64_t row = (int64_t)num_kv_heads * head_dim;
+  PKV_CHECK(num_blocks <= INT64_MAX / block_size / (4 * row) / num_layers,
+            PKV_ERR_INVALID_ARGUMENT, "pool too large");
+  if (num_rows == 0) return PKV_OK;
+  PKV_CHECK(k_cache && v_cache && pairs && lens, PKV_ERR_INVALID_ARGUMENT, "null pointer");
+  PKV_CHECK(aligned(pairs, 8) && aligned(lens, 4), PKV_ERR_INVALID_ARGUMENT, "misaligned pairs");
+  pkv::ForkCopyParams p = {};
+  p.pairs = pairs; p.lens = lens;
+  p.k = static_cast<uint8_t*>(k_cache); p.v = static_cast<uint8_t*>(v_cache);
+  p.v_row = fmt == PKV_KV_PLAIN ? row * (int64_t)elem_bytes(dtype)
+                                : (fmt == PKV_KV_INT4_HEAD ? row / 2 : row);
+  p.k_row = fmt == PKV_KV_BF16K_FP8V ? 2 * row : p.v_row;
+  p.k_layer = p.k_row * block_size * num_blocks;
+  p.v_layer = p.v_row * block_size * num_blocks;
+  p.num_blocks = num_blocks;
+  p.K = block_size;
+  if (fmt == PKV_KV_INT4_HEAD || fmt == PKV_KV_INT8_TOKEN) {
+    p.k_words = reinterpret_cast<uint32_t*>(quant->k_token_scales);
+    p.v_words = reinterpret_cast<uint32_t*>(quant->v_token_scales);
+    p.words = fmt == PKV_KV_INT4_HEAD ? num_kv_heads : 1;
+  }
+  // (a token's bytes divide a layer's, so every layer's rows are as aligned as the first's)
+  const int vw = std::min(vec_width(p.k_row, {k_cache}), vec_width(p.v_row, {v_cache}));
+  const int64_t slices = ceil_div((block_size - 1) * std::max(p.k_row, p.v_row) / vw,
+                                  pkv::kForkCopyThreads * pkv::kForkCopyUnroll);
+  PKV_CHECK(slices <= 65535, PKV_ERR_UNSUPPORTED, "block too large");
+  const dim3 grid((unsigned)num_rows, (unsigned)std::max<int64_t>(slices, 1), 2 * num_layers);
+  const dim3 block(pkv::kForkCopyThreads);
+  cudaStream_t st = as_stream(stream);
+  switch (vw) {
+    case 16: PKV_CUDA(launch_pdl(pkv::fork_copy_kernel<16>, grid, block, 0, st, p)); break;
+    case 8: PKV_CUDA(launch_pdl(pkv::fork_copy_kernel<8>, grid, block, 0, st, p)); break;
+    case 4: PKV_CUDA(launch_pdl(pkv::fork_copy_kernel<4>, grid, block, 0, st, p)); break;
+    case 2: PKV_CUDA(launch_pdl(pkv::fork_copy_kernel<2>, grid, block, 0, st, p)); break;
+    default: PKV_CUDA(launch_pdl(pkv::fork_copy_kernel<1>, grid, block, 0, st, p)); break;
+  }
+  return PKV_OK;
 }
 
 pkv_status pkv_get_device_error(int32_t* code, void* stream) {

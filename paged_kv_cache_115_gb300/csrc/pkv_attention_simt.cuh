@@ -3,6 +3,7 @@
 #pragma once
 
 #include "pkv_attention_common.cuh"
+#include "pkv_int4.cuh"
 
 namespace pkv {
 
@@ -17,22 +18,24 @@ constexpr int kSimtThreads = 128;
 constexpr int kSimtMaxPS = 1024;
 
 // K/V row loaders: element e of lane `lane` of the row starting at element
-// `row` (= (slot * H_kv + j) * D) of the pool, as float.
+// `row` (= (slot * H_kv + j) * D) of the pool, as float.  Arguments: the
+// element's index in the pool, its slot, and the word of its block, head and
+// offset ((block * H_kv + j) * K + offset).
 template <typename T>
 struct KvPlain {          // pool stored in the query dtype
   const T* k;
   const T* v;
-  __device__ __forceinline__ float ld_k(int64_t i, int64_t) const { return to_f32(k[i]); }
-  __device__ __forceinline__ float ld_v(int64_t i, int64_t) const { return to_f32(v[i]); }
+  __device__ __forceinline__ float ld_k(int64_t i, int64_t, int64_t) const { return to_f32(k[i]); }
+  __device__ __forceinline__ float ld_v(int64_t i, int64_t, int64_t) const { return to_f32(v[i]); }
 };
 struct KvFp8 {            // e4m3 codes, one scale per tensor
   const uint8_t* k;
   const uint8_t* v;
   float k_scale, v_scale;
-  __device__ __forceinline__ float ld_k(int64_t i, int64_t) const {
+  __device__ __forceinline__ float ld_k(int64_t i, int64_t, int64_t) const {
     return e4m3_to_f32(k[i]) * k_scale;
   }
-  __device__ __forceinline__ float ld_v(int64_t i, int64_t) const {
+  __device__ __forceinline__ float ld_v(int64_t i, int64_t, int64_t) const {
     return e4m3_to_f32(v[i]) * v_scale;
   }
 };
@@ -40,8 +43,8 @@ struct KvBf16Fp8 {        // bf16 K pool, e4m3 V codes with one scale
   const __nv_bfloat16* k;
   const uint8_t* v;
   float v_scale;
-  __device__ __forceinline__ float ld_k(int64_t i, int64_t) const { return __bfloat162float(k[i]); }
-  __device__ __forceinline__ float ld_v(int64_t i, int64_t) const {
+  __device__ __forceinline__ float ld_k(int64_t i, int64_t, int64_t) const { return __bfloat162float(k[i]); }
+  __device__ __forceinline__ float ld_v(int64_t i, int64_t, int64_t) const {
     return e4m3_to_f32(v[i]) * v_scale;
   }
 };
@@ -50,11 +53,27 @@ struct KvInt8 {           // int8 codes, one scale per token slot
   const int8_t* v;
   const float* k_ts;
   const float* v_ts;
-  __device__ __forceinline__ float ld_k(int64_t i, int64_t slot) const {
+  __device__ __forceinline__ float ld_k(int64_t i, int64_t slot, int64_t) const {
     return (float)k[i] * k_ts[slot];
   }
-  __device__ __forceinline__ float ld_v(int64_t i, int64_t slot) const {
+  __device__ __forceinline__ float ld_v(int64_t i, int64_t slot, int64_t) const {
     return (float)v[i] * v_ts[slot];
+  }
+};
+
+struct KvInt4 {           // 4-bit codes, (scale, offset) per token and head
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint32_t* k_words;
+  const uint32_t* v_words;
+  static __device__ __forceinline__ float value(uint8_t byte, int64_t i, uint32_t w) {
+    return fmaf((float)((i & 1) ? byte >> 4 : byte & 15), int4_scale(w), int4_offset(w));
+  }
+  __device__ __forceinline__ float ld_k(int64_t i, int64_t, int64_t w) const {
+    return value(k[i >> 1], i, k_words[w]);
+  }
+  __device__ __forceinline__ float ld_v(int64_t i, int64_t, int64_t w) const {
+    return value(v[i >> 1], i, v_words[w]);
   }
 };
 
@@ -120,11 +139,11 @@ attn_simt_kernel(const T* __restrict__ q, KV kv, const int32_t* __restrict__ blo
     float kr[E], vr[E];
     if (phys >= 0) {
       const int64_t slot = (int64_t)phys * K + off;
-      const int64_t row = (slot * H_kv + j) * D;
+      const int64_t row = (slot * H_kv + j) * D, word = ((int64_t)phys * H_kv + j) * K + off;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        kr[e] = kv.ld_k(row + lane + 32 * e, slot);
-        vr[e] = kv.ld_v(row + lane + 32 * e, slot);
+        kr[e] = kv.ld_k(row + lane + 32 * e, slot, word);
+        vr[e] = kv.ld_v(row + lane + 32 * e, slot, word);
       }
     } else {
 #pragma unroll

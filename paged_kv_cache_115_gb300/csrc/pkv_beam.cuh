@@ -1,0 +1,388 @@
+// Selection of beam search: the best candidates over a request's beams and the
+// vocabulary, from the model's output and the beams' scores.
+//
+//   candidate (b, v) = score_b + logit_bv - log sum_v' exp(logit_bv'),
+// ordered by value, then by the lowest b V + v.  One pass over the logits: a CTA
+// takes a tile of a row into registers and leaves the tile's largest logit m,
+// its sum of exp(x - m) and its best candidates; a second kernel joins the tiles
+// of a request's beams.  A row's order among its own candidates is that of its
+// logits, so the sum is only needed there; joined in 64 bits, because candidates
+// of two beams may lie next to each other.
+#pragma once
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+constexpr int kBeamThreads = 256;
+constexpr int kBeamWarps = kBeamThreads / 32;
+constexpr int kBeamMax = 32;                 // beams of a request, candidates asked for
+constexpr int kBeamBuffer = 512;             // candidates at or above a tile's bound
+
+struct BeamParams {
+  const void* logits;
+  int64_t stride;              // elements between rows
+  const float* scores;         // [R][B]
+  const uint8_t* finished;     // [R][B] or null
+  int32_t* tokens;             // [R][N]
+  int32_t* parents;
+  float* scores_out;
+  uint8_t* finished_out;       // or null
+  float2* tile_ms;             // [R B][tiles]: m, sum of exp(x - m)
+  float* tile_x;               // [R B][tiles][N]: best logits of a tile, -inf: none
+  int32_t* tile_v;             // and their tokens
+  int R, B, V, N, tiles, eos;
+};
+
+// Sorts a value a lane in descending order.
+template <typename T>
+__device__ __forceinline__ T warp_sort_desc(T x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1) {
+#pragma unroll
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      const T y = __shfl_xor_sync(0xffffffffu, x, j);
+      const bool lower = (lane & j) == 0, down = (lane & k) == 0;
+      x = (lower == down) ? (x > y ? x : y) : (x < y ? x : y);
+    }
+  }
+  return x;
+}
+
+// A value's bits in its order (adding 0 makes one of the two zeros).
+__device__ __forceinline__ uint32_t beam_order(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t beam_order(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x + 0.);
+  return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+
+// EPT values a thread: a tile of kBeamThreads * EPT values of a row, counted
+// from the 16-byte boundary at or in front of the row (rows of an odd vocabulary
+// start anywhere); what does not belong to the row counts as -inf.
+template <typename T, int EPT>
+__global__ void __launch_bounds__(kBeamThreads)
+beam_tiles_kernel(const __grid_constant__ BeamParams p) {
+  constexpr int VE = 16 / sizeof(T), NV = EPT / VE;
+  __shared__ float s_m[kBeamWarps], s_s[kBeamWarps], s_tau[kBeamWarps];
+  __shared__ int s_n;
+  __shared__ uint64_t s_key[kBeamBuffer], s_best[kBeamWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles;
+  if (tid == 0) s_n = 0;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (p.finished != nullptr && p.finished[row]) return;       // its one candidate needs no logits
+  const T* base = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
+  const int lead = (int)((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(T));
+  const uint4* vec = reinterpret_cast<const uint4*>(base - lead);
+  const int nvec = (lead + p.V + VE - 1) / VE;
+  const int v0 = tile * (kBeamThreads * NV) + tid;
+  constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  uint4 raw[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int v = v0 + j * kBeamThreads;
+    raw[j] = make_uint4(kNone, kNone, kNone, kNone);
+    if (v < nvec) raw[j] = __ldcs(vec + v);
+  }
+  auto words = [&](int j, int i) -> uint32_t {
+    return i == 0 ? raw[j].x : (i == 1 ? raw[j].y : (i == 2 ? raw[j].z : raw[j].w));
+  };
+  auto value = [&](int j, int e) -> float {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(words(j, e));
+    const uint32_t w = words(j, e >> 1);
+    return __uint_as_float((e & 1) ? w & 0xffff0000u : w << 16);
+  };
+  // the first and the last block of a row hold values of its neighbours
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e0 = (v0 + j * kBeamThreads) * VE - lead;
+    if (e0 < 0 || (e0 < p.V && e0 + VE > p.V)) {
+      uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        if (e0 + e < 0 || e0 + e >= p.V) {
+          if constexpr (sizeof(T) == 4) w[e] = kNone;
+          else w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | 0xff800000u : (w[e >> 1] & 0xffff0000u) | 0xff80u;
+        }
+      }
+      raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  float mx = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) mx = fmaxf(mx, value(j, e));
+  // bound of the warp: its N-th largest thread maximum has N values at or above it
+  const float sorted = warp_sort_desc(mx);
+  const float mw = __shfl_sync(0xffffffffu, sorted, 0);
+  const float tau_w = __shfl_sync(0xffffffffu, sorted, p.N - 1);
+  const float mu = mw == -INFINITY ? 0.f : mw;
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) sum += ex2_approx_ftz((value(j, e) - mu) * 1.44269504f);
+  sum = warp_sum(sum);
+  if (lane == 0) {
+    s_m[warp] = mw;
+    s_s[warp] = sum;
+    s_tau[warp] = tau_w;
+  }
+  __syncthreads();
+  float m = s_m[0], tau = s_tau[0];
+#pragma unroll
+  for (int w = 1; w < kBeamWarps; ++w) {
+    m = fmaxf(m, s_m[w]);
+    tau = fmaxf(tau, s_tau[w]);
+  }
+  const int64_t slot = (int64_t)row * p.tiles + tile;
+  if (tid == 0) {
+    float s = 0.f;
+    for (int w = 0; w < kBeamWarps; ++w)
+      if (s_m[w] != -INFINITY || s_s[w] != 0.f)
+        s += s_s[w] * exp2f((s_m[w] == -INFINITY ? 0.f : s_m[w] - m) * 1.44269504f);
+    p.tile_ms[slot] = make_float2(m, s);
+  }
+  auto key_of = [&](int j, int e) -> uint64_t {
+    const uint32_t v = (uint32_t)((v0 + j * kBeamThreads) * VE - lead + e);
+    return (uint64_t)beam_order(value(j, e)) << 32 | (0xffffffffu - v);
+  };
+  if (mx >= tau && mx > -INFINITY) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float x = value(j, e);
+        if (x >= tau && x > -INFINITY) {
+          const int i = atomicAdd(&s_n, 1);
+          if (i < kBeamBuffer) s_key[i] = key_of(j, e);
+        }
+      }
+  }
+  __syncthreads();
+  const int n = s_n;
+  float* out_x = p.tile_x + slot * p.N;
+  int32_t* out_v = p.tile_v + slot * p.N;
+  auto store = [&](int r, uint64_t key) {
+    const uint32_t o = (uint32_t)(key >> 32);
+    out_x[r] = __uint_as_float(o ^ ((uint32_t)((int32_t)~o >> 31) | 0x80000000u));
+    out_v[r] = (int32_t)(0xffffffffu - (uint32_t)key);
+  };
+  if (n <= kBeamBuffer) {
+    // each candidate counts those in front of it (keys are distinct)
+    for (int i = tid; i < n; i += kBeamThreads) {
+      const uint64_t key = s_key[i];
+      int rank = 0;
+      for (int k = 0; k < n; ++k) rank += s_key[k] > key;
+      if (rank < p.N) store(rank, key);
+    }
+    for (int r = n + tid; r < p.N; r += kBeamThreads) out_x[r] = -INFINITY;
+  } else {
+    // a tile of very many equal values: one after the other
+    uint64_t last = ~0ull;
+    for (int r = 0; r < p.N; ++r) {
+      uint64_t best = 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const uint64_t key = key_of(j, e);
+          if (value(j, e) > -INFINITY && key < last && key > best) best = key;
+        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t y = __shfl_xor_sync(0xffffffffu, best, o);
+        best = y > best ? y : best;
+      }
+      __syncthreads();
+      if (lane == 0) s_best[warp] = best;
+      __syncthreads();
+      best = s_best[0];
+#pragma unroll
+      for (int w = 1; w < kBeamWarps; ++w) best = s_best[w] > best ? s_best[w] : best;
+      last = best;
+      if (tid == 0) store(r, best);               // (more than kBeamBuffer values: there are N)
+    }
+  }
+}
+
+// One CTA a request: the sums of its beams' rows, then the best of all tiles'
+// candidates and the finished beams.
+constexpr int kBeamPickBuffer = 1024;
+
+__global__ void __launch_bounds__(kBeamThreads)
+beam_pick_kernel(const __grid_constant__ BeamParams p) {
+  __shared__ double s_add[kBeamMax];             // score - log sum exp; -inf: no candidates
+  __shared__ uint8_t s_over[kBeamMax];
+  __shared__ uint64_t s_tau[kBeamWarps];
+  __shared__ uint64_t s_key[kBeamPickBuffer];
+  __shared__ uint32_t s_at[kBeamPickBuffer];
+  __shared__ uint64_t s_bk[kBeamWarps];
+  __shared__ uint32_t s_ba[kBeamWarps];
+  __shared__ int s_n;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = blockIdx.x;
+  if (tid == 0) s_n = 0;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  for (int b = warp; b < p.B; b += kBeamWarps) {
+    const int row = r * p.B + b;
+    const float score = p.scores[row];
+    const bool over = p.finished != nullptr && p.finished[row];
+    double add = over ? (double)score : -INFINITY;
+    if (!over) {
+      float m = -INFINITY;
+      bool bad = false;
+      for (int c = lane; c < p.tiles; c += 32) {
+        const float2 ms = p.tile_ms[(int64_t)row * p.tiles + c];
+        m = fmaxf(m, ms.x);
+        bad |= !(ms.x < INFINITY) || !(ms.y < INFINITY);
+      }
+      m = warp_max(m);
+      bad = __any_sync(0xffffffffu, bad);
+      double s = 0;
+      for (int c = lane; c < p.tiles; c += 32) {
+        const float2 ms = p.tile_ms[(int64_t)row * p.tiles + c];
+        if (ms.x > -INFINITY && !bad) s += (double)ms.y * exp((double)ms.x - (double)m);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (bad) {
+        if (lane == 0) record_error(PKV_DEVERR_BEAM);
+      } else if (m > -INFINITY) {
+        add = (double)score - ((double)m + log(s));
+      }
+    }
+    if (lane == 0) {
+      s_add[b] = add;
+      s_over[b] = over;
+    }
+  }
+  __syncthreads();
+  // candidate i: beam, tile and place; a finished beam has one, its end token
+  const int per = p.tiles * p.N, total = p.B * per;
+  auto load = [&](int i, uint64_t& key, uint32_t& at) -> bool {
+    const int b = i / per, j = i - b * per;
+    const double add = s_add[b];
+    double c;
+    int v;
+    if (s_over[b]) {
+      if (j != 0) return false;
+      c = add;
+      v = p.eos;
+    } else {
+      const int64_t e = (int64_t)(r * p.B + b) * per + j;
+      const float x = p.tile_x[e];
+      if (!(x > -INFINITY)) return false;
+      c = (double)x + add;
+      v = p.tile_v[e];
+    }
+    if (!(c > -INFINITY && c < INFINITY)) return false;
+    key = beam_order(c);
+    at = (uint32_t)(b * p.V + v);
+    return true;
+  };
+  // bound: the N-th largest thread maximum of a warp
+  uint64_t tau = 0;
+  if (total > kBeamThreads) {
+    uint64_t mx = 0, key;
+    uint32_t at;
+    for (int i = tid; i < total; i += kBeamThreads)
+      if (load(i, key, at) && key > mx) mx = key;
+    const uint64_t sorted = warp_sort_desc(mx);
+    const uint64_t t = __shfl_sync(0xffffffffu, sorted, p.N - 1);
+    if (lane == 0) s_tau[warp] = t;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kBeamWarps; ++w) tau = s_tau[w] > tau ? s_tau[w] : tau;
+  }
+  for (int i = tid; i < total; i += kBeamThreads) {
+    uint64_t key;
+    uint32_t at;
+    if (load(i, key, at) && key >= tau) {
+      const int k = atomicAdd(&s_n, 1);
+      if (k < kBeamPickBuffer) {
+        s_key[k] = key;
+        s_at[k] = at;
+      }
+    }
+  }
+  __syncthreads();
+  const int n = s_n;
+  auto store = [&](int k, uint64_t key, uint32_t at) {
+    const double c = __longlong_as_double(
+        (long long)(key ^ ((uint64_t)((int64_t)~key >> 63) | 0x8000000000000000ull)));
+    const int b = (int)(at / (uint32_t)p.V), v = (int)(at - (uint32_t)b * (uint32_t)p.V);
+    const int64_t o = (int64_t)r * p.N + k;
+    p.tokens[o] = v;
+    p.parents[o] = b;
+    p.scores_out[o] = (float)c;
+    if (p.finished_out != nullptr) p.finished_out[o] = s_over[b] || v == p.eos;
+  };
+  if (n <= kBeamPickBuffer) {
+    for (int i = tid; i < n; i += kBeamThreads) {
+      const uint64_t key = s_key[i];
+      const uint32_t at = s_at[i];
+      int rank = 0;
+      for (int k = 0; k < n; ++k) rank += s_key[k] > key || (s_key[k] == key && s_at[k] < at);
+      if (rank < p.N) store(rank, key, at);
+    }
+  } else {
+    // very many equal candidates (beams alike): one after the other
+    uint64_t last_key = ~0ull;
+    uint32_t last_at = 0;
+    for (int k = 0; k < p.N; ++k) {
+      uint64_t bk = 0;
+      uint32_t ba = 0xffffffffu;
+      for (int i = tid; i < total; i += kBeamThreads) {
+        uint64_t key;
+        uint32_t at;
+        if (!load(i, key, at)) continue;
+        const bool behind = key < last_key || (key == last_key && at > last_at);
+        if (behind && (key > bk || (key == bk && at < ba))) {
+          bk = key;
+          ba = at;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t yk = __shfl_xor_sync(0xffffffffu, bk, o);
+        const uint32_t ya = __shfl_xor_sync(0xffffffffu, ba, o);
+        if (yk > bk || (yk == bk && ya < ba)) {
+          bk = yk;
+          ba = ya;
+        }
+      }
+      __syncthreads();
+      if (lane == 0) {
+        s_bk[warp] = bk;
+        s_ba[warp] = ba;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kBeamWarps; ++w)
+        if (s_bk[w] > bk || (s_bk[w] == bk && s_ba[w] < ba)) {
+          bk = s_bk[w];
+          ba = s_ba[w];
+        }
+      last_key = bk;
+      last_at = ba;
+      if (tid == 0) store(k, bk, ba);             // (more than kBeamPickBuffer: there are N)
+    }
+  }
+  for (int k = n + tid; k < p.N; k += kBeamThreads) {
+    const int64_t o = (int64_t)r * p.N + k;
+    p.tokens[o] = -1;
+    p.parents[o] = -1;
+    p.scores_out[o] = -INFINITY;
+    if (p.finished_out != nullptr) p.finished_out[o] = 1;
+  }
+}
+
+}  // namespace pkv

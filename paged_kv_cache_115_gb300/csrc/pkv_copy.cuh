@@ -161,7 +161,8 @@ __global__ void kv_append_varlen_kernel(const uint8_t* __restrict__ k,
   *reinterpret_cast<V*>(dst) = __ldg(reinterpret_cast<const V*>(src));
 }
 
-// a1 + a2 into a quantized pool.  grid = (tokens, 2 for K/V), 128 threads.
+// a1 + a2 into a quantized pool (slots_in null: slots from positions and
+// tables), or a2 at given slots.  grid = (tokens, 2 for K/V), 128 threads.
 // FMT 1: e4m3(x / scale) per element (per-tensor scale).  FMT 2: the token's
 // row (all heads) gets scale = max|x| / 127 and codes rint(x / scale), the
 // scale stored at the token's slot.  FMT 3: K rows as bfloat16 (rounded to
@@ -176,16 +177,23 @@ kv_append_quant_kernel(const TIN* __restrict__ k, const TIN* __restrict__ v,
                        int32_t log2_bs, int64_t num_blocks, uint8_t* __restrict__ k_cache,
                        uint8_t* __restrict__ v_cache, int64_t row_elems, float k_scale,
                        float v_scale, float* __restrict__ k_ts, float* __restrict__ v_ts,
-                       int64_t* __restrict__ slots) {
+                       int64_t* __restrict__ slots, const int64_t* __restrict__ slots_in,
+                       int64_t k_stride, int64_t v_stride) {
   __shared__ float s_red[kQuantThreads / 32];
   pdl_wait_primary();
   pdl_launch_dependents();
   const int64_t i = blockIdx.x;
   const int z = blockIdx.y;
   const bool leader = threadIdx.x == 0 && z == 0;
-  const int t = positions[i];
+  const int t = slots_in != nullptr ? -1 : positions[i];
   int64_t slot = -1;
-  if (t >= 0) {
+  if (slots_in != nullptr) {
+    slot = slots_in[i];
+    if (slot < 0 || slot >= num_blocks * block_size) {
+      if (slot != -1 && leader) record_error(PKV_DEVERR_SLOT);
+      slot = -1;
+    }
+  } else if (t >= 0) {
     const int lb = log2_bs >= 0 ? (t >> log2_bs) : (t / block_size);
     const int off = log2_bs >= 0 ? (t & (block_size - 1)) : (t - lb * block_size);
     if (lb >= max_blocks_per_seq) {
@@ -201,7 +209,7 @@ kv_append_quant_kernel(const TIN* __restrict__ k, const TIN* __restrict__ v,
   }
   if (leader && slots != nullptr) slots[i] = slot;
   if (slot < 0) return;
-  const TIN* src = (z ? v : k) + i * row_elems;
+  const TIN* src = z ? v + i * v_stride : k + i * k_stride;
   uint8_t* dst = (z ? v_cache : k_cache) + slot * row_elems;
   if (FMT == 3 && z == 0) {
     __nv_bfloat16* kd = reinterpret_cast<__nv_bfloat16*>(k_cache) + slot * row_elems;

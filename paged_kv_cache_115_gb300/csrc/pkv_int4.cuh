@@ -1,0 +1,194 @@
+// 4-bit KV pages: quantizing writes and the description of a pool.
+//
+// Per token and KV head a row x of D values is stored as 4-bit codes with one
+// bf16 scale s and one bf16 offset z:
+//   z = min x rounded down to bf16, s = bf16((max x - z) / 15), r = 1 / s,
+//   code = clamp(rint((x - z) r), 0, 15), read back as z + s code,
+// all in float32 (each step rounded to nearest even), so that codes, scales and
+// offsets are fixed to the bit.  Rounding z down keeps every x - z >= 0 whatever
+// the row's distance from zero is next to its spread: the error stays below
+// 0.57 s (half a step, and 15 codes of a scale that is off by 2^-8 at most).  A
+// scale below 2^-126 has no float32 reciprocal: r = 0, the row reads as z.  A row
+// with a NaN or an infinity (or whose offset or scale overflows) gets s = z = NaN
+// and reads as NaN, as it would in a bf16 pool.
+//
+// Element 2 i of a row is the low half of its byte i.  A token's (s, z) is one
+// 32-bit word, s in the low half; the words of a pool are [num_blocks, H_kv,
+// block_size], so that the words of a block's tokens lie together for each head.
+#pragma once
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+__device__ __forceinline__ float int4_scale(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float int4_offset(uint32_t w) {
+  return __uint_as_float(w & 0xffff0000u);
+}
+
+struct Int4Row {
+  float z, r;
+  uint32_t word;     // (s, z) as stored
+  bool bad;          // not finite: codes 0
+};
+
+// From a row's least and largest value and whether all of it is finite.
+__device__ __forceinline__ Int4Row int4_row(float lo, float hi, bool finite) {
+  Int4Row q;
+  const __nv_bfloat16 z = __float2bfloat16_rd(lo);
+  q.z = __bfloat162float(z);
+  const __nv_bfloat16 s = __float2bfloat16_rn(__fdiv_rn(hi - q.z, 15.f));
+  const float sf = __bfloat162float(s);
+  q.bad = !finite || !(fabsf(q.z) < INFINITY) || !(sf < INFINITY);
+  q.r = sf >= 1.17549435e-38f ? __frcp_rn(sf) : 0.f;
+  q.word = q.bad ? 0x7fff7fffu
+                 : (uint32_t)__bfloat16_as_ushort(s) | (uint32_t)__bfloat16_as_ushort(z) << 16;
+  return q;
+}
+
+// N codes (4 or 8) packed, the first in the lowest bits.  Clamping first is the
+// same (the bounds are whole); adding 1.5 * 2^23 rounds to nearest even into the
+// low bits, and the constant's own bits come off the packed word at once.
+template <int N>
+__device__ __forceinline__ uint32_t int4_pack(const Int4Row& q, const float* x) {
+  constexpr uint32_t kMagic = 0x4b400000u;      // 12582912.0f
+  uint32_t w = 0, off = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float y = fminf(fmaxf((x[i] - q.z) * q.r, 0.f), 15.f);
+    w += __float_as_uint(y + 12582912.f) << (4 * i);
+    off += kMagic << (4 * i);
+  }
+  w -= off;
+  if constexpr (N < 8) w &= (1u << (4 * N)) - 1;
+  return q.bad ? 0u : w;
+}
+
+struct Int4WriteParams {
+  const void* k;
+  const void* v;
+  int64_t k_stride, v_stride;        // elements between tokens
+  const int64_t* slots;              // or null: slots from positions and tables
+  const int32_t* positions;
+  const int32_t* block_tables;       // row i of token i
+  int64_t* slots_out;                // may be null (with tables)
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  uint32_t* k_words;
+  uint32_t* v_words;
+  int64_t num_blocks;
+  int max_blocks, block_size, log2_bs;
+  int T, H;
+};
+
+constexpr int kInt4Threads = 256;
+
+// A row takes D / V lanes, V values (16 bytes) a lane; each lane has U rows in
+// flight.  WIDE: rows on 16-byte boundaries, else value by value.
+// Bound by HBM: (2 e D + D + 8) H bytes a token.
+template <typename TIN, int D, int U, bool WIDE>
+__global__ void __launch_bounds__(kInt4Threads)
+kv_write_int4_kernel(const __grid_constant__ Int4WriteParams p) {
+  constexpr int V = 16 / sizeof(TIN), LANES = D / V, RPI = kInt4Threads / LANES;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int li = threadIdx.x % LANES;
+  const int rows = 2 * p.H;                      // of a token: K heads, V heads
+  const unsigned total = (unsigned)p.T * rows;   // below 2^31
+  const unsigned r0 = blockIdx.x * (RPI * U) + threadIdx.x / LANES;
+  float x[U][V];
+  int64_t blk[U];
+  int off[U], zh[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const unsigned r = r0 + u * RPI;
+    blk[u] = -1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[u][i] = 0.f;
+    if (r < total) {
+      const int t = (int)(r / rows);
+      zh[u] = (int)(r - (unsigned)t * rows);
+      const bool leader = zh[u] == 0 && li == 0;
+      int64_t b = -1;
+      int o = 0;
+      if (p.slots != nullptr) {
+        const int64_t slot = p.slots[t];
+        if (slot >= 0 && (p.log2_bs >= 0 ? slot >> p.log2_bs : slot / p.block_size) < p.num_blocks) {
+          b = p.log2_bs >= 0 ? slot >> p.log2_bs : slot / p.block_size;
+          o = (int)(slot - b * p.block_size);
+        } else if (slot != -1 && leader) {
+          record_error(PKV_DEVERR_SLOT);
+        }
+      } else {
+        const int pos = p.positions[t];
+        if (pos >= 0) {
+          const int lb = p.log2_bs >= 0 ? pos >> p.log2_bs : pos / p.block_size;
+          if (lb >= p.max_blocks) {
+            if (leader) record_error(PKV_DEVERR_POSITION);
+          } else {
+            const int64_t phys = p.block_tables[(int64_t)t * p.max_blocks + lb];
+            if (phys < 0 || phys >= p.num_blocks) {
+              if (leader) record_error(PKV_DEVERR_BLOCK_ID);
+            } else {
+              b = phys;
+              o = pos - lb * p.block_size;
+            }
+          }
+        }
+        if (leader && p.slots_out != nullptr) p.slots_out[t] = b < 0 ? -1 : b * p.block_size + o;
+      }
+      blk[u] = b;
+      off[u] = o;
+      if (b >= 0) {
+        const bool z = zh[u] >= p.H;
+        const TIN* src = static_cast<const TIN*>(z ? p.v : p.k) +
+                         t * (z ? p.v_stride : p.k_stride) + (zh[u] - (z ? p.H : 0)) * D + li * V;
+        if constexpr (WIDE) {
+          const uint4 raw = __ldg(reinterpret_cast<const uint4*>(src));
+          if constexpr (sizeof(TIN) == 4) {
+            x[u][0] = __uint_as_float(raw.x); x[u][1] = __uint_as_float(raw.y);
+            x[u][2] = __uint_as_float(raw.z); x[u][3] = __uint_as_float(raw.w);
+          } else {
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[u][2 * i] = __uint_as_float(w[i] << 16);
+              x[u][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[u][i] = to_f32(src[i]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float lo = x[u][0], hi = x[u][0], fin = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      lo = fminf(lo, x[u][i]);
+      hi = fmaxf(hi, x[u][i]);
+      fin = fmaf(x[u][i], 0.f, fin);             // NaN once a value is not finite
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      fin += __shfl_xor_sync(0xffffffffu, fin, o);
+    }
+    if (blk[u] < 0) continue;
+    const Int4Row q = int4_row(lo, hi, fin == 0.f);
+    const bool z = zh[u] >= p.H;
+    const int h = zh[u] - (z ? p.H : 0);
+    uint8_t* dst = (z ? p.v_cache : p.k_cache) +
+                   ((blk[u] * p.block_size + off[u]) * p.H + h) * (D / 2) + li * (V / 2);
+    if constexpr (V == 8) *reinterpret_cast<uint32_t*>(dst) = int4_pack<8>(q, x[u]);
+    else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)int4_pack<4>(q, x[u]);
+    if (li == 0)
+      (z ? p.v_words : p.k_words)[(blk[u] * p.H + h) * p.block_size + off[u]] = q.word;
+  }
+}
+
+}  // namespace pkv

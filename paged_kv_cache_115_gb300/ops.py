@@ -35,6 +35,7 @@ DEVICE_ERRORS = {
     0: "none", 1: "block id out of range", 2: "slot out of range", 3: "copy pair out of range",
     4: "context length out of range", 5: "position beyond block-table row", 6: "pipeline timeout",
     7: "step refused", 8: "draft token, cu_seqlens or probabilities out of range",
+    9: "logits with a NaN or +infinity",
 }
 
 c_i32, c_i64, c_vp, c_sz, c_f = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
@@ -46,12 +47,13 @@ class AttentionConfig(ctypes.Structure):
 
 
 class KvQuant(ctypes.Structure):
-    """pkv_kv_quant: format 1 = FP8 e4m3 (per-tensor scales), 2 = INT8 per token."""
+    """pkv_kv_quant: format 1 = FP8 e4m3 (per-tensor scales), 2 = INT8 per token,
+    3 = bf16 K with FP8 V, 4 = INT4 per token and head."""
     _fields_ = [("format", c_i32), ("k_scale", c_f), ("v_scale", c_f),
                 ("k_token_scales", c_vp), ("v_token_scales", c_vp)]
 
 
-KV_FP8_E4M3, KV_INT8_TOKEN, KV_BF16K_FP8V = 1, 2, 3
+KV_FP8_E4M3, KV_INT8_TOKEN, KV_BF16K_FP8V, KV_INT4_HEAD = 1, 2, 3, 4
 
 
 def _sig(name, restype, *argtypes):
@@ -116,6 +118,18 @@ _prefix_ws = _sig("pkv_attention_decode_prefix_workspace_bytes", c_i32, c_i32, c
                   c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_sz))
 _verify = _sig("pkv_verify_draft_tokens", c_i32, c_vp, c_i64, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp,
                c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_i32, c_vp)
+_write_quant = _sig("pkv_kv_write_quant", c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i32, c_vp, c_vp,
+                    c_i64, c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(KvQuant), c_vp)
+_beam = _sig("pkv_beam_select", c_i32, c_vp, c_i64, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32,
+             c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_i32, c_vp)
+_beam_ws = _sig("pkv_beam_select_workspace_bytes", c_i32, c_i32, c_i32, c_i32, c_i32,
+                ctypes.POINTER(c_sz))
+_fork = _sig("pkv_fork_tables", c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_i64, c_vp,
+             c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp)
+_fork_ws = _sig("pkv_fork_tables_workspace_bytes", c_i32, c_i32, c_i32, c_i32,
+                ctypes.POINTER(c_sz))
+_fork_copy = _sig("pkv_kv_fork_copy", c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i64, c_i32,
+                  c_i32, c_i32, c_i32, ctypes.POINTER(KvQuant), c_vp)
 _dev_error = _sig("pkv_get_device_error", c_i32, ctypes.POINTER(c_i32), c_vp)
 
 # bytes of the library's fixed attention scratch (PKV_NOALLOC_SCRATCH_BYTES)
@@ -130,7 +144,9 @@ EXPORTED = ("pkv_status_string", "pkv_last_error_message", "pkv_version", "pkv_s
             "pkv_attention_prefill", "pkv_attention_prefill_workspace_bytes",
             "pkv_kv_append_varlen", "pkv_step_tables", "pkv_qk_norm_rope_append",
             "pkv_attention_decode_prefix", "pkv_attention_decode_prefix_workspace_bytes",
-            "pkv_verify_draft_tokens", "pkv_get_device_error")
+            "pkv_verify_draft_tokens", "pkv_kv_write_quant", "pkv_beam_select",
+            "pkv_beam_select_workspace_bytes", "pkv_fork_tables",
+            "pkv_fork_tables_workspace_bytes", "pkv_kv_fork_copy", "pkv_get_device_error")
 
 
 class PagedKVError(RuntimeError):
@@ -443,15 +459,19 @@ def get_device_error(device=None) -> int:
 
 
 # ---------------------------------------------------------------------------
-# quantized KV cache (FP8 e4m3 per-tensor scale, INT8 per-token scale)
+# quantized KV cache (FP8 e4m3 per-tensor scale, INT8 per-token scale, INT4
+# with a scale and an offset per token and head)
 # ---------------------------------------------------------------------------
 
 def kv_quant(fmt: str, k_scale: float = 1.0, v_scale: float = 1.0,
              k_token_scales: Optional[torch.Tensor] = None,
              v_token_scales: Optional[torch.Tensor] = None) -> KvQuant:
     """Describe a quantized pool: ``fmt`` "fp8" (scales per tensor), "int8"
-    (float32 CUDA tensors of one scale per token slot) or "k16v8" (a bf16 K
-    pool with an FP8 V pool of scale ``v_scale``).  The description holds
+    (float32 CUDA tensors of one scale per token slot), "k16v8" (a bf16 K
+    pool with an FP8 V pool of scale ``v_scale``) or "int4" (uint8 pools
+    [num_blocks, block_size, H_kv, D / 2] of two codes a byte; ``*_token_scales``
+    bfloat16 CUDA tensors [num_blocks, H_kv, block_size, 2], the scale and the
+    offset of each token and head).  The description holds
     references to the scale tensors, so that their memory lives as long as
     it does."""
     qd = KvQuant()
@@ -466,6 +486,20 @@ def kv_quant(fmt: str, k_scale: float = 1.0, v_scale: float = 1.0,
                 raise ValueError(f"int8 pools need {name}")
             _need(t, name, torch.float32, 1)
         qd.format = KV_INT8_TOKEN
+        qd.k_token_scales = k_token_scales.data_ptr()
+        qd.v_token_scales = v_token_scales.data_ptr()
+        qd._scale_tensors = (k_token_scales, v_token_scales)
+    elif fmt == "int4":
+        for name, t in (("k_token_scales", k_token_scales), ("v_token_scales", v_token_scales)):
+            if t is None:
+                raise ValueError(f"int4 pools need {name}")
+            _need(t, name, torch.bfloat16)
+            if t.dim() not in (4, 5) or t.shape[-1] != 2:
+                raise ValueError(f"{name} must be [(layers,) num_blocks, H_kv, block_size, 2]")
+        if k_token_scales.shape != v_token_scales.shape or \
+                k_token_scales.get_device() != v_token_scales.get_device():
+            raise ValueError("k_token_scales and v_token_scales must match in shape and device")
+        qd.format = KV_INT4_HEAD
         qd.k_token_scales = k_token_scales.data_ptr()
         qd.v_token_scales = v_token_scales.data_ptr()
         qd._scale_tensors = (k_token_scales, v_token_scales)
@@ -484,15 +518,39 @@ def _need_pool(t: torch.Tensor, name: str, quant: Optional[KvQuant] = None) -> N
         raise TypeError(f"{name} must hold one-byte codes (uint8 / int8 / float8_e4m3fn)")
 
 
+def _one_layer(k_cache: torch.Tensor) -> None:
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must have 4 dims (one layer)")
+
+
+def _quant_pool(k_cache: torch.Tensor, v_cache: torch.Tensor, quant: KvQuant):
+    """Checks a quantized pool pair against its description; (num_blocks,
+    block_size, H_kv, head_dim) of one layer."""
+    if quant.format == KV_INT4_HEAD:
+        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _need(t, name, torch.uint8)
+        if k_cache.dim() not in (4, 5) or v_cache.shape != k_cache.shape:
+            raise ValueError("INT4 pools must be [(layers,) num_blocks, block_size, H_kv, D / 2]")
+        nb, K, H, half = k_cache.shape[-4:]
+        for t in getattr(quant, "_scale_tensors", ()):
+            if t.shape != (*k_cache.shape[:-4], nb, H, K, 2) or \
+                    t.get_device() != k_cache.get_device():
+                raise ValueError("int4 scales must be [(layers,) num_blocks, H_kv, block_size, 2] "
+                                 "of the pool, on its device")
+        return nb, K, H, 2 * half
+    _need_pool(k_cache, "k_cache", quant)
+    _need_pool(v_cache, "v_cache")
+    return tuple(k_cache.shape)
+
+
 @_device_call
 def paged_kv_append_quant(k: torch.Tensor, v: torch.Tensor, block_tables: torch.Tensor,
                           positions: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                           quant: KvQuant,
                           slot_mapping_out: Optional[torch.Tensor] = None) -> None:
     """Slot mapping + quantized KV write in one launch (rows k, v in bf16/fp32)."""
-    _need_pool(k_cache, "k_cache", quant)
-    _need_pool(v_cache, "v_cache")
-    nb, K, H, D = k_cache.shape
+    nb, K, H, D = _quant_pool(k_cache, v_cache, quant)
+    _one_layer(k_cache)
     _need(k, "k", None, 3)
     _need(v, "v", k.dtype, 3)
     _need(block_tables, "block_tables", torch.int32, 2)
@@ -511,14 +569,39 @@ def paged_kv_append_quant(k: torch.Tensor, v: torch.Tensor, block_tables: torch.
            "pkv_kv_append_quant")
 
 
+def paged_kv_write_quant(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                         k_cache: torch.Tensor, v_cache: torch.Tensor, quant: KvQuant) -> None:
+    """Quantized KV write at given slots (int64 [T], -1: none), every quantized
+    format.  k, v [T, H_kv, D] in bf16 / fp32 may be cut out of one
+    projection's output (any distance between tokens)."""
+    nb, K, H, D = _quant_pool(k_cache, v_cache, quant)
+    _one_layer(k_cache)
+    T, dtype = k.shape[0], k.dtype
+    dev = _device_of(k, "k")
+    _in_32_bits(T)
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError("paged_kv_write_quant: CUDA tensors on several devices")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    if quant.format == KV_INT8_TOKEN:
+        for t in getattr(quant, "_scale_tensors", ()):
+            if t.shape[0] != nb * K or t.get_device() != dev:
+                raise ValueError("token scales must cover every slot of the pool, on its device")
+    ks, vs = _token_rows(k, "k", dtype, T, H, D, dev), _token_rows(v, "v", dtype, T, H, D, dev)
+    _call_on(dev, _write_quant,
+             (k.data_ptr(), ks, v.data_ptr(), vs, _vec(slots, "slots", torch.int64, T, dev), T,
+              k_cache.data_ptr(), v_cache.data_ptr(), nb, K, H, D, _dtype_code(k),
+              ctypes.byref(quant)), "pkv_kv_write_quant")
+
+
 @_device_call
 def kv_block_copy_quant(k_cache: torch.Tensor, v_cache: torch.Tensor,
                         src_dst_pairs: torch.Tensor, quant: KvQuant) -> None:
-    """Copy-on-write block copy of a quantized pool (codes and, for INT8, scales)."""
-    _need_pool(k_cache, "k_cache", quant)
-    _need_pool(v_cache, "v_cache")
+    """Copy-on-write block copy of a quantized pool (codes and, for INT8 and
+    INT4, scales)."""
+    nb, K, H, D = _quant_pool(k_cache, v_cache, quant)
+    _one_layer(k_cache)
     _need(src_dst_pairs, "src_dst_pairs", torch.int64, 2)
-    nb, K, H, D = k_cache.shape
     _check(_copy_quant(_ptr(k_cache), _ptr(v_cache), _ptr(src_dst_pairs), src_dst_pairs.shape[0],
                        nb, K, H, D, ctypes.byref(quant), _stream(k_cache.device)),
            "pkv_kv_block_copy_quant")
@@ -526,9 +609,10 @@ def kv_block_copy_quant(k_cache: torch.Tensor, v_cache: torch.Tensor,
 
 def attention_quant_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                                     max_context_len, q_dtype: torch.dtype, quant: KvQuant,
-                                    kernel: int = 0, num_splits: int = 0) -> int:
+                                    kernel: int = 0, num_splits: int = 0,
+                                    share_prefix: bool = False) -> int:
     out = c_sz(0)
-    cfg = _cfg(kernel, num_splits)
+    cfg = _cfg(kernel, num_splits, share_prefix)
     code = PKV_BF16 if q_dtype == torch.bfloat16 else PKV_F32
     _check(_ws_quant(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
                      code, ctypes.byref(quant), ctypes.byref(cfg), ctypes.byref(out)),
@@ -543,15 +627,18 @@ def paged_attention_decode_quant(q: torch.Tensor, k_cache: torch.Tensor, v_cache
                                  out: Optional[torch.Tensor] = None,
                                  max_context_len: Optional[int] = None,
                                  workspace: Optional[torch.Tensor] = None,
-                                 kernel: int = 0, num_splits: int = 0) -> torch.Tensor:
-    """Decode attention over a quantized pool (values read back as code * scale)."""
+                                 kernel: int = 0, num_splits: int = 0,
+                                 share_prefix: bool = False) -> torch.Tensor:
+    """Decode attention over a quantized pool (values read back as code * scale,
+    INT4: offset + code * scale).  ``share_prefix``: stage blocks that
+    consecutive sequences share (the beams of a request) once per group, as in
+    :func:`paged_attention_decode`; INT4 pools, ignored by the others."""
     _need(q, "q", None, 3)
-    _need_pool(k_cache, "k_cache", quant)
-    _need_pool(v_cache, "v_cache")
+    nb, K, H_kv, D2 = _quant_pool(k_cache, v_cache, quant)
+    _one_layer(k_cache)
     _need(block_tables, "block_tables", torch.int32, 2)
     _need(context_lens, "context_lens", torch.int32, 1)
     S, H_q, D = q.shape
-    nb, K, H_kv, D2 = k_cache.shape
     if D2 != D or v_cache.shape != k_cache.shape or context_lens.shape[0] != S \
             or block_tables.shape[0] != S:
         raise ValueError("shape mismatch between q, caches, tables and lengths")
@@ -561,11 +648,11 @@ def paged_attention_decode_quant(q: torch.Tensor, k_cache: torch.Tensor, v_cache
     if max_context_len is None:
         max_context_len = int(context_lens.max().item()) if S else 0
     need = attention_quant_workspace_bytes(S, H_q, H_kv, D, K, max_context_len, q.dtype, quant,
-                                           kernel, num_splits)
+                                           kernel, num_splits, share_prefix)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     _need(workspace, "workspace", torch.uint8, 1)
-    cfg = _cfg(kernel, num_splits)
+    cfg = _cfg(kernel, num_splits, share_prefix)
     _check(_attention_quant(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                             block_tables.shape[1], _ptr(context_lens), max_context_len, S, H_q,
                             H_kv, D, K, nb, float(scale), _ptr(out), _ptr(workspace),
@@ -844,6 +931,8 @@ def paged_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if q_out is None:
         q_out = torch.empty((T, H_q, D), dtype=q.dtype, device=q.device)
     dev, dtype = _device_of(q, "q"), q.dtype
+    if quant is not None and quant.format == KV_INT4_HEAD:
+        raise ValueError("int4 pools: paged_kv_write_quant stores the rotated rows")
     if D2 != D or v_cache.shape != k_cache.shape:
         raise ValueError("pools must be [num_blocks, block_size, H_kv, D] of q's head size")
     if quant is None:
@@ -981,3 +1070,184 @@ def verify_draft_tokens(target_probs: torch.Tensor, draft_probs: Optional[torch.
               _vec(num_new, "num_new", i32, S, dev),
               _dtype_code(target_probs)), "pkv_verify_draft_tokens")
     return out_tokens, num_new
+
+
+# ---------------------------------------------------------------------------
+# beam search: selection over beams and vocabulary, forks of the block tables
+# ---------------------------------------------------------------------------
+
+def beam_select_workspace_bytes(num_requests: int, num_beams: int, vocab: int,
+                                num_select: int) -> int:
+    """Workspace bytes of :func:`beam_select`."""
+    _in_32_bits(num_requests | num_beams | vocab | num_select)
+    out = c_sz(0)
+    _check(_beam_ws(num_requests, num_beams, vocab, num_select, ctypes.byref(out)),
+           "pkv_beam_select_workspace_bytes")
+    return int(out.value)
+
+
+def _byte_flags(t: torch.Tensor, name: str, shape, dev: int) -> int:
+    if t.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"{name} must be bool or uint8, got {t.dtype}")
+    return _whole(t, name, t.dtype, shape, dev)
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_select: int,
+                finished: Optional[torch.Tensor] = None, eos_token: int = -1,
+                tokens: Optional[torch.Tensor] = None, parents: Optional[torch.Tensor] = None,
+                scores_out: Optional[torch.Tensor] = None,
+                finished_out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None):
+    """The best ``num_select`` candidates of each request over its beams and the
+    vocabulary: ``logits`` [R * B, V] (rows contiguous, any distance between
+    them), ``scores`` float32 [R, B] the beams' sums of log-probabilities,
+    ``finished`` bool [R, B]: beams whose one candidate is ``eos_token`` at
+    their score.  Returns (tokens int32, parents int32: beam within the request,
+    scores float32, finished bool), each [R, num_select] in descending order,
+    equal candidates by the lowest beam, then token; places without a candidate
+    (all others -infinity) hold -1, -1, -infinity, True."""
+    dev, i32 = _device_of(logits, "logits"), torch.int32
+    if scores.dim() != 2 or logits.dim() != 2:
+        raise ValueError("scores must be [R, B], logits [R * B, V]")
+    R, B = scores.shape
+    rows, V = logits.shape
+    N = int(num_select)
+    _in_32_bits(rows | V | N | eos_token)
+    if rows != R * B:
+        raise ValueError(f"logits must have {R * B} rows, got {rows}")
+    ls, one = logits.stride()
+    if one != 1 and V > 1:
+        raise ValueError("logits: a row must be contiguous")
+
+    def new(dtype):
+        return torch.empty((R, N), dtype=dtype, device=logits.device)
+    if tokens is None:
+        tokens = new(i32)
+    if parents is None:
+        parents = new(i32)
+    if scores_out is None:
+        scores_out = new(torch.float32)
+    if finished_out is None:
+        finished_out = new(torch.bool)
+    if workspace is None:
+        workspace = torch.empty(max(beam_select_workspace_bytes(R, B, V, N), 256),
+                                dtype=torch.uint8, device=logits.device)
+    ws_bytes = workspace.shape[0]
+    _call_on(dev, _beam,
+             (logits.data_ptr(), ls if rows > 1 else V,
+              _whole(scores, "scores", torch.float32, (R, B), dev),
+              None if finished is None else _byte_flags(finished, "finished", (R, B), dev), R, B,
+              V, N, eos_token, _whole(tokens, "tokens", i32, (R, N), dev),
+              _whole(parents, "parents", i32, (R, N), dev),
+              _whole(scores_out, "scores_out", torch.float32, (R, N), dev),
+              _byte_flags(finished_out, "finished_out", (R, N), dev),
+              _vec(workspace, "workspace", torch.uint8, ws_bytes, dev), ws_bytes,
+              _dtype_code(logits)), "pkv_beam_select")
+    return tokens, parents, scores_out, finished_out
+
+
+def fork_workspace_bytes(num_groups: int, group_rows: int, max_blocks_per_seq: int) -> int:
+    """Workspace bytes of :func:`fork_tables`."""
+    _in_32_bits(num_groups | group_rows | max_blocks_per_seq)
+    out = c_sz(0)
+    _check(_fork_ws(num_groups, group_rows, max_blocks_per_seq, ctypes.byref(out)),
+           "pkv_fork_tables_workspace_bytes")
+    return int(out.value)
+
+
+def fork_tables(parents: torch.Tensor, lens: torch.Tensor, held: torch.Tensor,
+                block_tables: torch.Tensor, ring: torch.Tensor, ring_state: torch.Tensor,
+                block_size: int, shared: Optional[torch.Tensor] = None,
+                block_tables_out: Optional[torch.Tensor] = None,
+                lens_out: Optional[torch.Tensor] = None, held_out: Optional[torch.Tensor] = None,
+                ring_state_out: Optional[torch.Tensor] = None,
+                pairs: Optional[torch.Tensor] = None, totals: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None) -> dict:
+    """Block tables after a selection of beams: row (r, i) of groups of B rows
+    continues row ``parents[r, i]`` of its group (int32 [R, B], -1: none).
+    ``lens`` int32 [R * B] cached tokens, ``held`` int32 listed blocks,
+    ``block_tables`` int32 [R * B, max_blocks], ``ring`` int32 with
+    ``ring_state`` int64 [2] the free blocks (as in :func:`step_tables`),
+    ``shared`` int32 leading entries that are never given back.  The first row
+    that continues a parent keeps all its blocks; the others share the full ones
+    and get a fresh block in place of a partly filled one, to be copied by
+    :func:`kv_fork_copy`.  Blocks that no row of the group lists any more return
+    to the ring.  Returns a dict of block_tables_out, lens_out, held_out,
+    ring_state_out, pairs (int64 [R * B, 2], -1: no copy) and totals = {code,
+    rows in use, blocks taken, blocks given back} (code 0: done, else nothing
+    changed); outputs that are given are written, ``block_tables_out`` may be
+    ``block_tables`` (the default), ``lens_out`` ``lens``, ``held_out`` ``held``
+    and ``ring_state_out`` ``ring_state``.  Entries behind a row's end stay."""
+    dev, i32, i64 = _device_of(parents, "parents"), torch.int32, torch.int64
+    if parents.dim() != 2 or block_tables.dim() != 2:
+        raise ValueError("parents must be [groups, rows of a group], block_tables [rows, max_blocks]")
+    R, B = parents.shape
+    S, width = R * B, block_tables.shape[1]
+    if block_tables_out is None:
+        block_tables_out = block_tables
+    if lens_out is None:
+        lens_out = torch.empty(S, dtype=i32, device=parents.device)
+    if held_out is None:
+        held_out = torch.empty(S, dtype=i32, device=parents.device)
+    if ring_state_out is None:
+        ring_state_out = torch.empty(2, dtype=i64, device=parents.device)
+    if pairs is None:
+        pairs = torch.empty((S, 2), dtype=i64, device=parents.device)
+    if totals is None:
+        totals = torch.empty(4, dtype=i32, device=parents.device)
+    if workspace is None:
+        workspace = torch.empty(max(fork_workspace_bytes(R, B, width), 256), dtype=torch.uint8,
+                                device=parents.device)
+    ring_size, ws_bytes = ring.shape[0], workspace.shape[0]
+    _in_32_bits(S | width | block_size)
+    _call_on(dev, _fork,
+             (_whole(parents, "parents", i32, (R, B), dev), _vec(lens, "lens", i32, S, dev),
+              _vec(held, "held", i32, S, dev),
+              None if shared is None else _vec(shared, "shared", i32, S, dev),
+              _table(block_tables, "block_tables", i32, S, dev), width,
+              _vec(ring, "ring", i32, ring_size, dev), ring_size,
+              _vec(ring_state, "ring_state", i64, 2, dev), R, B, block_size,
+              _whole(block_tables_out, "block_tables_out", i32, (S, width), dev),
+              _vec(lens_out, "lens_out", i32, S, dev), _vec(held_out, "held_out", i32, S, dev),
+              _vec(ring_state_out, "ring_state_out", i64, 2, dev),
+              _whole(pairs, "pairs", i64, (S, 2), dev), _vec(totals, "totals", i32, 4, dev),
+              _vec(workspace, "workspace", torch.uint8, ws_bytes, dev), ws_bytes),
+             "pkv_fork_tables")
+    return dict(block_tables_out=block_tables_out, lens_out=lens_out, held_out=held_out,
+                ring_state_out=ring_state_out, pairs=pairs, totals=totals)
+
+
+def kv_fork_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tensor,
+                 lens: torch.Tensor, quant: Optional[KvQuant] = None) -> None:
+    """The copies of :func:`fork_tables`: for each row the leading ``lens[i] %
+    block_size`` tokens of block ``pairs[i][0]`` to block ``pairs[i][1]``
+    (-1 -1: none), K and V, scales with codes.  Pools [num_blocks, block_size,
+    H_kv, D] in any format; plain and int4 pools also [layers, num_blocks, ...],
+    every layer in one launch.  ``lens``: the ``lens_out`` of the fork."""
+    dev = _device_of(k_cache, "k_cache")
+    S = lens.shape[0]
+    if quant is None:
+        _whole(k_cache, "k_cache", k_cache.dtype, k_cache.shape, dev)
+        _whole(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev)
+        code = _dtype_code(k_cache)
+        if k_cache.dim() not in (4, 5):
+            raise ValueError("pools must be [(layers,) num_blocks, block_size, H_kv, D]")
+        nb, K, H, D = k_cache.shape[-4:]
+    else:
+        code = PKV_BF16
+        if quant.format != KV_INT4_HEAD:
+            _one_layer(k_cache)
+        nb, K, H, D = _quant_pool(k_cache, v_cache, quant)
+        if v_cache.shape != k_cache.shape or v_cache.get_device() != dev:
+            raise ValueError("k_cache and v_cache must match in shape and device")
+        if quant.format == KV_INT8_TOKEN:
+            for t in getattr(quant, "_scale_tensors", ()):
+                if t.shape[0] != nb * K or t.get_device() != dev:
+                    raise ValueError("token scales must cover every slot of the pool, on its device")
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    _in_32_bits(S | layers | K | H | D)
+    _call_on(dev, _fork_copy,
+             (k_cache.data_ptr(), v_cache.data_ptr(),
+              _whole(pairs, "pairs", torch.int64, (S, 2), dev),
+              _vec(lens, "lens", torch.int32, S, dev), S, layers, nb, K, H, D, code,
+              None if quant is None else ctypes.byref(quant)), "pkv_kv_fork_copy")
