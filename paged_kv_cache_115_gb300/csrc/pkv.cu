@@ -187,7 +187,7 @@ WsLayout ws_layout(const AttnPlan& p, int H_q, int H_kv, int D) {
 
 pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, int64_t num_blocks,
                           pkv_dtype dt, const pkv_attention_config* cfg, bool tma_aligned,
-                          AttnPlan* plan) {
+                          AttnPlan* plan, int ct = 0) {
   PKV_CHECK(S >= 0 && H_q > 0 && H_kv > 0 && D > 0 && K > 0 && K <= 1024 && max_len >= 0,
             PKV_ERR_INVALID_ARGUMENT, "bad attention sizes");
   PKV_CHECK(H_q % H_kv == 0, PKV_ERR_INVALID_ARGUMENT, "num_q_heads %% num_kv_heads != 0");
@@ -211,7 +211,8 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
     p.kind = KIND_TC;
     p.hpc = tc_hpc(H_kv);
     p.groups = H_kv / p.hpc;
-    const int total = sms;   // one CTA per SM (shared memory bound)
+    // one CTA per SM (shared memory bound), or as many as a pool format takes
+    const int total = sms * pkv::tc_ctas(ct, p.hpc, c.share_prefix != 0);
     p.n_per_group = c.num_splits ? c.num_splits : (total / p.groups > 0 ? total / p.groups : 1);
     const int max_chunks = (int)ceil_div(max_len, pkv::kTcChunk);
     p.pmax = std::max(1, std::min(p.n_per_group, max_chunks));
@@ -258,21 +259,24 @@ pkv_status plan_attention_quant(int S, int H_q, int H_kv, int D, int K, int max_
   PKV_CHECK(D == 64 || D == 128, PKV_ERR_UNSUPPORTED, "quantized pools need head_dim 64 or 128");
   PKV_CHECK(H_q > 0 && H_kv > 0 && H_q % H_kv == 0, PKV_ERR_INVALID_ARGUMENT,
             "num_q_heads %% num_kv_heads != 0");
-  bool scales_ok = quant->format != PKV_KV_INT4_HEAD;
-  if (quant->format == PKV_KV_INT8_TOKEN && quant->k_token_scales && quant->v_token_scales)
+  const bool int4 = quant->format == PKV_KV_INT4_HEAD;
+  bool scales_ok = true;
+  if ((int4 || quant->format == PKV_KV_INT8_TOKEN) && quant->k_token_scales && quant->v_token_scales)
     scales_ok = aligned(quant->k_token_scales, 16) && aligned(quant->v_token_scales, 16);
   const bool tc_ok = q_dt == PKV_BF16 && D == 128 && tc_shape_ok(H_q / H_kv, D, K, num_blocks,
                                                                   PKV_BF16) &&
                      aligned_ok && scales_ok &&
+                     (!int4 || num_blocks * H_kv < (int64_t(1) << 31) - 64) &&
                      (quant->format != PKV_KV_BF16K_FP8V || K % 16 == 0);
   if (c.kernel == 1 || (c.kernel == 0 && tc_ok)) {
     PKV_CHECK(tc_ok, PKV_ERR_UNSUPPORTED,
-              "tensor-core kernel on a one-byte pool needs bf16 queries, head_dim 128, G <= 8, "
+              "tensor-core kernel on a quantized pool needs bf16 queries, head_dim 128, G <= 8, "
               "block_size 8 or a multiple of 16 (a multiple of 16 with a bf16 K pool) and "
               "16-byte aligned pools and scales");
     c.kernel = 1;
-    c.share_prefix = 0;   // shared-prefix groups are a bf16-pool mode
-    return plan_attention(S, H_q, H_kv, D, K, max_len, num_blocks, PKV_BF16, &c, true, plan);
+    if (!int4) c.share_prefix = 0;   // shared-prefix groups: bf16 and INT4 pools
+    return plan_attention(S, H_q, H_kv, D, K, max_len, num_blocks, PKV_BF16, &c, true, plan,
+                          int4 ? 4 : 0);
   }
   c.kernel = 2;
   c.share_prefix = 0;
@@ -300,11 +304,14 @@ template <int D, int HPC, int CT, bool B8, bool SH = false, bool PX = false>
 struct TcInst {
   // stages: as many as fit in ~192 KiB (bf16) / ~203 KiB (one-byte pools)
   // of shared memory, between 2 and 8
-  static constexpr int STAGE_BYTES = pkv::TcCfg<D, HPC, 2, CT>::STAGE;
-  static constexpr int BUDGET = CT ? 217088 - 9216 : 196608;
+  static constexpr int STAGE_BYTES = pkv::TcCfg<D, HPC, 2, CT, B8 && CT == 4>::STAGE;
+  static constexpr int CTAS = pkv::tc_ctas(CT, HPC, SH);    // share the SM's 228 KiB
+  static constexpr int BUDGET =
+      CTAS > 1 ? 233472 / CTAS - 1024 - 9472 : (CT ? 217088 - 9216 : 196608);
   static constexpr int NS_FIT = BUDGET / STAGE_BYTES;
   static constexpr int NS = NS_FIT < 2 ? 2 : (NS_FIT > 8 ? 8 : NS_FIT);
   using C = pkv::TcCfg<D, HPC, NS, CT, B8>;
+  static_assert((C::SMEM + 1024) * CTAS <= 233472, "shared memory of an SM");
   static std::once_flag flags[kMaxDevices];
   static cudaError_t errs[kMaxDevices];
   static pkv_status launch(const pkv::TcParams& prm, int n, int groups, cudaStream_t st, int dev) {
@@ -482,14 +489,14 @@ pkv_status launch_tc_hpc(int hpc, const pkv::TcParams& prm, int n, int groups, c
 
 // 8-token blocks take the kernel's B8 layout; block sizes that are multiples
 // of 16 the plain one (tensor maps from encode_pool_map_heads for both).
-// Shared-prefix groups (prm.share_m > 1) exist for bf16 pools only.
+// Shared-prefix groups (prm.share_m > 1) exist for bf16 and INT4 pools.
 template <int D, int CT>
 pkv_status launch_tc_d(int hpc, int block_size, const pkv::TcParams& prm, int n, int groups,
                        cudaStream_t st, int dev) {
   if constexpr (CT == 3) {
     return launch_tc_hpc<D, CT, false>(hpc, prm, n, groups, st, dev);   // 16-row tiles only
   }
-  if constexpr (CT == 0) {
+  if constexpr (CT == 0 || CT == 4) {
     if (prm.share_m > 1)
       return block_size < pkv::kTile
                  ? launch_tc_hpc<D, CT, true, true>(hpc, prm, n, groups, st, dev)
@@ -535,8 +542,9 @@ pkv_status encode_pool_map_heads(CUtensorMap* map, const void* pool, int64_t num
   pkv_status st = get_encode(&enc);
   if (st != PKV_OK) return st;
   const cuuint64_t eb = one_byte ? 1 : 2;
-  const cuuint64_t c0 = 128 / eb;                 // elements of a 128-byte column
-  const cuuint64_t nh = (cuuint64_t)D * eb / 128; // column groups of a head row
+  const bool narrow = (cuuint64_t)D * eb < 128;   // INT4: 64-byte rows, 64-byte swizzle
+  const cuuint64_t c0 = (narrow ? 64 : 128) / eb; // elements of a column group
+  const cuuint64_t nh = narrow ? 1 : (cuuint64_t)D * eb / 128; // column groups of a head row
   cuuint64_t dims[4] = {c0, (cuuint64_t)(num_blocks * K), nh, (cuuint64_t)H_kv};
   cuuint64_t strides[3] = {(cuuint64_t)H_kv * D * eb, 128, (cuuint64_t)D * eb};
   cuuint32_t box[4] = {(cuuint32_t)c0, (cuuint32_t)std::min(K, pkv::kTile), (cuuint32_t)nh,
@@ -544,9 +552,28 @@ pkv_status encode_pool_map_heads(CUtensorMap* map, const void* pool, int64_t num
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(map, one_byte ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                    4, const_cast<void*>(pool), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   PKV_CHECK(r == CUDA_SUCCESS, PKV_ERR_CUDA, "cuTensorMapEncodeTiled (heads) failed (%d)", (int)r);
+  return PKV_OK;
+}
+
+// Tensor map over the (scale, offset) words of an INT4 pool, [num_blocks * H_kv]
+// rows of K words: boxes of min(K, 16) words x hpc heads.
+pkv_status encode_word_map(CUtensorMap* map, const void* words, int64_t num_blocks, int K, int H_kv,
+                           int hpc) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+  pkv_status st = get_encode(&enc);
+  if (st != PKV_OK) return st;
+  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)(num_blocks * H_kv)};
+  cuuint64_t strides[1] = {(cuuint64_t)K * 4};
+  cuuint32_t box[2] = {(cuuint32_t)std::min(K, pkv::kTile), (cuuint32_t)hpc};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(words), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  PKV_CHECK(r == CUDA_SUCCESS, PKV_ERR_CUDA, "cuTensorMapEncodeTiled (words) failed (%d)", (int)r);
   return PKV_OK;
 }
 
@@ -1506,12 +1533,22 @@ pkv_status attention_impl(const void* q, const void* k_cache, const void* v_cach
     memset(&prm, 0, sizeof(prm));
     // one-byte tiles for quantized pools, except the bf16 K pool of the pair
     const bool k16 = quant != nullptr && quant->format == PKV_KV_BF16K_FP8V;
-    st = encode_pool_map_heads(&prm.tmap_k, k_cache, num_blocks, block_size, H_kv, D, plan.hpc,
+    const bool i4 = quant != nullptr && quant->format == PKV_KV_INT4_HEAD;
+    const int cols = i4 ? D / 2 : D;               // bytes of a quantized row
+    st = encode_pool_map_heads(&prm.tmap_k, k_cache, num_blocks, block_size, H_kv, cols, plan.hpc,
                                quant != nullptr && !k16);
     if (st != PKV_OK) return st;
-    st = encode_pool_map_heads(&prm.tmap_v, v_cache, num_blocks, block_size, H_kv, D, plan.hpc,
+    st = encode_pool_map_heads(&prm.tmap_v, v_cache, num_blocks, block_size, H_kv, cols, plan.hpc,
                                quant != nullptr);
     if (st != PKV_OK) return st;
+    if (i4) {
+      st = encode_word_map(&prm.tmap_ks, quant->k_token_scales, num_blocks, block_size, H_kv,
+                           plan.hpc);
+      if (st == PKV_OK)
+        st = encode_word_map(&prm.tmap_vs, quant->v_token_scales, num_blocks, block_size, H_kv,
+                             plan.hpc);
+      if (st != PKV_OK) return st;
+    }
     if (quant) {
       prm.v_scale = quant->format == PKV_KV_INT8_TOKEN ? 1.f : quant->v_scale;
       prm.k_ts = quant->k_token_scales;
@@ -1562,6 +1599,9 @@ pkv_status attention_impl(const void* q, const void* k_cache, const void* v_cach
                                  dev);
       } else if (quant->format == PKV_KV_BF16K_FP8V) {
         st = launch_tc_d<128, 3>(plan.hpc, block_size, prm, plan.n_per_group, plan.groups, strm,
+                                 dev);
+      } else if (quant->format == PKV_KV_INT4_HEAD) {
+        st = launch_tc_d<128, 4>(plan.hpc, block_size, prm, plan.n_per_group, plan.groups, strm,
                                  dev);
       } else {
         st = launch_tc_d<128, 2>(plan.hpc, block_size, prm, plan.n_per_group, plan.groups, strm,

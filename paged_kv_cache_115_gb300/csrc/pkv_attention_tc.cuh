@@ -1,17 +1,18 @@
 // TMA + tensor-core decode-attention partition kernel (bf16 queries; bf16,
-// FP8 e4m3 or INT8 pools).
+// FP8 e4m3, INT8 or INT4 pools).
 #pragma once
 
 #include "pkv_attention_common.cuh"
+#include "pkv_int4.cuh"
 
 namespace pkv {
 
 // ===========================================================================
 // TMA + tensor-core partition kernel (bf16 queries, block_size % 16 == 0,
-// G <= 8; bf16 pools with D in {64, 128}, one-byte pools with D = 128).
+// G <= 8; bf16 pools with D in {64, 128}, quantized pools with D = 128).
 //
 // Work decomposition: the token range of the batch is cut into chunks (16
-// tokens for bf16 pools, 32 for one-byte pools), numbered sequence-major;
+// tokens for bf16 pools, 32 for quantized ones), numbered sequence-major;
 // with T chunks and n CTAs per KV-head group, CTA i owns chunks
 // [floor(i T / n), floor((i+1) T / n)) — equal work per CTA whatever the
 // length mix.  A run of chunks of one sequence inside a CTA is a split-K
@@ -42,8 +43,15 @@ constexpr int kTcMaxShareSeqs = 1024;
 constexpr int kBoxBytes = kTile * 128;
 
 // tokens per stream-K chunk for a pool format (0 bf16, 1 FP8, 2 INT8,
-// 3 bf16 K with FP8 V)
-constexpr int tc_chunk_tokens(int ct) { return ct == 1 || ct == 2 ? 2 * kTile : kTile; }
+// 3 bf16 K with FP8 V, 4 INT4)
+constexpr int tc_chunk_tokens(int ct) { return ct == 0 || ct == 3 ? kTile : 2 * kTile; }
+
+// CTAs that share an SM.  4-bit pools bring twice the values a byte and are bound
+// by what their warps issue, so more warps than heads work on an SM; with the two
+// column blocks of shared-prefix groups the accumulators need the registers.
+constexpr int tc_ctas(int ct, int hpc, bool sh) {
+  return ct != 4 || sh ? 1 : (hpc == 8 ? 2 : (hpc == 4 ? 3 : (hpc == 2 ? 6 : 8)));
+}
 
 // Attention behind a shared prefix (pkv_prefix.cuh): the prefix kernel and
 // this kernel (instantiated with PX, on the tokens from prefix_len on) share
@@ -110,6 +118,8 @@ __host__ __device__ __forceinline__ int px_ctas(const PxSplit& x, long long work
 struct TcParams {
   CUtensorMap tmap_k;
   CUtensorMap tmap_v;
+  CUtensorMap tmap_ks;      // INT4: (scale, offset) words of K and V
+  CUtensorMap tmap_vs;
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
   const int32_t* block_tables;
@@ -153,7 +163,7 @@ struct TcParams {
 
 // Pool formats of the kernel: CT 0 = bf16, 1 = FP8 e4m3 (per-tensor scale),
 // 2 = INT8 (per-slot scale), 3 = bf16 K pool with an FP8 e4m3 V pool
-// (per-tensor V scale).  A head's row is one 128-byte column group in a
+// (per-tensor V scale), 4 = INT4 (scale and offset per token and head).  A head's row is one 128-byte column group in a
 // one-byte pool of D = 128, D / 64 groups in a bf16 pool.  One-byte tiles are read straight
 // into f16 mma fragments (e4m3 and int8 codes are exact in f16); bf16 tiles
 // go through ldmatrix into bf16 mma fragments.
@@ -164,6 +174,10 @@ struct TcParams {
 // c at chunk c ^ (r & 7)).  A row of a pool block holds every KV head
 // contiguously, so one 4-D TMA copy (column, row, column group, head) brings
 // a tile's rows for all HPC heads and column groups of the CTA at once.
+//
+// INT4 pools (CT 4): a head's row is 64 bytes, boxes of 64-byte rows in the
+// 64-byte swizzle (row r's 16-byte chunk c at chunk c ^ (r / 2 & 3)), then the
+// (scale, offset) words of each tile as [head][16 tokens].  See below at "INT4".
 //
 // 8-token blocks (B8): a tile spans two blocks, one copy each, laid out
 // [tile][block half][head][column group][8 rows x 128 bytes]: rows 8..15 of
@@ -196,6 +210,45 @@ __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t w, uint32_t& lo, uint
 // multiplies o once per partition instead.
 constexpr float kQuantSlack = 4.f;
 
+// INT4.  With row t's scale s_t and offset z_t and codes c,
+//   q . K_t = s_t (q . c_t) + z_t sum(q),
+//   sum_t p_t V_t = sum_t (p_t s_t) c_t + sum_t p_t z_t,
+// so codes enter the tensor core as they are, scales and offsets act on scores
+// and weights, and no value is dequantized by itself.  A 32-bit word holds eight
+// codes of a row; a mask and an exponent make f16 pairs of the codes at nibbles
+// (i, i + 4):
+//   w & 0x000f000f | 0x6400 6400 = 1024 + c (1024 taken off exactly),
+//   w & 0x00f000f0 | 0x5400 5400 = 64 + c   (left in: 64 sum(q) over those
+//     columns comes off the score, 64 sum(w) off those rows of o at the end),
+// twice, the second time from w >> 8: five integer operations and two additions
+// for eight codes.  The mma k order (K) and row order (V) are permuted to fit.
+// K: lane (g, tq) holds columns 32 tq .. 32 tq + 31 of token pi(g) (and pi(g) +
+// 8): one 16-byte load a row.  V: lane (g, tq) holds columns 16 g .. 16 g + 15 of
+// tokens pi(2 tq), pi(2 tq + 1) (and + 8), 8 bytes each, paired by byte permutes
+// of two words.  pi = 0 3 1 2 4 7 5 6 keeps both free of bank conflicts.
+__device__ __forceinline__ uint32_t int4_lo(uint32_t w) {          // nibbles 0 and 4
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(0x000f000fu), "r"(0x64006400u));
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&r), __floats2half2_rn(1024.f, 1024.f));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t int4_hi64(uint32_t w) {        // nibbles 1 and 5, + 64
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(0x00f000f0u), "r"(0x54005400u));
+  return r;
+}
+__device__ __forceinline__ int int4_pi(int g) { return (g & 4) | ((0x2130 >> ((g & 3) * 4)) & 3); }
+
+// 2-D tiled load global -> shared, completion counted on an mbarrier.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int c0, int c1, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 // 4-D tiled load global -> shared, completion counted on an mbarrier.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int c0, int c1, int c2, int c3, uint64_t policy) {
@@ -211,39 +264,52 @@ template <int D, int HPC, int NS, int CT = 0, bool B8 = false>
 struct TcCfg {
   static constexpr bool KB = CT == 0 || CT == 3;          // K tiles in bf16
   static constexpr bool VB = CT == 0;                     // V tiles in bf16
-  static constexpr int TL = CT == 1 || CT == 2 ? 2 : 1;   // 16-row tiles per chunk
+  static constexpr bool I4 = CT == 4;
+  static constexpr int TL = tc_chunk_tokens(CT) / kTile;  // 16-row tiles per chunk
   static constexpr int CH = kTile * TL;                   // tokens per chunk
   static constexpr int NHK = KB ? D / 64 : 1;             // boxes per head row, K
   static constexpr int NHV = VB ? D / 64 : 1;             // boxes per head row, V
   static constexpr int NH = NHV;                          // (V tile rows, zeroed past the end)
-  static constexpr int KPART = HPC * TL * NHK * kBoxBytes;
-  static constexpr int VPART = HPC * TL * NHV * kBoxBytes;
+  static constexpr int ROWB = I4 ? 64 : 128;              // bytes of a box row
+  static constexpr int BOX = kTile * ROWB;                // one head's rows of a tile
+  static constexpr int KPART = HPC * TL * NHK * BOX;
+  static constexpr int VPART = HPC * TL * NHV * BOX;
   static constexpr int SCALE_OFF = KPART + VPART;
-  static constexpr int SCALE_BYTES = CT == 2 ? 2 * TL * kTile * 4 : 0;
+  // INT4: words of one box (a tile, or half of one: B8), on a 128-byte boundary
+  static constexpr int SUB = B8 ? 2 : 1;
+  static constexpr int SWORDS = kTile / SUB;
+  static constexpr int SBOX = HPC * SWORDS * 4 < 128 ? 128 : HPC * SWORDS * 4;
+  static constexpr int SCALE_BYTES =
+      I4 ? 2 * TL * SUB * SBOX : (CT == 2 ? 2 * TL * kTile * 4 : 0);
   static constexpr int STAGE = ((KPART + VPART + SCALE_BYTES + 1023) / 1024) * 1024;
   static constexpr int THREADS = (HPC + 1) * 32;
   static constexpr int BAR_OFF = NS * STAGE;
   static constexpr int CSTART_OFF = BAR_OFF + 2 * NS * 8 + 16;
   static constexpr int SMEM = CSTART_OFF + (kTcMaxSeqs + 1) * 4 + 1024;  // + alignment slack
-  static constexpr uint32_t TX = KPART + VPART + SCALE_BYTES;  // bytes landing per stage
-  static_assert(CT == 0 || D == 128, "one-byte pools need head_dim 128");
+  static constexpr uint32_t TX =                               // bytes landing per stage
+      KPART + VPART + (I4 ? 2 * TL * HPC * kTile * 4 : SCALE_BYTES);
+  static_assert(CT == 0 || D == 128, "quantized pools need head_dim 128");
   static_assert(CT != 3 || !B8, "the bf16-K / FP8-V pair needs 16-token tiles of one block");
-  static_assert(tc_chunk_tokens(CT) == CH, "chunk size");
-  static constexpr int TBOXK = HPC * NHK * kBoxBytes;  // one tile, all heads of the CTA
-  static constexpr int TBOXV = HPC * NHV * kBoxBytes;
+  static constexpr int TBOXK = HPC * NHK * BOX;        // one tile, all heads of the CTA
+  static constexpr int TBOXV = HPC * NHV * BOX;
   static constexpr int TBOX = TBOXK;                   // (formats with equal K and V tiles)
-  static constexpr int UST = HPC * NHK * 1024;         // B8: one block half of a tile, all heads
-  static constexpr int RSTEP8 = B8 ? UST : 1024;       // rows 8..15 relative to rows 0..7
-  static constexpr int HSTR = B8 ? 1024 : kBoxBytes;   // column group stride
+  static constexpr int UST = HPC * NHK * 8 * ROWB;     // B8: one block half of a tile, all heads
+  static constexpr int RSTEP8 = B8 ? UST : 8 * ROWB;   // rows 8..15 relative to rows 0..7
+  static constexpr int HSTR = B8 ? 8 * ROWB : BOX;     // column group stride
   // smem offset of row 0 of head h's box (tile t, column group half) of K
   // (kv 0) or V; the B8 layout exists for formats whose K and V tiles match
   __host__ __device__ static constexpr int box_off(int kv, int h, int t, int half) {
-    return B8 ? kv * KPART + t * 2 * UST + (h * NHK + half) * 1024
-              : (kv ? KPART + t * TBOXV + (h * NHV + half) * kBoxBytes
-                    : t * TBOXK + (h * NHK + half) * kBoxBytes);
+    return B8 ? kv * KPART + t * 2 * UST + (h * NHK + half) * 8 * ROWB
+              : (kv ? KPART + t * TBOXV + (h * NHV + half) * BOX
+                    : t * TBOXK + (h * NHK + half) * BOX);
   }
   // offset of row r (0..15) inside a box
-  __host__ __device__ static constexpr int row_off(int r) { return (r & 7) * 128 + (r >> 3) * RSTEP8; }
+  __host__ __device__ static constexpr int row_off(int r) { return (r & 7) * ROWB + (r >> 3) * RSTEP8; }
+  // INT4: offset of the word of row r of tile t of head h
+  __host__ __device__ static constexpr int word_off(int kv, int h, int t, int r) {
+    return SCALE_OFF + ((kv * TL + t) * SUB + (B8 ? r >> 3 : 0)) * SBOX +
+           (h * SWORDS + (B8 ? r & 7 : r)) * 4;
+  }
 };
 
 // Largest CTA index i whose range starts at or before chunk c.
@@ -305,14 +371,15 @@ __host__ __device__ __forceinline__ int4 tc_seq_meta(const int* cstart, int s, i
 }
 
 template <int D, int HPC, int NS, int CT = 0, bool B8 = false, bool SH = false, bool PX = false>
-__global__ void __launch_bounds__(TcCfg<D, HPC, NS, CT, B8>::THREADS, 1)
+__global__ void __launch_bounds__(TcCfg<D, HPC, NS, CT, B8>::THREADS, tc_ctas(CT, HPC, SH))
 attn_tc_kernel(const __grid_constant__ TcParams p) {
   using C = TcCfg<D, HPC, NS, CT, B8>;
   constexpr int TL = C::TL, CH = C::CH;
   // 8-column blocks of the score tile: two in shared-prefix mode (the query
   // heads of a group's members side by side), one otherwise
   constexpr int NB = SH ? 2 : 1;
-  static_assert(!SH || CT == 0, "shared-prefix groups need bf16 pools");
+  constexpr bool I4 = C::I4;
+  static_assert(!SH || CT == 0 || CT == 4, "shared-prefix groups need bf16 or INT4 pools");
   static_assert(!PX || (CT == 0 && !SH), "shared-prefix attention needs bf16 pools");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -548,6 +615,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     if (lane == 0) {
       prefetch_tensormap(&p.tmap_k);
       prefetch_tensormap(&p.tmap_v);
+      if constexpr (I4) {
+        prefetch_tensormap(&p.tmap_ks);
+        prefetch_tensormap(&p.tmap_vs);
+      }
     }
     const uint64_t policy = l2_policy_evict_first();
     int k = 0;
@@ -576,7 +647,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           // one 4-D box per (K / V, tile, block half): all heads of the CTA,
           // all column groups, 8 rows; then (INT8) the scales of each half
           constexpr int NB = 4 * TL;
-          for (int i = lane; i < NB + (CT == 2 ? NB : 0); i += 32) {
+          for (int i = lane; i < NB + (CT == 2 || I4 ? NB : 0); i += 32) {
             const int j = i < NB ? i : i - NB;
             const int kv = j / (2 * TL), t = (j >> 1) % TL, u = j & 1;
             const int r0 = t ? r[TL - 1][0] : r[0][0];
@@ -586,6 +657,13 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
               tma_load_4d(smem_u32(sb + kv * C::KPART + (2 * t + u) * C::UST),
                           kv ? &p.tmap_v : &p.tmap_k, bar_full + 8 * stage, 0, rr, 0, head0,
                           policy);
+            } else if constexpr (I4) {
+              // no rows: words out of bounds too, which TMA fills with zeros
+              const int blk = rr >= 0 ? rr / K : 0;
+              tma_load_2d(smem_u32(sb + C::word_off(kv, 0, t, 8 * u)),
+                          kv ? &p.tmap_vs : &p.tmap_ks, bar_full + 8 * stage,
+                          rr >= 0 ? rr - blk * K : 0,
+                          rr >= 0 ? blk * (int)(gridDim.y * HPC) + head0 : -2 * HPC, policy);
             } else if constexpr (CT == 2) {
               // a half tile with no rows reads slot 0's scales, which meet zero codes
               const float* src = (kv ? p.v_ts : p.k_ts) + (rr >= 0 ? rr : 0);
@@ -597,13 +675,19 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           // one 4-D box per (K / V, tile): 16 rows of all heads of the CTA and
           // all column groups; then (INT8) each tile's 16 per-slot scales
           constexpr int NB = 2 * TL;
-          for (int i = lane; i < NB + (CT == 2 ? NB : 0); i += 32) {
+          for (int i = lane; i < NB + (CT == 2 || I4 ? NB : 0); i += 32) {
             const int j = i < NB ? i : i - NB;
             const int kv = j / TL, t = j - kv * TL;
             const int rr = t ? r[TL - 1][0] : r[0][0];
             if (i < NB) {
               tma_load_4d(smem_u32(sb + C::box_off(kv, 0, t, 0)), kv ? &p.tmap_v : &p.tmap_k,
                           bar_full + 8 * stage, 0, rr, 0, head0, policy);
+            } else if constexpr (I4) {
+              const int blk = rr >= 0 ? rr / K : 0;
+              tma_load_2d(smem_u32(sb + C::word_off(kv, 0, t, 0)),
+                          kv ? &p.tmap_vs : &p.tmap_ks, bar_full + 8 * stage,
+                          rr >= 0 ? rr - blk * K : 0,
+                          rr >= 0 ? blk * (int)(gridDim.y * HPC) + head0 : -2 * HPC, policy);
             } else if constexpr (CT == 2) {
               // a tile with no rows reads slot 0's scales, which meet zero codes
               const float* src = (kv ? p.v_ts : p.k_ts) + (rr >= 0 ? rr : 0);
@@ -632,12 +716,23 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
 
   uint32_t qf[NB][D / 16][2];
   float o[NB][D / 16][4];
-  float slc0 = sl, slc1 = sl;   // per score column (one-byte pools: q's 2^e folded in)
+  float slc0[NB], slc1[NB];     // per score column (one-byte pools: q's 2^e folded in)
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) slc0[nb] = slc1[nb] = sl;
+  // INT4, per score column: slc times 64 sum(q) over the columns read as 64 + code,
+  // and times sum(q)
+  float off0[I4 ? NB : 1], off1[I4 ? NB : 1], qs0[I4 ? NB : 1], qs1[I4 ? NB : 1];
+  const int pg = I4 ? int4_pi(g) : g;     // token row of a tile that mma row g holds
+  // INT4: V scales enter times vinv, the power of two that puts the largest seen
+  // (up to vcap) at 1 .. 8, so that f16 weights neither overflow nor fade
+  float vinv = 1.f, vcap = 0.f;
   float m0[NB], m1[NB], l0[NB], l1[NB];
   // INT8 pools: V enters the tensor core as 1152 + code (the exact f16 the
   // byte permute makes, without the subtraction); vw = sum of weight x V
   // scale per column, so that 1152 vw is taken off o at the partition end
-  float vw0 = 0.f, vw1 = 0.f;
+  float vw0[NB], vw1[NB];
+  // INT4: vw = sum of the weights as they enter, vz = sum of weight x V offset
+  float vz0[NB], vz1[NB];
   int u = seq_of_chunk(cstart, NU, cb);
   int ut0 = 0, uend = 0, ulim = 0;   // the unit's tokens [ut0, uend); min column limit
   int qr0 = 0, nq = 0, ncol = 0;     // first query row, query rows, valid score columns
@@ -682,6 +777,64 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
             }
           }
         }
+      } else if constexpr (I4) {
+        // f16 fragments in the order of the K words (see "INT4"), each head
+        // scaled by a power of two as below
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int cq = 8 * nb + g;
+          const __nv_bfloat16* qrow =
+              p.q + ((int64_t)(qr0 + (cq < ncol ? cq / G : 0)) * H_q + j * G + cq % G) * D + 32 * tq;
+          float qv[4][8];
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (cq < ncol) raw = __ldg(reinterpret_cast<const uint4*>(qrow) + i);
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              qv[i][2 * e] = __uint_as_float(w[e] << 16);
+              qv[i][2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+              amax = fmaxf(amax, fmaxf(fabsf(qv[i][2 * e]), fabsf(qv[i][2 * e + 1])));
+            }
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          const int eg = amax > 0.f ? ilogbf(amax) - 14 : 0;
+          const float down = ldexpf(1.f, -eg);
+          float even = 0.f, odd = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float* x = qv[i];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= down;
+            qf[nb][2 * i][0] = pack_f16x2(x[0], x[4]);
+            qf[nb][2 * i][1] = pack_f16x2(x[1], x[5]);
+            qf[nb][2 * i + 1][0] = pack_f16x2(x[2], x[6]);
+            qf[nb][2 * i + 1][1] = pack_f16x2(x[3], x[7]);
+            even += (x[0] + x[2]) + (x[4] + x[6]);
+            odd += (x[1] + x[3]) + (x[5] + x[7]);
+          }
+#pragma unroll
+          for (int o1 = 1; o1 < 4; o1 <<= 1) {
+            even += __shfl_xor_sync(0xffffffffu, even, o1);
+            odd += __shfl_xor_sync(0xffffffffu, odd, o1);
+          }
+          // score columns of this thread are 2tq, 2tq+1 (held by lanes 8tq, 8tq+4)
+          slc0[nb] = ldexpf(sl, __shfl_sync(0xffffffffu, eg, 8 * tq));
+          slc1[nb] = ldexpf(sl, __shfl_sync(0xffffffffu, eg, 8 * tq + 4));
+          const float e0 = __shfl_sync(0xffffffffu, even, 8 * tq);
+          const float e1 = __shfl_sync(0xffffffffu, even, 8 * tq + 4);
+          const float d0 = __shfl_sync(0xffffffffu, odd, 8 * tq);
+          const float d1 = __shfl_sync(0xffffffffu, odd, 8 * tq + 4);
+          off0[nb] = slc0[nb] * (64.f * d0);
+          off1[nb] = slc1[nb] * (64.f * d1);
+          qs0[nb] = slc0[nb] * (e0 + d0);
+          qs1[nb] = slc1[nb] * (e1 + d1);
+        }
+        vinv = 1.f;
+        vcap = 0.f;
       } else {
         // f16 fragments.  The mma k order inside each 16-column step is
         // permuted (k 2tq, 2tq+1 -> d 4tq, 4tq+1; k 2tq+8, 2tq+9 -> d 4tq+2,
@@ -718,8 +871,8 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         // score columns of this thread are heads 2tq, 2tq+1 (held by lanes 8tq, 8tq+4)
         const int e0 = __shfl_sync(0xffffffffu, eg, 8 * tq);
         const int e1 = __shfl_sync(0xffffffffu, eg, 8 * tq + 4);
-        slc0 = ldexpf(sl, e0);
-        slc1 = ldexpf(sl, e1);
+        slc0[0] = ldexpf(sl, e0);
+        slc1[0] = ldexpf(sl, e1);
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -728,8 +881,8 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           o[nb][mt][0] = o[nb][mt][1] = o[nb][mt][2] = o[nb][mt][3] = 0.f;
         m0[nb] = m1[nb] = -INFINITY;
         l0[nb] = l1[nb] = 0.f;
+        vw0[nb] = vw1[nb] = vz0[nb] = vz1[nb] = 0.f;
       }
-      vw0 = vw1 = 0.f;
     }
     const int cpos = ut0 + (c - a) * CH;                 // key position of chunk row 0
     const int valid = min(CH, uend - cpos);             // tokens of this chunk
@@ -742,9 +895,22 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     // per-token-row K scales and V scales (folded into P) of rows g, g+8 of
     // each tile: INT8 per slot, FP8 per tensor (K's folded into sl)
     float ksr[TL][2], vsr[TL][2];
+    float kzr[I4 ? TL : 1][2], vzr[I4 ? TL : 1][2];       // INT4: offsets
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
-      if constexpr (CT == 2) {
+      if constexpr (I4) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t kw = *reinterpret_cast<const uint32_t*>(sb + C::word_off(0, w, t, pg + 8 * r));
+          uint32_t vw = *reinterpret_cast<const uint32_t*>(sb + C::word_off(1, w, t, pg + 8 * r));
+          // words past the end may hold anything: 0-weight x V must stay 0
+          if (t * kTile + pg + 8 * r >= valid) vw = 0u;
+          ksr[t][r] = int4_scale(kw);
+          kzr[t][r] = int4_offset(kw);
+          vsr[t][r] = int4_scale(vw);
+          vzr[t][r] = int4_offset(vw);
+        }
+      } else if constexpr (CT == 2) {
         const float* kscl = reinterpret_cast<const float*>(sb + C::SCALE_OFF + t * 64);
         const float* vscl = reinterpret_cast<const float*>(sb + C::SCALE_OFF + (TL + t) * 64);
         // slots past the sequence end may hold anything; their weight is 0
@@ -758,7 +924,36 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         vsr[t][0] = vsr[t][1] = 1.f;      // FP8: the V scale multiplies o at the end
       }
     }
-    if (valid < CH) {
+    if constexpr (I4) {
+      float vmx = 0.f;
+#pragma unroll
+      for (int t = 0; t < TL; ++t) vmx = fmaxf(vmx, fmaxf(vsr[t][0], vsr[t][1]));
+      if (__any_sync(0xffffffffu, vmx > vcap)) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+          vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, off));
+        const int ev = max(-120, min(120, ilogbf(vmx)));
+        const float was = vinv;
+        vinv = ldexpf(1.f, -ev);
+        vcap = ldexpf(8.f, ev);
+        const float f = vinv / was;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          vw0[nb] *= f;
+          vw1[nb] *= f;
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nb][mt][e] *= f;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < TL; ++t) {
+        vsr[t][0] *= vinv;
+        vsr[t][1] *= vinv;
+      }
+    }
+    if (!I4 && valid < CH) {
       // rows past the sequence end may hold anything (stale slots, NaN
       // codes): give them zero V so that 0-weight x V stays 0 in the tensor core
       const int nvec = (CH - valid) * C::NH * 8;
@@ -806,6 +1001,27 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) sacc[0][0][e] += sodd[e];
       }
+    } else if constexpr (I4) {
+#pragma unroll
+      for (int t = 0; t < TL; ++t) {
+        const uint8_t* kt = sb + C::box_off(0, w, t, 0) + C::row_off(pg) + ((tq ^ ((pg >> 1) & 3)) << 4);
+        const uint4 ra = *reinterpret_cast<const uint4*>(kt);
+        const uint4 rb = *reinterpret_cast<const uint4*>(kt + C::RSTEP8);
+        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t x = hf ? wa[i] >> 8 : wa[i], y = hf ? wb[i] >> 8 : wb[i];
+            const uint32_t a0 = int4_lo(x), a1 = int4_lo(y), a2 = int4_hi64(x), a3 = int4_hi64(y);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              if (nb < nbv)
+                mma_f16_16816(sacc[nb][t], a0, a1, a2, a3, qf[nb][2 * i + hf][0],
+                              qf[nb][2 * i + hf][1]);
+          }
+        }
+      }
     } else {
       // byte tiles: rows g and g+8 share a swizzle phase; the 16-code chunk
       // ks holds d = 16 ks .. 16 ks + 15, this thread's 4 codes at byte 4 tq
@@ -842,14 +1058,24 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
       for (int t = 0; t < TL; ++t) {
-        x[t][0] = sacc[nb][t][0] * slc0 * ksr[t][0];
-        x[t][1] = sacc[nb][t][1] * slc1 * ksr[t][0];
-        x[t][2] = sacc[nb][t][2] * slc0 * ksr[t][1];
-        x[t][3] = sacc[nb][t][3] * slc1 * ksr[t][1];
+        if constexpr (I4) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            x[t][2 * r] = fmaf(ksr[t][r], fmaf(sacc[nb][t][2 * r], slc0[nb], -off0[nb]),
+                               kzr[t][r] * qs0[nb]);
+            x[t][2 * r + 1] = fmaf(ksr[t][r], fmaf(sacc[nb][t][2 * r + 1], slc1[nb], -off1[nb]),
+                                   kzr[t][r] * qs1[nb]);
+          }
+        } else {
+          x[t][0] = sacc[nb][t][0] * slc0[nb] * ksr[t][0];
+          x[t][1] = sacc[nb][t][1] * slc1[nb] * ksr[t][0];
+          x[t][2] = sacc[nb][t][2] * slc0[nb] * ksr[t][1];
+          x[t][3] = sacc[nb][t][3] * slc1[nb] * ksr[t][1];
+        }
         // causal limit of each score column (decode: the unit's end); a
         // chunk wholly below every column's limit needs no mask
         if (cmask) {
-          const int kp = cpos + t * kTile + g;   // key position of row g
+          const int kp = cpos + t * kTile + pg;  // key position of row g
           const int limA = col_lim(8 * nb + 2 * tq), limB = col_lim(8 * nb + 2 * tq + 1);
           if (kp > limA) x[t][0] = -INFINITY;
           if (kp > limB) x[t][1] = -INFINITY;
@@ -898,27 +1124,29 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         // o and l are rescaled rarely; the weights stay below 2^kQuantSlack and
         // the final o / l is the same softmax.  A column that has seen no
         // visible key keeps (-inf, 0, 0).
-        const bool need = mx0 > m0[0] + kQuantSlack || mx1 > m1[0] + kQuantSlack;
+        const bool need = mx0 > m0[nb] + kQuantSlack || mx1 > m1[nb] + kQuantSlack;
         if (__any_sync(0xffffffffu, need)) {
-          const float mn0 = fmaxf(m0[0], mx0), mn1 = fmaxf(m1[0], mx1);
+          const float mn0 = fmaxf(m0[nb], mx0), mn1 = fmaxf(m1[nb], mx1);
           const float mu0 = mn0 == -INFINITY ? 0.f : mn0, mu1 = mn1 == -INFINITY ? 0.f : mn1;
-          const float al0 = exp2f(m0[0] - mu0), al1 = exp2f(m1[0] - mu1);
-          l0[0] *= al0;
-          l1[0] *= al1;
-          vw0 *= al0;
-          vw1 *= al1;
-          m0[0] = mn0;
-          m1[0] = mn1;
+          const float al0 = exp2f(m0[nb] - mu0), al1 = exp2f(m1[nb] - mu1);
+          l0[nb] *= al0;
+          l1[nb] *= al1;
+          vw0[nb] *= al0;
+          vw1[nb] *= al1;
+          vz0[nb] *= al0;
+          vz1[nb] *= al1;
+          m0[nb] = mn0;
+          m1[nb] = mn1;
 #pragma unroll
           for (int mt = 0; mt < D / 16; ++mt) {
-            o[0][mt][0] *= al0;
-            o[0][mt][1] *= al1;
-            o[0][mt][2] *= al0;
-            o[0][mt][3] *= al1;
+            o[nb][mt][0] *= al0;
+            o[nb][mt][1] *= al1;
+            o[nb][mt][2] *= al0;
+            o[nb][mt][3] *= al1;
           }
         }
-        const float mu0 = m0[0] == -INFINITY ? 0.f : m0[0];
-        const float mu1 = m1[0] == -INFINITY ? 0.f : m1[0];
+        const float mu0 = m0[nb] == -INFINITY ? 0.f : m0[nb];
+        const float mu1 = m1[nb] == -INFINITY ? 0.f : m1[nb];
 #pragma unroll
         for (int t = 0; t < TL; ++t) {
           pr[t][0] = ex2_approx_ftz(x[t][0] - mu0);
@@ -928,8 +1156,8 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           ps0 += pr[t][0] + pr[t][2];
           ps1 += pr[t][1] + pr[t][3];
         }
-        l0[0] += ps0;
-        l1[0] += ps1;
+        l0[nb] += ps0;
+        l1[nb] += ps1;
       }
       // P enters the tensor core as a hi + lo pair of 16-bit terms so that the
       // product carries ~16 significant bits of each weight (one bf16 rounding
@@ -944,9 +1172,13 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         } else {
           const float w0 = pr[t][0] * vsr[t][0], w1 = pr[t][1] * vsr[t][0];
           const float w2 = pr[t][2] * vsr[t][1], w3 = pr[t][3] * vsr[t][1];
-          if constexpr (CT == 2) {
-            vw0 += w0 + w2;
-            vw1 += w1 + w3;
+          if constexpr (CT == 2 || I4) {
+            vw0[nb] += w0 + w2;
+            vw1[nb] += w1 + w3;
+          }
+          if constexpr (I4) {
+            vz0[nb] = fmaf(pr[t][0], vzr[t][0], fmaf(pr[t][2], vzr[t][1], vz0[nb]));
+            vz1[nb] = fmaf(pr[t][1], vzr[t][0], fmaf(pr[t][3], vzr[t][1], vz1[nb]));
           }
           split_f16x2(w0, w1, ph01, pl01);
           split_f16x2(w2, w3, ph23, pl23);
@@ -959,7 +1191,45 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     }
     // ---- O^T[D x 8] += V^T[D x 16 tok] . P^T[16 tok x 8], per tile and
     // column block (one V fragment feeds every column block)
-    if constexpr (!C::VB) {
+    if constexpr (I4) {
+      // rows of m tile mt: row g -> d = 16 g + 2 mt, row g + 8 -> the one behind it
+      const int j0 = (tq & 1) | ((tq & 2) << 1), j1 = j0 ^ 3;        // pi(2 tq), pi(2 tq + 1)
+#pragma unroll
+      for (int t = 0; t < TL; ++t) {
+        const uint8_t* vt = sb + C::box_off(1, w, t, 0) + (g & 1) * 8;
+        const uint8_t* v0 = vt + C::row_off(j0) + (((g >> 1) ^ (j0 >> 1 & 3)) << 4);
+        const uint8_t* v1 = vt + C::row_off(j1) + (((g >> 1) ^ (j1 >> 1 & 3)) << 4);
+        const uint2 r0 = *reinterpret_cast<const uint2*>(v0), r1 = *reinterpret_cast<const uint2*>(v1);
+        const uint2 r2 = *reinterpret_cast<const uint2*>(v0 + C::RSTEP8);
+        const uint2 r3 = *reinterpret_cast<const uint2*>(v1 + C::RSTEP8);
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {            // words (q4 / 2), their halves
+          const uint32_t sel = q4 & 1 ? 0x7632u : 0x5410u;
+          const uint32_t lo = __byte_perm(q4 < 2 ? r0.x : r0.y, q4 < 2 ? r1.x : r1.y, sel);
+          const uint32_t hi = __byte_perm(q4 < 2 ? r2.x : r2.y, q4 < 2 ? r3.x : r3.y, sel);
+          uint32_t af[2][4];
+#pragma unroll
+          for (int uu = 0; uu < 2; ++uu) {
+            const uint32_t x = uu ? lo >> 8 : lo, y = uu ? hi >> 8 : hi;
+            af[uu][0] = int4_lo(x);
+            af[uu][1] = int4_hi64(x);
+            af[uu][2] = int4_lo(y);
+            af[uu][3] = int4_hi64(y);
+          }
+#pragma unroll
+          for (int lo_ = 0; lo_ < 2; ++lo_)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              if (nb < nbv) {
+                const uint32_t* pp = lo_ ? pc[nb][t] : pb[nb][t];
+#pragma unroll
+                for (int uu = 0; uu < 2; ++uu)
+                  mma_f16_16816(o[nb][2 * q4 + uu], af[uu][0], af[uu][1], af[uu][2], af[uu][3],
+                                pp[0], pp[1]);
+              }
+        }
+      }
+    } else if constexpr (!C::VB) {
       // byte tiles; the rows of each 16-row m tile are permuted: row g -> d =
       // 16 mt + 2g, row g + 8 -> d = 16 mt + 2g + 1.  ldmatrix.trans over 8
       // token rows x 16 bytes (byte pairs as 16-bit elements) hands this
@@ -1044,8 +1314,28 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[0][mt][e] *= p.v_scale;
+      } else if constexpr (I4) {
+        const float up = 1.f / vinv;                // a power of two
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float b0 = 64.f * vw0[nb], b1 = 64.f * vw1[nb], z0 = vz0[nb], z1 = vz1[nb];
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            b0 += __shfl_xor_sync(0xffffffffu, b0, off);
+            b1 += __shfl_xor_sync(0xffffffffu, b1, off);
+            z0 += __shfl_xor_sync(0xffffffffu, z0, off);
+            z1 += __shfl_xor_sync(0xffffffffu, z1, off);
+          }
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            o[nb][mt][0] = fmaf(o[nb][mt][0], up, z0);
+            o[nb][mt][1] = fmaf(o[nb][mt][1], up, z1);
+            o[nb][mt][2] = fmaf(o[nb][mt][2] - b0, up, z0);
+            o[nb][mt][3] = fmaf(o[nb][mt][3] - b1, up, z1);
+          }
+        }
       } else if constexpr (CT == 2) {
-        float vt0 = vw0, vt1 = vw1;
+        float vt0 = vw0[0], vt1 = vw1[0];
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
           vt0 += __shfl_xor_sync(0xffffffffu, vt0, off);
@@ -1100,7 +1390,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
               // O^T rows g and g+8 of tile mt are d0 and d1 (see the PV product)
-              const int d0 = C::VB ? mt * 16 + g : mt * 16 + 2 * g;
+              const int d0 = C::VB ? mt * 16 + g : (I4 ? 16 * g + 2 * mt : mt * 16 + 2 * g);
               const int d1 = C::VB ? d0 + 8 : d0 + 1;
               orow[d0] = __float2bfloat16_rn(o[nb][mt][col] * inv);
               orow[d1] = __float2bfloat16_rn(o[nb][mt][2 + col] * inv);
@@ -1111,7 +1401,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
             float* orow = p.ws.o + pa * D;
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
-              const int d0 = C::VB ? mt * 16 + g : mt * 16 + 2 * g;
+              const int d0 = C::VB ? mt * 16 + g : (I4 ? 16 * g + 2 * mt : mt * 16 + 2 * g);
               const int d1 = C::VB ? d0 + 8 : d0 + 1;
               orow[d0] = o[nb][mt][col];
               orow[d1] = o[nb][mt][2 + col];

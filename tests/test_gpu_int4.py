@@ -259,3 +259,64 @@ def test_attention_reads_nan_of_rows_that_were_not_finite(ops):
     g = on_gpu(ops, c)
     out = ops.paged_attention_decode_quant(*g[:5], 0.1, g[5], max_context_len=20).cpu()
     assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
+
+
+# the tensor-core kernel: head counts that give 8, 4, 2 and 1 heads a CTA, several
+# groups of KV heads, 8-token blocks, long tables, splits
+TC_LENS = [[1], [31, 32, 33], [0, 17, 1, 0, 600, 64, 0], [3000, 5, 1025]]
+
+
+@pytest.mark.parametrize("lens", TC_LENS)
+@pytest.mark.parametrize("H_q,H_kv,K", [(32, 8, 16), (8, 8, 8), (16, 16, 32), (28, 4, 16), (12, 12, 8), (16, 2, 8),
+                                        (2, 2, 64), (7, 1, 16), (8, 1, 8), (24, 3, 48), (40, 10, 16)])
+def test_attention_tensor_cores(ops, lens, H_q, H_kv, K):
+    c = make(lens, H_q, H_kv, 128, K, torch.bfloat16, seed=sum(lens) + H_q + K)
+    a = check(ops, c, 128 ** -0.5, kernel=1)
+    b = check(ops, c, 128 ** -0.5, kernel=1, num_splits=3)
+    assert (a.float() - b.float()).abs().max() < 4e-3
+    assert torch.equal(a, check(ops, c, 128 ** -0.5, kernel=1))
+
+
+@pytest.mark.parametrize("kernel", [1, 2])
+@pytest.mark.parametrize("spread,shift,scale", [(1e-4, 0, 30.0), (1e4, 0, 1e-6), (0.1, 30.0, 1e-3), (1.0, 0.0, 2.0),
+                                                (3e-30, 0, 0.0), (1.0, 3.0, -0.1)])
+def test_attention_sizes_of_values(ops, spread, shift, scale, kernel):
+    # V from far below to far above 1, offsets far from 0, sharp and flat softmax; the
+    # tolerance scales with the largest output
+    c = make([500, 77], 16, 4, 128, 16, torch.bfloat16, seed=11, spread=spread, shift=shift)
+    q, kc, vc, ks, vs, bt, lens = c
+    g = on_gpu(ops, c)
+    out = as_f64(ops.paged_attention_decode_quant(*g[:5], scale, g[5], max_context_len=500, kernel=kernel))
+    ref = Q.paged_attention_decode_int4(storage(q), kc, vc, ks, vs, bt, lens, scale, "bf16")
+    top = np.abs(ref).max()
+    assert np.isfinite(out).all()
+    assert (np.abs(out - ref) <= 2e-3 * top + 1e-2 * np.abs(ref)).all()
+
+
+def test_attention_scale_jumps(ops):
+    # V scales that grow and shrink by powers of ten along a sequence
+    c = make([700], 8, 2, 128, 16, torch.bfloat16, seed=12)
+    q, kc, vc, ks, vs, bt, lens = c
+    rng = np.random.default_rng(0)
+    for t in range(700):
+        f = np.float32(10.0 ** rng.integers(-6, 3))
+        for h in range(2):
+            w = (vs[bt[0, t // 16], h, t % 16].astype(np.uint32) << np.uint32(16)).view(np.float32) * f
+            vs[bt[0, t // 16], h, t % 16] = Q.bf16_encode(w)
+    g = on_gpu(ops, c)
+    for kernel in (1, 2):
+        out = as_f64(ops.paged_attention_decode_quant(*g[:5], 0.1, g[5], max_context_len=700, kernel=kernel))
+        ref = Q.paged_attention_decode_int4(storage(q), kc, vc, ks, vs, bt, lens, 0.1, "bf16")
+        assert (np.abs(out - ref) <= 2e-3 * np.abs(ref).max() + 1e-2 * np.abs(ref)).all()
+
+
+@pytest.mark.parametrize("H_q,H_kv,K,group", [(32, 8, 16, 4), (16, 8, 16, 3), (8, 8, 8, 16), (28, 4, 32, 2),
+                                              (8, 1, 16, 5), (6, 2, 8, 5), (16, 16, 16, 8)])
+def test_attention_shared_prefix(ops, H_q, H_kv, K, group):
+    rng = np.random.default_rng(H_q + K)
+    lens = [int(x) for x in rng.integers(1, 400, 3 * group + 1)]
+    lens[1], lens[-1] = 0, 900
+    for share in (0, 1, 7, 30):
+        c = make(lens, H_q, H_kv, 128, K, torch.bfloat16, seed=share, share=share, group=group)
+        check(ops, c, 128 ** -0.5, share_prefix=True)
+        check(ops, c, 128 ** -0.5, share_prefix=True, kernel=1, num_splits=5)
