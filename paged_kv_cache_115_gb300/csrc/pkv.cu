@@ -162,9 +162,12 @@ bool simt_shape_ok(int G, int D) {
   return (D == 32 || D == 64 || D == 128 || D == 256) && G >= 1 && G <= 16;
 }
 
-int tc_hpc(int H_kv) {
+#ifndef PKV_I4_HPC
+#define PKV_I4_HPC 4
+#endif
+int tc_hpc(int H_kv, int ct = 0) {
   for (int h : {8, 4, 2, 1})
-    if (H_kv % h == 0) return h;
+    if (H_kv % h == 0 && (ct != 4 || h <= PKV_I4_HPC)) return h;
   return 1;
 }
 
@@ -209,7 +212,7 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
     pkv_status st = device_facts(&dev, &sms);
     if (st != PKV_OK) return st;
     p.kind = KIND_TC;
-    p.hpc = tc_hpc(H_kv);
+    p.hpc = tc_hpc(H_kv, ct);
     p.groups = H_kv / p.hpc;
     // one CTA per SM (shared memory bound), or as many as a pool format takes
     const int total = sms * pkv::tc_ctas(ct, p.hpc, c.share_prefix != 0);

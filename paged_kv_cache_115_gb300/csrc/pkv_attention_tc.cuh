@@ -50,7 +50,8 @@ constexpr int tc_chunk_tokens(int ct) { return ct == 0 || ct == 3 ? kTile : 2 * 
 // by what their warps issue, so more warps than heads work on an SM; with the two
 // column blocks of shared-prefix groups the accumulators need the registers.
 constexpr int tc_ctas(int ct, int hpc, bool sh) {
-  return ct != 4 || sh ? 1 : (hpc == 8 ? 2 : (hpc == 4 ? 3 : (hpc == 2 ? 6 : 8)));
+  return ct != 4 ? 1 : (sh ? (hpc == 8 ? 1 : (hpc == 4 ? 2 : 4))
+                           : (hpc == 8 ? 2 : (hpc == 4 ? 3 : (hpc == 2 ? 6 : 8))));
 }
 
 // Attention behind a shared prefix (pkv_prefix.cuh): the prefix kernel and
@@ -212,30 +213,57 @@ constexpr float kQuantSlack = 4.f;
 
 // INT4.  With row t's scale s_t and offset z_t and codes c,
 //   q . K_t = s_t (q . c_t) + z_t sum(q),
-//   sum_t p_t V_t = sum_t (p_t s_t) c_t + sum_t p_t z_t,
+//   sum_t p_t V_t = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (z_t + 8 s_t),
 // so codes enter the tensor core as they are, scales and offsets act on scores
 // and weights, and no value is dequantized by itself.  A 32-bit word holds eight
 // codes of a row; a mask and an exponent make f16 pairs of the codes at nibbles
-// (i, i + 4):
-//   w & 0x000f000f | 0x6400 6400 = 1024 + c (1024 taken off exactly),
-//   w & 0x00f000f0 | 0x5400 5400 = 64 + c   (left in: 64 sum(q) over those
-//     columns comes off the score, 64 sum(w) off those rows of o at the end),
-// twice, the second time from w >> 8: five integer operations and two additions
-// for eight codes.  The mma k order (K) and row order (V) are permuted to fit.
+// (i, i + 4), twice, the second time from w >> 8:
+//   w & 0x000f000f | 0x6400 6400 = 1024 + c,  w & 0x00f000f0 | 0x5400 5400 = 64 + c.
+// K leaves these numbers in: 1024 sum(q) over the one half of the columns and 64
+// sum(q) over the other come off the score, whose few steps in float32 they do not
+// harm (the same error for every key of a query, 2^-24 of a sum of |q|).  V takes
+// them off and centres the codes: o sums thousands of rows, the tensor core cuts
+// its sums towards zero, and sums without a common sign lose nothing that adds up.
+// The mma k order (K) and row order (V) are permuted to fit.
 // K: lane (g, tq) holds columns 32 tq .. 32 tq + 31 of token pi(g) (and pi(g) +
 // 8): one 16-byte load a row.  V: lane (g, tq) holds columns 16 g .. 16 g + 15 of
 // tokens pi(2 tq), pi(2 tq + 1) (and + 8), 8 bytes each, paired by byte permutes
 // of two words.  pi = 0 3 1 2 4 7 5 6 keeps both free of bank conflicts.
-__device__ __forceinline__ uint32_t int4_lo(uint32_t w) {          // nibbles 0 and 4
+// (8-bit products, which would take the codes as e4m3 by a mask alone, are no way
+// out: with operands that change, m16n8k32 of e4m3 runs at 0.15 a clock and SM,
+// m16n8k16 of f16 at 0.5.)
+__device__ __forceinline__ uint32_t int4_lo(uint32_t w) {          // nibbles 0 and 4, + 1024
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(0x000f000fu), "r"(0x64006400u));
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&r), __floats2half2_rn(1024.f, 1024.f));
-  return *reinterpret_cast<const uint32_t*>(&h);
+  return r;
 }
-__device__ __forceinline__ uint32_t int4_hi64(uint32_t w) {        // nibbles 1 and 5, + 64
+__device__ __forceinline__ uint32_t int4_hi(uint32_t w) {          // nibbles 1 and 5, + 64
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(0x00f000f0u), "r"(0x54005400u));
   return r;
+}
+__device__ __forceinline__ uint32_t f16x2_less(uint32_t x, float c) {
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(c, c));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Loads from shared memory by their 32-bit address (a pointer that went through an
+// integer is generic: its loads pass through the global path).
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
 }
 __device__ __forceinline__ int int4_pi(int g) { return (g & 4) | ((0x2130 >> ((g & 3) * 4)) & 3); }
 
@@ -719,19 +747,19 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   float slc0[NB], slc1[NB];     // per score column (one-byte pools: q's 2^e folded in)
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) slc0[nb] = slc1[nb] = sl;
-  // INT4, per score column: slc times 64 sum(q) over the columns read as 64 + code,
-  // and times sum(q)
+  // INT4, per score column: slc times what the codes' 1024 and 64 add, and times sum(q)
   float off0[I4 ? NB : 1], off1[I4 ? NB : 1], qs0[I4 ? NB : 1], qs1[I4 ? NB : 1];
   const int pg = I4 ? int4_pi(g) : g;     // token row of a tile that mma row g holds
-  // INT4: V scales enter times vinv, the power of two that puts the largest seen
-  // (up to vcap) at 1 .. 8, so that f16 weights neither overflow nor fade
+  // INT4: V scales enter times vinv, a power of two that puts the largest seen (up
+  // to vcap) at 2^8 .. 2^11: weights of up to 2^kQuantSlack stay inside f16, and
+  // down to 2^-22 of the largest they are normal f16 numbers
   float vinv = 1.f, vcap = 0.f;
   float m0[NB], m1[NB], l0[NB], l1[NB];
   // INT8 pools: V enters the tensor core as 1152 + code (the exact f16 the
   // byte permute makes, without the subtraction); vw = sum of weight x V
   // scale per column, so that 1152 vw is taken off o at the partition end
   float vw0[NB], vw1[NB];
-  // INT4: vw = sum of the weights as they enter, vz = sum of weight x V offset
+  // INT4: sum of weight x V offset per column
   float vz0[NB], vz1[NB];
   int u = seq_of_chunk(cstart, NU, cb);
   int ut0 = 0, uend = 0, ulim = 0;   // the unit's tokens [ut0, uend); min column limit
@@ -828,8 +856,8 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           const float e1 = __shfl_sync(0xffffffffu, even, 8 * tq + 4);
           const float d0 = __shfl_sync(0xffffffffu, odd, 8 * tq);
           const float d1 = __shfl_sync(0xffffffffu, odd, 8 * tq + 4);
-          off0[nb] = slc0[nb] * (64.f * d0);
-          off1[nb] = slc1[nb] * (64.f * d1);
+          off0[nb] = slc0[nb] * (1024.f * e0 + 64.f * d0);
+          off1[nb] = slc1[nb] * (1024.f * e1 + 64.f * d1);
           qs0[nb] = slc0[nb] * (e0 + d0);
           qs1[nb] = slc1[nb] * (e1 + d1);
         }
@@ -892,6 +920,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       return;
     }
     uint8_t* sb = smem + stage * C::STAGE;
+    const uint32_t sa = smem_u32(sb);
     // per-token-row K scales and V scales (folded into P) of rows g, g+8 of
     // each tile: INT8 per slot, FP8 per tensor (K's folded into sl)
     float ksr[TL][2], vsr[TL][2];
@@ -901,14 +930,14 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       if constexpr (I4) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t kw = *reinterpret_cast<const uint32_t*>(sb + C::word_off(0, w, t, pg + 8 * r));
-          uint32_t vw = *reinterpret_cast<const uint32_t*>(sb + C::word_off(1, w, t, pg + 8 * r));
+          const uint32_t kw = lds32(sa + C::word_off(0, w, t, pg + 8 * r));
+          uint32_t vw = lds32(sa + C::word_off(1, w, t, pg + 8 * r));
           // words past the end may hold anything: 0-weight x V must stay 0
-          if (t * kTile + pg + 8 * r >= valid) vw = 0u;
+          if (valid < CH && t * kTile + pg + 8 * r >= valid) vw = 0u;
           ksr[t][r] = int4_scale(kw);
           kzr[t][r] = int4_offset(kw);
           vsr[t][r] = int4_scale(vw);
-          vzr[t][r] = int4_offset(vw);
+          vzr[t][r] = fmaf(8.f, vsr[t][r], int4_offset(vw));
         }
       } else if constexpr (CT == 2) {
         const float* kscl = reinterpret_cast<const float*>(sb + C::SCALE_OFF + t * 64);
@@ -932,15 +961,13 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
           vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, off));
-        const int ev = max(-120, min(120, ilogbf(vmx)));
+        const int ev = max(-110, min(120, ilogbf(vmx)));
         const float was = vinv;
-        vinv = ldexpf(1.f, -ev);
+        vinv = ldexpf(1.f, 8 - ev);
         vcap = ldexpf(8.f, ev);
         const float f = vinv / was;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          vw0[nb] *= f;
-          vw1[nb] *= f;
 #pragma unroll
           for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
@@ -1004,16 +1031,15 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     } else if constexpr (I4) {
 #pragma unroll
       for (int t = 0; t < TL; ++t) {
-        const uint8_t* kt = sb + C::box_off(0, w, t, 0) + C::row_off(pg) + ((tq ^ ((pg >> 1) & 3)) << 4);
-        const uint4 ra = *reinterpret_cast<const uint4*>(kt);
-        const uint4 rb = *reinterpret_cast<const uint4*>(kt + C::RSTEP8);
+        const uint32_t kt = sa + C::box_off(0, w, t, 0) + C::row_off(pg) + ((tq ^ ((pg >> 1) & 3)) << 4);
+        const uint4 ra = lds128(kt), rb = lds128(kt + C::RSTEP8);
         const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const uint32_t x = hf ? wa[i] >> 8 : wa[i], y = hf ? wb[i] >> 8 : wb[i];
-            const uint32_t a0 = int4_lo(x), a1 = int4_lo(y), a2 = int4_hi64(x), a3 = int4_hi64(y);
+            const uint32_t a0 = int4_lo(x), a1 = int4_lo(y), a2 = int4_hi(x), a3 = int4_hi(y);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
               if (nb < nbv)
@@ -1159,6 +1185,18 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         l0[nb] += ps0;
         l1[nb] += ps1;
       }
+      if constexpr (I4) {
+        // weights times V scales as one f16 number (half a step is 2^-12 of it, a
+        // sixteenth of the output's own rounding; the codes carry four bits)
+#pragma unroll
+        for (int t = 0; t < TL; ++t) {
+          vz0[nb] = fmaf(pr[t][0], vzr[t][0], fmaf(pr[t][2], vzr[t][1], vz0[nb]));
+          vz1[nb] = fmaf(pr[t][1], vzr[t][0], fmaf(pr[t][3], vzr[t][1], vz1[nb]));
+          pb[nb][t][0] = movmatrix_trans(pack_f16x2(pr[t][0] * vsr[t][0], pr[t][1] * vsr[t][0]));
+          pb[nb][t][1] = movmatrix_trans(pack_f16x2(pr[t][2] * vsr[t][1], pr[t][3] * vsr[t][1]));
+        }
+        continue;
+      }
       // P enters the tensor core as a hi + lo pair of 16-bit terms so that the
       // product carries ~16 significant bits of each weight (one bf16 rounding
       // of P costs up to 2^-9 relative per weight); one-byte pools: f16 terms
@@ -1172,13 +1210,9 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         } else {
           const float w0 = pr[t][0] * vsr[t][0], w1 = pr[t][1] * vsr[t][0];
           const float w2 = pr[t][2] * vsr[t][1], w3 = pr[t][3] * vsr[t][1];
-          if constexpr (CT == 2 || I4) {
+          if constexpr (CT == 2) {
             vw0[nb] += w0 + w2;
             vw1[nb] += w1 + w3;
-          }
-          if constexpr (I4) {
-            vz0[nb] = fmaf(pr[t][0], vzr[t][0], fmaf(pr[t][2], vzr[t][1], vz0[nb]));
-            vz1[nb] = fmaf(pr[t][1], vzr[t][0], fmaf(pr[t][3], vzr[t][1], vz1[nb]));
           }
           split_f16x2(w0, w1, ph01, pl01);
           split_f16x2(w2, w3, ph23, pl23);
@@ -1196,37 +1230,26 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       const int j0 = (tq & 1) | ((tq & 2) << 1), j1 = j0 ^ 3;        // pi(2 tq), pi(2 tq + 1)
 #pragma unroll
       for (int t = 0; t < TL; ++t) {
-        const uint8_t* vt = sb + C::box_off(1, w, t, 0) + (g & 1) * 8;
-        const uint8_t* v0 = vt + C::row_off(j0) + (((g >> 1) ^ (j0 >> 1 & 3)) << 4);
-        const uint8_t* v1 = vt + C::row_off(j1) + (((g >> 1) ^ (j1 >> 1 & 3)) << 4);
-        const uint2 r0 = *reinterpret_cast<const uint2*>(v0), r1 = *reinterpret_cast<const uint2*>(v1);
-        const uint2 r2 = *reinterpret_cast<const uint2*>(v0 + C::RSTEP8);
-        const uint2 r3 = *reinterpret_cast<const uint2*>(v1 + C::RSTEP8);
+        const uint32_t vt = sa + C::box_off(1, w, t, 0) + (g & 1) * 8;
+        const uint32_t v0 = vt + C::row_off(j0) + (((g >> 1) ^ (j0 >> 1 & 3)) << 4);
+        const uint32_t v1 = vt + C::row_off(j1) + (((g >> 1) ^ (j1 >> 1 & 3)) << 4);
+        const uint2 r0 = lds64(v0), r1 = lds64(v1);
+        const uint2 r2 = lds64(v0 + C::RSTEP8), r3 = lds64(v1 + C::RSTEP8);
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {            // words (q4 / 2), their halves
           const uint32_t sel = q4 & 1 ? 0x7632u : 0x5410u;
           const uint32_t lo = __byte_perm(q4 < 2 ? r0.x : r0.y, q4 < 2 ? r1.x : r1.y, sel);
           const uint32_t hi = __byte_perm(q4 < 2 ? r2.x : r2.y, q4 < 2 ? r3.x : r3.y, sel);
-          uint32_t af[2][4];
 #pragma unroll
           for (int uu = 0; uu < 2; ++uu) {
             const uint32_t x = uu ? lo >> 8 : lo, y = uu ? hi >> 8 : hi;
-            af[uu][0] = int4_lo(x);
-            af[uu][1] = int4_hi64(x);
-            af[uu][2] = int4_lo(y);
-            af[uu][3] = int4_hi64(y);
-          }
-#pragma unroll
-          for (int lo_ = 0; lo_ < 2; ++lo_)
+            const uint32_t a0 = f16x2_less(int4_lo(x), 1032.f), a1 = f16x2_less(int4_hi(x), 72.f);
+            const uint32_t a2 = f16x2_less(int4_lo(y), 1032.f), a3 = f16x2_less(int4_hi(y), 72.f);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
-              if (nb < nbv) {
-                const uint32_t* pp = lo_ ? pc[nb][t] : pb[nb][t];
-#pragma unroll
-                for (int uu = 0; uu < 2; ++uu)
-                  mma_f16_16816(o[nb][2 * q4 + uu], af[uu][0], af[uu][1], af[uu][2], af[uu][3],
-                                pp[0], pp[1]);
-              }
+              if (nb < nbv)
+                mma_f16_16816(o[nb][2 * q4 + uu], a0, a1, a2, a3, pb[nb][t][0], pb[nb][t][1]);
+          }
         }
       }
     } else if constexpr (!C::VB) {
@@ -1318,11 +1341,9 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         const float up = 1.f / vinv;                // a power of two
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          float b0 = 64.f * vw0[nb], b1 = 64.f * vw1[nb], z0 = vz0[nb], z1 = vz1[nb];
+          float z0 = vz0[nb], z1 = vz1[nb];
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) {
-            b0 += __shfl_xor_sync(0xffffffffu, b0, off);
-            b1 += __shfl_xor_sync(0xffffffffu, b1, off);
             z0 += __shfl_xor_sync(0xffffffffu, z0, off);
             z1 += __shfl_xor_sync(0xffffffffu, z1, off);
           }
@@ -1330,8 +1351,8 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           for (int mt = 0; mt < D / 16; ++mt) {
             o[nb][mt][0] = fmaf(o[nb][mt][0], up, z0);
             o[nb][mt][1] = fmaf(o[nb][mt][1], up, z1);
-            o[nb][mt][2] = fmaf(o[nb][mt][2] - b0, up, z0);
-            o[nb][mt][3] = fmaf(o[nb][mt][3] - b1, up, z1);
+            o[nb][mt][2] = fmaf(o[nb][mt][2], up, z0);
+            o[nb][mt][3] = fmaf(o[nb][mt][3], up, z1);
           }
         }
       } else if constexpr (CT == 2) {
