@@ -163,7 +163,7 @@ bool simt_shape_ok(int G, int D) {
 }
 
 #ifndef PKV_I4_HPC
-#define PKV_I4_HPC 4
+#define PKV_I4_HPC 8
 #endif
 int tc_hpc(int H_kv, int ct = 0) {
   for (int h : {8, 4, 2, 1})
@@ -1537,12 +1537,13 @@ pkv_status attention_impl(const void* q, const void* k_cache, const void* v_cach
     // one-byte tiles for quantized pools, except the bf16 K pool of the pair
     const bool k16 = quant != nullptr && quant->format == PKV_KV_BF16K_FP8V;
     const bool i4 = quant != nullptr && quant->format == PKV_KV_INT4_HEAD;
-    const int cols = i4 ? D / 2 : D;               // bytes of a quantized row
-    st = encode_pool_map_heads(&prm.tmap_k, k_cache, num_blocks, block_size, H_kv, cols, plan.hpc,
-                               quant != nullptr && !k16);
+    // INT4: two heads' 64-byte rows as one of 128 bytes, or single ones
+    const int per = i4 && plan.hpc % 2 == 0 ? 2 : 1, cols = i4 ? per * D / 2 : D;
+    st = encode_pool_map_heads(&prm.tmap_k, k_cache, num_blocks, block_size, H_kv / per, cols,
+                               plan.hpc / per, quant != nullptr && !k16);
     if (st != PKV_OK) return st;
-    st = encode_pool_map_heads(&prm.tmap_v, v_cache, num_blocks, block_size, H_kv, cols, plan.hpc,
-                               quant != nullptr);
+    st = encode_pool_map_heads(&prm.tmap_v, v_cache, num_blocks, block_size, H_kv / per, cols,
+                               plan.hpc / per, quant != nullptr);
     if (st != PKV_OK) return st;
     if (i4) {
       st = encode_word_map(&prm.tmap_ks, quant->k_token_scales, num_blocks, block_size, H_kv,

@@ -47,11 +47,12 @@ constexpr int kBoxBytes = kTile * 128;
 constexpr int tc_chunk_tokens(int ct) { return ct == 0 || ct == 3 ? kTile : 2 * kTile; }
 
 // CTAs that share an SM.  4-bit pools bring twice the values a byte and are bound
-// by what their warps issue, so more warps than heads work on an SM; with the two
-// column blocks of shared-prefix groups the accumulators need the registers.
+// by what their warps issue: 16 consumer warps an SM, no producer warp among them
+// (the consumers take turns), so that each has 128 registers.  The two column
+// blocks of shared-prefix groups need 227: 8 warps.
+// (One head a CTA: 8, what shared memory holds with two stages or more.)
 constexpr int tc_ctas(int ct, int hpc, bool sh) {
-  return ct != 4 ? 1 : (sh ? (hpc == 8 ? 1 : (hpc == 4 ? 2 : 4))
-                           : (hpc == 8 ? 2 : (hpc == 4 ? 3 : (hpc == 2 ? 6 : 8))));
+  return ct != 4 ? 1 : (hpc == 1 ? 8 : (sh ? 8 : 16) / hpc);
 }
 
 // Attention behind a shared prefix (pkv_prefix.cuh): the prefix kernel and
@@ -176,9 +177,10 @@ struct TcParams {
 // contiguously, so one 4-D TMA copy (column, row, column group, head) brings
 // a tile's rows for all HPC heads and column groups of the CTA at once.
 //
-// INT4 pools (CT 4): a head's row is 64 bytes, boxes of 64-byte rows in the
-// 64-byte swizzle (row r's 16-byte chunk c at chunk c ^ (r / 2 & 3)), then the
-// (scale, offset) words of each tile as [head][16 tokens].  See below at "INT4".
+// INT4 pools (CT 4): a head's row is 64 bytes, boxes hold two heads' rows side by
+// side in the 128-byte swizzle (with one head a CTA: one, in the 64-byte swizzle,
+// row r's 16-byte chunk c at chunk c ^ (r / 2 & 3)), then the (scale, offset) words
+// of each tile as [head][16 tokens].  See below at "INT4".
 //
 // 8-token blocks (B8): a tile spans two blocks, one copy each, laid out
 // [tile][block half][head][column group][8 rows x 128 bytes]: rows 8..15 of
@@ -228,7 +230,9 @@ constexpr float kQuantSlack = 4.f;
 // K: lane (g, tq) holds columns 32 tq .. 32 tq + 31 of token pi(g) (and pi(g) +
 // 8): one 16-byte load a row.  V: lane (g, tq) holds columns 16 g .. 16 g + 15 of
 // tokens pi(2 tq), pi(2 tq + 1) (and + 8), 8 bytes each, paired by byte permutes
-// of two words.  pi = 0 3 1 2 4 7 5 6 keeps both free of bank conflicts.
+// of two words.  pi keeps both free of bank conflicts: 0 5 2 7 4 1 6 3 under the
+// 128-byte swizzle (rows of two heads: 64-byte rows, twice the requests a byte, keep
+// TMA below 4.8 TB/s), 0 3 1 2 4 7 5 6 under the 64-byte one (a head a CTA).
 // (8-bit products, which would take the codes as e4m3 by a mask alone, are no way
 // out: with operands that change, m16n8k32 of e4m3 runs at 0.15 a clock and SM,
 // m16n8k16 of f16 at 0.5.)
@@ -247,25 +251,10 @@ __device__ __forceinline__ uint32_t f16x2_less(uint32_t x, float c) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Loads from shared memory by their 32-bit address (a pointer that went through an
-// integer is generic: its loads pass through the global path).
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
+template <bool PAIR>
+__device__ __forceinline__ int int4_pi(int g) {
+  return PAIR ? g ^ ((g & 1) << 2) : (g & 4) | ((0x2130 >> ((g & 3) * 4)) & 3);
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ int int4_pi(int g) { return (g & 4) | ((0x2130 >> ((g & 3) * 4)) & 3); }
 
 // 2-D tiled load global -> shared, completion counted on an mbarrier.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
@@ -298,10 +287,12 @@ struct TcCfg {
   static constexpr int NHK = KB ? D / 64 : 1;             // boxes per head row, K
   static constexpr int NHV = VB ? D / 64 : 1;             // boxes per head row, V
   static constexpr int NH = NHV;                          // (V tile rows, zeroed past the end)
-  static constexpr int ROWB = I4 ? 64 : 128;              // bytes of a box row
-  static constexpr int BOX = kTile * ROWB;                // one head's rows of a tile
-  static constexpr int KPART = HPC * TL * NHK * BOX;
-  static constexpr int VPART = HPC * TL * NHV * BOX;
+  static constexpr bool PAIR = I4 && HPC % 2 == 0;        // two heads side by side in a box row
+  static constexpr int HB = PAIR ? HPC / 2 : HPC;         // boxes of a tile (and column group)
+  static constexpr int ROWB = I4 && !PAIR ? 64 : 128;     // bytes of a box row
+  static constexpr int BOX = kTile * ROWB;                // rows of a tile
+  static constexpr int KPART = HB * TL * NHK * BOX;
+  static constexpr int VPART = HB * TL * NHV * BOX;
   static constexpr int SCALE_OFF = KPART + VPART;
   // INT4: words of one box (a tile, or half of one: B8), on a 128-byte boundary
   static constexpr int SUB = B8 ? 2 : 1;
@@ -310,7 +301,7 @@ struct TcCfg {
   static constexpr int SCALE_BYTES =
       I4 ? 2 * TL * SUB * SBOX : (CT == 2 ? 2 * TL * kTile * 4 : 0);
   static constexpr int STAGE = ((KPART + VPART + SCALE_BYTES + 1023) / 1024) * 1024;
-  static constexpr int THREADS = (HPC + 1) * 32;
+  static constexpr int THREADS = (I4 ? HPC : HPC + 1) * 32;   // (INT4: no producer warp)
   static constexpr int BAR_OFF = NS * STAGE;
   static constexpr int CSTART_OFF = BAR_OFF + 2 * NS * 8 + 16;
   static constexpr int SMEM = CSTART_OFF + (kTcMaxSeqs + 1) * 4 + 1024;  // + alignment slack
@@ -318,21 +309,26 @@ struct TcCfg {
       KPART + VPART + (I4 ? 2 * TL * HPC * kTile * 4 : SCALE_BYTES);
   static_assert(CT == 0 || D == 128, "quantized pools need head_dim 128");
   static_assert(CT != 3 || !B8, "the bf16-K / FP8-V pair needs 16-token tiles of one block");
-  static constexpr int TBOXK = HPC * NHK * BOX;        // one tile, all heads of the CTA
-  static constexpr int TBOXV = HPC * NHV * BOX;
+  static constexpr int TBOXK = HB * NHK * BOX;         // one tile, all heads of the CTA
+  static constexpr int TBOXV = HB * NHV * BOX;
   static constexpr int TBOX = TBOXK;                   // (formats with equal K and V tiles)
-  static constexpr int UST = HPC * NHK * 8 * ROWB;     // B8: one block half of a tile, all heads
+  static constexpr int UST = HB * NHK * 8 * ROWB;      // B8: one block half of a tile, all heads
   static constexpr int RSTEP8 = B8 ? UST : 8 * ROWB;   // rows 8..15 relative to rows 0..7
   static constexpr int HSTR = B8 ? 8 * ROWB : BOX;     // column group stride
   // smem offset of row 0 of head h's box (tile t, column group half) of K
   // (kv 0) or V; the B8 layout exists for formats whose K and V tiles match
-  __host__ __device__ static constexpr int box_off(int kv, int h, int t, int half) {
+  __host__ __device__ static constexpr int box_off(int kv, int head, int t, int half) {
+    const int h = PAIR ? head >> 1 : head;
     return B8 ? kv * KPART + t * 2 * UST + (h * NHK + half) * 8 * ROWB
               : (kv ? KPART + t * TBOXV + (h * NHV + half) * BOX
                     : t * TBOXK + (h * NHK + half) * BOX);
   }
   // offset of row r (0..15) inside a box
   __host__ __device__ static constexpr int row_off(int r) { return (r & 7) * ROWB + (r >> 3) * RSTEP8; }
+  // INT4: offset of 16-byte chunk c of head h in row r, under the swizzle
+  __host__ __device__ static constexpr int chunk_off(int h, int r, int c) {
+    return (PAIR ? ((h & 1) * 4 + c) ^ (r & 7) : c ^ (r >> 1 & 3)) << 4;
+  }
   // INT4: offset of the word of row r of tile t of head h
   __host__ __device__ static constexpr int word_off(int kv, int h, int t, int r) {
     return SCALE_OFF + ((kv * TL + t) * SUB + (B8 ? r >> 3 : 0)) * SBOX +
@@ -342,7 +338,10 @@ struct TcCfg {
 
 // Largest CTA index i whose range starts at or before chunk c.
 __host__ __device__ __forceinline__ int cta_of_chunk(long long c, long long T, int n) {
-  return (int)(((c + 1) * (long long)n - 1) / T);
+  const long long x = (c + 1) * (long long)n - 1;
+  // (a 64-bit division is ten times a 32-bit one; T > c, so it fits where x does)
+  if (x >> 32 == 0) return (int)((uint32_t)x / (uint32_t)T);
+  return (int)(x / T);
 }
 
 // Largest s in [0, S) with cstart[s] <= c (c < cstart[S]).
@@ -410,8 +409,9 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   static_assert(!SH || CT == 0 || CT == 4, "shared-prefix groups need bf16 or INT4 pools");
   static_assert(!PX || (CT == 0 && !SH), "shared-prefix attention needs bf16 pools");
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a rounded pointer: through an integer the loads below would be
+  // generic ones, which pass through the global path)
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   const uint32_t bar_full = smem_u32(smem + C::BAR_OFF);   // + 8 * stage
   const uint32_t bar_empty = bar_full + 8 * NS;
   int* cstart = reinterpret_cast<int*>(smem + C::CSTART_OFF);
@@ -548,6 +548,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   const int n = (int)(T < most ? (T > 0 ? T : 1) : most);
   const int cta = blockIdx.x, group = blockIdx.y;
   const int head0 = group * HPC;
+  const int box0 = C::PAIR ? head0 / 2 : head0;      // its first box
   const int G = p.G, H_q = p.H_q;
   const int cb = cta < n ? (int)((long long)cta * T / n) : 0;
   const int ce = cta < n ? (int)((long long)(cta + 1) * T / n) : 0;
@@ -592,7 +593,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   // no kernel that lets this one start before it ends) before waiting for the
   // previous kernel
   int row[TL][2];
-  if (warp == HPC && cb < ce) tile_rows(cb, row);
+  if ((I4 || warp == HPC) && cb < ce) tile_rows(cb, row);
   if constexpr (!SH && !PX) pdl_wait_primary();
   // behind a shared prefix: the kernel in front (the prefix part) released
   // this one after its own wait, so what earlier kernels wrote is there; this
@@ -638,15 +639,71 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     return;
   }
 
-  if (warp == HPC) {
+  // the copies of one chunk (tile rows r) into a stage, by a whole warp
+  auto issue = [&](int stage, const int (&r)[TL][2], uint64_t policy) {
+    if (lane == 0) mbar_arrive_expect_tx(bar_full + 8 * stage, C::TX);
+    __syncwarp();
+    uint8_t* sb = smem + stage * C::STAGE;
+    if constexpr (B8) {
+      // one 4-D box per (K / V, tile, block half): all heads of the CTA,
+      // all column groups, 8 rows; then (INT8) the scales of each half
+      constexpr int NB = 4 * TL;
+      for (int i = lane; i < NB + (CT == 2 || I4 ? NB : 0); i += 32) {
+        const int j = i < NB ? i : i - NB;
+        const int kv = j / (2 * TL), t = (j >> 1) % TL, u = j & 1;
+        const int r0 = t ? r[TL - 1][0] : r[0][0];
+        const int r1 = t ? r[TL - 1][1] : r[0][1];
+        const int rr = u ? r1 : r0;
+        if (i < NB) {
+          tma_load_4d(smem_u32(sb + kv * C::KPART + (2 * t + u) * C::UST),
+                      kv ? &p.tmap_v : &p.tmap_k, bar_full + 8 * stage, 0, rr, 0, box0,
+                      policy);
+        } else if constexpr (I4) {
+          // no rows: words out of bounds too, which TMA fills with zeros
+          const int blk = rr >= 0 ? rr / K : 0;
+          tma_load_2d(smem_u32(sb + C::word_off(kv, 0, t, 8 * u)),
+                      kv ? &p.tmap_vs : &p.tmap_ks, bar_full + 8 * stage,
+                      rr >= 0 ? rr - blk * K : 0,
+                      rr >= 0 ? blk * (int)(gridDim.y * HPC) + head0 : -2 * HPC, policy);
+        } else if constexpr (CT == 2) {
+          // a half tile with no rows reads slot 0's scales, which meet zero codes
+          const float* src = (kv ? p.v_ts : p.k_ts) + (rr >= 0 ? rr : 0);
+          bulk_load(smem_u32(sb + C::SCALE_OFF + (kv * TL + t) * 64 + u * 32), src, 32,
+                    bar_full + 8 * stage);
+        }
+      }
+    } else {
+      // one 4-D box per (K / V, tile): 16 rows of all heads of the CTA and
+      // all column groups; then (INT8) each tile's 16 per-slot scales
+      constexpr int NB = 2 * TL;
+      for (int i = lane; i < NB + (CT == 2 || I4 ? NB : 0); i += 32) {
+        const int j = i < NB ? i : i - NB;
+        const int kv = j / TL, t = j - kv * TL;
+        const int rr = t ? r[TL - 1][0] : r[0][0];
+        if (i < NB) {
+          tma_load_4d(smem_u32(sb + C::box_off(kv, 0, t, 0)), kv ? &p.tmap_v : &p.tmap_k,
+                      bar_full + 8 * stage, 0, rr, 0, box0, policy);
+        } else if constexpr (I4) {
+          const int blk = rr >= 0 ? rr / K : 0;
+          tma_load_2d(smem_u32(sb + C::word_off(kv, 0, t, 0)),
+                      kv ? &p.tmap_vs : &p.tmap_ks, bar_full + 8 * stage,
+                      rr >= 0 ? rr - blk * K : 0,
+                      rr >= 0 ? blk * (int)(gridDim.y * HPC) + head0 : -2 * HPC, policy);
+        } else if constexpr (CT == 2) {
+          // a tile with no rows reads slot 0's scales, which meet zero codes
+          const float* src = (kv ? p.v_ts : p.k_ts) + (rr >= 0 ? rr : 0);
+          bulk_load(smem_u32(sb + C::SCALE_OFF + (kv * TL + t) * 64), src, 64,
+                    bar_full + 8 * stage);
+        }
+      }
+    }
+  };
+
+  if (!I4 && warp == HPC) {
     // =================== producer ===================
     if (lane == 0) {
       prefetch_tensormap(&p.tmap_k);
       prefetch_tensormap(&p.tmap_v);
-      if constexpr (I4) {
-        prefetch_tensormap(&p.tmap_ks);
-        prefetch_tensormap(&p.tmap_vs);
-      }
     }
     const uint64_t policy = l2_policy_evict_first();
     int k = 0;
@@ -668,62 +725,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(bar_full + 8 * stage, C::TX);
-        __syncwarp();
-        uint8_t* sb = smem + stage * C::STAGE;
-        if constexpr (B8) {
-          // one 4-D box per (K / V, tile, block half): all heads of the CTA,
-          // all column groups, 8 rows; then (INT8) the scales of each half
-          constexpr int NB = 4 * TL;
-          for (int i = lane; i < NB + (CT == 2 || I4 ? NB : 0); i += 32) {
-            const int j = i < NB ? i : i - NB;
-            const int kv = j / (2 * TL), t = (j >> 1) % TL, u = j & 1;
-            const int r0 = t ? r[TL - 1][0] : r[0][0];
-            const int r1 = t ? r[TL - 1][1] : r[0][1];
-            const int rr = u ? r1 : r0;
-            if (i < NB) {
-              tma_load_4d(smem_u32(sb + kv * C::KPART + (2 * t + u) * C::UST),
-                          kv ? &p.tmap_v : &p.tmap_k, bar_full + 8 * stage, 0, rr, 0, head0,
-                          policy);
-            } else if constexpr (I4) {
-              // no rows: words out of bounds too, which TMA fills with zeros
-              const int blk = rr >= 0 ? rr / K : 0;
-              tma_load_2d(smem_u32(sb + C::word_off(kv, 0, t, 8 * u)),
-                          kv ? &p.tmap_vs : &p.tmap_ks, bar_full + 8 * stage,
-                          rr >= 0 ? rr - blk * K : 0,
-                          rr >= 0 ? blk * (int)(gridDim.y * HPC) + head0 : -2 * HPC, policy);
-            } else if constexpr (CT == 2) {
-              // a half tile with no rows reads slot 0's scales, which meet zero codes
-              const float* src = (kv ? p.v_ts : p.k_ts) + (rr >= 0 ? rr : 0);
-              bulk_load(smem_u32(sb + C::SCALE_OFF + (kv * TL + t) * 64 + u * 32), src, 32,
-                        bar_full + 8 * stage);
-            }
-          }
-        } else {
-          // one 4-D box per (K / V, tile): 16 rows of all heads of the CTA and
-          // all column groups; then (INT8) each tile's 16 per-slot scales
-          constexpr int NB = 2 * TL;
-          for (int i = lane; i < NB + (CT == 2 || I4 ? NB : 0); i += 32) {
-            const int j = i < NB ? i : i - NB;
-            const int kv = j / TL, t = j - kv * TL;
-            const int rr = t ? r[TL - 1][0] : r[0][0];
-            if (i < NB) {
-              tma_load_4d(smem_u32(sb + C::box_off(kv, 0, t, 0)), kv ? &p.tmap_v : &p.tmap_k,
-                          bar_full + 8 * stage, 0, rr, 0, head0, policy);
-            } else if constexpr (I4) {
-              const int blk = rr >= 0 ? rr / K : 0;
-              tma_load_2d(smem_u32(sb + C::word_off(kv, 0, t, 0)),
-                          kv ? &p.tmap_vs : &p.tmap_ks, bar_full + 8 * stage,
-                          rr >= 0 ? rr - blk * K : 0,
-                          rr >= 0 ? blk * (int)(gridDim.y * HPC) + head0 : -2 * HPC, policy);
-            } else if constexpr (CT == 2) {
-              // a tile with no rows reads slot 0's scales, which meet zero codes
-              const float* src = (kv ? p.v_ts : p.k_ts) + (rr >= 0 ? rr : 0);
-              bulk_load(smem_u32(sb + C::SCALE_OFF + (kv * TL + t) * 64), src, 64,
-                        bar_full + 8 * stage);
-            }
-          }
-        }
+        issue(stage, r, policy);
         __syncwarp();
       }
     }
@@ -747,9 +749,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   float slc0[NB], slc1[NB];     // per score column (one-byte pools: q's 2^e folded in)
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) slc0[nb] = slc1[nb] = sl;
-  // INT4, per score column: slc times what the codes' 1024 and 64 add, and times sum(q)
+  // INT4, per score column: minus what the codes' 1024 and 64 add to a product, and
+  // scale_log2 times sum(q); slc0 is one factor for all columns
   float off0[I4 ? NB : 1], off1[I4 ? NB : 1], qs0[I4 ? NB : 1], qs1[I4 ? NB : 1];
-  const int pg = I4 ? int4_pi(g) : g;     // token row of a tile that mma row g holds
+  const int pg = I4 ? int4_pi<C::PAIR>(g) : g;     // token row of a tile that mma row g holds
   // INT4: V scales enter times vinv, a power of two that puts the largest seen (up
   // to vcap) at 2^8 .. 2^11: weights of up to 2^kQuantSlack stay inside f16, and
   // down to 2^-22 of the largest they are normal f16 numbers
@@ -772,7 +775,53 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     return cc < ncol && cu ? uend - nq + cc / G : uend - 1;
   };
   int k = 0;
+  // INT4: chunk k is brought by warp k mod HPC, a stage ahead of the ring's end
+  const uint64_t policy = I4 ? l2_policy_evict_first() : 0;
+  const int total = ce - cb;
+  int window = 0;                       // chunks that `row` stands for, by 32
+  auto produce = [&](int kk) {
+    if ((kk >> 5) != window) {
+      window = kk >> 5;
+      tile_rows(cb + (window << 5), row);
+    }
+    int r[TL][2];
+#pragma unroll
+    for (int t = 0; t < TL; ++t) {
+      r[t][0] = __shfl_sync(0xffffffffu, row[t][0], kk & 31);
+      r[t][1] = __shfl_sync(0xffffffffu, row[t][1], kk & 31);
+    }
+    issue(kk % NS, r, policy);
+    __syncwarp();
+  };
+  // gives up: does not leave the CTA while copies of this warp may still land
+  auto give_up = [&](int kk) {
+    record_error(PKV_DEVERR_TIMEOUT);
+    if constexpr (I4) {
+      for (int i = max(0, kk - NS); i < kk; ++i)
+        if (i % HPC == w) mbar_wait_bounded(bar_full + 8 * (i % NS), (i / NS) & 1);
+    }
+  };
+  if constexpr (I4) {
+    if (w == 0 && lane == 0) {
+      prefetch_tensormap(&p.tmap_k);
+      prefetch_tensormap(&p.tmap_v);
+      prefetch_tensormap(&p.tmap_ks);
+      prefetch_tensormap(&p.tmap_vs);
+    }
+    for (int kk = 0; kk < min(NS, total); ++kk)
+      if (kk % HPC == w) produce(kk);
+  }
   for (int c = cb; c < ce; ++c, ++k) {
+    if constexpr (I4) {
+      const int kk = k + NS - 1;
+      if (k > 0 && kk < total && kk % HPC == w) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_empty + 8 * (kk % NS), ((kk / NS) & 1) ^ 1))) {
+          give_up(kk);
+          return;
+        }
+        produce(kk);
+      }
+    }
     while (c >= cstart[u + 1]) ++u;
     const int a = cstart[u], b = cstart[u + 1];
     if (c == cb || c == a) {
@@ -806,37 +855,43 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           }
         }
       } else if constexpr (I4) {
-        // f16 fragments in the order of the K words (see "INT4"), each head
-        // scaled by a power of two as below
+        // f16 fragments in the order of the K words (see "INT4"), scaled by one power
+        // of two that puts the largest |q| of the warp's heads in [2^14, 2^15): exact
+        // down to 2^-29 of it, far inside the f16 range
+        float amax = 0.f;
+        uint4 raw[NB][4];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const int cq = 8 * nb + g;
           const __nv_bfloat16* qrow =
               p.q + ((int64_t)(qr0 + (cq < ncol ? cq / G : 0)) * H_q + j * G + cq % G) * D + 32 * tq;
-          float qv[4][8];
-          float amax = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (cq < ncol) raw = __ldg(reinterpret_cast<const uint4*>(qrow) + i);
-            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+            raw[nb][i] = make_uint4(0, 0, 0, 0);
+            if (cq < ncol) raw[nb][i] = __ldg(reinterpret_cast<const uint4*>(qrow) + i);
+            const uint32_t w4[4] = {raw[nb][i].x, raw[nb][i].y, raw[nb][i].z, raw[nb][i].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              qv[i][2 * e] = __uint_as_float(w[e] << 16);
-              qv[i][2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-              amax = fmaxf(amax, fmaxf(fabsf(qv[i][2 * e]), fabsf(qv[i][2 * e + 1])));
-            }
+            for (int e = 0; e < 4; ++e)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w4[e] << 16)),
+                                       fabsf(__uint_as_float(w4[e] & 0xffff0000u))));
           }
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          const int eg = amax > 0.f ? ilogbf(amax) - 14 : 0;
-          const float down = ldexpf(1.f, -eg);
+        }
+        amax = warp_max(amax);
+        const int eg = amax > 0.f ? max(-100, min(120, ilogbf(amax) - 14)) : 0;
+        const float down = ldexpf(1.f, -eg);
+        slc0[0] = ldexpf(sl, eg);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
           float even = 0.f, odd = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float* x = qv[i];
+            const uint32_t w4[4] = {raw[nb][i].x, raw[nb][i].y, raw[nb][i].z, raw[nb][i].w};
+            float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= down;
+            for (int e = 0; e < 4; ++e) {
+              x[2 * e] = __uint_as_float(w4[e] << 16) * down;
+              x[2 * e + 1] = __uint_as_float(w4[e] & 0xffff0000u) * down;
+            }
             qf[nb][2 * i][0] = pack_f16x2(x[0], x[4]);
             qf[nb][2 * i][1] = pack_f16x2(x[1], x[5]);
             qf[nb][2 * i + 1][0] = pack_f16x2(x[2], x[6]);
@@ -850,16 +905,14 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
             odd += __shfl_xor_sync(0xffffffffu, odd, o1);
           }
           // score columns of this thread are 2tq, 2tq+1 (held by lanes 8tq, 8tq+4)
-          slc0[nb] = ldexpf(sl, __shfl_sync(0xffffffffu, eg, 8 * tq));
-          slc1[nb] = ldexpf(sl, __shfl_sync(0xffffffffu, eg, 8 * tq + 4));
           const float e0 = __shfl_sync(0xffffffffu, even, 8 * tq);
           const float e1 = __shfl_sync(0xffffffffu, even, 8 * tq + 4);
           const float d0 = __shfl_sync(0xffffffffu, odd, 8 * tq);
           const float d1 = __shfl_sync(0xffffffffu, odd, 8 * tq + 4);
-          off0[nb] = slc0[nb] * (1024.f * e0 + 64.f * d0);
-          off1[nb] = slc1[nb] * (1024.f * e1 + 64.f * d1);
-          qs0[nb] = slc0[nb] * (e0 + d0);
-          qs1[nb] = slc1[nb] * (e1 + d1);
+          off0[nb] = -(1024.f * e0 + 64.f * d0);
+          off1[nb] = -(1024.f * e1 + 64.f * d1);
+          qs0[nb] = slc0[0] * (e0 + d0);
+          qs1[nb] = slc0[0] * (e1 + d1);
         }
         vinv = 1.f;
         vcap = 0.f;
@@ -907,7 +960,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt)
           o[nb][mt][0] = o[nb][mt][1] = o[nb][mt][2] = o[nb][mt][3] = 0.f;
-        m0[nb] = m1[nb] = -INFINITY;
+        m0[nb] = m1[nb] = I4 ? 0.f : -INFINITY;       // (INT4: set by the first chunk)
         l0[nb] = l1[nb] = 0.f;
         vw0[nb] = vw1[nb] = vz0[nb] = vz1[nb] = 0.f;
       }
@@ -916,11 +969,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     const int valid = min(CH, uend - cpos);             // tokens of this chunk
     const int stage = k % NS;
     if (!mbar_wait_bounded(bar_full + 8 * stage, (k / NS) & 1)) {
-      record_error(PKV_DEVERR_TIMEOUT);
+      give_up(min(k + NS, total));
       return;
     }
     uint8_t* sb = smem + stage * C::STAGE;
-    const uint32_t sa = smem_u32(sb);
     // per-token-row K scales and V scales (folded into P) of rows g, g+8 of
     // each tile: INT8 per slot, FP8 per tensor (K's folded into sl)
     float ksr[TL][2], vsr[TL][2];
@@ -930,11 +982,9 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       if constexpr (I4) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t kw = lds32(sa + C::word_off(0, w, t, pg + 8 * r));
-          uint32_t vw = lds32(sa + C::word_off(1, w, t, pg + 8 * r));
-          // words past the end may hold anything: 0-weight x V must stay 0
-          if (valid < CH && t * kTile + pg + 8 * r >= valid) vw = 0u;
-          ksr[t][r] = int4_scale(kw);
+          const uint32_t kw = *reinterpret_cast<const uint32_t*>(sb + C::word_off(0, w, t, pg + 8 * r));
+          const uint32_t vw = *reinterpret_cast<const uint32_t*>(sb + C::word_off(1, w, t, pg + 8 * r));
+          ksr[t][r] = int4_scale(kw) * slc0[0];
           kzr[t][r] = int4_offset(kw);
           vsr[t][r] = int4_scale(vw);
           vzr[t][r] = fmaf(8.f, vsr[t][r], int4_offset(vw));
@@ -954,33 +1004,15 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       }
     }
     if constexpr (I4) {
-      float vmx = 0.f;
+      // words past the end may hold anything: 0-weight x V must stay 0
+      if (valid < CH) {
 #pragma unroll
-      for (int t = 0; t < TL; ++t) vmx = fmaxf(vmx, fmaxf(vsr[t][0], vsr[t][1]));
-      if (__any_sync(0xffffffffu, vmx > vcap)) {
+        for (int t = 0; t < TL; ++t)
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1)
-          vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, off));
-        const int ev = max(-110, min(120, ilogbf(vmx)));
-        const float was = vinv;
-        vinv = ldexpf(1.f, 8 - ev);
-        vcap = ldexpf(8.f, ev);
-        const float f = vinv / was;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-          for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nb][mt][e] *= f;
-        }
+          for (int r = 0; r < 2; ++r)
+            if (t * kTile + pg + 8 * r >= valid) vsr[t][r] = vzr[t][r] = 0.f;
       }
-#pragma unroll
-      for (int t = 0; t < TL; ++t) {
-        vsr[t][0] *= vinv;
-        vsr[t][1] *= vinv;
-      }
-    }
-    if (!I4 && valid < CH) {
+    } else if (valid < CH) {
       // rows past the sequence end may hold anything (stale slots, NaN
       // codes): give them zero V so that 0-weight x V stays 0 in the tensor core
       const int nvec = (CH - valid) * C::NH * 8;
@@ -1000,7 +1032,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int t = 0; t < TL; ++t) sacc[nb][t][0] = sacc[nb][t][1] = sacc[nb][t][2] = sacc[nb][t][3] = 0.f;
+      for (int t = 0; t < TL; ++t) {
+        sacc[nb][t][0] = sacc[nb][t][2] = I4 ? off0[I4 ? nb : 0] : 0.f;
+        sacc[nb][t][1] = sacc[nb][t][3] = I4 ? off1[I4 ? nb : 0] : 0.f;
+      }
     if constexpr (C::KB) {
       const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
       const int chs = lane >> 4;
@@ -1031,8 +1066,9 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     } else if constexpr (I4) {
 #pragma unroll
       for (int t = 0; t < TL; ++t) {
-        const uint32_t kt = sa + C::box_off(0, w, t, 0) + C::row_off(pg) + ((tq ^ ((pg >> 1) & 3)) << 4);
-        const uint4 ra = lds128(kt), rb = lds128(kt + C::RSTEP8);
+        const uint8_t* kt = sb + C::box_off(0, w, t, 0) + C::row_off(pg) + C::chunk_off(w, pg, tq);
+        const uint4 ra = *reinterpret_cast<const uint4*>(kt);
+        const uint4 rb = *reinterpret_cast<const uint4*>(kt + C::RSTEP8);
         const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1077,27 +1113,128 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     // ---- online softmax on (tok 16t+g / 16t+g+8) x (column 8nb+2tq / 8nb+2tq+1)
     const bool cmask = cpos + CH - 1 > ulim;
     uint32_t pb[NB][TL][2], pc[NB][TL][2];
+    if constexpr (I4) {
+      // scores x relative to the exponent base m of their column.  m is raised only
+      // when a score exceeds it by more than 2^kQuantSlack (seen by a vote, without a
+      // reduction), so weights stay below 2^kQuantSlack; the first chunk of a
+      // partition sets it.
+      float x[NB][TL][4];
+      float over = -INFINITY, vmx = 0.f;
+#pragma unroll
+      for (int t = 0; t < TL; ++t) {
+        vmx = fmaxf(vmx, fmaxf(vsr[t][0], vsr[t][1]));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            x[nb][t][2 * r] = fmaf(ksr[t][r], sacc[nb][t][2 * r], fmaf(kzr[t][r], qs0[nb], -m0[nb]));
+            x[nb][t][2 * r + 1] =
+                fmaf(ksr[t][r], sacc[nb][t][2 * r + 1], fmaf(kzr[t][r], qs1[nb], -m1[nb]));
+          }
+        }
+      }
+      if (valid < CH) {                 // keys past the end
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int t = 0; t < TL; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (t * kTile + pg + 8 * r >= valid)
+                x[nb][t][2 * r] = x[nb][t][2 * r + 1] = -INFINITY;
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        if (nb < nbv)
+#pragma unroll
+          for (int t = 0; t < TL; ++t)
+            over = fmaxf(over, fmaxf(fmaxf(x[nb][t][0], x[nb][t][1]), fmaxf(x[nb][t][2], x[nb][t][3])));
+      const bool first = c == cb || c == a;
+      if (first || __any_sync(0xffffffffu, over > kQuantSlack || vmx > vcap)) {
+        // V scales: the largest of this chunk to 2^8
+        float f = 1.f;
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, off));
+        if (vmx > vcap) {
+          const int ev = max(-110, min(120, ilogbf(vmx)));
+          const float was = vinv;
+          vinv = ldexpf(1.f, 8 - ev);
+          vcap = ldexpf(8.f, ev);
+          f = vinv / was;
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float up0 = -INFINITY, up1 = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < TL; ++t) {
+            up0 = fmaxf(up0, fmaxf(x[nb][t][0], x[nb][t][2]));
+            up1 = fmaxf(up1, fmaxf(x[nb][t][1], x[nb][t][3]));
+          }
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            up0 = fmaxf(up0, __shfl_xor_sync(0xffffffffu, up0, off));
+            up1 = fmaxf(up1, __shfl_xor_sync(0xffffffffu, up1, off));
+          }
+          // (a chunk without a finite score leaves the base where it is)
+          if (!first) {
+            up0 = fmaxf(up0, 0.f);
+            up1 = fmaxf(up1, 0.f);
+          }
+          if (!(fabsf(up0) < INFINITY)) up0 = 0.f;
+          if (!(fabsf(up1) < INFINITY)) up1 = 0.f;
+          const float al0 = first ? 1.f : exp2f(-up0), al1 = first ? 1.f : exp2f(-up1);
+          m0[nb] += up0;
+          m1[nb] += up1;
+          l0[nb] *= al0;
+          l1[nb] *= al1;
+          vz0[nb] *= al0;
+          vz1[nb] *= al1;
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            o[nb][mt][0] *= al0 * f;
+            o[nb][mt][1] *= al1 * f;
+            o[nb][mt][2] *= al0 * f;
+            o[nb][mt][3] *= al1 * f;
+          }
+#pragma unroll
+          for (int t = 0; t < TL; ++t) {
+            x[nb][t][0] -= up0;
+            x[nb][t][1] -= up1;
+            x[nb][t][2] -= up0;
+            x[nb][t][3] -= up1;
+          }
+        }
+      }
+      // weights times V scales as one f16 number (half a step is 2^-12 of it, an
+      // eighth of the output's own rounding; the codes carry four bits)
+#pragma unroll
+      for (int t = 0; t < TL; ++t) {
+        const float v0 = vsr[t][0] * vinv, v1 = vsr[t][1] * vinv;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          if (nb >= nbv) continue;
+          const float p0 = ex2_approx_ftz(x[nb][t][0]), p1 = ex2_approx_ftz(x[nb][t][1]);
+          const float p2 = ex2_approx_ftz(x[nb][t][2]), p3 = ex2_approx_ftz(x[nb][t][3]);
+          l0[nb] += p0 + p2;
+          l1[nb] += p1 + p3;
+          vz0[nb] = fmaf(p0, vzr[t][0], fmaf(p2, vzr[t][1], vz0[nb]));
+          vz1[nb] = fmaf(p1, vzr[t][0], fmaf(p3, vzr[t][1], vz1[nb]));
+          pb[nb][t][0] = movmatrix_trans(pack_f16x2(p0 * v0, p1 * v0));
+          pb[nb][t][1] = movmatrix_trans(pack_f16x2(p2 * v1, p3 * v1));
+        }
+      }
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      if (nb >= nbv) continue;
+      if (I4 || nb >= nbv) continue;
       float x[TL][4];
       float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
       for (int t = 0; t < TL; ++t) {
-        if constexpr (I4) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            x[t][2 * r] = fmaf(ksr[t][r], fmaf(sacc[nb][t][2 * r], slc0[nb], -off0[nb]),
-                               kzr[t][r] * qs0[nb]);
-            x[t][2 * r + 1] = fmaf(ksr[t][r], fmaf(sacc[nb][t][2 * r + 1], slc1[nb], -off1[nb]),
-                                   kzr[t][r] * qs1[nb]);
-          }
-        } else {
-          x[t][0] = sacc[nb][t][0] * slc0[nb] * ksr[t][0];
-          x[t][1] = sacc[nb][t][1] * slc1[nb] * ksr[t][0];
-          x[t][2] = sacc[nb][t][2] * slc0[nb] * ksr[t][1];
-          x[t][3] = sacc[nb][t][3] * slc1[nb] * ksr[t][1];
-        }
+        x[t][0] = sacc[nb][t][0] * slc0[nb] * ksr[t][0];
+        x[t][1] = sacc[nb][t][1] * slc1[nb] * ksr[t][0];
+        x[t][2] = sacc[nb][t][2] * slc0[nb] * ksr[t][1];
+        x[t][3] = sacc[nb][t][3] * slc1[nb] * ksr[t][1];
         // causal limit of each score column (decode: the unit's end); a
         // chunk wholly below every column's limit needs no mask
         if (cmask) {
@@ -1185,18 +1322,6 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         l0[nb] += ps0;
         l1[nb] += ps1;
       }
-      if constexpr (I4) {
-        // weights times V scales as one f16 number (half a step is 2^-12 of it, a
-        // sixteenth of the output's own rounding; the codes carry four bits)
-#pragma unroll
-        for (int t = 0; t < TL; ++t) {
-          vz0[nb] = fmaf(pr[t][0], vzr[t][0], fmaf(pr[t][2], vzr[t][1], vz0[nb]));
-          vz1[nb] = fmaf(pr[t][1], vzr[t][0], fmaf(pr[t][3], vzr[t][1], vz1[nb]));
-          pb[nb][t][0] = movmatrix_trans(pack_f16x2(pr[t][0] * vsr[t][0], pr[t][1] * vsr[t][0]));
-          pb[nb][t][1] = movmatrix_trans(pack_f16x2(pr[t][2] * vsr[t][1], pr[t][3] * vsr[t][1]));
-        }
-        continue;
-      }
       // P enters the tensor core as a hi + lo pair of 16-bit terms so that the
       // product carries ~16 significant bits of each weight (one bf16 rounding
       // of P costs up to 2^-9 relative per weight); one-byte pools: f16 terms
@@ -1227,14 +1352,15 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     // column block (one V fragment feeds every column block)
     if constexpr (I4) {
       // rows of m tile mt: row g -> d = 16 g + 2 mt, row g + 8 -> the one behind it
-      const int j0 = (tq & 1) | ((tq & 2) << 1), j1 = j0 ^ 3;        // pi(2 tq), pi(2 tq + 1)
+      const int j0 = int4_pi<C::PAIR>(2 * tq), j1 = int4_pi<C::PAIR>(2 * tq + 1);
 #pragma unroll
       for (int t = 0; t < TL; ++t) {
-        const uint32_t vt = sa + C::box_off(1, w, t, 0) + (g & 1) * 8;
-        const uint32_t v0 = vt + C::row_off(j0) + (((g >> 1) ^ (j0 >> 1 & 3)) << 4);
-        const uint32_t v1 = vt + C::row_off(j1) + (((g >> 1) ^ (j1 >> 1 & 3)) << 4);
-        const uint2 r0 = lds64(v0), r1 = lds64(v1);
-        const uint2 r2 = lds64(v0 + C::RSTEP8), r3 = lds64(v1 + C::RSTEP8);
+        const uint8_t* vt = sb + C::box_off(1, w, t, 0) + (g & 1) * 8;
+        const uint8_t* v0 = vt + C::row_off(j0) + C::chunk_off(w, j0, g >> 1);
+        const uint8_t* v1 = vt + C::row_off(j1) + C::chunk_off(w, j1, g >> 1);
+        const uint2 r0 = *reinterpret_cast<const uint2*>(v0), r1 = *reinterpret_cast<const uint2*>(v1);
+        const uint2 r2 = *reinterpret_cast<const uint2*>(v0 + C::RSTEP8);
+        const uint2 r3 = *reinterpret_cast<const uint2*>(v1 + C::RSTEP8);
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {            // words (q4 / 2), their halves
           const uint32_t sel = q4 & 1 ? 0x7632u : 0x5410u;
@@ -1371,6 +1497,8 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           o[0][mt][3] -= c1;
         }
       }
+      // (without shared-prefix groups all columns of a decode unit are one sequence's)
+      const int unit_np = !SH && !PX && cu == nullptr ? tc_unit_parts(cstart, u, T, n) : 0;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         if (nb >= nbv) continue;
@@ -1394,6 +1522,9 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           if constexpr (PX) {
             np = 2;                              // merged with the prefix part
             slot = (cta + u) * p.px.max_q + cc / G;
+          } else if (!SH && cu == nullptr) {
+            np = unit_np;
+            slot = cta + u;
           } else if (cu == nullptr) {
             const int4 mt = tc_seq_meta(cstart, row / H_q, M, T, n, p.slot_stride);
             np = mt.y + mt.w;
