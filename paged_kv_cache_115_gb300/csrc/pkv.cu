@@ -149,6 +149,7 @@ struct AttnPlan {
   int64_t slots = 0;                         // partial slots of the workspace
   int64_t slot_stride = 0;                   // tensor-core kernel: slots per member region
   bool reduce = false;                       // a split-K reduce launch follows
+  bool wide_merge = false;                   // by a CTA a row
   int seq_batch = 0;
   size_t ws_bytes = 0;
 };
@@ -162,6 +163,9 @@ bool simt_shape_ok(int G, int D) {
   return (D == 32 || D == 64 || D == 128 || D == 256) && G >= 1 && G <= 16;
 }
 
+#ifndef PKV_ONE
+#define PKV_ONE 4
+#endif
 #ifndef PKV_I4_HPC
 #define PKV_I4_HPC 8
 #endif
@@ -215,7 +219,11 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
     p.hpc = tc_hpc(H_kv, ct);
     p.groups = H_kv / p.hpc;
     // one CTA per SM (shared memory bound), or as many as a pool format takes
-    const int total = sms * pkv::tc_ctas(ct, p.hpc, c.share_prefix != 0);
+    // members of a shared-prefix group: the columns of two blocks; INT4 pools with G
+    // <= 4 those of one, which leaves registers for twice the warps
+    const bool one_block = ct == 4 && G <= PKV_ONE;
+    const int share_m = !c.share_prefix ? 1 : (one_block ? 8 : 16) / G;
+    const int total = sms * pkv::tc_ctas(ct, p.hpc, share_m > 1 && !one_block);
     p.n_per_group = c.num_splits ? c.num_splits : (total / p.groups > 0 ? total / p.groups : 1);
     const int max_chunks = (int)ceil_div(max_len, pkv::kTcChunk);
     p.pmax = std::max(1, std::min(p.n_per_group, max_chunks));
@@ -223,7 +231,7 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
     if (c.share_prefix && G <= 8) {
       // groups of 16 / G sequences fill the kernel's two 8-column blocks; a
       // sequence's partials are its group's shared unit's, then its own's
-      p.share_m = 16 / G;
+      p.share_m = share_m;
       p.seq_batch = std::min(S, pkv::kTcMaxShareSeqs);
     }
     // decode partials: slot CTA + unit (one region per member of a shared
@@ -231,6 +239,9 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
     p.slot_stride = (int64_t)p.n_per_group + pkv::tc_num_units(std::max(p.seq_batch, 1), p.share_m);
     p.slots = p.slot_stride * p.share_m;   // a region per member of a shared unit
     p.reduce = max_chunks > 1;
+    // partials of a row: the CTAs of a group over its sequences, or fewer
+    p.wide_merge = ct == 4 && (int64_t)S * H_q <= 8 * sms &&
+                   p.n_per_group > 16 * std::max(p.seq_batch, 1) && max_chunks > 32;
   } else {
     PKV_CHECK(simt_shape_ok(G, D), PKV_ERR_UNSUPPORTED,
               "unsupported shape: head_dim must be 32/64/128/256 and G <= 16");
@@ -303,12 +314,12 @@ int* carve_glen(void* ws, const AttnPlan& p, int H_q, int H_kv, int D) {
 }
 
 // ---- tensor-core kernel dispatch ------------------------------------------------
-template <int D, int HPC, int CT, bool B8, bool SH = false, bool PX = false>
+template <int D, int HPC, int CT, bool B8, int SH = 0, bool PX = false>
 struct TcInst {
   // stages: as many as fit in ~192 KiB (bf16) / ~203 KiB (one-byte pools)
   // of shared memory, between 2 and 8
   static constexpr int STAGE_BYTES = pkv::TcCfg<D, HPC, 2, CT, B8 && CT == 4>::STAGE;
-  static constexpr int CTAS = pkv::tc_ctas(CT, HPC, SH);    // share the SM's 228 KiB
+  static constexpr int CTAS = pkv::tc_ctas(CT, HPC, SH == 1);    // share the SM's 228 KiB
   static constexpr int BUDGET =
       CTAS > 1 ? 233472 / CTAS - 1024 - 9472 : (CT ? 217088 - 9216 : 196608);
   static constexpr int NS_FIT = BUDGET / STAGE_BYTES;
@@ -325,9 +336,9 @@ struct TcInst {
     return PKV_OK;
   }
 };
-template <int D, int HPC, int CT, bool B8, bool SH, bool PX>
+template <int D, int HPC, int CT, bool B8, int SH, bool PX>
 std::once_flag TcInst<D, HPC, CT, B8, SH, PX>::flags[kMaxDevices];
-template <int D, int HPC, int CT, bool B8, bool SH, bool PX>
+template <int D, int HPC, int CT, bool B8, int SH, bool PX>
 cudaError_t TcInst<D, HPC, CT, B8, SH, PX>::errs[kMaxDevices];
 
 // ---- multi-query (prefill) kernel dispatch -----------------------------------------
@@ -479,7 +490,7 @@ pkv_status plan_prefill(int num_seqs, int num_tokens, int max_query_len, int max
   return PKV_OK;
 }
 
-template <int D, int CT, bool B8, bool SH = false, bool PX = false>
+template <int D, int CT, bool B8, int SH = 0, bool PX = false>
 pkv_status launch_tc_hpc(int hpc, const pkv::TcParams& prm, int n, int groups, cudaStream_t st,
                          int dev) {
   switch (hpc) {
@@ -499,11 +510,17 @@ pkv_status launch_tc_d(int hpc, int block_size, const pkv::TcParams& prm, int n,
   if constexpr (CT == 3) {
     return launch_tc_hpc<D, CT, false>(hpc, prm, n, groups, st, dev);   // 16-row tiles only
   }
+  if constexpr (CT == 4) {
+    if (prm.share_m > 1 && prm.share_m * prm.G <= 8)
+      return block_size < pkv::kTile
+                 ? launch_tc_hpc<D, CT, true, 2>(hpc, prm, n, groups, st, dev)
+                 : launch_tc_hpc<D, CT, false, 2>(hpc, prm, n, groups, st, dev);
+  }
   if constexpr (CT == 0 || CT == 4) {
     if (prm.share_m > 1)
       return block_size < pkv::kTile
-                 ? launch_tc_hpc<D, CT, true, true>(hpc, prm, n, groups, st, dev)
-                 : launch_tc_hpc<D, CT, false, true>(hpc, prm, n, groups, st, dev);
+                 ? launch_tc_hpc<D, CT, true, 1>(hpc, prm, n, groups, st, dev)
+                 : launch_tc_hpc<D, CT, false, 1>(hpc, prm, n, groups, st, dev);
   }
   if constexpr (CT != 3) {
     return block_size < pkv::kTile ? launch_tc_hpc<D, CT, true>(hpc, prm, n, groups, st, dev)
@@ -664,6 +681,16 @@ pkv_status launch_simt_any(pkv_dtype dt, const pkv_kv_quant* quant, int D, const
 }
 
 // ---- split-K reduce dispatch -----------------------------------------------------
+// INT4 pools split over two CTAs an SM: few rows of many partials are merged by a
+// CTA each.  (4 sequences of 131072 tokens, 64 heads, 76 partials a row: 27 us with a
+// warp each, cold.)
+template <typename T>
+pkv_status launch_reduce_wide(pkv::Workspace ws, int S, int H_q, void* out, cudaStream_t st) {
+  PKV_CUDA(launch_pdl(pkv::attn_reduce_wide_kernel<T, 128>, dim3((unsigned)(S * H_q)),
+                      dim3(pkv::kReduceWarps * 32), 0, st, ws, H_q, static_cast<T*>(out)));
+  return PKV_OK;
+}
+
 template <typename T>
 pkv_status launch_reduce(int D, pkv::Workspace ws, int S, int H_q, void* out, cudaStream_t st) {
   const int64_t pairs = (int64_t)S * H_q;
@@ -783,25 +810,14 @@ pkv_status check_quant(const pkv_kv_quant* q, bool need_token_scales) {
 // ---- quantizing writes ----------------------------------------------------------
 template <typename TIN, int D>
 pkv_status launch_write_int4(const pkv::Int4WriteParams& p, cudaStream_t st) {
-  constexpr int RPI = pkv::kInt4Threads / (D / (16 / (int)sizeof(TIN)));
+  constexpr int RPI = pkv::kInt4Threads / (D / (16 / (int)sizeof(TIN) * pkv::kInt4Loads));
   const bool wide = aligned(p.k, 16) && aligned(p.v, 16) && p.k_stride % (16 / sizeof(TIN)) == 0 &&
                     p.v_stride % (16 / sizeof(TIN)) == 0;
-  int dev, sms;
-  pkv_status s = device_facts(&dev, &sms);
-  if (s != PKV_OK) return s;
-  const int64_t rows = (int64_t)p.T * 2 * p.H;
-  const int64_t ctas = ceil_div(rows, RPI);
-  const dim3 block(pkv::kInt4Threads);
-  if (!wide) {
-    PKV_CUDA(launch_pdl(pkv::kv_write_int4_kernel<TIN, D, 1, false>, dim3((unsigned)ctas), block, 0,
-                        st, p));
-  } else if (ctas >= 8 * sms) {
-    PKV_CUDA(launch_pdl(pkv::kv_write_int4_kernel<TIN, D, 4, true>,
-                        dim3((unsigned)ceil_div(rows, 4 * RPI)), block, 0, st, p));
-  } else {
-    PKV_CUDA(launch_pdl(pkv::kv_write_int4_kernel<TIN, D, 1, true>, dim3((unsigned)ctas), block, 0,
-                        st, p));
-  }
+  const dim3 grid((unsigned)ceil_div((int64_t)p.T * 2 * p.H, RPI)), block(pkv::kInt4Threads);
+  if (wide)
+    PKV_CUDA(launch_pdl(pkv::kv_write_int4_kernel<TIN, D, true>, grid, block, 0, st, p));
+  else
+    PKV_CUDA(launch_pdl(pkv::kv_write_int4_kernel<TIN, D, false>, grid, block, 0, st, p));
   return PKV_OK;
 }
 
@@ -873,14 +889,15 @@ pkv_status write_quant(const void* k, int64_t k_stride, const void* v, int64_t v
 }
 
 // ---- beam selection dispatch ------------------------------------------------------
-// Values a thread: 64 where that fills the SMs twice over, else 16, so that a few
-// rows still spread over the machine.
-constexpr int kBeamWide = 64, kBeamNarrow = 16;
-int beam_tiles(int64_t V, int ept) {
-  return (int)ceil_div(V + 7, (int64_t)pkv::kBeamThreads * ept);
+// 16-byte blocks a thread: 8 (128 bytes in flight each) where that fills the SMs
+// twice over, else 2, so that a few rows still spread over the machine.
+constexpr int kBeamWide = 8, kBeamNarrow = 2;
+int beam_tiles(int64_t V, int blocks, int elem) {
+  const int per = 16 / elem;
+  return (int)ceil_div(V + per - 1, (int64_t)pkv::kBeamThreads * blocks * per);
 }
-int beam_ept(int64_t rows, int64_t V, int sms) {
-  return rows * beam_tiles(V, kBeamWide) >= 2 * sms ? kBeamWide : kBeamNarrow;
+int beam_blocks(int64_t rows, int64_t V, int elem, int sms) {
+  return rows * beam_tiles(V, kBeamWide, elem) >= 2 * sms ? kBeamWide : kBeamNarrow;
 }
 
 struct BeamWs {
@@ -899,15 +916,15 @@ pkv_status check_beam(int R, int B, int V, int N) {
   PKV_CHECK(B <= pkv::kBeamMax && N <= pkv::kBeamMax && V <= (1 << 22), PKV_ERR_UNSUPPORTED,
             "beam selection takes at most %d beams, %d candidates and a vocabulary of 2^22",
             pkv::kBeamMax, pkv::kBeamMax);
-  PKV_CHECK((int64_t)R * B * beam_tiles(V, kBeamNarrow) <= 2147483647, PKV_ERR_UNSUPPORTED,
+  PKV_CHECK((int64_t)R * B * beam_tiles(V, kBeamNarrow, 4) <= 2147483647, PKV_ERR_UNSUPPORTED,
             "too many rows");
   return PKV_OK;
 }
 
 template <typename T>
-pkv_status launch_beam(const pkv::BeamParams& p, int ept, cudaStream_t st) {
+pkv_status launch_beam(const pkv::BeamParams& p, int blocks, cudaStream_t st) {
   const dim3 grid((unsigned)((int64_t)p.R * p.B * p.tiles)), block(pkv::kBeamThreads);
-  if (ept == kBeamWide)
+  if (blocks == kBeamWide)
     PKV_CUDA(launch_pdl(pkv::beam_tiles_kernel<T, kBeamWide>, grid, block, 0, st, p));
   else
     PKV_CUDA(launch_pdl(pkv::beam_tiles_kernel<T, kBeamNarrow>, grid, block, 0, st, p));
@@ -1587,8 +1604,7 @@ pkv_status attention_impl(const void* q, const void* k_cache, const void* v_cach
         int* glen = carve_glen(workspace, plan, H_q, H_kv, D);
         const int ngroups = (int)ceil_div(S, plan.share_m);
         PKV_CUDA(launch_pdl(pkv::share_prefix_kernel,
-                            dim3((unsigned)ceil_div(ngroups, pkv::kShareWarps)),
-                            dim3(pkv::kShareWarps * 32), 0, strm, btb, max_blocks_per_seq, lb,
+                            dim3((unsigned)ngroups), dim3(pkv::kShareThreads), 0, strm, btb, max_blocks_per_seq, lb,
                             max_context_len, S, block_size, plan.share_m, glen));
         prm.glen = glen;
       }
@@ -1617,7 +1633,10 @@ pkv_status attention_impl(const void* q, const void* k_cache, const void* v_cach
       st = launch_simt_any(dtype, quant, D, qb, k_cache, v_cache, ob, a, strm);
     }
     if (st != PKV_OK) return st;
-    if (plan.reduce) {
+    if (plan.reduce && plan.wide_merge) {
+      st = launch_reduce_wide<__nv_bfloat16>(ws, S, H_q, ob, strm);
+      if (st != PKV_OK) return st;
+    } else if (plan.reduce) {
       st = dtype == PKV_BF16
                ? launch_reduce<__nv_bfloat16>(D, ws, S, H_q, ob, strm)
                : launch_reduce<float>(D, ws, S, H_q, ob, strm);
@@ -2133,11 +2152,11 @@ pkv_status pkv_attention_decode_prefix(
   if (st != PKV_OK) return st;
   const bool b8 = block_size < pkv::kTile;
   if (D == 64)
-    st = b8 ? launch_tc_hpc<64, 0, true, false, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev)
-            : launch_tc_hpc<64, 0, false, false, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev);
+    st = b8 ? launch_tc_hpc<64, 0, true, 0, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev)
+            : launch_tc_hpc<64, 0, false, 0, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev);
   else
-    st = b8 ? launch_tc_hpc<128, 0, true, false, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev)
-            : launch_tc_hpc<128, 0, false, false, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev);
+    st = b8 ? launch_tc_hpc<128, 0, true, 0, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev)
+            : launch_tc_hpc<128, 0, false, 0, true>(plan.hpc, t, plan.n_per_group, plan.split.groups, strm, plan.dev);
   if (st != PKV_OK) return st;
   return D == 64 ? launch_prefix_merge<64>(p, plan, strm) : launch_prefix_merge<128>(p, plan, strm);
 }
@@ -2185,7 +2204,12 @@ pkv_status pkv_beam_select_workspace_bytes(int32_t num_requests, int32_t num_bea
   st = device_facts(&dev, &sms);
   if (st != PKV_OK) return st;
   const int64_t rows = (int64_t)num_requests * num_beams;
-  *bytes = beam_ws(rows, beam_tiles(vocab, beam_ept(rows, vocab, sms)), num_select).total;
+  // (the larger of both types' needs: the call takes either)
+  size_t need = 0;
+  for (int elem : {2, 4})
+    need = std::max(need, beam_ws(rows, beam_tiles(vocab, beam_blocks(rows, vocab, elem, sms), elem),
+                                  num_select).total);
+  *bytes = need;
   return PKV_OK;
 }
 
@@ -2212,7 +2236,8 @@ pkv_status pkv_beam_select(const void* logits, int64_t logits_stride, const floa
   int dev, sms;
   st = device_facts(&dev, &sms);
   if (st != PKV_OK) return st;
-  const int ept = beam_ept(rows, vocab, sms), tiles = beam_tiles(vocab, ept);
+  const int elem = (int)elem_bytes(dtype), blocks = beam_blocks(rows, vocab, elem, sms);
+  const int tiles = beam_tiles(vocab, blocks, elem);
   const BeamWs w = beam_ws(rows, tiles, num_select);
   PKV_CHECK(workspace_bytes >= w.total, PKV_ERR_WORKSPACE_TOO_SMALL,
             "workspace %zu bytes < %zu needed", workspace_bytes, w.total);
@@ -2221,8 +2246,8 @@ pkv_status pkv_beam_select(const void* logits, int64_t logits_stride, const floa
                        finished_out, reinterpret_cast<float2*>(ws),
                        reinterpret_cast<float*>(ws + w.x), reinterpret_cast<int32_t*>(ws + w.v),
                        num_requests, num_beams, vocab, num_select, tiles, eos_token};
-  return dtype == PKV_BF16 ? launch_beam<__nv_bfloat16>(p, ept, as_stream(stream))
-                           : launch_beam<float>(p, ept, as_stream(stream));
+  return dtype == PKV_BF16 ? launch_beam<__nv_bfloat16>(p, blocks, as_stream(stream))
+                           : launch_beam<float>(p, blocks, as_stream(stream));
 }
 
 pkv_status pkv_fork_tables_workspace_bytes(int32_t num_groups, int32_t group_rows,

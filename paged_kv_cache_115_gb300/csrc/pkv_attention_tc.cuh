@@ -397,14 +397,16 @@ __host__ __device__ __forceinline__ int4 tc_seq_meta(const int* cstart, int s, i
   return r;
 }
 
-template <int D, int HPC, int NS, int CT = 0, bool B8 = false, bool SH = false, bool PX = false>
-__global__ void __launch_bounds__(TcCfg<D, HPC, NS, CT, B8>::THREADS, tc_ctas(CT, HPC, SH))
+template <int D, int HPC, int NS, int CT = 0, bool B8 = false, int SH = 0, bool PX = false>
+__global__ void __launch_bounds__(TcCfg<D, HPC, NS, CT, B8>::THREADS, tc_ctas(CT, HPC, SH == 1))
 attn_tc_kernel(const __grid_constant__ TcParams p) {
   using C = TcCfg<D, HPC, NS, CT, B8>;
   constexpr int TL = C::TL, CH = C::CH;
   // 8-column blocks of the score tile: two in shared-prefix mode (the query
-  // heads of a group's members side by side), one otherwise
-  constexpr int NB = SH ? 2 : 1;
+  // heads of a group's members side by side), one otherwise (SH 2: groups whose
+  // members fit one block)
+  constexpr int NB = SH == 1 ? 2 : 1;
+  static_assert(SH != 2 || CT == 4, "groups of one column block: INT4 pools");
   constexpr bool I4 = C::I4;
   static_assert(!SH || CT == 0 || CT == 4, "shared-prefix groups need bf16 or INT4 pools");
   static_assert(!PX || (CT == 0 && !SH), "shared-prefix attention needs bf16 pools");
@@ -421,6 +423,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   const int S = p.num_seqs;
   const int K = p.block_size;
   const int row_tokens = p.max_blocks_per_seq * K;
+  const int log2k = (K & (K - 1)) == 0 ? __ffs(K) - 1 : -1;
   const int M = SH ? p.share_m : 1;
   // several query tokens per sequence (never with shared-prefix groups)
   const int32_t* const cu = SH ? nullptr : p.cu_seqlens;
@@ -660,7 +663,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
                       policy);
         } else if constexpr (I4) {
           // no rows: words out of bounds too, which TMA fills with zeros
-          const int blk = rr >= 0 ? rr / K : 0;
+          const int blk = rr < 0 ? 0 : (log2k >= 0 ? rr >> log2k : rr / K);
           tma_load_2d(smem_u32(sb + C::word_off(kv, 0, t, 8 * u)),
                       kv ? &p.tmap_vs : &p.tmap_ks, bar_full + 8 * stage,
                       rr >= 0 ? rr - blk * K : 0,
@@ -684,7 +687,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           tma_load_4d(smem_u32(sb + C::box_off(kv, 0, t, 0)), kv ? &p.tmap_v : &p.tmap_k,
                       bar_full + 8 * stage, 0, rr, 0, box0, policy);
         } else if constexpr (I4) {
-          const int blk = rr >= 0 ? rr / K : 0;
+          const int blk = rr < 0 ? 0 : (log2k >= 0 ? rr >> log2k : rr / K);
           tma_load_2d(smem_u32(sb + C::word_off(kv, 0, t, 0)),
                       kv ? &p.tmap_vs : &p.tmap_ks, bar_full + 8 * stage,
                       rr >= 0 ? rr - blk * K : 0,
@@ -779,7 +782,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   const uint64_t policy = I4 ? l2_policy_evict_first() : 0;
   const int total = ce - cb;
   int window = 0;                       // chunks that `row` stands for, by 32
-  auto produce = [&](int kk) {
+  auto produce = [&](int kk, int at) {
     if ((kk >> 5) != window) {
       window = kk >> 5;
       tile_rows(cb + (window << 5), row);
@@ -790,7 +793,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       r[t][0] = __shfl_sync(0xffffffffu, row[t][0], kk & 31);
       r[t][1] = __shfl_sync(0xffffffffu, row[t][1], kk & 31);
     }
-    issue(kk % NS, r, policy);
+    issue(at, r, policy);
     __syncwarp();
   };
   // gives up: does not leave the CTA while copies of this warp may still land
@@ -809,21 +812,30 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
       prefetch_tensormap(&p.tmap_vs);
     }
     for (int kk = 0; kk < min(NS, total); ++kk)
-      if (kk % HPC == w) produce(kk);
+      if (kk % HPC == w) produce(kk, kk);
   }
+  int stage = 0;                        // k mod NS
+  uint32_t phase = 0;                   // k / NS, its lowest bit
+  int a = cstart[u], b = cstart[u + 1]; // chunks of the unit
   for (int c = cb; c < ce; ++c, ++k) {
     if constexpr (I4) {
       const int kk = k + NS - 1;
       if (k > 0 && kk < total && kk % HPC == w) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_empty + 8 * (kk % NS), ((kk / NS) & 1) ^ 1))) {
+        // (chunk kk reuses the stage of chunk k - 1)
+        const int at = stage == 0 ? NS - 1 : stage - 1;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_empty + 8 * at,
+                                                       stage == 0 ? phase ^ 1 : phase))) {
           give_up(kk);
           return;
         }
-        produce(kk);
+        produce(kk, at);
       }
     }
-    while (c >= cstart[u + 1]) ++u;
-    const int a = cstart[u], b = cstart[u + 1];
+    if (c >= b) {
+      do ++u; while (c >= cstart[u + 1]);
+      a = cstart[u];
+      b = cstart[u + 1];
+    }
     if (c == cb || c == a) {
       // ---- new partition: load the q-group(s) as the B fragments of Q^T
       int s0, rows;
@@ -967,8 +979,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     }
     const int cpos = ut0 + (c - a) * CH;                 // key position of chunk row 0
     const int valid = min(CH, uend - cpos);             // tokens of this chunk
-    const int stage = k % NS;
-    if (!mbar_wait_bounded(bar_full + 8 * stage, (k / NS) & 1)) {
+    if (!mbar_wait_bounded(bar_full + 8 * stage, phase)) {
       give_up(min(k + NS, total));
       return;
     }
@@ -1454,6 +1465,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_empty + 8 * stage);
+    if (++stage == NS) {
+      stage = 0;
+      phase ^= 1;
+    }
 
     if (c == ce - 1 || c == b - 1) {
       // ---- end of partition: write the final output or a partial state of
@@ -1572,54 +1587,53 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
 // glen[g] = the number of leading tokens that every member reads from the
 // same physical blocks: the leading run of block-table entries equal in all
 // members' rows, times the block size, capped at the shortest member's length
-// and rounded down to whole 16-token chunks (0 for a group of one).  One warp
-// per group compares 32 entries at a time and stops at the first difference;
+// and rounded down to whole 16-token chunks (0 for a group of one).  One CTA
+// per group compares 256 entries at a time and stops at the first difference;
 // only entries inside every member's length are read.  Lengths are clamped as
 // the attention kernel clamps them (which also reports them).
 // ===========================================================================
-constexpr int kShareWarps = 8;
+constexpr int kShareThreads = 256;
 
-__global__ void __launch_bounds__(kShareWarps * 32)
+// A CTA a group: 256 entries at a time (a warp a group took 16 us for tables of 257
+// blocks, most of it waiting for one round of loads after the other).
+__global__ void __launch_bounds__(kShareThreads)
 share_prefix_kernel(const int32_t* __restrict__ block_tables, int max_blocks_per_seq,
                     const int32_t* __restrict__ context_lens, int max_len, int S, int K, int m,
                     int* __restrict__ glen) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = blockIdx.x * kShareWarps + warp;
-  const int ngroups = (S + m - 1) / m;
+  __shared__ int s_run;
+  const int g = blockIdx.x, tid = threadIdx.x;
   const int cap = min(max_len, max_blocks_per_seq * K);
+  const int s0 = g * m, cnt = min(m, S - s0);
   int lg = 0;
-  if (g < ngroups) {
-    const int s0 = g * m, cnt = min(m, S - s0);
-    if (cnt >= 2) {
-      int lmin = cap;
-      for (int i = 0; i < cnt; ++i) {
-        const int L = context_lens[s0 + i];
-        lmin = min(lmin, L < 0 ? 0 : min(L, cap));
-      }
-      const int nblk = (lmin + K - 1) / K;
-      int run = nblk;
-      for (int b0 = 0; b0 < nblk; b0 += 32) {
-        const int b = b0 + lane;
-        bool same = true;
-        if (b < nblk) {
-          const int e0 = block_tables[(int64_t)s0 * max_blocks_per_seq + b];
-          for (int i = 1; i < cnt; ++i)
-            same = same && block_tables[(int64_t)(s0 + i) * max_blocks_per_seq + b] == e0;
-        }
-        const unsigned diff = __ballot_sync(0xffffffffu, !same);
-        if (diff) {
-          run = b0 + __ffs(diff) - 1;
-          break;
-        }
-      }
-      lg = min(run * K, lmin) / kTile * kTile;
+  if (cnt >= 2) {
+    int lmin = cap;
+    for (int i = 0; i < cnt; ++i) {
+      const int L = context_lens[s0 + i];
+      lmin = min(lmin, L < 0 ? 0 : min(L, cap));
     }
+    const int nblk = (lmin + K - 1) / K;
+    if (tid == 0) s_run = nblk;
+    for (int b0 = 0; b0 < nblk; b0 += kShareThreads) {
+      const int b = b0 + tid;
+      bool same = true;
+      if (b < nblk) {
+        const int e0 = block_tables[(int64_t)s0 * max_blocks_per_seq + b];
+#pragma unroll 4
+        for (int i = 1; i < cnt; ++i)
+          same = same && block_tables[(int64_t)(s0 + i) * max_blocks_per_seq + b] == e0;
+      }
+      __syncthreads();                       // (s_run is set, or was read)
+      if (!same) atomicMin(&s_run, b);
+      if (__syncthreads_or(!same)) break;
+    }
+    __syncthreads();
+    lg = min(s_run * K, lmin) / kTile * kTile;
   }
   // the tables and lengths are written by no kernel that lets this one start
   // before it ends; the workspace may still be read by the previous launch
   pdl_wait_primary();
   pdl_launch_dependents();
-  if (g < ngroups && lane == 0) glen[g] = lg;
+  if (tid == 0) glen[g] = lg;
 }
 
 }  // namespace pkv

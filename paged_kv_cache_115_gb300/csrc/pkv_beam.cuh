@@ -60,13 +60,93 @@ __device__ __forceinline__ uint64_t beam_order(double x) {
   return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
 }
 
-// EPT values a thread: a tile of kBeamThreads * EPT values of a row, counted
-// from the 16-byte boundary at or in front of the row (rows of an odd vocabulary
-// start anywhere); what does not belong to the row counts as -inf.
-template <typename T, int EPT>
-__global__ void __launch_bounds__(kBeamThreads)
+// The larger of each half of two bf16 pairs (a NaN gives way).
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+// The largest value of a 16-byte block.
+template <typename T>
+__device__ __forceinline__ float beam_block_max(const uint4& r) {
+  if constexpr (sizeof(T) == 4)
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
+                 fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  const uint32_t m = bf16x2_max(bf16x2_max(r.x, r.y), bf16x2_max(r.z, r.w));
+  return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+}
+
+// Value e of a block; `w` through an empty asm, so that the compiler keeps the block
+// packed between its uses instead of all 64 values in registers.
+template <typename T>
+__device__ __forceinline__ float beam_value(const uint4& r, int e) {
+  constexpr int P = sizeof(T) == 4 ? 1 : 2;
+  uint32_t w = e / P == 0 ? r.x : (e / P == 1 ? r.y : (e / P == 2 ? r.z : r.w));
+  asm volatile("" : "+r"(w));
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+  return __uint_as_float((e & 1) ? w & 0xffff0000u : w << 16);
+}
+__device__ __forceinline__ uint64_t beam_key(float x, int v) {
+  return (uint64_t)beam_order(x) << 32 | (0xffffffffu - (uint32_t)v);
+}
+
+// A block's values at or above tau into the buffer (first value: token v).
+template <typename T>
+__device__ __noinline__ void beam_push(uint4 r, int v, float tau, int* n, uint64_t* key) {
+#pragma unroll
+  for (int e = 0; e < (int)(16 / sizeof(T)); ++e) {
+    const float x = beam_value<T>(r, e);
+    if (x >= tau && x > -INFINITY) {
+      const int i = atomicAdd(n, 1);
+      if (i < kBeamBuffer) key[i] = beam_key(x, v + e);
+    }
+  }
+}
+
+// A tile of very many equal values: its N best one after the other, read again.
+template <typename T, int NV>
+__device__ __noinline__ void beam_tile_slow(const T* base, int V, int first, int N, float* out_x,
+                                            int32_t* out_v, uint64_t* s_best) {
+  constexpr int VE = 16 / sizeof(T);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int end = min(V, first + kBeamThreads * NV * VE);
+  uint64_t last = ~0ull;
+  for (int r = 0; r < N; ++r) {
+    uint64_t best = 0;
+    for (int v = max(0, first) + threadIdx.x; v < end; v += kBeamThreads) {
+      const float x = to_f32(base[v]);
+      const uint64_t key = beam_key(x, v);
+      if (x > -INFINITY && key < last && key > best) best = key;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t y = __shfl_xor_sync(0xffffffffu, best, o);
+      best = y > best ? y : best;
+    }
+    __syncthreads();
+    if (lane == 0) s_best[warp] = best;
+    __syncthreads();
+    best = s_best[0];
+#pragma unroll
+    for (int w = 1; w < kBeamWarps; ++w) best = s_best[w] > best ? s_best[w] : best;
+    last = best;
+    if (threadIdx.x == 0) {                         // (more than kBeamBuffer values: there are N)
+      const uint32_t o = (uint32_t)(best >> 32);
+      out_x[r] = __uint_as_float(o ^ ((uint32_t)((int32_t)~o >> 31) | 0x80000000u));
+      out_v[r] = (int32_t)(0xffffffffu - (uint32_t)best);
+    }
+  }
+}
+
+// NV 16-byte blocks a thread, all in flight at once: a tile of a row, counted from
+// the 16-byte boundary at or in front of the row (rows of an odd vocabulary start
+// anywhere); what does not belong to the row counts as -inf.  Four CTAs an SM: the
+// blocks stay packed in registers and are unpacked as they are used.
+// Bound by HBM (V e bytes a row).
+template <typename T, int NV>
+__global__ void __launch_bounds__(kBeamThreads, 4)
 beam_tiles_kernel(const __grid_constant__ BeamParams p) {
-  constexpr int VE = 16 / sizeof(T), NV = EPT / VE;
+  constexpr int VE = 16 / sizeof(T);
   __shared__ float s_m[kBeamWarps], s_s[kBeamWarps], s_tau[kBeamWarps];
   __shared__ int s_n;
   __shared__ uint64_t s_key[kBeamBuffer], s_best[kBeamWarps];
@@ -89,14 +169,6 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
     raw[j] = make_uint4(kNone, kNone, kNone, kNone);
     if (v < nvec) raw[j] = __ldcs(vec + v);
   }
-  auto words = [&](int j, int i) -> uint32_t {
-    return i == 0 ? raw[j].x : (i == 1 ? raw[j].y : (i == 2 ? raw[j].z : raw[j].w));
-  };
-  auto value = [&](int j, int e) -> float {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(words(j, e));
-    const uint32_t w = words(j, e >> 1);
-    return __uint_as_float((e & 1) ? w & 0xffff0000u : w << 16);
-  };
   // the first and the last block of a row hold values of its neighbours
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -115,9 +187,7 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
   }
   float mx = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < VE; ++e) mx = fmaxf(mx, value(j, e));
+  for (int j = 0; j < NV; ++j) mx = fmaxf(mx, beam_block_max<T>(raw[j]));
   // bound of the warp: its N-th largest thread maximum has N values at or above it
   const float sorted = warp_sort_desc(mx);
   const float mw = __shfl_sync(0xffffffffu, sorted, 0);
@@ -127,7 +197,8 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < VE; ++e) sum += ex2_approx_ftz((value(j, e) - mu) * 1.44269504f);
+    for (int e = 0; e < VE; ++e)
+      sum += ex2_approx_ftz((beam_value<T>(raw[j], e) - mu) * 1.44269504f);
   sum = warp_sum(sum);
   if (lane == 0) {
     s_m[warp] = mw;
@@ -149,21 +220,11 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
         s += s_s[w] * exp2f((s_m[w] == -INFINITY ? 0.f : s_m[w] - m) * 1.44269504f);
     p.tile_ms[slot] = make_float2(m, s);
   }
-  auto key_of = [&](int j, int e) -> uint64_t {
-    const uint32_t v = (uint32_t)((v0 + j * kBeamThreads) * VE - lead + e);
-    return (uint64_t)beam_order(value(j, e)) << 32 | (0xffffffffu - v);
-  };
   if (mx >= tau && mx > -INFINITY) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float x = value(j, e);
-        if (x >= tau && x > -INFINITY) {
-          const int i = atomicAdd(&s_n, 1);
-          if (i < kBeamBuffer) s_key[i] = key_of(j, e);
-        }
-      }
+      if (beam_block_max<T>(raw[j]) >= tau)
+        beam_push<T>(raw[j], (v0 + j * kBeamThreads) * VE - lead, tau, &s_n, s_key);
   }
   __syncthreads();
   const int n = s_n;
@@ -184,31 +245,7 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
     }
     for (int r = n + tid; r < p.N; r += kBeamThreads) out_x[r] = -INFINITY;
   } else {
-    // a tile of very many equal values: one after the other
-    uint64_t last = ~0ull;
-    for (int r = 0; r < p.N; ++r) {
-      uint64_t best = 0;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const uint64_t key = key_of(j, e);
-          if (value(j, e) > -INFINITY && key < last && key > best) best = key;
-        }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t y = __shfl_xor_sync(0xffffffffu, best, o);
-        best = y > best ? y : best;
-      }
-      __syncthreads();
-      if (lane == 0) s_best[warp] = best;
-      __syncthreads();
-      best = s_best[0];
-#pragma unroll
-      for (int w = 1; w < kBeamWarps; ++w) best = s_best[w] > best ? s_best[w] : best;
-      last = best;
-      if (tid == 0) store(r, best);               // (more than kBeamBuffer values: there are N)
-    }
+    beam_tile_slow<T, NV>(base, p.V, tile * (kBeamThreads * NV * VE) - lead, p.N, out_x, out_v, s_best);
   }
 }
 

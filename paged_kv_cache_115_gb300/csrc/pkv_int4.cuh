@@ -46,22 +46,34 @@ __device__ __forceinline__ Int4Row int4_row(float lo, float hi, bool finite) {
   return q;
 }
 
-// N codes (4 or 8) packed, the first in the lowest bits.  Clamping first is the
-// same (the bounds are whole); adding 1.5 * 2^23 rounds to nearest even into the
-// low bits, and the constant's own bits come off the packed word at once.
+// N codes (4 or 8) packed, the first in the lowest bits.  (x - z) r of a finite row
+// lies in [0, 15.1): the clamp of the definition changes nothing.  Adding 1.5 * 2^23
+// rounds to nearest even into the low bits, and the constant's own bits come off
+// the packed word at once.
 template <int N>
 __device__ __forceinline__ uint32_t int4_pack(const Int4Row& q, const float* x) {
   constexpr uint32_t kMagic = 0x4b400000u;      // 12582912.0f
   uint32_t w = 0, off = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float y = fminf(fmaxf((x[i] - q.z) * q.r, 0.f), 15.f);
-    w += __float_as_uint(y + 12582912.f) << (4 * i);
+    w += __float_as_uint(__fmul_rn(x[i] - q.z, q.r) + 12582912.f) << (4 * i);
     off += kMagic << (4 * i);
   }
   w -= off;
   if constexpr (N < 8) w &= (1u << (4 * N)) - 1;
   return q.bad ? 0u : w;
+}
+
+// Least and largest value, NaN once there is one.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 struct Int4WriteParams {
@@ -82,113 +94,109 @@ struct Int4WriteParams {
 };
 
 constexpr int kInt4Threads = 256;
+constexpr int kInt4Loads = 4;            // 16-byte loads a lane
 
-// A row takes D / V lanes, V values (16 bytes) a lane; each lane has U rows in
-// flight.  WIDE: rows on 16-byte boundaries, else value by value.
+// A row takes LANES lanes of four 16-byte blocks each (32 bf16 or 16 float32 values):
+// what is done once a row (scale, reciprocal, slot) counts for many values, and a
+// lane has 64 bytes in flight.  WIDE: rows on 16-byte boundaries, else value by value.
 // Bound by HBM: (2 e D + D + 8) H bytes a token.
-template <typename TIN, int D, int U, bool WIDE>
+template <typename TIN, int D, bool WIDE>
 __global__ void __launch_bounds__(kInt4Threads)
 kv_write_int4_kernel(const __grid_constant__ Int4WriteParams p) {
-  constexpr int V = 16 / sizeof(TIN), LANES = D / V, RPI = kInt4Threads / LANES;
+  constexpr int V = 16 / sizeof(TIN), LANES = D / (V * kInt4Loads), RPI = kInt4Threads / LANES;
   pdl_wait_primary();
   pdl_launch_dependents();
   const int li = threadIdx.x % LANES;
-  const int rows = 2 * p.H;                      // of a token: K heads, V heads
-  const unsigned total = (unsigned)p.T * rows;   // below 2^31
-  const unsigned r0 = blockIdx.x * (RPI * U) + threadIdx.x / LANES;
-  float x[U][V];
-  int64_t blk[U];
-  int off[U], zh[U];
+  const unsigned rows = 2 * p.H;                 // of a token: K heads, V heads
+  const unsigned r = blockIdx.x * RPI + threadIdx.x / LANES;
+  const bool in = r < (unsigned)p.T * rows;      // below 2^31
+  const int t = in ? (int)(r / rows) : 0;
+  const int zh = (int)(r - (unsigned)t * rows);
+  const bool z = zh >= p.H;
+  const int h = zh - (z ? p.H : 0);
+  const TIN* src = static_cast<const TIN*>(z ? p.v : p.k) + t * (z ? p.v_stride : p.k_stride) +
+                   (in ? h * D : 0);
+  // (the rows are read before their slots are known: one wait for memory, not two)
+  uint4 raw[kInt4Loads];
+  if constexpr (WIDE) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const unsigned r = r0 + u * RPI;
-    blk[u] = -1;
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[u][i] = 0.f;
-    if (r < total) {
-      const int t = (int)(r / rows);
-      zh[u] = (int)(r - (unsigned)t * rows);
-      const bool leader = zh[u] == 0 && li == 0;
-      int64_t b = -1;
-      int o = 0;
-      if (p.slots != nullptr) {
-        const int64_t slot = p.slots[t];
-        if (slot >= 0 && (p.log2_bs >= 0 ? slot >> p.log2_bs : slot / p.block_size) < p.num_blocks) {
-          b = p.log2_bs >= 0 ? slot >> p.log2_bs : slot / p.block_size;
-          o = (int)(slot - b * p.block_size);
-        } else if (slot != -1 && leader) {
-          record_error(PKV_DEVERR_SLOT);
-        }
-      } else {
-        const int pos = p.positions[t];
-        if (pos >= 0) {
-          const int lb = p.log2_bs >= 0 ? pos >> p.log2_bs : pos / p.block_size;
-          if (lb >= p.max_blocks) {
-            if (leader) record_error(PKV_DEVERR_POSITION);
-          } else {
-            const int64_t phys = p.block_tables[(int64_t)t * p.max_blocks + lb];
-            if (phys < 0 || phys >= p.num_blocks) {
-              if (leader) record_error(PKV_DEVERR_BLOCK_ID);
-            } else {
-              b = phys;
-              o = pos - lb * p.block_size;
-            }
-          }
-        }
-        if (leader && p.slots_out != nullptr) p.slots_out[t] = b < 0 ? -1 : b * p.block_size + o;
+    for (int i = 0; i < kInt4Loads; ++i)
+      raw[i] = in ? __ldcs(reinterpret_cast<const uint4*>(src) + i * LANES + li) : make_uint4(0, 0, 0, 0);
+  }
+  int64_t blk = -1;
+  int off = 0;
+  if (in) {
+    const bool leader = zh == 0 && li == 0;
+    if (p.slots != nullptr) {
+      const int64_t slot = p.slots[t];
+      const int64_t b = p.log2_bs >= 0 ? slot >> p.log2_bs : slot / p.block_size;
+      if (slot >= 0 && b < p.num_blocks) {
+        blk = b;
+        off = (int)(slot - b * p.block_size);
+      } else if (slot != -1 && leader) {
+        record_error(PKV_DEVERR_SLOT);
       }
-      blk[u] = b;
-      off[u] = o;
-      if (b >= 0) {
-        const bool z = zh[u] >= p.H;
-        const TIN* src = static_cast<const TIN*>(z ? p.v : p.k) +
-                         t * (z ? p.v_stride : p.k_stride) + (zh[u] - (z ? p.H : 0)) * D + li * V;
-        if constexpr (WIDE) {
-          const uint4 raw = __ldg(reinterpret_cast<const uint4*>(src));
-          if constexpr (sizeof(TIN) == 4) {
-            x[u][0] = __uint_as_float(raw.x); x[u][1] = __uint_as_float(raw.y);
-            x[u][2] = __uint_as_float(raw.z); x[u][3] = __uint_as_float(raw.w);
-          } else {
-            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[u][2 * i] = __uint_as_float(w[i] << 16);
-              x[u][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-          }
+    } else {
+      const int pos = p.positions[t];
+      if (pos >= 0) {
+        const int lb = p.log2_bs >= 0 ? pos >> p.log2_bs : pos / p.block_size;
+        if (lb >= p.max_blocks) {
+          if (leader) record_error(PKV_DEVERR_POSITION);
         } else {
+          const int64_t phys = p.block_tables[(int64_t)t * p.max_blocks + lb];
+          if (phys < 0 || phys >= p.num_blocks) {
+            if (leader) record_error(PKV_DEVERR_BLOCK_ID);
+          } else {
+            blk = phys;
+            off = pos - lb * p.block_size;
+          }
+        }
+      }
+      if (leader && p.slots_out != nullptr) p.slots_out[t] = blk < 0 ? -1 : blk * p.block_size + off;
+    }
+  }
+  float x[kInt4Loads][V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) x[u][i] = to_f32(src[i]);
+  for (int i = 0; i < kInt4Loads; ++i) {
+    if constexpr (!WIDE) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[i][e] = in ? to_f32(src[(i * LANES + li) * V + e]) : 0.f;
+    } else {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(TIN) == 4) {
+          x[i][e] = __uint_as_float(w[e]);
+        } else {
+          x[i][2 * e] = __uint_as_float(w[e] << 16);
+          x[i][2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
         }
       }
     }
   }
+  float lo = x[0][0], hi = x[0][0];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float lo = x[u][0], hi = x[u][0], fin = 0.f;
+  for (int i = 0; i < kInt4Loads; ++i)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      lo = fminf(lo, x[u][i]);
-      hi = fmaxf(hi, x[u][i]);
-      fin = fmaf(x[u][i], 0.f, fin);             // NaN once a value is not finite
+    for (int e = 0; e < V; ++e) {
+      lo = min_nan(lo, x[i][e]);
+      hi = max_nan(hi, x[i][e]);
     }
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      fin += __shfl_xor_sync(0xffffffffu, fin, o);
-    }
-    if (blk[u] < 0) continue;
-    const Int4Row q = int4_row(lo, hi, fin == 0.f);
-    const bool z = zh[u] >= p.H;
-    const int h = zh[u] - (z ? p.H : 0);
-    uint8_t* dst = (z ? p.v_cache : p.k_cache) +
-                   ((blk[u] * p.block_size + off[u]) * p.H + h) * (D / 2) + li * (V / 2);
-    if constexpr (V == 8) *reinterpret_cast<uint32_t*>(dst) = int4_pack<8>(q, x[u]);
-    else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)int4_pack<4>(q, x[u]);
-    if (li == 0)
-      (z ? p.v_words : p.k_words)[(blk[u] * p.H + h) * p.block_size + off[u]] = q.word;
+  for (int o = LANES / 2; o > 0; o >>= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
+  if (blk < 0) return;
+  const Int4Row q = int4_row(lo, hi, fabsf(lo) < INFINITY && fabsf(hi) < INFINITY);
+  uint8_t* dst = (z ? p.v_cache : p.k_cache) + ((blk * p.block_size + off) * p.H + h) * (D / 2);
+#pragma unroll
+  for (int i = 0; i < kInt4Loads; ++i) {
+    uint8_t* d = dst + (i * LANES + li) * (V / 2);
+    if constexpr (V == 8) *reinterpret_cast<uint32_t*>(d) = int4_pack<8>(q, x[i]);
+    else *reinterpret_cast<uint16_t*>(d) = (uint16_t)int4_pack<4>(q, x[i]);
+  }
+  if (li == 0) (z ? p.v_words : p.k_words)[(blk * p.H + h) * p.block_size + off] = q.word;
 }
 
 }  // namespace pkv

@@ -114,4 +114,68 @@ attn_reduce_kernel(Workspace ws, int S, int H_q, T* __restrict__ out) {
   for (int e = 0; e < V; ++e) dst[e] = from_f32<T>(acc[e]);
 }
 
+// The same merge by a CTA a row, for few rows of many partials: warp w takes
+// partials w, w + 8, ..., its state joins the others' in shared memory.
+template <typename T, int D>
+__global__ void __launch_bounds__(kReduceWarps * 32)
+attn_reduce_wide_kernel(Workspace ws, int H_q, T* __restrict__ out) {
+  constexpr int V = D / 32, W = kReduceWarps;
+  __shared__ float s_m[W], s_l[W];
+  __shared__ float s_o[W][D];
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = blockIdx.x / H_q, h = blockIdx.x - s * H_q;
+  const int4 mt = ws.meta[s];
+  const int np = mt.y + mt.w;
+  if (np <= 1) return;                    // the whole CTA: the output is written
+  auto idx = [&](int p) -> int64_t {
+    return (int64_t)(p < mt.y ? mt.x + p : mt.z + (p - mt.y)) * H_q + h;
+  };
+  const int mine = warp < np ? (np - warp + W - 1) / W : 0;       // partials of this warp
+  float M = -INFINITY, l = 0.f, acc[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  for (int i0 = 0; i0 < mine; i0 += 32) {
+    const int i = i0 + lane;
+    const float2 ml = i < mine ? ws.ml[idx(warp + i * W)] : make_float2(-INFINITY, 0.f);
+    const float mn = fmaxf(M, warp_max(ml.x));
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    const float al = exp2f(M - mu), wt = exp2f(ml.x - mu);
+    l = l * al + warp_sum(ml.y * wt);
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] *= al;
+    M = mn;
+    const int cnt = min(32, mine - i0);
+#pragma unroll 8
+    for (int u = 0; u < cnt; ++u) {
+      const float wu = __shfl_sync(0xffffffffu, wt, u);
+      float v[V];
+      load_f<V>(ws.o + idx(warp + (i0 + u) * W) * D + lane * V, v);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(wu, v[e], acc[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
+  if (lane == 0) {
+    s_m[warp] = M;
+    s_l[warp] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float Mx = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < W; ++w) Mx = fmaxf(Mx, s_m[w]);
+  const float mu = Mx == -INFINITY ? 0.f : Mx;
+  float sum = 0.f, x = 0.f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const float f = exp2f(s_m[w] - mu);
+    sum = fmaf(s_l[w], f, sum);
+    x = fmaf(s_o[w][threadIdx.x], f, x);
+  }
+  out[(int64_t)blockIdx.x * D + threadIdx.x] = from_f32<T>(x / sum);
+}
+
 }  // namespace pkv
