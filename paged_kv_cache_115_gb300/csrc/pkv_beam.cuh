@@ -34,20 +34,36 @@ struct BeamParams {
   int R, B, V, N, tiles, eos;
 };
 
-// Sorts a value a lane in descending order.
-template <typename T>
-__device__ __forceinline__ T warp_sort_desc(T x) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int k = 2; k <= 32; k <<= 1) {
-#pragma unroll
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      const T y = __shfl_xor_sync(0xffffffffu, x, j);
-      const bool lower = (lane & j) == 0, down = (lane & k) == 0;
-      x = (lower == down) ? (x > y ? x : y) : (x < y ? x : y);
-    }
+// A bound of the warp: at least n of its lanes' values are at or above it (0 with
+// fewer than n lanes that have one).  The n-th largest but for equal values, which
+// count once.
+__device__ __forceinline__ uint32_t warp_bound(uint32_t x, int n) {
+  uint32_t top = 0;
+  for (int i = 0; i < n; ++i) {
+    top = __reduce_max_sync(0xffffffffu, x);
+    if (x == top) x = 0;
   }
-  return x;
+  return top;
+}
+
+// The sum of exp(x) is kept as s 2^b, b = beam_base(m) whole: terms 2^(x c - b) with c
+// the float32 next to log2 e, one fused operation an argument, and sums of different
+// tiles join by exact powers of two.  Far from zero (a row of masks at the type's
+// lowest value) whole b no longer serve: there s is the sum of exp(x - m).
+constexpr float kBeamLog2e = 1.44269504f;
+__device__ __forceinline__ float beam_base(float m) { return ceilf(m * kBeamLog2e); }
+// 2^d of a whole d <= 0
+__device__ __forceinline__ float beam_pow2(float d) {
+  return d < -126.f ? 0.f : __uint_as_float((uint32_t)((int)d + 127) << 23);
+}
+
+__device__ __forceinline__ bool beam_far(float m) { return !(fabsf(m) < 65536.f); }
+// s of a part with maximum m as a share of a whole with maximum M >= m
+__device__ __forceinline__ float beam_join(float m, float s, float M) {
+  if (m == -INFINITY) return s;                    // 0, or NaN
+  const float from = beam_far(m) ? m * kBeamLog2e : beam_base(m);
+  if (!beam_far(M)) return s * beam_pow2(beam_far(m) ? -INFINITY : from - beam_base(M));
+  return s * exp2f(beam_far(m) ? (m - M) * kBeamLog2e : from - M * kBeamLog2e);
 }
 
 // A value's bits in its order (adding 0 makes one of the two zeros).
@@ -92,11 +108,11 @@ __device__ __forceinline__ uint64_t beam_key(float x, int v) {
 
 // A block's values at or above tau into the buffer (first value: token v).
 template <typename T>
-__device__ __noinline__ void beam_push(uint4 r, int v, float tau, int* n, uint64_t* key) {
+__device__ __noinline__ void beam_push(uint4 r, int v, uint32_t tau, int* n, uint64_t* key) {
 #pragma unroll
   for (int e = 0; e < (int)(16 / sizeof(T)); ++e) {
     const float x = beam_value<T>(r, e);
-    if (x >= tau && x > -INFINITY) {
+    if (x > -INFINITY && beam_order(x) >= tau) {
       const int i = atomicAdd(n, 1);
       if (i < kBeamBuffer) key[i] = beam_key(x, v + e);
     }
@@ -147,7 +163,8 @@ template <typename T, int NV>
 __global__ void __launch_bounds__(kBeamThreads, 4)
 beam_tiles_kernel(const __grid_constant__ BeamParams p) {
   constexpr int VE = 16 / sizeof(T);
-  __shared__ float s_m[kBeamWarps], s_s[kBeamWarps], s_tau[kBeamWarps];
+  __shared__ float s_m[kBeamWarps], s_s[kBeamWarps];
+  __shared__ uint32_t s_tau[kBeamWarps];
   __shared__ int s_n;
   __shared__ uint64_t s_key[kBeamBuffer], s_best[kBeamWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -188,42 +205,52 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
   float mx = -INFINITY;
 #pragma unroll
   for (int j = 0; j < NV; ++j) mx = fmaxf(mx, beam_block_max<T>(raw[j]));
-  // bound of the warp: its N-th largest thread maximum has N values at or above it
-  const float sorted = warp_sort_desc(mx);
-  const float mw = __shfl_sync(0xffffffffu, sorted, 0);
-  const float tau_w = __shfl_sync(0xffffffffu, sorted, p.N - 1);
-  const float mu = mw == -INFINITY ? 0.f : mw;
-  float sum = 0.f;
+  // bound of the warp: N threads' largest values are at or above it
+  const uint32_t order = mx > -INFINITY ? beam_order(mx) : 0u;
+  const float mw = warp_max(mx);
+  const uint32_t tau_w = warp_bound(order, p.N);
+  float sum0 = 0.f, sum1 = 0.f;
+  if (!beam_far(mw)) {
+    const float base_w = beam_base(mw);
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < VE; ++e)
-      sum += ex2_approx_ftz((beam_value<T>(raw[j], e) - mu) * 1.44269504f);
-  sum = warp_sum(sum);
+      for (int e = 0; e < VE; e += 2) {
+        sum0 += ex2_approx_ftz(fmaf(beam_value<T>(raw[j], e), kBeamLog2e, -base_w));
+        sum1 += ex2_approx_ftz(fmaf(beam_value<T>(raw[j], e + 1), kBeamLog2e, -base_w));
+      }
+  } else {
+    const float mu = mw == -INFINITY ? 0.f : mw;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        sum0 += ex2_approx_ftz((beam_value<T>(raw[j], e) - mu) * kBeamLog2e);
+  }
+  const float sum = warp_sum(sum0 + sum1);
   if (lane == 0) {
     s_m[warp] = mw;
     s_s[warp] = sum;
     s_tau[warp] = tau_w;
   }
   __syncthreads();
-  float m = s_m[0], tau = s_tau[0];
+  float m = s_m[0];
+  uint32_t tau = s_tau[0];
 #pragma unroll
   for (int w = 1; w < kBeamWarps; ++w) {
     m = fmaxf(m, s_m[w]);
-    tau = fmaxf(tau, s_tau[w]);
+    tau = s_tau[w] > tau ? s_tau[w] : tau;
   }
   const int64_t slot = (int64_t)row * p.tiles + tile;
   if (tid == 0) {
     float s = 0.f;
-    for (int w = 0; w < kBeamWarps; ++w)
-      if (s_m[w] != -INFINITY || s_s[w] != 0.f)
-        s += s_s[w] * exp2f((s_m[w] == -INFINITY ? 0.f : s_m[w] - m) * 1.44269504f);
+    for (int w = 0; w < kBeamWarps; ++w) s += beam_join(s_m[w], s_s[w], m);
     p.tile_ms[slot] = make_float2(m, s);
   }
-  if (mx >= tau && mx > -INFINITY) {
+  if (order >= tau && order > 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (beam_block_max<T>(raw[j]) >= tau)
+      if (beam_order(beam_block_max<T>(raw[j])) >= tau)
         beam_push<T>(raw[j], (v0 + j * kBeamThreads) * VE - lead, tau, &s_n, s_key);
   }
   __syncthreads();
@@ -257,7 +284,9 @@ __global__ void __launch_bounds__(kBeamThreads)
 beam_pick_kernel(const __grid_constant__ BeamParams p) {
   __shared__ double s_add[kBeamMax];             // score - log sum exp; -inf: no candidates
   __shared__ uint8_t s_over[kBeamMax];
-  __shared__ uint64_t s_tau[kBeamWarps];
+  __shared__ double s_sum[kBeamMax];
+  __shared__ float s_top[kBeamMax];
+  __shared__ uint32_t s_tau[kBeamWarps];
   __shared__ uint64_t s_key[kBeamPickBuffer];
   __shared__ uint32_t s_at[kBeamPickBuffer];
   __shared__ uint64_t s_bk[kBeamWarps];
@@ -270,12 +299,11 @@ beam_pick_kernel(const __grid_constant__ BeamParams p) {
   pdl_launch_dependents();
   for (int b = warp; b < p.B; b += kBeamWarps) {
     const int row = r * p.B + b;
-    const float score = p.scores[row];
     const bool over = p.finished != nullptr && p.finished[row];
-    double add = over ? (double)score : -INFINITY;
+    float m = -INFINITY;
+    bool bad = false;
+    double s = 0;
     if (!over) {
-      float m = -INFINITY;
-      bool bad = false;
       for (int c = lane; c < p.tiles; c += 32) {
         const float2 ms = p.tile_ms[(int64_t)row * p.tiles + c];
         m = fmaxf(m, ms.x);
@@ -283,23 +311,35 @@ beam_pick_kernel(const __grid_constant__ BeamParams p) {
       }
       m = warp_max(m);
       bad = __any_sync(0xffffffffu, bad);
-      double s = 0;
       for (int c = lane; c < p.tiles; c += 32) {
         const float2 ms = p.tile_ms[(int64_t)row * p.tiles + c];
-        if (ms.x > -INFINITY && !bad) s += (double)ms.y * exp((double)ms.x - (double)m);
+        if (!bad) s += (double)beam_join(ms.x, ms.y, m);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (bad) {
-        if (lane == 0) record_error(PKV_DEVERR_BEAM);
-      } else if (m > -INFINITY) {
-        add = (double)score - ((double)m + log(s));
-      }
+      if (bad && lane == 0) record_error(PKV_DEVERR_BEAM);
     }
     if (lane == 0) {
-      s_add[b] = add;
       s_over[b] = over;
+      s_top[b] = bad ? -INFINITY : m;
+      s_sum[b] = s;
     }
+  }
+  __syncthreads();
+  // one lane a beam: 64-bit logarithms are slow, one after the other even more so
+  if (tid < p.B) {
+    const float score = p.scores[r * p.B + tid], m = s_top[tid];
+    double add = -INFINITY;
+    if (s_over[tid]) {
+      add = (double)score;
+    } else if (m > -INFINITY) {
+      // 2^(x c) with the float32 c is exp(x (1 + e)): e m comes off, what weighs is
+      // within a few units of m
+      constexpr double kLn2 = 0.69314718055994530942, kE = (double)kBeamLog2e * kLn2 - 1.;
+      const double base = beam_far(m) ? (double)m : (double)beam_base(m) * kLn2 - kE * (double)m;
+      add = (double)score - (base + log(s_sum[tid]));
+    }
+    s_add[tid] = add;
   }
   __syncthreads();
   // candidate i: beam, tile and place; a finished beam has one, its end token
@@ -325,16 +365,16 @@ beam_pick_kernel(const __grid_constant__ BeamParams p) {
     at = (uint32_t)(b * p.V + v);
     return true;
   };
-  // bound: the N-th largest thread maximum of a warp
-  uint64_t tau = 0;
-  if (total > kBeamThreads) {
-    uint64_t mx = 0, key;
+  // bound on the upper halves of the keys: N threads' largest are at or above it
+  uint32_t tau = 0;
+  {
+    uint32_t mx = 0;
+    uint64_t key;
     uint32_t at;
     for (int i = tid; i < total; i += kBeamThreads)
-      if (load(i, key, at) && key > mx) mx = key;
-    const uint64_t sorted = warp_sort_desc(mx);
-    const uint64_t t = __shfl_sync(0xffffffffu, sorted, p.N - 1);
-    if (lane == 0) s_tau[warp] = t;
+      if (load(i, key, at)) mx = (uint32_t)(key >> 32) > mx ? (uint32_t)(key >> 32) : mx;
+    mx = warp_bound(mx, p.N);
+    if (lane == 0) s_tau[warp] = mx;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kBeamWarps; ++w) tau = s_tau[w] > tau ? s_tau[w] : tau;
@@ -342,7 +382,7 @@ beam_pick_kernel(const __grid_constant__ BeamParams p) {
   for (int i = tid; i < total; i += kBeamThreads) {
     uint64_t key;
     uint32_t at;
-    if (load(i, key, at) && key >= tau) {
+    if (load(i, key, at) && (uint32_t)(key >> 32) >= tau) {
       const int k = atomicAdd(&s_n, 1);
       if (k < kBeamPickBuffer) {
         s_key[k] = key;
