@@ -71,8 +71,12 @@ __device__ __forceinline__ uint32_t beam_order(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
+// (by its bits alone: 64-bit floating-point operations are rare here; 0 for a value
+// that is not finite)
 __device__ __forceinline__ uint64_t beam_order(double x) {
-  const uint64_t b = (uint64_t)__double_as_longlong(x + 0.);
+  uint64_t b = (uint64_t)__double_as_longlong(x);
+  if ((b << 1) == 0) b = 0;
+  if ((b & 0x7ff0000000000000ull) == 0x7ff0000000000000ull) return 0;
   return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
 }
 
@@ -92,15 +96,17 @@ __device__ __forceinline__ float beam_block_max(const uint4& r) {
   return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
 }
 
-// Value e of a block; `w` through an empty asm, so that the compiler keeps the block
-// packed between its uses instead of all 64 values in registers.
+// Value e of a block, unpacked by an asm that is not shared between its uses: the
+// compiler then keeps the block packed instead of all 64 values in registers.
 template <typename T>
 __device__ __forceinline__ float beam_value(const uint4& r, int e) {
   constexpr int P = sizeof(T) == 4 ? 1 : 2;
-  uint32_t w = e / P == 0 ? r.x : (e / P == 1 ? r.y : (e / P == 2 ? r.z : r.w));
-  asm volatile("" : "+r"(w));
+  const uint32_t w = e / P == 0 ? r.x : (e / P == 1 ? r.y : (e / P == 2 ? r.z : r.w));
   if constexpr (sizeof(T) == 4) return __uint_as_float(w);
-  return __uint_as_float((e & 1) ? w & 0xffff0000u : w << 16);
+  uint32_t x;
+  if (e & 1) asm volatile("and.b32 %0, %1, 0xffff0000;" : "=r"(x) : "r"(w));
+  else asm volatile("shl.b32 %0, %1, 16;" : "=r"(x) : "r"(w));
+  return __uint_as_float(x);
 }
 __device__ __forceinline__ uint64_t beam_key(float x, int v) {
   return (uint64_t)beam_order(x) << 32 | (0xffffffffu - (uint32_t)v);
@@ -156,15 +162,15 @@ __device__ __noinline__ void beam_tile_slow(const T* base, int V, int first, int
 
 // NV 16-byte blocks a thread, all in flight at once: a tile of a row, counted from
 // the 16-byte boundary at or in front of the row (rows of an odd vocabulary start
-// anywhere); what does not belong to the row counts as -inf.  Four CTAs an SM: the
-// blocks stay packed in registers and are unpacked as they are used.
+// anywhere); what does not belong to the row counts as -inf.  Four CTAs an SM
+// (three for float32): the blocks stay packed in registers and are unpacked as they are used.
 // Bound by HBM (V e bytes a row).
 template <typename T, int NV>
-__global__ void __launch_bounds__(kBeamThreads, 4)
+__global__ void __launch_bounds__(kBeamThreads, sizeof(T) == 2 ? 4 : 3)
 beam_tiles_kernel(const __grid_constant__ BeamParams p) {
   constexpr int VE = 16 / sizeof(T);
   __shared__ float s_m[kBeamWarps], s_s[kBeamWarps];
-  __shared__ uint32_t s_tau[kBeamWarps];
+  __shared__ uint32_t s_order[kBeamThreads], s_tau;
   __shared__ int s_n;
   __shared__ uint64_t s_key[kBeamBuffer], s_best[kBeamWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -178,37 +184,52 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
   const uint4* vec = reinterpret_cast<const uint4*>(base - lead);
   const int nvec = (lead + p.V + VE - 1) / VE;
   const int v0 = tile * (kBeamThreads * NV) + tid;
-  constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-  uint4 raw[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int v = v0 + j * kBeamThreads;
-    raw[j] = make_uint4(kNone, kNone, kNone, kNone);
-    if (v < nvec) raw[j] = __ldcs(vec + v);
+  const int64_t slot = (int64_t)row * p.tiles + tile;
+  float* out_x = p.tile_x + slot * p.N;
+  int32_t* out_v = p.tile_v + slot * p.N;
+  const int first = tile * (kBeamThreads * NV * VE) - lead;      // token of the tile's first value
+  if (first >= p.V) {                                             // nothing of the row
+    if (tid == 0) p.tile_ms[slot] = make_float2(-INFINITY, 0.f);
+    if (tid < p.N) out_x[tid] = -INFINITY;
+    return;
   }
-  // the first and the last block of a row hold values of its neighbours
+  uint4 raw[NV];
+  if (first >= 0 && first + kBeamThreads * NV * VE <= p.V) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int e0 = (v0 + j * kBeamThreads) * VE - lead;
-    if (e0 < 0 || (e0 < p.V && e0 + VE > p.V)) {
-      uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+    for (int j = 0; j < NV; ++j) raw[j] = __ldcs(vec + v0 + j * kBeamThreads);
+  } else {
+    // the first and the last block of a row hold values of its neighbours
+    constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        if (e0 + e < 0 || e0 + e >= p.V) {
-          if constexpr (sizeof(T) == 4) w[e] = kNone;
-          else w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | 0xff800000u : (w[e >> 1] & 0xffff0000u) | 0xff80u;
+    for (int j = 0; j < NV; ++j) {
+      const int v = v0 + j * kBeamThreads;
+      raw[j] = make_uint4(kNone, kNone, kNone, kNone);
+      if (v < nvec) raw[j] = __ldcs(vec + v);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e0 = (v0 + j * kBeamThreads) * VE - lead;
+      if (e0 < 0 || (e0 < p.V && e0 + VE > p.V)) {
+        uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          if (e0 + e < 0 || e0 + e >= p.V) {
+            if constexpr (sizeof(T) == 4) w[e] = kNone;
+            else w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | 0xff800000u : (w[e >> 1] & 0xffff0000u) | 0xff80u;
+          }
         }
+        raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  float mx = -INFINITY;
+  float top[NV], mx = -INFINITY;                 // largest value of each block
 #pragma unroll
-  for (int j = 0; j < NV; ++j) mx = fmaxf(mx, beam_block_max<T>(raw[j]));
-  // bound of the warp: N threads' largest values are at or above it
+  for (int j = 0; j < NV; ++j) {
+    top[j] = beam_block_max<T>(raw[j]);
+    mx = fmaxf(mx, top[j]);
+  }
   const uint32_t order = mx > -INFINITY ? beam_order(mx) : 0u;
   const float mw = warp_max(mx);
-  const uint32_t tau_w = warp_bound(order, p.N);
   float sum0 = 0.f, sum1 = 0.f;
   if (!beam_far(mw)) {
     const float base_w = beam_base(mw);
@@ -231,32 +252,40 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
   if (lane == 0) {
     s_m[warp] = mw;
     s_s[warp] = sum;
-    s_tau[warp] = tau_w;
   }
+  s_order[tid] = order;
   __syncthreads();
-  float m = s_m[0];
-  uint32_t tau = s_tau[0];
+  // a bound that the largest values of N threads reach, by one warp (the bound of a
+  // warp's own 32 threads lets seven times as many values through)
+  if (warp == 0) {
+    uint32_t x[kBeamWarps], tau = 0;
 #pragma unroll
-  for (int w = 1; w < kBeamWarps; ++w) {
-    m = fmaxf(m, s_m[w]);
-    tau = s_tau[w] > tau ? s_tau[w] : tau;
-  }
-  const int64_t slot = (int64_t)row * p.tiles + tile;
-  if (tid == 0) {
-    float s = 0.f;
+    for (int w = 0; w < kBeamWarps; ++w) x[w] = s_order[w * 32 + lane];
+    for (int i = 0; i < p.N; ++i) {
+      uint32_t t = x[0];
+#pragma unroll
+      for (int w = 1; w < kBeamWarps; ++w) t = max(t, x[w]);
+      tau = __reduce_max_sync(0xffffffffu, t);
+#pragma unroll
+      for (int w = 0; w < kBeamWarps; ++w)
+        if (x[w] == tau) x[w] = 0;
+    }
+    if (lane == 0) s_tau = tau;
+  } else if (tid == 32) {
+    float m = s_m[0], s = 0.f;
+    for (int w = 1; w < kBeamWarps; ++w) m = fmaxf(m, s_m[w]);
     for (int w = 0; w < kBeamWarps; ++w) s += beam_join(s_m[w], s_s[w], m);
     p.tile_ms[slot] = make_float2(m, s);
   }
+  __syncthreads();
+  const uint32_t tau = s_tau;
   if (order >= tau && order > 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (beam_order(beam_block_max<T>(raw[j])) >= tau)
-        beam_push<T>(raw[j], (v0 + j * kBeamThreads) * VE - lead, tau, &s_n, s_key);
+      if (beam_order(top[j]) >= tau) beam_push<T>(raw[j], first + (tid + j * kBeamThreads) * VE, tau, &s_n, s_key);
   }
   __syncthreads();
   const int n = s_n;
-  float* out_x = p.tile_x + slot * p.N;
-  int32_t* out_v = p.tile_v + slot * p.N;
   auto store = [&](int r, uint64_t key) {
     const uint32_t o = (uint32_t)(key >> 32);
     out_x[r] = __uint_as_float(o ^ ((uint32_t)((int32_t)~o >> 31) | 0x80000000u));
@@ -272,13 +301,14 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
     }
     for (int r = n + tid; r < p.N; r += kBeamThreads) out_x[r] = -INFINITY;
   } else {
-    beam_tile_slow<T, NV>(base, p.V, tile * (kBeamThreads * NV * VE) - lead, p.N, out_x, out_v, s_best);
+    beam_tile_slow<T, NV>(base, p.V, first, p.N, out_x, out_v, s_best);
   }
 }
 
 // One CTA a request: the sums of its beams' rows, then the best of all tiles'
 // candidates and the finished beams.
 constexpr int kBeamPickBuffer = 1024;
+constexpr int kBeamAhead = 2;                // candidates a thread holds from the start
 
 __global__ void __launch_bounds__(kBeamThreads)
 beam_pick_kernel(const __grid_constant__ BeamParams p) {
@@ -297,22 +327,40 @@ beam_pick_kernel(const __grid_constant__ BeamParams p) {
   if (tid == 0) s_n = 0;
   pdl_wait_primary();
   pdl_launch_dependents();
+  // the first candidates of this thread, and a beam's score, while the sums are joined
+  const int per = p.tiles * p.N, total = p.B * per;
+  float x0[kBeamAhead];
+  int v0[kBeamAhead];
+#pragma unroll
+  for (int i = 0; i < kBeamAhead; ++i) {
+    const int at = tid + i * kBeamThreads;
+    x0[i] = -INFINITY;
+    v0[i] = 0;
+    if (at < total) {
+      x0[i] = p.tile_x[(int64_t)r * total + at];
+      v0[i] = p.tile_v[(int64_t)r * total + at];
+    }
+  }
+  const float my_score = tid < p.B ? p.scores[r * p.B + tid] : 0.f;
   for (int b = warp; b < p.B; b += kBeamWarps) {
     const int row = r * p.B + b;
+    // (a finished beam's sums are stale numbers that nothing uses)
+    float2 ms0 = make_float2(-INFINITY, 0.f);
+    if (lane < p.tiles) ms0 = p.tile_ms[(int64_t)row * p.tiles + lane];
     const bool over = p.finished != nullptr && p.finished[row];
     float m = -INFINITY;
     bool bad = false;
     double s = 0;
     if (!over) {
       for (int c = lane; c < p.tiles; c += 32) {
-        const float2 ms = p.tile_ms[(int64_t)row * p.tiles + c];
+        const float2 ms = c < 32 ? ms0 : p.tile_ms[(int64_t)row * p.tiles + c];
         m = fmaxf(m, ms.x);
         bad |= !(ms.x < INFINITY) || !(ms.y < INFINITY);
       }
       m = warp_max(m);
       bad = __any_sync(0xffffffffu, bad);
       for (int c = lane; c < p.tiles; c += 32) {
-        const float2 ms = p.tile_ms[(int64_t)row * p.tiles + c];
+        const float2 ms = c < 32 ? ms0 : p.tile_ms[(int64_t)row * p.tiles + c];
         if (!bad) s += (double)beam_join(ms.x, ms.y, m);
       }
 #pragma unroll
@@ -328,7 +376,7 @@ beam_pick_kernel(const __grid_constant__ BeamParams p) {
   __syncthreads();
   // one lane a beam: 64-bit logarithms are slow, one after the other even more so
   if (tid < p.B) {
-    const float score = p.scores[r * p.B + tid], m = s_top[tid];
+    const float score = my_score, m = s_top[tid];
     double add = -INFINITY;
     if (s_over[tid]) {
       add = (double)score;
@@ -343,7 +391,6 @@ beam_pick_kernel(const __grid_constant__ BeamParams p) {
   }
   __syncthreads();
   // candidate i: beam, tile and place; a finished beam has one, its end token
-  const int per = p.tiles * p.N, total = p.B * per;
   auto load = [&](int i, uint64_t& key, uint32_t& at) -> bool {
     const int b = i / per, j = i - b * per;
     const double add = s_add[b];
@@ -354,24 +401,37 @@ beam_pick_kernel(const __grid_constant__ BeamParams p) {
       c = add;
       v = p.eos;
     } else {
-      const int64_t e = (int64_t)(r * p.B + b) * per + j;
-      const float x = p.tile_x[e];
+      float x;
+      if (i < kBeamAhead * kBeamThreads) {
+        x = i < kBeamThreads ? x0[0] : x0[1];
+        v = i < kBeamThreads ? v0[0] : v0[1];
+      } else {
+        x = p.tile_x[(int64_t)r * total + i];
+        v = p.tile_v[(int64_t)r * total + i];
+      }
       if (!(x > -INFINITY)) return false;
       c = (double)x + add;
-      v = p.tile_v[e];
     }
-    if (!(c > -INFINITY && c < INFINITY)) return false;
     key = beam_order(c);
     at = (uint32_t)(b * p.V + v);
-    return true;
+    return key != 0;
   };
+  uint64_t key0[kBeamAhead];
+  uint32_t at0[kBeamAhead];
+#pragma unroll
+  for (int i = 0; i < kBeamAhead; ++i) {
+    at0[i] = 0;
+    if (tid + i * kBeamThreads >= total || !load(tid + i * kBeamThreads, key0[i], at0[i])) key0[i] = 0;
+  }
   // bound on the upper halves of the keys: N threads' largest are at or above it
   uint32_t tau = 0;
   {
     uint32_t mx = 0;
     uint64_t key;
     uint32_t at;
-    for (int i = tid; i < total; i += kBeamThreads)
+#pragma unroll
+    for (int i = 0; i < kBeamAhead; ++i) mx = max(mx, (uint32_t)(key0[i] >> 32));
+    for (int i = tid + kBeamAhead * kBeamThreads; i < total; i += kBeamThreads)
       if (load(i, key, at)) mx = (uint32_t)(key >> 32) > mx ? (uint32_t)(key >> 32) : mx;
     mx = warp_bound(mx, p.N);
     if (lane == 0) s_tau[warp] = mx;
@@ -379,16 +439,20 @@ beam_pick_kernel(const __grid_constant__ BeamParams p) {
 #pragma unroll
     for (int w = 0; w < kBeamWarps; ++w) tau = s_tau[w] > tau ? s_tau[w] : tau;
   }
-  for (int i = tid; i < total; i += kBeamThreads) {
+  auto push = [&](uint64_t key, uint32_t at) {
+    const int k = atomicAdd(&s_n, 1);
+    if (k < kBeamPickBuffer) {
+      s_key[k] = key;
+      s_at[k] = at;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kBeamAhead; ++i)
+    if (key0[i] != 0 && (uint32_t)(key0[i] >> 32) >= tau) push(key0[i], at0[i]);
+  for (int i = tid + kBeamAhead * kBeamThreads; i < total; i += kBeamThreads) {
     uint64_t key;
     uint32_t at;
-    if (load(i, key, at) && (uint32_t)(key >> 32) >= tau) {
-      const int k = atomicAdd(&s_n, 1);
-      if (k < kBeamPickBuffer) {
-        s_key[k] = key;
-        s_at[k] = at;
-      }
-    }
+    if (load(i, key, at) && (uint32_t)(key >> 32) >= tau) push(key, at);
   }
   __syncthreads();
   const int n = s_n;

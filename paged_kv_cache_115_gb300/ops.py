@@ -527,14 +527,18 @@ def _quant_pool(k_cache: torch.Tensor, v_cache: torch.Tensor, quant: KvQuant):
     """Checks a quantized pool pair against its description; (num_blocks,
     block_size, H_kv, head_dim) of one layer."""
     if quant.format == KV_INT4_HEAD:
-        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-            _need(t, name, torch.uint8)
-        if k_cache.dim() not in (4, 5) or v_cache.shape != k_cache.shape:
+        shape, dev = k_cache.shape, k_cache.get_device()
+        if k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8 or dev < 0 or \
+                v_cache.get_device() != dev or not k_cache.is_contiguous() or \
+                not v_cache.is_contiguous():
+            for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+                _need(t, name, torch.uint8)
+            raise ValueError("k_cache and v_cache: CUDA tensors on several devices")
+        if len(shape) not in (4, 5) or v_cache.shape != shape:
             raise ValueError("INT4 pools must be [(layers,) num_blocks, block_size, H_kv, D / 2]")
-        nb, K, H, half = k_cache.shape[-4:]
+        nb, K, H, half = shape[-4:]
         for t in getattr(quant, "_scale_tensors", ()):
-            if t.shape != (*k_cache.shape[:-4], nb, H, K, 2) or \
-                    t.get_device() != k_cache.get_device():
+            if t.shape != (*shape[:-4], nb, H, K, 2) or t.get_device() != dev:
                 raise ValueError("int4 scales must be [(layers,) num_blocks, H_kv, block_size, 2] "
                                  "of the pool, on its device")
         return nb, K, H, 2 * half
@@ -620,7 +624,6 @@ def attention_quant_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_di
     return int(out.value)
 
 
-@_device_call
 def paged_attention_decode_quant(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                  block_tables: torch.Tensor, context_lens: torch.Tensor,
                                  scale: float, quant: KvQuant,
@@ -633,32 +636,34 @@ def paged_attention_decode_quant(q: torch.Tensor, k_cache: torch.Tensor, v_cache
     INT4: offset + code * scale).  ``share_prefix``: stage blocks that
     consecutive sequences share (the beams of a request) once per group, as in
     :func:`paged_attention_decode`; INT4 pools, ignored by the others."""
-    _need(q, "q", None, 3)
+    dev, dtype, i32 = _device_of(q, "q"), q.dtype, torch.int32
     nb, K, H_kv, D2 = _quant_pool(k_cache, v_cache, quant)
     _one_layer(k_cache)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(context_lens, "context_lens", torch.int32, 1)
     S, H_q, D = q.shape
-    if D2 != D or v_cache.shape != k_cache.shape or context_lens.shape[0] != S \
-            or block_tables.shape[0] != S:
-        raise ValueError("shape mismatch between q, caches, tables and lengths")
+    if D2 != D or v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch between q and the pools")
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError("paged_attention_decode_quant: CUDA tensors on several devices")
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", q.dtype, 3)
     if max_context_len is None:
         max_context_len = int(context_lens.max().item()) if S else 0
-    need = attention_quant_workspace_bytes(S, H_q, H_kv, D, K, max_context_len, q.dtype, quant,
-                                           kernel, num_splits, share_prefix)
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    _need(workspace, "workspace", torch.uint8, 1)
+    max_context_len = int(max_context_len)
     cfg = _cfg(kernel, num_splits, share_prefix)
-    _check(_attention_quant(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                            block_tables.shape[1], _ptr(context_lens), max_context_len, S, H_q,
-                            H_kv, D, K, nb, float(scale), _ptr(out), _ptr(workspace),
-                            workspace.numel(), _dtype_code(q), ctypes.byref(quant),
-                            ctypes.byref(cfg), _stream(q.device)),
-           "pkv_attention_decode_quant")
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = attention_quant_workspace_bytes(S, H_q, H_kv, D, K, max_context_len, dtype,
+                                                   quant, kernel, num_splits, share_prefix)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    ws_bytes = workspace.shape[0]
+    _in_32_bits(S | max_context_len)
+    _call_on(dev, _attention_quant,
+             (_whole(q, "q", dtype, q.shape, dev), k_cache.data_ptr(), v_cache.data_ptr(),
+              _table(block_tables, "block_tables", i32, S, dev), block_tables.shape[1],
+              _vec(context_lens, "context_lens", i32, S, dev), max_context_len, S, H_q, H_kv, D, K,
+              nb, float(scale), _whole(out, "out", dtype, q.shape, dev),
+              _vec(workspace, "workspace", torch.uint8, ws_bytes, dev), ws_bytes, _dtype_code(q),
+              ctypes.byref(quant), ctypes.byref(cfg)), "pkv_attention_decode_quant")
     return out
 
 
