@@ -176,13 +176,14 @@ __global__ void __launch_bounds__(kForkThreads)
 fork_apply_kernel(const __grid_constant__ ForkParams p) {
   extern __shared__ int32_t s_id[];              // [B][kForkThreads]
   __shared__ ForkGroup s_f;
-  __shared__ int s_w[kForkThreads / 32];
+  __shared__ int s_w[kForkThreads / 32], s_sum[6][kForkThreads / 32];
   __shared__ int s_rank[kForkMaxRows];           // fresh blocks of the group's earlier rows
   int32_t(*id)[kForkThreads] = reinterpret_cast<int32_t(*)[kForkThreads]>(s_id);
   const int g = blockIdx.x, chunk = blockIdx.y, tid = threadIdx.x;
   pdl_wait_primary();
   // ---- what the groups in front take and give, and all of them
   int take0 = 0, take = 0, live = 0, bad = 0, give0 = 0, give = 0;
+  const int64_t head = p.w_state[0], tail = p.w_state[1];
   for (int i = tid; i < p.R; i += kForkThreads) {
     const int4 w = p.w_group[i];
     take += w.x;
@@ -196,13 +197,21 @@ fork_apply_kernel(const __grid_constant__ ForkParams p) {
     give += n;
     if (i < here) give0 += n;
   }
-  take0 = fork_block_sum(take0, s_w);
-  take = fork_block_sum(take, s_w);
-  give0 = fork_block_sum(give0, s_w);
-  give = fork_block_sum(give, s_w);
-  live = fork_block_sum(live, s_w);
-  bad = __syncthreads_or(bad);
-  const int64_t head = p.w_state[0], tail = p.w_state[1];
+  {
+    const int part[6] = {take0, take, give0, give, live, bad};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      const int x = __reduce_add_sync(0xffffffffu, part[i]);
+      if ((tid & 31) == 0) s_sum[i][tid >> 5] = x;
+    }
+    __syncthreads();
+    int sum[6] = {0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+#pragma unroll
+      for (int w = 0; w < kForkThreads / 32; ++w) sum[i] += s_sum[i][w];
+    take0 = sum[0]; take = sum[1]; give0 = sum[2]; give = sum[3]; live = sum[4]; bad = sum[5];
+  }
   int code = 0;
   if (bad || head < 0 || tail < head || tail - head > p.ring_size ||
       tail + give - head > p.ring_size)
