@@ -163,15 +163,9 @@ bool simt_shape_ok(int G, int D) {
   return (D == 32 || D == 64 || D == 128 || D == 256) && G >= 1 && G <= 16;
 }
 
-#ifndef PKV_ONE
-#define PKV_ONE 4
-#endif
-#ifndef PKV_I4_HPC
-#define PKV_I4_HPC 8
-#endif
 int tc_hpc(int H_kv, int ct = 0) {
   for (int h : {8, 4, 2, 1})
-    if (H_kv % h == 0 && (ct != 4 || h <= PKV_I4_HPC)) return h;
+    if (H_kv % h == 0 && (ct != 4 || h <= 4)) return h;
   return 1;
 }
 
@@ -221,7 +215,7 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
     // one CTA per SM (shared memory bound), or as many as a pool format takes
     // members of a shared-prefix group: the columns of two blocks; INT4 pools with G
     // <= 4 those of one, which leaves registers for twice the warps
-    const bool one_block = ct == 4 && G <= PKV_ONE;
+    const bool one_block = ct == 4 && G <= 4;
     const int share_m = !c.share_prefix ? 1 : (one_block ? 8 : 16) / G;
     const int total = sms * pkv::tc_ctas(ct, p.hpc, share_m > 1 && !one_block);
     p.n_per_group = c.num_splits ? c.num_splits : (total / p.groups > 0 ? total / p.groups : 1);
@@ -493,8 +487,10 @@ pkv_status plan_prefill(int num_seqs, int num_tokens, int max_query_len, int max
 template <int D, int CT, bool B8, int SH = 0, bool PX = false>
 pkv_status launch_tc_hpc(int hpc, const pkv::TcParams& prm, int n, int groups, cudaStream_t st,
                          int dev) {
+  if constexpr (CT != 4) {
+    if (hpc == 8) return TcInst<D, 8, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
+  }
   switch (hpc) {
-    case 8: return TcInst<D, 8, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
     case 4: return TcInst<D, 4, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
     case 2: return TcInst<D, 2, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
     default: return TcInst<D, 1, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);

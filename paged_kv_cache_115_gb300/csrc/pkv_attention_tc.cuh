@@ -47,12 +47,16 @@ constexpr int kBoxBytes = kTile * 128;
 constexpr int tc_chunk_tokens(int ct) { return ct == 0 || ct == 3 ? kTile : 2 * kTile; }
 
 // CTAs that share an SM.  4-bit pools bring twice the values a byte and are bound
-// by what their warps issue: 16 consumer warps an SM, no producer warp among them
-// (the consumers take turns), so that each has 128 registers.  The two column
-// blocks of shared-prefix groups need 227: 8 warps.
-// (One head a CTA: 8, what shared memory holds with two stages or more.)
-constexpr int tc_ctas(int ct, int hpc, bool sh) {
-  return ct != 4 ? 1 : (hpc == 1 ? 8 : (sh ? 8 : 16) / hpc);
+// by what their warps issue, so more warps than heads work on an SM: with four heads
+// (and a producer warp) a CTA three of them, 15 warps of 128 registers.  (Two CTAs of
+// eight heads: 18 warps, 96 registers, spills, 188 us for 128 sequences of ~4600
+// tokens; eight heads without a producer warp, the consumers taking turns: 134 us,
+// the last warp out of a stage filling it: 147 us; these three: 122 us.)  The two
+// column blocks of shared-prefix groups take 168 registers.
+constexpr int tc_ctas(int ct, int hpc, bool two_blocks) {
+  return ct != 4 ? 1
+                 : (two_blocks ? (hpc == 4 ? 2 : (hpc == 2 ? 4 : 6))
+                               : (hpc == 4 ? 3 : (hpc == 2 ? 5 : 8)));
 }
 
 // Attention behind a shared prefix (pkv_prefix.cuh): the prefix kernel and
@@ -301,7 +305,7 @@ struct TcCfg {
   static constexpr int SCALE_BYTES =
       I4 ? 2 * TL * SUB * SBOX : (CT == 2 ? 2 * TL * kTile * 4 : 0);
   static constexpr int STAGE = ((KPART + VPART + SCALE_BYTES + 1023) / 1024) * 1024;
-  static constexpr int THREADS = (I4 ? HPC : HPC + 1) * 32;   // (INT4: no producer warp)
+  static constexpr int THREADS = (HPC + 1) * 32;
   static constexpr int BAR_OFF = NS * STAGE;
   static constexpr int CSTART_OFF = BAR_OFF + 2 * NS * 8 + 16;
   static constexpr int SMEM = CSTART_OFF + (kTcMaxSeqs + 1) * 4 + 1024;  // + alignment slack
@@ -596,7 +600,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   // no kernel that lets this one start before it ends) before waiting for the
   // previous kernel
   int row[TL][2];
-  if ((I4 || warp == HPC) && cb < ce) tile_rows(cb, row);
+  if (warp == HPC && cb < ce) tile_rows(cb, row);
   if constexpr (!SH && !PX) pdl_wait_primary();
   // behind a shared prefix: the kernel in front (the prefix part) released
   // this one after its own wait, so what earlier kernels wrote is there; this
@@ -702,11 +706,15 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     }
   };
 
-  if (!I4 && warp == HPC) {
+  if (warp == HPC) {
     // =================== producer ===================
     if (lane == 0) {
       prefetch_tensormap(&p.tmap_k);
       prefetch_tensormap(&p.tmap_v);
+      if constexpr (I4) {
+        prefetch_tensormap(&p.tmap_ks);
+        prefetch_tensormap(&p.tmap_vs);
+      }
     }
     const uint64_t policy = l2_policy_evict_first();
     int k = 0;
@@ -778,59 +786,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     return cc < ncol && cu ? uend - nq + cc / G : uend - 1;
   };
   int k = 0;
-  // INT4: chunk k is brought by warp k mod HPC, a stage ahead of the ring's end
-  const uint64_t policy = I4 ? l2_policy_evict_first() : 0;
-  const int total = ce - cb;
-  int window = 0;                       // chunks that `row` stands for, by 32
-  auto produce = [&](int kk, int at) {
-    if ((kk >> 5) != window) {
-      window = kk >> 5;
-      tile_rows(cb + (window << 5), row);
-    }
-    int r[TL][2];
-#pragma unroll
-    for (int t = 0; t < TL; ++t) {
-      r[t][0] = __shfl_sync(0xffffffffu, row[t][0], kk & 31);
-      r[t][1] = __shfl_sync(0xffffffffu, row[t][1], kk & 31);
-    }
-    issue(at, r, policy);
-    __syncwarp();
-  };
-  // gives up: does not leave the CTA while copies of this warp may still land
-  auto give_up = [&](int kk) {
-    record_error(PKV_DEVERR_TIMEOUT);
-    if constexpr (I4) {
-      for (int i = max(0, kk - NS); i < kk; ++i)
-        if (i % HPC == w) mbar_wait_bounded(bar_full + 8 * (i % NS), (i / NS) & 1);
-    }
-  };
-  if constexpr (I4) {
-    if (w == 0 && lane == 0) {
-      prefetch_tensormap(&p.tmap_k);
-      prefetch_tensormap(&p.tmap_v);
-      prefetch_tensormap(&p.tmap_ks);
-      prefetch_tensormap(&p.tmap_vs);
-    }
-    for (int kk = 0; kk < min(NS, total); ++kk)
-      if (kk % HPC == w) produce(kk, kk);
-  }
   int stage = 0;                        // k mod NS
   uint32_t phase = 0;                   // k / NS, its lowest bit
   int a = cstart[u], b = cstart[u + 1]; // chunks of the unit
   for (int c = cb; c < ce; ++c, ++k) {
-    if constexpr (I4) {
-      const int kk = k + NS - 1;
-      if (k > 0 && kk < total && kk % HPC == w) {
-        // (chunk kk reuses the stage of chunk k - 1)
-        const int at = stage == 0 ? NS - 1 : stage - 1;
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_empty + 8 * at,
-                                                       stage == 0 ? phase ^ 1 : phase))) {
-          give_up(kk);
-          return;
-        }
-        produce(kk, at);
-      }
-    }
     if (c >= b) {
       do ++u; while (c >= cstart[u + 1]);
       a = cstart[u];
@@ -980,7 +939,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
     const int cpos = ut0 + (c - a) * CH;                 // key position of chunk row 0
     const int valid = min(CH, uend - cpos);             // tokens of this chunk
     if (!mbar_wait_bounded(bar_full + 8 * stage, phase)) {
-      give_up(min(k + NS, total));
+      record_error(PKV_DEVERR_TIMEOUT);
       return;
     }
     uint8_t* sb = smem + stage * C::STAGE;
