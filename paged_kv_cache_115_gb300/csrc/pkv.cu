@@ -221,12 +221,12 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
     p.n_per_group = c.num_splits ? c.num_splits : (total / p.groups > 0 ? total / p.groups : 1);
     const int max_chunks = (int)ceil_div(max_len, pkv::kTcChunk);
     p.pmax = std::max(1, std::min(p.n_per_group, max_chunks));
-    p.seq_batch = std::min(S, pkv::kTcMaxSeqs);
+    p.seq_batch = std::min(S, pkv::tc_max_seqs(ct));
     if (c.share_prefix && G <= 8) {
       // groups of 16 / G sequences fill the kernel's two 8-column blocks; a
       // sequence's partials are its group's shared unit's, then its own's
       p.share_m = share_m;
-      p.seq_batch = std::min(S, pkv::kTcMaxShareSeqs);
+      p.seq_batch = std::min(S, pkv::tc_max_share_seqs(ct));
     }
     // decode partials: slot CTA + unit (one region per member of a shared
     // unit); any sequence of two or more chunks may be split
@@ -315,7 +315,7 @@ struct TcInst {
   static constexpr int STAGE_BYTES = pkv::TcCfg<D, HPC, 2, CT, B8 && CT == 4>::STAGE;
   static constexpr int CTAS = pkv::tc_ctas(CT, HPC, SH == 1);    // share the SM's 228 KiB
   static constexpr int BUDGET =
-      CTAS > 1 ? 233472 / CTAS - 1024 - 9472 : (CT ? 217088 - 9216 : 196608);
+      CTAS > 1 ? 233472 / CTAS - 1024 - (pkv::tc_max_seqs(CT) + 1) * 4 - 1024 - 512 : (CT ? 217088 - 9216 : 196608);
   static constexpr int NS_FIT = BUDGET / STAGE_BYTES;
   static constexpr int NS = NS_FIT < 2 ? 2 : (NS_FIT > 8 ? 8 : NS_FIT);
   using C = pkv::TcCfg<D, HPC, NS, CT, B8>;

@@ -40,6 +40,9 @@ constexpr int kTcMaxSeqs = 2048;
 // shared-prefix mode: sequences per launch, so that the units (at most
 // 3/2 of them with groups of two or more) fit the kTcMaxSeqs + 1 chunk starts
 constexpr int kTcMaxShareSeqs = 1024;
+// INT4: fewer sequences per launch, which leaves room for a fourth stage
+constexpr int tc_max_seqs(int ct) { return ct == 4 ? 1024 : kTcMaxSeqs; }
+constexpr int tc_max_share_seqs(int ct) { return ct == 4 ? 640 : kTcMaxShareSeqs; }
 constexpr int kBoxBytes = kTile * 128;
 
 // tokens per stream-K chunk for a pool format (0 bf16, 1 FP8, 2 INT8,
@@ -308,7 +311,7 @@ struct TcCfg {
   static constexpr int THREADS = (HPC + 1) * 32;
   static constexpr int BAR_OFF = NS * STAGE;
   static constexpr int CSTART_OFF = BAR_OFF + 2 * NS * 8 + 16;
-  static constexpr int SMEM = CSTART_OFF + (kTcMaxSeqs + 1) * 4 + 1024;  // + alignment slack
+  static constexpr int SMEM = CSTART_OFF + (tc_max_seqs(CT) + 1) * 4 + 1024;  // + alignment slack
   static constexpr uint32_t TX =                               // bytes landing per stage
       KPART + VPART + (I4 ? 2 * TL * HPC * kTile * 4 : SCALE_BYTES);
   static_assert(CT == 0 || D == 128, "quantized pools need head_dim 128");
@@ -1422,6 +1425,9 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
               }
       }
     }
+    // the stage's rows are in registers before it is given back: without the fence a
+    // warp behind the others saw rows of the tile that is copied over them
+    __threadfence_block();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_empty + 8 * stage);
     if (++stage == NS) {
