@@ -155,10 +155,11 @@ typedef struct {
                             group (0 = SM count x CTAs per SM).  kernel 2:
                             tokens per partition (0 = automatic).              */
   int32_t share_prefix;  /* 0 = off.  1 = shared-prefix groups (decode with the
-                            tensor-core kernel on bf16 pools; ignored by the
-                            other plans): consecutive sequences are taken in
+                            tensor-core kernel on bf16 and INT4 pools; ignored by
+                            the other plans): consecutive sequences are taken in
                             aligned groups of m = 16 / G (G = num_q_heads /
-                            num_kv_heads, so G <= 8 gives m >= 2); the
+                            num_kv_heads, so G <= 8 gives m >= 2; INT4 pools with
+                            G <= 4: 8 / G); the
                             leading tokens whose block-table entries are the
                             same physical blocks in every member's row
                             ("推理与 KV Cache 02", 前缀索引与 Block Table: whole
@@ -170,7 +171,7 @@ typedef struct {
                             share blocks (forks of one request, requests of
                             one prompt) next to each other.  Adds one small
                             launch that compares the table rows, and at most
-                            1024 sequences go into one partition launch.   */
+                            1024 (INT4: 640) sequences go into one launch.  */
   int32_t reserved[5];   /* must be zero */
 } pkv_attention_config;
 

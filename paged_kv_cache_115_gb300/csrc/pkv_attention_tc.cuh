@@ -54,7 +54,8 @@ constexpr int tc_chunk_tokens(int ct) { return ct == 0 || ct == 3 ? kTile : 2 * 
 // (and a producer warp) a CTA three of them, 15 warps of 128 registers.  (Two CTAs of
 // eight heads: 18 warps, 96 registers, spills, 188 us for 128 sequences of ~4600
 // tokens; eight heads without a producer warp, the consumers taking turns: 134 us,
-// the last warp out of a stage filling it: 147 us; these three: 122 us.)  The two
+// the last warp out of a stage filling it: 147 us; these three: 122 us,
+// 118 with a fourth stage.)  The two
 // column blocks of shared-prefix groups take 168 registers.
 constexpr int tc_ctas(int ct, int hpc, bool two_blocks) {
   return ct != 4 ? 1

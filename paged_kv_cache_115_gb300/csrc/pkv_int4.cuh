@@ -99,7 +99,9 @@ constexpr int kInt4Loads = 4;            // 16-byte loads a lane
 // A row takes LANES lanes of four 16-byte blocks each (32 bf16 or 16 float32 values):
 // what is done once a row (scale, reciprocal, slot) counts for many values, and a
 // lane has 64 bytes in flight.  WIDE: rows on 16-byte boundaries, else value by value.
-// Bound by HBM: (2 e D + D + 8) H bytes a token.
+// Bound by HBM: (2 e D + D + 8) H bytes a token.  16381 tokens of 8 heads of 128 in
+// bf16: 17.8 us, 4.8 TB/s with the call (a lane to 16 bytes, which repeats the row's
+// work eight times: 47 us); 64 tokens: 9.5 us, the host's.
 template <typename TIN, int D, bool WIDE>
 __global__ void __launch_bounds__(kInt4Threads)
 kv_write_int4_kernel(const __grid_constant__ Int4WriteParams p) {
