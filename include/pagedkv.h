@@ -149,8 +149,10 @@ PKV_API pkv_status pkv_kv_block_copy(void* k_cache, void* v_cache, const int64_t
 typedef struct {
   int32_t kernel;        /* 0 = automatic, 1 = TMA + tensor-core kernel
                             (bf16, block_size 8 or a multiple of 16, head_dim
-                            64 or 128, G <= 8), 2 = CUDA-core kernel (any
-                            supported shape) */
+                            64 or 128, G <= 8, pools on 16-byte boundaries,
+                            queries on 4-byte ones: 8 over FP8 and INT8 pools,
+                            16 over INT4), 2 = CUDA-core kernel (any supported
+                            shape and boundary).  Automatic takes 1 where it can */
   int32_t num_splits;    /* kernel 1: CTAs sharing the token range of one KV-head
                             group (0 = SM count x CTAs per SM).  kernel 2:
                             tokens per partition (0 = automatic).              */
@@ -451,8 +453,9 @@ PKV_API pkv_status pkv_attention_decode_quant(
  *                  of 128 rows (two per CTA sharing every K/V tile; one per
  *                  CTA when no KV head has more than 128 rows), except that
  *                  9 .. 64 rows with fewer (sequence, KV head) pairs than SMs,
- *                  or scale <= 0, take mma.sync tiles of 16 / 32 / 64 rows.
- *                  1 = tcgen05 (scale > 0, no split),
+ *                  scale <= 0, or q or out off a 16-byte boundary (4 is the
+ *                  least) take mma.sync tiles of 16 / 32 / 64 rows.
+ *                  1 = tcgen05 (scale > 0, no split, 16-byte boundaries),
  *                  2 = mma.sync, 3 = stream-K decode kernel (at most 8 rows
  *                  per KV head, at most 2048 sequences, no split).
  *                  num_splits (mma.sync

@@ -187,7 +187,7 @@ WsLayout ws_layout(const AttnPlan& p, int H_q, int H_kv, int D) {
 }
 
 pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, int64_t num_blocks,
-                          pkv_dtype dt, const pkv_attention_config* cfg, bool tma_aligned,
+                          pkv_dtype dt, const pkv_attention_config* cfg, bool tc_aligned,
                           AttnPlan* plan, int ct = 0) {
   PKV_CHECK(S >= 0 && H_q > 0 && H_kv > 0 && D > 0 && K > 0 && K <= 1024 && max_len >= 0,
             PKV_ERR_INVALID_ARGUMENT, "bad attention sizes");
@@ -200,12 +200,12 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
                 (c.share_prefix == 0 || c.share_prefix == 1),
             PKV_ERR_INVALID_ARGUMENT, "bad attention config");
   const int G = H_q / H_kv;
-  const bool tc_ok = tc_shape_ok(G, D, K, num_blocks, dt) && tma_aligned;
+  const bool tc_ok = tc_shape_ok(G, D, K, num_blocks, dt) && tc_aligned;
   AttnPlan p;
   if (c.kernel == 1 || (c.kernel == 0 && tc_ok)) {
     PKV_CHECK(tc_ok, PKV_ERR_UNSUPPORTED,
-              "tensor-core kernel needs bf16, head_dim 64/128, G <= 8, block_size 8 or a multiple of 16 "
-              "and a 16-byte aligned pool");
+              "tensor-core kernel needs bf16, head_dim 64/128, G <= 8, block_size 8 or a multiple of 16, "
+              "a 16-byte aligned pool and 4-byte aligned queries");
     int dev, sms;
     pkv_status st = device_facts(&dev, &sms);
     if (st != PKV_OK) return st;
@@ -256,7 +256,7 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
 
 // Plan for a quantized pool: the tensor-core kernel when the shape allows it
 // (bf16 queries, head_dim 128, G <= 8, block_size 8 or a multiple of 16, 16-byte aligned
-// pools and scales), else the CUDA-core kernel (head_dim 64 / 128, G <= 16).
+// pools and scales, queries aligned for its loads), else the CUDA-core kernel (head_dim 64 / 128, G <= 16).
 pkv_status plan_attention_quant(int S, int H_q, int H_kv, int D, int K, int max_len,
                                 int64_t num_blocks, pkv_dtype q_dt, const pkv_kv_quant* quant,
                                 const pkv_attention_config* cfg, bool aligned_ok,
@@ -279,8 +279,9 @@ pkv_status plan_attention_quant(int S, int H_q, int H_kv, int D, int K, int max_
   if (c.kernel == 1 || (c.kernel == 0 && tc_ok)) {
     PKV_CHECK(tc_ok, PKV_ERR_UNSUPPORTED,
               "tensor-core kernel on a quantized pool needs bf16 queries, head_dim 128, G <= 8, "
-              "block_size 8 or a multiple of 16 (a multiple of 16 with a bf16 K pool) and "
-              "16-byte aligned pools and scales");
+              "block_size 8 or a multiple of 16 (a multiple of 16 with a bf16 K pool), "
+              "16-byte aligned pools and scales, and queries on 16-byte (INT4), 8-byte (FP8, INT8) "
+              "or 4-byte (bf16 K) boundaries");
     c.kernel = 1;
     if (!int4) c.share_prefix = 0;   // shared-prefix groups: bf16 and INT4 pools
     return plan_attention(S, H_q, H_kv, D, K, max_len, num_blocks, PKV_BF16, &c, true, plan,
@@ -1511,14 +1512,19 @@ pkv_status attention_impl(const void* q, const void* k_cache, const void* v_cach
                           void* stream) {
   PKV_CHECK(num_seqs >= 0 && max_blocks_per_seq >= 1 && num_blocks >= 1,
             PKV_ERR_INVALID_ARGUMENT, "bad attention sizes");
-  const bool tma_aligned = aligned(k_cache, 16) && aligned(v_cache, 16);
+  // the tensor-core kernel: TMA on the pools, loads of 4 (bf16 K), 8 (FP8, INT8) or 16
+  // (INT4) bytes on the queries
+  const size_t q_load = quant == nullptr || quant->format == PKV_KV_BF16K_FP8V
+                            ? 4
+                            : (quant->format == PKV_KV_INT4_HEAD ? 16 : 8);
+  const bool tc_aligned = aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(q, q_load);
   AttnPlan plan;
   pkv_status st = quant ? plan_attention_quant(num_seqs, num_q_heads, num_kv_heads, head_dim,
                                                block_size, max_context_len, num_blocks, dtype,
-                                               quant, config, tma_aligned, &plan)
+                                               quant, config, tc_aligned, &plan)
                         : plan_attention(num_seqs, num_q_heads, num_kv_heads, head_dim,
                                          block_size, max_context_len, num_blocks, dtype, config,
-                                         tma_aligned, &plan);
+                                         tc_aligned, &plan);
   if (st != PKV_OK) return st;
   if (num_seqs == 0) return PKV_OK;
   PKV_CHECK(q && k_cache && v_cache && block_tables && context_lens && out && workspace,
@@ -1530,8 +1536,8 @@ pkv_status attention_impl(const void* q, const void* k_cache, const void* v_cach
   const size_t pool_eb = quant ? 1 : eb;
   const size_t k_eb = quant && quant->format == PKV_KV_BF16K_FP8V ? 2 : pool_eb;
   PKV_CHECK(aligned(q, eb) && aligned(out, eb) && aligned(k_cache, k_eb) &&
-                aligned(v_cache, pool_eb),
-            PKV_ERR_INVALID_ARGUMENT, "misaligned q/out/pool");
+                aligned(v_cache, pool_eb) && aligned(block_tables, 4) && aligned(context_lens, 4),
+            PKV_ERR_INVALID_ARGUMENT, "misaligned q/out/pool/tables/lengths");
   PKV_CHECK((int64_t)max_blocks_per_seq * block_size <= 2147483647, PKV_ERR_UNSUPPORTED,
             "table row too long");
   const double log2e = 1.4426950408889634;
@@ -1771,6 +1777,19 @@ pkv_status pkv_attention_prefill(const void* q, const void* k_cache, const void*
             PKV_ERR_INVALID_ARGUMENT, "null pointer");
   PKV_CHECK(aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(q, 4) && aligned(out, 4),
             PKV_ERR_INVALID_ARGUMENT, "pools must be 16-byte aligned, q and out 4-byte aligned");
+  PKV_CHECK(aligned(block_tables, 4) && aligned(cu_seqlens, 4) && aligned(context_lens, 4),
+            PKV_ERR_INVALID_ARGUMENT, "misaligned tables or lengths");
+  if (plan.tc05 && !(aligned(q, 16) && aligned(out, 16))) {
+    // the tcgen05 kernel moves 16 bytes at a time: the mma.sync kernel without a
+    // key-range split, which needs no workspace
+    PKV_CHECK(config == nullptr || config->kernel != 1, PKV_ERR_UNSUPPORTED,
+              "the tcgen05 prefill kernel needs q and out on 16-byte boundaries");
+    const int64_t rows = (int64_t)max_query_len * (num_q_heads / num_kv_heads);
+    plan.tc05 = false;
+    plan.nw = prefill_warps(rows);
+    plan.tiles = std::max<int64_t>(1, ceil_div(rows, 16 * plan.nw));
+    PKV_CHECK(plan.tiles <= 2147483647, PKV_ERR_UNSUPPORTED, "too many query rows");
+  }
   PKV_CHECK(workspace_bytes >= plan.ws_bytes && (plan.ws_bytes == 0 || workspace != nullptr),
             PKV_ERR_WORKSPACE_TOO_SMALL, "prefill workspace: need %zu bytes", plan.ws_bytes);
   PKV_CHECK(plan.ws_bytes == 0 || aligned(workspace, 256), PKV_ERR_INVALID_ARGUMENT,
