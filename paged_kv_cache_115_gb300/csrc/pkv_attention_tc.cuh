@@ -761,11 +761,11 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
 
   uint32_t qf[NB][D / 16][2];
   float o[NB][D / 16][4];
-  float slc0[NB], slc1[NB];     // per score column (one-byte pools: q's 2^e folded in)
+  float slc0[NB], slc1[NB];     // per score column (quantized pools: q's 2^e folded in)
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) slc0[nb] = slc1[nb] = sl;
   // INT4, per score column: minus what the codes' 1024 and 64 add to a product, and
-  // scale_log2 times sum(q); slc0 is one factor for all columns
+  // scale_log2 times sum(q)
   float off0[I4 ? NB : 1], off1[I4 ? NB : 1], qs0[I4 ? NB : 1], qs1[I4 ? NB : 1];
   const int pg = I4 ? int4_pi<C::PAIR>(g) : g;     // token row of a tile that mma row g holds
   // INT4: V scales enter times vinv, a power of two that puts the largest seen (up
@@ -830,37 +830,36 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           }
         }
       } else if constexpr (I4) {
-        // f16 fragments in the order of the K words (see "INT4"), scaled by one power
-        // of two that puts the largest |q| of the warp's heads in [2^14, 2^15): exact
-        // down to 2^-29 of it, far inside the f16 range
-        float amax = 0.f;
-        uint4 raw[NB][4];
+        // f16 fragments in the order of the K words (see "INT4"), each column scaled by
+        // a power of two of its own that puts its largest |q| in [2^14, 2^15): exact
+        // down to 2^-29 of it, far inside the f16 range, and whatever another head or
+        // another member of a group holds (an infinity, values of another size) is
+        // nothing to it
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+          float amax = 0.f;
+          uint4 raw[4];
           const int cq = 8 * nb + g;
           const __nv_bfloat16* qrow =
               p.q + ((int64_t)(qr0 + (cq < ncol ? cq / G : 0)) * H_q + j * G + cq % G) * D + 32 * tq;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            raw[nb][i] = make_uint4(0, 0, 0, 0);
-            if (cq < ncol) raw[nb][i] = __ldg(reinterpret_cast<const uint4*>(qrow) + i);
-            const uint32_t w4[4] = {raw[nb][i].x, raw[nb][i].y, raw[nb][i].z, raw[nb][i].w};
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (cq < ncol) raw[i] = __ldg(reinterpret_cast<const uint4*>(qrow) + i);
+            const uint32_t w4[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w4[e] << 16)),
                                        fabsf(__uint_as_float(w4[e] & 0xffff0000u))));
           }
-        }
-        amax = warp_max(amax);
-        const int eg = amax > 0.f ? max(-100, min(120, ilogbf(amax) - 14)) : 0;
-        const float down = ldexpf(1.f, -eg);
-        slc0[0] = ldexpf(sl, eg);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));   // column cq's
+          const int eg = amax > 0.f ? max(-100, min(120, ilogbf(amax) - 14)) : 0;
+          const float down = ldexpf(1.f, -eg);
           float even = 0.f, odd = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t w4[4] = {raw[nb][i].x, raw[nb][i].y, raw[nb][i].z, raw[nb][i].w};
+            const uint32_t w4[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
             float x[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -886,8 +885,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           const float d1 = __shfl_sync(0xffffffffu, odd, 8 * tq + 4);
           off0[nb] = -(1024.f * e0 + 64.f * d0);
           off1[nb] = -(1024.f * e1 + 64.f * d1);
-          qs0[nb] = slc0[0] * (e0 + d0);
-          qs1[nb] = slc0[0] * (e1 + d1);
+          slc0[nb] = ldexpf(sl, __shfl_sync(0xffffffffu, eg, 8 * tq));
+          slc1[nb] = ldexpf(sl, __shfl_sync(0xffffffffu, eg, 8 * tq + 4));
+          qs0[nb] = slc0[nb] * (e0 + d0);
+          qs1[nb] = slc1[nb] * (e1 + d1);
         }
         vinv = 1.f;
         vcap = 0.f;
@@ -958,7 +959,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         for (int r = 0; r < 2; ++r) {
           const uint32_t kw = *reinterpret_cast<const uint32_t*>(sb + C::word_off(0, w, t, pg + 8 * r));
           const uint32_t vw = *reinterpret_cast<const uint32_t*>(sb + C::word_off(1, w, t, pg + 8 * r));
-          ksr[t][r] = int4_scale(kw) * slc0[0];
+          ksr[t][r] = int4_scale(kw);
           kzr[t][r] = int4_offset(kw);
           vsr[t][r] = int4_scale(vw);
           vzr[t][r] = fmaf(8.f, vsr[t][r], int4_offset(vw));
@@ -1101,9 +1102,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            x[nb][t][2 * r] = fmaf(ksr[t][r], sacc[nb][t][2 * r], fmaf(kzr[t][r], qs0[nb], -m0[nb]));
-            x[nb][t][2 * r + 1] =
-                fmaf(ksr[t][r], sacc[nb][t][2 * r + 1], fmaf(kzr[t][r], qs1[nb], -m1[nb]));
+            x[nb][t][2 * r] = fmaf(ksr[t][r] * slc0[nb], sacc[nb][t][2 * r],
+                                   fmaf(kzr[t][r], qs0[nb], -m0[nb]));
+            x[nb][t][2 * r + 1] = fmaf(ksr[t][r] * slc1[nb], sacc[nb][t][2 * r + 1],
+                                       fmaf(kzr[t][r], qs1[nb], -m1[nb]));
           }
         }
       }
