@@ -58,12 +58,16 @@ __device__ __forceinline__ float beam_pow2(float d) {
 }
 
 __device__ __forceinline__ bool beam_far(float m) { return !(fabsf(m) < 65536.f); }
-// s of a part with maximum m as a share of a whole with maximum M >= m
+// s of a part with maximum m as a share of a whole with maximum M >= m.  Where either
+// is far, through the distance m - M and what either's base lies above its maximum (0
+// to 1: one fused operation, since b and m c themselves are large there).
 __device__ __forceinline__ float beam_join(float m, float s, float M) {
   if (m == -INFINITY) return s;                    // 0, or NaN
-  const float from = beam_far(m) ? m * kBeamLog2e : beam_base(m);
-  if (!beam_far(M)) return s * beam_pow2(beam_far(m) ? -INFINITY : from - beam_base(M));
-  return s * exp2f(beam_far(m) ? (m - M) * kBeamLog2e : from - M * kBeamLog2e);
+  const bool fm = beam_far(m), fM = beam_far(M);
+  if (!fm && !fM) return s * beam_pow2(beam_base(m) - beam_base(M));
+  const float up = fm ? 0.f : -fmaf(m, kBeamLog2e, -beam_base(m));
+  const float down = fM ? 0.f : -fmaf(M, kBeamLog2e, -beam_base(M));
+  return s * exp2f(fmaf(m - M, kBeamLog2e, up - down));
 }
 
 // A value's bits in its order (adding 0 makes one of the two zeros).
