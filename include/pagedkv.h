@@ -696,8 +696,11 @@ PKV_API pkv_status pkv_verify_draft_tokens(
  * vocabulary.  With row = r * num_beams + b of the logits,
  *   candidate (b, v) = scores[r][b] + logits[row][v]
  *                      - log sum_v' exp(logits[row][v']),
- * in descending order; equal ones go to the lowest b * vocab + v.  Sums and
- * candidates are joined in 64 bits (terms of the sum in float32).  A finished
+ * in descending order; equal ones go to the lowest b * vocab + v.  A row's sum is
+ * formed in float32 over parts of a few thousand values, which are joined in 64
+ * bits, as candidates are: rows that hold the same values have the same sum,
+ * wherever they lie, and tie; candidates of different rows that are closer than
+ * the sums' error (about 1e-6 of a unit) may stand in either order.  A finished
  * beam has one candidate: eos_token at its score as it is; its logits are not
  * read.  Candidates of -infinity (a logit or score of -infinity) are none: a
  * first step gives every beam but one the score -infinity, or num_beams = 1

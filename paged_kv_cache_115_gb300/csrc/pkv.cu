@@ -890,8 +890,7 @@ pkv_status write_quant(const void* k, int64_t k_stride, const void* v, int64_t v
 // twice over, else 2, so that a few rows still spread over the machine.
 constexpr int kBeamWide = 8, kBeamNarrow = 2;
 int beam_tiles(int64_t V, int blocks, int elem) {
-  const int per = 16 / elem;
-  return (int)ceil_div(V + per - 1, (int64_t)pkv::kBeamThreads * blocks * per);
+  return (int)ceil_div(V, (int64_t)pkv::kBeamThreads * blocks * (16 / elem));
 }
 int beam_blocks(int64_t rows, int64_t V, int elem, int sms) {
   return rows * beam_tiles(V, kBeamWide, elem) >= 2 * sms ? kBeamWide : kBeamNarrow;

@@ -129,6 +129,23 @@ __device__ __noinline__ void beam_push(uint4 r, int v, uint32_t tau, int* n, uin
   }
 }
 
+// Values lead .. of a block and the next one's behind them: the unaligned block of a
+// row whose first value is value `lead` of an aligned one.
+template <typename T>
+__device__ __forceinline__ uint4 beam_shift(const uint4& lo, const uint4& hi, int lead) {
+  const int bytes = lead * (int)sizeof(T);
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = (bytes & 8) ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = (bytes & 4) ? w[i + 1] : w[i];
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (bytes & 2) * 8);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A tile of very many equal values: its N best one after the other, read again.
 template <typename T, int NV>
 __device__ __noinline__ void beam_tile_slow(const T* base, int V, int first, int N, float* out_x,
@@ -139,7 +156,7 @@ __device__ __noinline__ void beam_tile_slow(const T* base, int V, int first, int
   uint64_t last = ~0ull;
   for (int r = 0; r < N; ++r) {
     uint64_t best = 0;
-    for (int v = max(0, first) + threadIdx.x; v < end; v += kBeamThreads) {
+    for (int v = first + threadIdx.x; v < end; v += kBeamThreads) {
       const float x = to_f32(base[v]);
       const uint64_t key = beam_key(x, v);
       if (x > -INFINITY && key < last && key > best) best = key;
@@ -164,9 +181,11 @@ __device__ __noinline__ void beam_tile_slow(const T* base, int V, int first, int
   }
 }
 
-// NV 16-byte blocks a thread, all in flight at once: a tile of a row, counted from
-// the 16-byte boundary at or in front of the row (rows of an odd vocabulary start
-// anywhere); what does not belong to the row counts as -inf.  Four CTAs an SM
+// NV 16-byte blocks a thread, all in flight at once: a tile of a row.  Rows of an odd
+// vocabulary start anywhere: a block is then cut out of two aligned ones (the second
+// comes from L1), so that a thread holds the same tokens, and a row's sum is the same
+// to the last bit, wherever the row lies: rows alike tie.  What does not belong to the
+// row counts as -inf.  Four CTAs an SM
 // (three for float32): the blocks stay packed in registers and are unpacked as they are used.
 // Bound by HBM (V e bytes a row) from afar: 512 rows of 131072 bf16 values in 38 us, of a
 // whole call's 51 where a copy would take 19; what a warp issues for the bound (the N-th
@@ -190,23 +209,17 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
   const T* base = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
   const int lead = (int)((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(T));
   const uint4* vec = reinterpret_cast<const uint4*>(base - lead);
-  const int nvec = (lead + p.V + VE - 1) / VE;
+  const int nvec = (lead + p.V + VE - 1) / VE;                    // aligned blocks of the row
   const int v0 = tile * (kBeamThreads * NV) + tid;
   const int64_t slot = (int64_t)row * p.tiles + tile;
   float* out_x = p.tile_x + slot * p.N;
   int32_t* out_v = p.tile_v + slot * p.N;
-  const int first = tile * (kBeamThreads * NV * VE) - lead;      // token of the tile's first value
-  if (first >= p.V) {                                             // nothing of the row
-    if (tid == 0) p.tile_ms[slot] = make_float2(-INFINITY, 0.f);
-    if (tid < p.N) out_x[tid] = -INFINITY;
-    return;
-  }
+  const int first = tile * (kBeamThreads * NV * VE);              // the tile's first token
   uint4 raw[NV];
-  if (first >= 0 && first + kBeamThreads * NV * VE <= p.V) {
+  if (lead == 0 && first + kBeamThreads * NV * VE <= p.V) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) raw[j] = __ldcs(vec + v0 + j * kBeamThreads);
   } else {
-    // the first and the last block of a row hold values of its neighbours
     constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -214,14 +227,24 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
       raw[j] = make_uint4(kNone, kNone, kNone, kNone);
       if (v < nvec) raw[j] = __ldcs(vec + v);
     }
+    if (lead > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int v = v0 + j * kBeamThreads + 1;
+        uint4 next = make_uint4(kNone, kNone, kNone, kNone);
+        if (v < nvec) next = __ldcs(vec + v);
+        raw[j] = beam_shift<T>(raw[j], next, lead);
+      }
+    }
+    // the row's last block, and those behind it, hold values of its neighbours
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e0 = (v0 + j * kBeamThreads) * VE - lead;
-      if (e0 < 0 || (e0 < p.V && e0 + VE > p.V)) {
+      const int e0 = (v0 + j * kBeamThreads) * VE;
+      if (e0 + VE > p.V) {
         uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          if (e0 + e < 0 || e0 + e >= p.V) {
+          if (e0 + e >= p.V) {
             if constexpr (sizeof(T) == 4) w[e] = kNone;
             else w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | 0xff800000u : (w[e >> 1] & 0xffff0000u) | 0xff80u;
           }
