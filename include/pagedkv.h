@@ -728,7 +728,8 @@ PKV_API pkv_status pkv_beam_select(const void* logits, int64_t logits_stride, co
                                    float* scores_out, uint8_t* finished_out, void* workspace,
                                    size_t workspace_bytes, pkv_dtype dtype, void* stream);
 
-/* Workspace bytes of pkv_beam_select for these sizes. */
+/* Workspace bytes of pkv_beam_select for these sizes and for any with fewer
+ * requests, beams or candidates asked for (the same vocabulary). */
 PKV_API pkv_status pkv_beam_select_workspace_bytes(int32_t num_requests, int32_t num_beams,
                                                    int32_t vocab, int32_t num_select,
                                                    size_t* bytes);

@@ -2218,11 +2218,16 @@ pkv_status pkv_beam_select_workspace_bytes(int32_t num_requests, int32_t num_bea
   st = device_facts(&dev, &sms);
   if (st != PKV_OK) return st;
   const int64_t rows = (int64_t)num_requests * num_beams;
-  // (the larger of both types' needs: the call takes either)
+  // The larger of both types' needs: the call takes either.  Fewer rows take narrow
+  // tiles, four times as many a row: the most rows that do count too, so that the
+  // buffer of a batch serves the smaller ones that follow it.
   size_t need = 0;
-  for (int elem : {2, 4})
-    need = std::max(need, beam_ws(rows, beam_tiles(vocab, beam_blocks(rows, vocab, elem, sms), elem),
-                                  num_select).total);
+  for (int elem : {2, 4}) {
+    const int64_t narrow = (2 * (int64_t)sms - 1) / beam_tiles(vocab, kBeamWide, elem);
+    for (int64_t r : {rows, std::min(rows, narrow)})
+      need = std::max(need, beam_ws(r, beam_tiles(vocab, beam_blocks(r, vocab, elem, sms), elem),
+                                    num_select).total);
+  }
   *bytes = need;
   return PKV_OK;
 }

@@ -1083,7 +1083,8 @@ def verify_draft_tokens(target_probs: torch.Tensor, draft_probs: Optional[torch.
 
 def beam_select_workspace_bytes(num_requests: int, num_beams: int, vocab: int,
                                 num_select: int) -> int:
-    """Workspace bytes of :func:`beam_select`."""
+    """Workspace bytes of :func:`beam_select`, for fewer requests, beams or
+    candidates too."""
     _in_32_bits(num_requests | num_beams | vocab | num_select)
     out = c_sz(0)
     _check(_beam_ws(num_requests, num_beams, vocab, num_select, ctypes.byref(out)),
