@@ -1118,7 +1118,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_select: int,
     R, B = scores.shape
     rows, V = logits.shape
     N = int(num_select)
-    _in_32_bits(rows | V | N | eos_token)
+    _in_32_bits(rows | V | N)
+    _in_32_bits(eos_token)                   # (-1, the default, would hide the others)
     if rows != R * B:
         raise ValueError(f"logits must have {R * B} rows, got {rows}")
     ls, one = logits.stride()
