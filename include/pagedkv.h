@@ -775,7 +775,8 @@ PKV_API pkv_status pkv_beam_select_workspace_bytes(int32_t num_requests, int32_t
  *   workspace: pkv_fork_tables_workspace_bytes bytes, 256-byte aligned; not
  *            shared with a call that overlaps on the GPU.
  * Supported: group_rows <= 32, num_groups * group_rows * max_blocks_per_seq <
- * 2^31.
+ * 2^31, max_blocks_per_seq * block_size < 2^31.  num_groups 0: nothing is
+ * launched and nothing written, ring_state_out and totals included.
  */
 PKV_API pkv_status pkv_fork_tables(const int32_t* parents, const int32_t* lens,
                                    const int32_t* held, const int32_t* shared,

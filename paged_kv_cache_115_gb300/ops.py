@@ -1220,6 +1220,9 @@ def fork_tables(parents: torch.Tensor, lens: torch.Tensor, held: torch.Tensor,
               _whole(pairs, "pairs", i64, (S, 2), dev), _vec(totals, "totals", i32, 4, dev),
               _vec(workspace, "workspace", torch.uint8, ws_bytes, dev), ws_bytes),
              "pkv_fork_tables")
+    if R == 0:                               # nothing was launched: the ring as it was
+        ring_state_out.copy_(ring_state)
+        totals.zero_()
     return dict(block_tables_out=block_tables_out, lens_out=lens_out, held_out=held_out,
                 ring_state_out=ring_state_out, pairs=pairs, totals=totals)
 
