@@ -581,7 +581,9 @@ PKV_API pkv_status pkv_step_tables(const int32_t* lens, const int32_t* counts,
  *   float32 and rounded once, to the type it is stored in.  q_out[t] receives
  *   the query rows; the key rows and v[t] as it is go to slot slots[t] of the
  *   pools, as pkv_kv_write (quant NULL) or, quantized per `quant`, as
- *   pkv_kv_append_quant store them.
+ *   pkv_kv_append_quant store them (not PKV_KV_INT4_HEAD: rotate into plain
+ *   pools of the step's tokens, slots 0, 1, ..., which are rows that
+ *   pkv_kv_write_quant then stores).
  *   q: [num_tokens, num_q_heads, head_dim], k, v: [num_tokens, num_kv_heads,
  *   head_dim], each with its own distance between tokens (elements; heads and
  *   values contiguous), so that they can be cut out of one projection's

@@ -2006,7 +2006,8 @@ pkv_status pkv_qk_norm_rope_append(
     pkv_status s = check_quant(quant, true);
     if (s != PKV_OK) return s;
     PKV_CHECK(quant->format != PKV_KV_INT4_HEAD, PKV_ERR_UNSUPPORTED,
-              "INT4 pools: pkv_kv_write_quant stores the rotated rows");
+              "INT4 pools: rotate into plain pools of the step's tokens (slots 0, 1, ...) and "
+              "store their rows by pkv_kv_write_quant");
     PKV_CHECK(quant->format != PKV_KV_INT8_TOKEN || kv_row <= pkv::kRopeMaxInt8Row,
               PKV_ERR_UNSUPPORTED, "INT8 pools: num_kv_heads * head_dim must be at most %d",
               pkv::kRopeMaxInt8Row);

@@ -929,7 +929,9 @@ def paged_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     write of K and V into the pages at ``slots`` (int64 [T], -1: none), in one
     pass.  q [T, H_q, D], k and v [T, H_kv, D] may be cut out of one
     projection's output (any distance between tokens).  Pools of the same
-    type, or one-byte pools described by ``quant``.  Returns ``q_out`` (new,
+    type, or one-byte pools described by ``quant`` (int4 pools: plain pools of
+    the step's tokens with slots 0, 1, ..., whose rows
+    :func:`paged_kv_write_quant` then stores).  Returns ``q_out`` (new,
     given, or ``q`` itself for in place)."""
     T, H_q, D = q.shape
     nb, K, H_kv, D2 = k_cache.shape
@@ -937,7 +939,8 @@ def paged_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         q_out = torch.empty((T, H_q, D), dtype=q.dtype, device=q.device)
     dev, dtype = _device_of(q, "q"), q.dtype
     if quant is not None and quant.format == KV_INT4_HEAD:
-        raise ValueError("int4 pools: paged_kv_write_quant stores the rotated rows")
+        raise ValueError("int4 pools: let k_cache and v_cache be plain pools of the step's tokens "
+                         "(slots 0, 1, ...), and store their rows by paged_kv_write_quant")
     if D2 != D or v_cache.shape != k_cache.shape:
         raise ValueError("pools must be [num_blocks, block_size, H_kv, D] of q's head size")
     if quant is None:
