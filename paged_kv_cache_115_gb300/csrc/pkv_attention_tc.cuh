@@ -226,14 +226,23 @@ constexpr float kQuantSlack = 4.f;
 //   sum_t p_t V_t = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (z_t + 8 s_t),
 // so codes enter the tensor core as they are, scales and offsets act on scores
 // and weights, and no value is dequantized by itself.  A 32-bit word holds eight
-// codes of a row; a mask and an exponent make f16 pairs of the codes at nibbles
-// (i, i + 4), twice, the second time from w >> 8:
-//   w & 0x000f000f | 0x6400 6400 = 1024 + c,  w & 0x00f000f0 | 0x5400 5400 = 64 + c.
-// K leaves these numbers in: 1024 sum(q) over the one half of the columns and 64
-// sum(q) over the other come off the score, whose few steps in float32 they do not
-// harm (the same error for every key of a query, 2^-24 of a sum of |q|).  V takes
-// them off and centres the codes: o sums thousands of rows, the tensor core cuts
-// its sums towards zero, and sums without a common sign lose nothing that adds up.
+// codes of a row; a mask makes pairs of the codes at nibbles (i, i + 4), twice, the
+// second time from w >> 8.
+// K: masked bits are f16 numbers below the normal ones, exactly
+//   w & 0x000f000f = 2^-24 c,  w & 0x00f000f0 = 2^-20 c.
+// The tensor core adds at its largest term's exponent, and takes such a number at the
+// lowest normal one, 2^-14: the second pairs lose three bits of a sum by that, the
+// first would lose seven and are multiplied by 2^15.  The queries' scales take up the
+// powers of two.  (Codes under an exponent, 1024 + c and 64 + c, without the product,
+// bring 1024 sum(q) and 64 sum(q) into a score.  With four channels of 100 beside ones
+// of 0.004, scale 8, scores were off by up to 0.58 so, 0.12 with all masked bits as they
+// stand, 0.012 like this, 0.009 with centred codes, three per cent slower; a float32 sum
+// on CUDA cores and the output's rounding leave 0.007.)
+// V: the mask and an exponent (a known way to turn small integers into f16: Kim, Henry,
+// Fahim and Awadalla, "Who Says Elephants Can't Run", 2022) give
+//   w & 0x000f000f | 0x6400 6400 = 1024 + c,  w & 0x00f000f0 | 0x5400 5400 = 64 + c,
+// which are taken off, centring the codes: o sums thousands of rows, the tensor core
+// cuts its sums towards zero, and sums without a common sign lose nothing that adds up.
 // The mma k order (K) and row order (V) are permuted to fit.
 // K: lane (g, tq) holds columns 32 tq .. 32 tq + 31 of token pi(g) (and pi(g) +
 // 8): one 16-byte load a row.  V: lane (g, tq) holds columns 16 g .. 16 g + 15 of
@@ -253,6 +262,10 @@ __device__ __forceinline__ uint32_t int4_hi(uint32_t w) {          // nibbles 1 
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(0x00f000f0u), "r"(0x54005400u));
   return r;
+}
+__device__ __forceinline__ uint32_t f16x2_times(uint32_t x, float c) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(c, c));
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint32_t f16x2_less(uint32_t x, float c) {
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(c, c));
@@ -764,9 +777,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   float slc0[NB], slc1[NB];     // per score column (quantized pools: q's 2^e folded in)
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) slc0[nb] = slc1[nb] = sl;
-  // INT4, per score column: minus what the codes' 1024 and 64 add to a product, and
-  // scale_log2 times sum(q)
-  float off0[I4 ? NB : 1], off1[I4 ? NB : 1], qs0[I4 ? NB : 1], qs1[I4 ? NB : 1];
+  float qs0[I4 ? NB : 1], qs1[I4 ? NB : 1];     // INT4, per score column: scale_log2 times sum(q)
   const int pg = I4 ? int4_pi<C::PAIR>(g) : g;     // token row of a tile that mma row g holds
   // INT4: V scales enter times vinv, a power of two that puts the largest seen (up
   // to vcap) at 2^8 .. 2^11: weights of up to 2^kQuantSlack stay inside f16, and
@@ -831,10 +842,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         }
       } else if constexpr (I4) {
         // f16 fragments in the order of the K words (see "INT4"), each column scaled by
-        // a power of two of its own that puts its largest |q| in [2^14, 2^15): exact
-        // down to 2^-29 of it, far inside the f16 range, and whatever another head or
-        // another member of a group holds (an infinity, values of another size) is
-        // nothing to it
+        // a power of two of its own that puts its largest |q| in [2^14, 2^15), the
+        // first pairs' in [2^3, 2^4): exact down to 2^-20 of it, below within 2^-28 of the
+        // largest, far inside the f16 range; and whatever another head or another member
+        // of a group holds (an infinity, values of another size) is nothing to it
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           float amax = 0.f;
@@ -856,7 +867,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));   // column cq's
           const int eg = amax > 0.f ? max(-100, min(120, ilogbf(amax) - 14)) : 0;
           const float down = ldexpf(1.f, -eg);
-          float even = 0.f, odd = 0.f;
+          float sum = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t w4[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -866,29 +877,23 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
               x[2 * e] = __uint_as_float(w4[e] << 16) * down;
               x[2 * e + 1] = __uint_as_float(w4[e] & 0xffff0000u) * down;
             }
-            qf[nb][2 * i][0] = pack_f16x2(x[0], x[4]);
+            qf[nb][2 * i][0] = pack_f16x2(x[0] * 0x1p-11f, x[4] * 0x1p-11f);
             qf[nb][2 * i][1] = pack_f16x2(x[1], x[5]);
-            qf[nb][2 * i + 1][0] = pack_f16x2(x[2], x[6]);
+            qf[nb][2 * i + 1][0] = pack_f16x2(x[2] * 0x1p-11f, x[6] * 0x1p-11f);
             qf[nb][2 * i + 1][1] = pack_f16x2(x[3], x[7]);
-            even += (x[0] + x[2]) + (x[4] + x[6]);
-            odd += (x[1] + x[3]) + (x[5] + x[7]);
+            sum += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
           }
-#pragma unroll
-          for (int o1 = 1; o1 < 4; o1 <<= 1) {
-            even += __shfl_xor_sync(0xffffffffu, even, o1);
-            odd += __shfl_xor_sync(0xffffffffu, odd, o1);
-          }
-          // score columns of this thread are 2tq, 2tq+1 (held by lanes 8tq, 8tq+4)
-          const float e0 = __shfl_sync(0xffffffffu, even, 8 * tq);
-          const float e1 = __shfl_sync(0xffffffffu, even, 8 * tq + 4);
-          const float d0 = __shfl_sync(0xffffffffu, odd, 8 * tq);
-          const float d1 = __shfl_sync(0xffffffffu, odd, 8 * tq + 4);
-          off0[nb] = -(1024.f * e0 + 64.f * d0);
-          off1[nb] = -(1024.f * e1 + 64.f * d1);
-          slc0[nb] = ldexpf(sl, __shfl_sync(0xffffffffu, eg, 8 * tq));
-          slc1[nb] = ldexpf(sl, __shfl_sync(0xffffffffu, eg, 8 * tq + 4));
-          qs0[nb] = slc0[nb] * (e0 + d0);
-          qs1[nb] = slc1[nb] * (e1 + d1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          // score columns of this thread are 2tq, 2tq+1 (held by lanes 8tq, 8tq+4).  Where
+          // 2^(eg + 20) scale_log2 is above 2^120 (|q| above 2^110 or so) all scores of the
+          // column are cut in size alike: its largest key keeps all the weight
+          const float f = fminf(fmaxf(ldexpf(sl, eg + 20), -0x1p120f), 0x1p120f);
+          sum *= f * 0x1p-20f;
+          slc0[nb] = __shfl_sync(0xffffffffu, f, 8 * tq);
+          slc1[nb] = __shfl_sync(0xffffffffu, f, 8 * tq + 4);
+          qs0[nb] = __shfl_sync(0xffffffffu, sum, 8 * tq);
+          qs1[nb] = __shfl_sync(0xffffffffu, sum, 8 * tq + 4);
         }
         vinv = 1.f;
         vcap = 0.f;
@@ -1007,10 +1012,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int t = 0; t < TL; ++t) {
-        sacc[nb][t][0] = sacc[nb][t][2] = I4 ? off0[I4 ? nb : 0] : 0.f;
-        sacc[nb][t][1] = sacc[nb][t][3] = I4 ? off1[I4 ? nb : 0] : 0.f;
-      }
+      for (int t = 0; t < TL; ++t) sacc[nb][t][0] = sacc[nb][t][1] = sacc[nb][t][2] = sacc[nb][t][3] = 0.f;
     if constexpr (C::KB) {
       const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
       const int chs = lane >> 4;
@@ -1050,7 +1052,9 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const uint32_t x = hf ? wa[i] >> 8 : wa[i], y = hf ? wb[i] >> 8 : wb[i];
-            const uint32_t a0 = int4_lo(x), a1 = int4_lo(y), a2 = int4_hi(x), a3 = int4_hi(y);
+            const uint32_t a0 = f16x2_times(x & 0x000f000fu, 32768.f);
+            const uint32_t a1 = f16x2_times(y & 0x000f000fu, 32768.f);
+            const uint32_t a2 = x & 0x00f000f0u, a3 = y & 0x00f000f0u;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
               if (nb < nbv)
