@@ -223,7 +223,7 @@ constexpr float kQuantSlack = 4.f;
 
 // INT4.  With row t's scale s_t and offset z_t and codes c,
 //   q . K_t = s_t (q . c_t) + z_t sum(q),
-//   sum_t p_t V_t = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (z_t + 8 s_t),
+//   sum_t p_t V_t = sum_t (p_t s_t) (c_t - m) + sum_t p_t (z_t + m s_t),
 // so codes enter the tensor core as they are, scales and offsets act on scores
 // and weights, and no value is dequantized by itself.  A 32-bit word holds eight
 // codes of a row; a mask makes pairs of the codes at nibbles (i, i + 4), twice, the
@@ -243,6 +243,9 @@ constexpr float kQuantSlack = 4.f;
 //   w & 0x000f000f | 0x6400 6400 = 1024 + c,  w & 0x00f000f0 | 0x5400 5400 = 64 + c,
 // which are taken off, centring the codes: o sums thousands of rows, the tensor core
 // cuts its sums towards zero, and sums without a common sign lose nothing that adds up.
+// Their centre is m = 8 in one 16-token tile and 7 in the next (7.5 itself is no f16
+// number above 1024): with 8 in all, half a step a row adds up, and what is cut of it
+// counts where an output is small beside its values.
 // The mma k order (K) and row order (V) are permuted to fit.
 // K: lane (g, tq) holds columns 32 tq .. 32 tq + 31 of token pi(g) (and pi(g) +
 // 8): one 16-byte load a row.  V: lane (g, tq) holds columns 16 g .. 16 g + 15 of
@@ -967,7 +970,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           ksr[t][r] = int4_scale(kw);
           kzr[t][r] = int4_offset(kw);
           vsr[t][r] = int4_scale(vw);
-          vzr[t][r] = fmaf(8.f, vsr[t][r], int4_offset(vw));
+          vzr[t][r] = fmaf(t & 1 ? 7.f : 8.f, vsr[t][r], int4_offset(vw));
         }
       } else if constexpr (CT == 2) {
         const float* kscl = reinterpret_cast<const float*>(sb + C::SCALE_OFF + t * 64);
@@ -1349,8 +1352,9 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
 #pragma unroll
           for (int uu = 0; uu < 2; ++uu) {
             const uint32_t x = uu ? lo >> 8 : lo, y = uu ? hi >> 8 : hi;
-            const uint32_t a0 = f16x2_less(int4_lo(x), 1032.f), a1 = f16x2_less(int4_hi(x), 72.f);
-            const uint32_t a2 = f16x2_less(int4_lo(y), 1032.f), a3 = f16x2_less(int4_hi(y), 72.f);
+            const float m = t & 1 ? 7.f : 8.f;
+            const uint32_t a0 = f16x2_less(int4_lo(x), 1024.f + m), a1 = f16x2_less(int4_hi(x), 64.f + m);
+            const uint32_t a2 = f16x2_less(int4_lo(y), 1024.f + m), a3 = f16x2_less(int4_hi(y), 64.f + m);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
               if (nb < nbv)
