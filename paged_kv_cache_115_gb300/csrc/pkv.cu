@@ -309,7 +309,7 @@ int* carve_glen(void* ws, const AttnPlan& p, int H_q, int H_kv, int D) {
 }
 
 // ---- tensor-core kernel dispatch ------------------------------------------------
-template <int D, int HPC, int CT, bool B8, int SH = 0, bool PX = false>
+template <int D, int HPC, int CT, bool B8, int SH = 0, bool PX = false, bool TWIN = false>
 struct TcInst {
   // stages: as many as fit in ~192 KiB (bf16) / ~203 KiB (one-byte pools)
   // of shared memory, between 2 and 8
@@ -324,17 +324,17 @@ struct TcInst {
   static std::once_flag flags[kMaxDevices];
   static cudaError_t errs[kMaxDevices];
   static pkv_status launch(const pkv::TcParams& prm, int n, int groups, cudaStream_t st, int dev) {
-    auto k = pkv::attn_tc_kernel<D, HPC, NS, CT, B8, SH, PX>;
+    auto k = pkv::attn_tc_kernel<D, HPC, NS, CT, B8, SH, PX, TWIN>;
     pkv_status s = set_smem_once(k, C::SMEM, flags, errs, dev);
     if (s != PKV_OK) return s;
     PKV_CUDA(launch_pdl(k, dim3(n, groups), dim3(C::THREADS), (size_t)C::SMEM, st, prm));
     return PKV_OK;
   }
 };
-template <int D, int HPC, int CT, bool B8, int SH, bool PX>
-std::once_flag TcInst<D, HPC, CT, B8, SH, PX>::flags[kMaxDevices];
-template <int D, int HPC, int CT, bool B8, int SH, bool PX>
-cudaError_t TcInst<D, HPC, CT, B8, SH, PX>::errs[kMaxDevices];
+template <int D, int HPC, int CT, bool B8, int SH, bool PX, bool TWIN>
+std::once_flag TcInst<D, HPC, CT, B8, SH, PX, TWIN>::flags[kMaxDevices];
+template <int D, int HPC, int CT, bool B8, int SH, bool PX, bool TWIN>
+cudaError_t TcInst<D, HPC, CT, B8, SH, PX, TWIN>::errs[kMaxDevices];
 
 // ---- multi-query (prefill) kernel dispatch -----------------------------------------
 template <int D, int NW>
@@ -485,16 +485,16 @@ pkv_status plan_prefill(int num_seqs, int num_tokens, int max_query_len, int max
   return PKV_OK;
 }
 
-template <int D, int CT, bool B8, int SH = 0, bool PX = false>
+template <int D, int CT, bool B8, int SH = 0, bool PX = false, bool TWIN = false>
 pkv_status launch_tc_hpc(int hpc, const pkv::TcParams& prm, int n, int groups, cudaStream_t st,
                          int dev) {
   if constexpr (CT != 4) {
-    if (hpc == 8) return TcInst<D, 8, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
+    if (hpc == 8) return TcInst<D, 8, CT, B8, SH, PX, TWIN>::launch(prm, n, groups, st, dev);
   }
   switch (hpc) {
-    case 4: return TcInst<D, 4, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
-    case 2: return TcInst<D, 2, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
-    default: return TcInst<D, 1, CT, B8, SH, PX>::launch(prm, n, groups, st, dev);
+    case 4: return TcInst<D, 4, CT, B8, SH, PX, TWIN>::launch(prm, n, groups, st, dev);
+    case 2: return TcInst<D, 2, CT, B8, SH, PX, TWIN>::launch(prm, n, groups, st, dev);
+    default: return TcInst<D, 1, CT, B8, SH, PX, TWIN>::launch(prm, n, groups, st, dev);
   }
 }
 
@@ -512,6 +512,12 @@ pkv_status launch_tc_d(int hpc, int block_size, const pkv::TcParams& prm, int n,
       return block_size < pkv::kTile
                  ? launch_tc_hpc<D, CT, true, 2>(hpc, prm, n, groups, st, dev)
                  : launch_tc_hpc<D, CT, false, 2>(hpc, prm, n, groups, st, dev);
+  }
+  if constexpr (CT == 4) {
+    if (prm.share_m == 1 && prm.G <= 4)
+      return block_size < pkv::kTile
+                 ? launch_tc_hpc<D, CT, true, 0, false, true>(hpc, prm, n, groups, st, dev)
+                 : launch_tc_hpc<D, CT, false, 0, false, true>(hpc, prm, n, groups, st, dev);
   }
   if constexpr (CT == 0 || CT == 4) {
     if (prm.share_m > 1)

@@ -275,6 +275,17 @@ __device__ __forceinline__ uint32_t f16x2_less(uint32_t x, float c) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The leading bits of a weight that an f16 number holds, and two numbers cut to f16:
+// what the first cuts off is exact, and enters as a second number.
+__device__ __forceinline__ float f16_part(float x) {
+  return __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+}
+__device__ __forceinline__ uint32_t cut_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 template <bool PAIR>
 __device__ __forceinline__ int int4_pi(int g) {
   return PAIR ? g ^ ((g & 1) << 2) : (g & 4) | ((0x2130 >> ((g & 3) * 4)) & 3);
@@ -421,7 +432,12 @@ __host__ __device__ __forceinline__ int4 tc_seq_meta(const int* cstart, int s, i
   return r;
 }
 
-template <int D, int HPC, int NS, int CT = 0, bool B8 = false, int SH = 0, bool PX = false>
+// TWIN (INT4): a weight enters the tensor core as two f16 numbers.  Up to four heads
+// leave half of the score columns free: columns 4 .. 7 repeat 0 .. 3 and hold the second
+// numbers, and one product forms both sums, joined at the partition's end.  Without
+// TWIN a second product adds them.
+template <int D, int HPC, int NS, int CT = 0, bool B8 = false, int SH = 0, bool PX = false,
+          bool TWIN = false>
 __global__ void __launch_bounds__(TcCfg<D, HPC, NS, CT, B8>::THREADS, tc_ctas(CT, HPC, SH == 1))
 attn_tc_kernel(const __grid_constant__ TcParams p) {
   using C = TcCfg<D, HPC, NS, CT, B8>;
@@ -431,6 +447,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   // members fit one block)
   constexpr int NB = SH == 1 ? 2 : 1;
   static_assert(SH != 2 || CT == 4, "groups of one column block: INT4 pools");
+  static_assert(!TWIN || (CT == 4 && !SH), "repeated columns: INT4 pools, one sequence a unit");
   constexpr bool I4 = C::I4;
   static_assert(!SH || CT == 0 || CT == 4, "shared-prefix groups need bf16 or INT4 pools");
   static_assert(!PX || (CT == 0 && !SH), "shared-prefix attention needs bf16 pools");
@@ -853,7 +870,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         for (int nb = 0; nb < NB; ++nb) {
           float amax = 0.f;
           uint4 raw[4];
-          const int cq = 8 * nb + g;
+          const int cq = TWIN ? g & 3 : 8 * nb + g;
           const __nv_bfloat16* qrow =
               p.q + ((int64_t)(qr0 + (cq < ncol ? cq / G : 0)) * H_q + j * G + cq % G) * D + 32 * tq;
 #pragma unroll
@@ -1188,8 +1205,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           }
         }
       }
-      // weights times V scales as one f16 number (half a step is 2^-12 of it, an
-      // eighth of the output's own rounding; the codes carry four bits)
+      // weights times V scales as two f16 numbers, 22 bits.  With one, 11 bits, one output
+      // in ten was a bf16 rounding off those of a float32 sum, now one in 2000 (over
+      // 131072 tokens one in 300); it took 129.5 us where this takes 131.4 (128 sequences,
+      // repeated columns), 116.6 where the second product makes it 126.8 (four documents).
 #pragma unroll
       for (int t = 0; t < TL; ++t) {
         const float v0 = vsr[t][0] * vinv, v1 = vsr[t][1] * vinv;
@@ -1202,8 +1221,18 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           l1[nb] += p1 + p3;
           vz0[nb] = fmaf(p0, vzr[t][0], fmaf(p2, vzr[t][1], vz0[nb]));
           vz1[nb] = fmaf(p1, vzr[t][0], fmaf(p3, vzr[t][1], vz1[nb]));
-          pb[nb][t][0] = movmatrix_trans(pack_f16x2(p0 * v0, p1 * v0));
-          pb[nb][t][1] = movmatrix_trans(pack_f16x2(p2 * v1, p3 * v1));
+          const float w0 = p0 * v0, w1 = p1 * v0, w2 = p2 * v1, w3 = p3 * v1;
+          const float h0 = f16_part(w0), h1 = f16_part(w1), h2 = f16_part(w2), h3 = f16_part(w3);
+          if constexpr (TWIN) {
+            const float less = tq >= 2 ? -1.f : 0.f;       // (0: the cut takes the rest off)
+            pb[nb][t][0] = movmatrix_trans(cut_f16x2(fmaf(less, h0, w0), fmaf(less, h1, w1)));
+            pb[nb][t][1] = movmatrix_trans(cut_f16x2(fmaf(less, h2, w2), fmaf(less, h3, w3)));
+          } else {
+            pb[nb][t][0] = movmatrix_trans(cut_f16x2(w0, w1));
+            pb[nb][t][1] = movmatrix_trans(cut_f16x2(w2, w3));
+            pc[nb][t][0] = movmatrix_trans(cut_f16x2(w0 - h0, w1 - h1));
+            pc[nb][t][1] = movmatrix_trans(cut_f16x2(w2 - h2, w3 - h3));
+          }
         }
       }
     }
@@ -1357,8 +1386,11 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
             const uint32_t a2 = f16x2_less(int4_lo(y), 1024.f + m), a3 = f16x2_less(int4_hi(y), 64.f + m);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
-              if (nb < nbv)
+              if (nb < nbv) {
                 mma_f16_16816(o[nb][2 * q4 + uu], a0, a1, a2, a3, pb[nb][t][0], pb[nb][t][1]);
+                if constexpr (!TWIN)
+                  mma_f16_16816(o[nb][2 * q4 + uu], a0, a1, a2, a3, pc[nb][t][0], pc[nb][t][1]);
+              }
           }
         }
       }
@@ -1463,6 +1495,13 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
           for (int off = 4; off < 32; off <<= 1) {
             z0 += __shfl_xor_sync(0xffffffffu, z0, off);
             z1 += __shfl_xor_sync(0xffffffffu, z1, off);
+          }
+          if constexpr (TWIN) {                     // the second numbers' sums, two lanes on
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[nb][mt][e] += __shfl_xor_sync(0xffffffffu, o[nb][mt][e], 2);
           }
 #pragma unroll
           for (int mt = 0; mt < D / 16; ++mt) {

@@ -1,5 +1,5 @@
-"""Attention over 4-bit pages: sums keep their digits where thousands of rows add up to
-little."""
+"""Attention over 4-bit pages: sums keep their digits where terms cancel (weights of
+two keys) and where thousands of rows add up to little."""
 
 import numpy as np
 import pytest
@@ -11,6 +11,36 @@ from tests.test_gpu_int4_scores import bf16_words
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+
+
+@pytest.mark.parametrize("H_q,H_kv,K,share", [(8, 2, 16, False), (3, 1, 8, False), (8, 1, 16, False), (5, 1, 8, False),
+                                              (8, 2, 16, True), (8, 8, 8, True), (7, 1, 16, True)])
+def test_weights_of_two_keys(ops, H_q, H_kv, K, share):
+    # Values 7 and -8 under weights of about 8 : 7.  The queries have one channel, so scores
+    # are exact but for a rounding or two.
+    rng = np.random.default_rng(H_q + K)
+    S, D, scale, ch = 48, 128, 1.0, 21
+    q = np.zeros((S, H_q, D))
+    q[..., ch] = (np.log(8 / 7) + 0.01 * rng.standard_normal((S, H_q))) / 5
+    q = torch.from_numpy(q).to(torch.bfloat16)
+    kc = torch.zeros((S, K, H_kv, D // 2), dtype=torch.uint8)
+    kc[:, 0, :, ch // 2] = 9 << 4                                           # codes 9 and 4: five apart
+    kc[:, 1, :, ch // 2] = 4 << 4
+    ks = bf16_words(1.0, -4.0).repeat(S, H_kv, K, 1)
+    vc = torch.zeros_like(kc)
+    vc[:, 0] = 0xFF                                                         # codes 15 and 0
+    vs = bf16_words(1.0, -8.0).repeat(S, H_kv, K, 1)
+    bt = torch.arange(S, dtype=torch.int32)[:, None]
+    g = [t.to(DEV) for t in (q, kc, vc, bt, torch.full((S,), 2, dtype=torch.int32))]
+    qd = ops.kv_quant("int4", k_token_scales=ks.to(DEV), v_token_scales=vs.to(DEV))
+    out = as_f64(ops.paged_attention_decode_quant(*g, scale, qd, max_context_len=2, kernel=1, share_prefix=share))
+    assert ops.get_device_error() == 0
+    p0 = 1 / (1 + np.exp(-5 * as_f64(q)[..., ch]))
+    want = (7 * p0 - 8 * (1 - p0))[..., None]
+    assert 0.005 < np.abs(want).mean() < 0.1
+    # the output's half step; weights of 7 + 8: two f16 numbers (2^-21), the exponential
+    # (2^-22), a score's roundings (three of 2^-24 of less than 1) and six of sums
+    assert (np.abs(out - want) <= np.abs(want) * 2.0 ** -8 + 15 * (2.0 ** -21 + 2.0 ** -22 + 9 * 2.0 ** -24)).all()
 
 
 def test_sum_of_many_rows(ops):
