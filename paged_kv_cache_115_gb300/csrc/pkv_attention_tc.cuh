@@ -768,7 +768,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
         }
         const int stage = k % NS;
         const uint32_t parity = ((k / NS) & 1) ^ 1;
-        if (!mbar_wait_bounded(bar_empty + 8 * stage, parity)) {
+        if (!ring_acquire(bar_empty + 8 * stage, parity)) {
           record_error(PKV_DEVERR_TIMEOUT);
           ok = false;
           break;
@@ -1468,11 +1468,7 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
               }
       }
     }
-    // the stage's rows are in registers before it is given back: without the fence a
-    // warp behind the others saw rows of the tile that is copied over them
-    __threadfence_block();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_empty + 8 * stage);
+    ring_release(bar_empty + 8 * stage, lane);
     if (++stage == NS) {
       stage = 0;
       phase ^= 1;

@@ -75,6 +75,25 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// A ring of shared-memory stages that copies of the async proxy fill and threads read
+// (and, for rows to be zeroed, write) through the generic proxy.  An arrival's release
+// and the producer's acquire order accesses of one proxy; between a read of the one and
+// the copy of the other that overwrites what was read PTX asks for a proxy fence too,
+// which the lanes that issue copies execute behind their wait.  The consumers' fence
+// makes each lane's own reads complete before lane 0's arrival speaks for them: without
+// either, rows of the next tile were read by warps that lagged (in up to six of ten
+// calls of one shape), with the consumers' alone in none of 600.
+__device__ __forceinline__ void ring_release(uint32_t bar_empty, int lane) {
+  __threadfence_block();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar_empty);
+}
+__device__ __forceinline__ bool ring_acquire(uint32_t bar_empty, uint32_t parity) {
+  const bool ok = mbar_wait_bounded(bar_empty, parity);
+  fence_proxy_async_smem();
+  return ok;
+}
+
 // ---------------------------------------------------------------------------
 // TMA: 3-D tiled load global -> shared, completion counted on an mbarrier.
 // ---------------------------------------------------------------------------

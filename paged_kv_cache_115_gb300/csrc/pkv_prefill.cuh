@@ -140,7 +140,7 @@ attn_prefill_kernel(const __grid_constant__ PfParams p) {
     for (int kt = kt0; kt < kt1; ++kt, ++k) {
       const int stage = k % kPfStages;
       const uint32_t parity = ((k / kPfStages) & 1) ^ 1;
-      if (!mbar_wait_bounded(bar_empty + 8 * stage, parity)) {
+      if (!ring_acquire(bar_empty + 8 * stage, parity)) {
         record_error(PKV_DEVERR_TIMEOUT);
         ok = false;
         break;
@@ -311,8 +311,7 @@ attn_prefill_kernel(const __grid_constant__ PfParams p) {
         }
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_empty + 8 * stage);
+    ring_release(bar_empty + 8 * stage, lane);
   }
 
   // ---- normalise and store

@@ -314,7 +314,7 @@ rope_ring_kernel(const __grid_constant__ RopeParams p, int stage_bytes) {
         const long long st = __shfl_sync(0xffffffffu, slot, l);
         const int stage = n % stages;
         ok = __all_sync(0xffffffffu,
-                        mbar_wait_bounded(smem_u32(&s_empty[stage]), ((n / stages) & 1) ^ 1));
+                        ring_acquire(smem_u32(&s_empty[stage]), ((n / stages) & 1) ^ 1));
         if (!ok) break;
         if (lane == 0) {
           const uint32_t full = smem_u32(&s_full[stage]);
@@ -502,8 +502,7 @@ rope_ring_kernel(const __grid_constant__ RopeParams p, int stage_bytes) {
         }
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s_empty[stage]));
+    ring_release(smem_u32(&s_empty[stage]), lane);
     if (++stage == stages) {
       stage = 0;
       ++round;
