@@ -160,8 +160,8 @@ typedef struct {
                             tensor-core kernel on bf16 and INT4 pools; ignored by
                             the other plans): consecutive sequences are taken in
                             aligned groups of m = 16 / G (G = num_q_heads /
-                            num_kv_heads, so G <= 8 gives m >= 2; INT4 pools with
-                            G <= 4: 8 / G); the
+                            num_kv_heads, so G <= 8 gives m >= 2; INT4 pools:
+                            8 / G, ignored with G above 4); the
                             leading tokens whose block-table entries are the
                             same physical blocks in every member's row
                             ("推理与 KV Cache 02", 前缀索引与 Block Table: whole
@@ -171,7 +171,14 @@ typedef struct {
                             are read on their own; the partial states merge
                             in the split-K reduce.  Put the sequences that
                             share blocks (forks of one request, requests of
-                            one prompt) next to each other.  Adds one small
+                            one prompt) next to each other.  Groups are cut
+                            every m sequences from the first, whatever belongs
+                            together: what the B sequences of a request share
+                            is read B / m times where m divides B; a group
+                            with sequences of two requests shares only what
+                            all its members list, and otherwise reads each
+                            one's own as without the mode, a comparison and
+                            wider partial states on top.  Adds one small
                             launch that compares the table rows, and at most
                             1024 (INT4: 640) sequences go into one launch.  */
   int32_t reserved[5];   /* must be zero */

@@ -212,18 +212,19 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
     p.kind = KIND_TC;
     p.hpc = tc_hpc(H_kv, ct);
     p.groups = H_kv / p.hpc;
+    // members of a shared-prefix group: the columns of two blocks; INT4 pools those of
+    // one with G <= 4, which leaves registers for twice the warps, and none above: two
+    // blocks took 1.2 to 1.9 times what reading every member's own took (G 5 and 8; 2, 3, 4,
+    // 8 and 16 beams, prompts of 512 to 131072 tokens).
+    const int share_m = !c.share_prefix ? 1 : (ct == 4 ? (G <= 4 ? 8 / G : 1) : 16 / G);
     // one CTA per SM (shared memory bound), or as many as a pool format takes
-    // members of a shared-prefix group: the columns of two blocks; INT4 pools with G
-    // <= 4 those of one, which leaves registers for twice the warps
-    const bool one_block = ct == 4 && G <= 4;
-    const int share_m = !c.share_prefix ? 1 : (one_block ? 8 : 16) / G;
-    const int total = sms * pkv::tc_ctas(ct, p.hpc, share_m > 1 && !one_block);
+    const int total = sms * pkv::tc_ctas(ct, p.hpc);
     p.n_per_group = c.num_splits ? c.num_splits : (total / p.groups > 0 ? total / p.groups : 1);
     const int max_chunks = (int)ceil_div(max_len, pkv::kTcChunk);
     p.pmax = std::max(1, std::min(p.n_per_group, max_chunks));
     p.seq_batch = std::min(S, pkv::tc_max_seqs(ct));
-    if (c.share_prefix && G <= 8) {
-      // groups of 16 / G sequences fill the kernel's two 8-column blocks; a
+    if (share_m > 1) {
+      // groups of 16 / G (8 / G) sequences fill the kernel's 8-column blocks; a
       // sequence's partials are its group's shared unit's, then its own's
       p.share_m = share_m;
       p.seq_batch = std::min(S, pkv::tc_max_share_seqs(ct));
@@ -314,7 +315,7 @@ struct TcInst {
   // stages: as many as fit in ~192 KiB (bf16) / ~203 KiB (one-byte pools)
   // of shared memory, between 2 and 8
   static constexpr int STAGE_BYTES = pkv::TcCfg<D, HPC, 2, CT, B8 && CT == 4>::STAGE;
-  static constexpr int CTAS = pkv::tc_ctas(CT, HPC, SH == 1);    // share the SM's 228 KiB
+  static constexpr int CTAS = pkv::tc_ctas(CT, HPC);             // share the SM's 228 KiB
   static constexpr int BUDGET =
       CTAS > 1 ? 233472 / CTAS - 1024 - (pkv::tc_max_seqs(CT) + 1) * 4 - 1024 - 512 : (CT ? 217088 - 9216 : 196608);
   static constexpr int NS_FIT = BUDGET / STAGE_BYTES;
@@ -508,18 +509,16 @@ pkv_status launch_tc_d(int hpc, int block_size, const pkv::TcParams& prm, int n,
     return launch_tc_hpc<D, CT, false>(hpc, prm, n, groups, st, dev);   // 16-row tiles only
   }
   if constexpr (CT == 4) {
-    if (prm.share_m > 1 && prm.share_m * prm.G <= 8)
+    if (prm.share_m > 1)
       return block_size < pkv::kTile
                  ? launch_tc_hpc<D, CT, true, 2>(hpc, prm, n, groups, st, dev)
                  : launch_tc_hpc<D, CT, false, 2>(hpc, prm, n, groups, st, dev);
-  }
-  if constexpr (CT == 4) {
-    if (prm.share_m == 1 && prm.G <= 4)
+    if (prm.G <= 4)
       return block_size < pkv::kTile
                  ? launch_tc_hpc<D, CT, true, 0, false, true>(hpc, prm, n, groups, st, dev)
                  : launch_tc_hpc<D, CT, false, 0, false, true>(hpc, prm, n, groups, st, dev);
   }
-  if constexpr (CT == 0 || CT == 4) {
+  if constexpr (CT == 0) {
     if (prm.share_m > 1)
       return block_size < pkv::kTile
                  ? launch_tc_hpc<D, CT, true, 1>(hpc, prm, n, groups, st, dev)

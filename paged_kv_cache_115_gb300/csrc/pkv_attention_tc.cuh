@@ -54,13 +54,11 @@ constexpr int tc_chunk_tokens(int ct) { return ct == 0 || ct == 3 ? kTile : 2 * 
 // (and a producer warp) a CTA three of them, 15 warps of 128 registers.  (Two CTAs of
 // eight heads: 18 warps, 96 registers, spills, 188 us for 128 sequences of ~4600
 // tokens; eight heads without a producer warp, the consumers taking turns: 134 us,
-// the last warp out of a stage filling it: 147 us; these three: 122 us,
-// 118 with a fourth stage.)  The two
-// column blocks of shared-prefix groups take 168 registers.
-constexpr int tc_ctas(int ct, int hpc, bool two_blocks) {
-  return ct != 4 ? 1
-                 : (two_blocks ? (hpc == 4 ? 2 : (hpc == 2 ? 4 : 6))
-                               : (hpc == 4 ? 3 : (hpc == 2 ? 5 : 8)));
+// the last warp out of a stage filling it: 147 us; these three: 122 us, 118 with a
+// fourth stage, all with weights of one f16 number and before scores and queries were
+// mended, which makes it 129.)
+constexpr int tc_ctas(int ct, int hpc) {
+  return ct != 4 ? 1 : (hpc == 4 ? 3 : (hpc == 2 ? 5 : 8));
 }
 
 // Attention behind a shared prefix (pkv_prefix.cuh): the prefix kernel and
@@ -438,7 +436,7 @@ __host__ __device__ __forceinline__ int4 tc_seq_meta(const int* cstart, int s, i
 // TWIN a second product adds them.
 template <int D, int HPC, int NS, int CT = 0, bool B8 = false, int SH = 0, bool PX = false,
           bool TWIN = false>
-__global__ void __launch_bounds__(TcCfg<D, HPC, NS, CT, B8>::THREADS, tc_ctas(CT, HPC, SH == 1))
+__global__ void __launch_bounds__(TcCfg<D, HPC, NS, CT, B8>::THREADS, tc_ctas(CT, HPC))
 attn_tc_kernel(const __grid_constant__ TcParams p) {
   using C = TcCfg<D, HPC, NS, CT, B8>;
   constexpr int TL = C::TL, CH = C::CH;
@@ -446,10 +444,10 @@ attn_tc_kernel(const __grid_constant__ TcParams p) {
   // heads of a group's members side by side), one otherwise (SH 2: groups whose
   // members fit one block)
   constexpr int NB = SH == 1 ? 2 : 1;
-  static_assert(SH != 2 || CT == 4, "groups of one column block: INT4 pools");
+  static_assert(!SH || (SH == 1 && CT == 0) || (SH == 2 && CT == 4),
+                "shared-prefix groups: bf16 pools in two column blocks, INT4 pools in one");
   static_assert(!TWIN || (CT == 4 && !SH), "repeated columns: INT4 pools, one sequence a unit");
   constexpr bool I4 = C::I4;
-  static_assert(!SH || CT == 0 || CT == 4, "shared-prefix groups need bf16 or INT4 pools");
   static_assert(!PX || (CT == 0 && !SH), "shared-prefix attention needs bf16 pools");
   extern __shared__ uint8_t smem_raw[];
   // (an offset, not a rounded pointer: through an integer the loads below would be

@@ -634,8 +634,10 @@ def paged_attention_decode_quant(q: torch.Tensor, k_cache: torch.Tensor, v_cache
                                  share_prefix: bool = False) -> torch.Tensor:
     """Decode attention over a quantized pool (values read back as code * scale,
     INT4: offset + code * scale).  ``share_prefix``: stage blocks that
-    consecutive sequences share (the beams of a request) once per group, as in
-    :func:`paged_attention_decode`; INT4 pools, ignored by the others."""
+    consecutive sequences share (the beams of a request) once per group of 8 / G
+    sequences, cut from the first on; for INT4 pools with G = H_q / H_kv up to
+    4, ignored otherwise.  It pays where a request's beams are a multiple of
+    8 / G; other groups hold rows of two requests and share little."""
     dev, dtype, i32 = _device_of(q, "q"), q.dtype, torch.int32
     nb, K, H_kv, D2 = _quant_pool(k_cache, v_cache, quant)
     _one_layer(k_cache)
