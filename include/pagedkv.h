@@ -316,7 +316,8 @@ PKV_API pkv_status pkv_selftest_wait_timeout(int64_t limit_cycles, void* stream)
  *   offset z, over the head's head_dim values x: z = min x rounded down to
  *   bf16, s = bf16((max x - z) / 15), code = clamp(round_half_even((x - z) *
  *   (1 / s)), 0, 15), each step in float32 (1 / s taken as 0 for s < 2^-126);
- *   read back as z + s * code, within 0.57 s of x.  A row with a NaN or an
+ *   read back as z + s * code, within 0.57 s of x (s below 2^-126: as z, less
+ *   than 2^-122 off).  A row with a NaN or an
  *   infinity (or whose z or s overflows) gets s = z = NaN and reads as NaN.
  *   head_dim 64 or 128.
  */

@@ -234,7 +234,12 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
     p.slot_stride = (int64_t)p.n_per_group + pkv::tc_num_units(std::max(p.seq_batch, 1), p.share_m);
     p.slots = p.slot_stride * p.share_m;   // a region per member of a shared unit
     p.reduce = max_chunks > 1;
-    // partials of a row: the CTAs of a group over its sequences, or fewer
+    // A CTA a row merges few rows of many partials (a row's: the CTAs of a group over
+    // its sequences, or its chunks).  A call with a warp a row / with a CTA a row, us, 8 KV
+    // heads: 228 partials 60.6 / 27.2 (32 heads, 65536 tokens), 57 78.8 / 69.1 (64 heads, 4 of
+    // 65536), 28 21.5 / 16.6 (32 heads, 8 of 2048); 14 19.2 / 16.7 (8 heads, 16 of 2048) to
+    // 27.7 / 27.9 (32 heads, 16 of 4096); up to 8, which a warp loads at once, 8.9 / 8.9 to
+    // 25.3 / 28.4 (32 heads, 64 of 1024).  The border at 16 leaves some of the gain between.
     p.wide_merge = ct == 4 && (int64_t)S * H_q <= 8 * sms &&
                    p.n_per_group > 16 * std::max(p.seq_batch, 1) && max_chunks > 32;
   } else {
@@ -683,9 +688,8 @@ pkv_status launch_simt_any(pkv_dtype dt, const pkv_kv_quant* quant, int D, const
 }
 
 // ---- split-K reduce dispatch -----------------------------------------------------
-// INT4 pools split over two CTAs an SM: few rows of many partials are merged by a
-// CTA each.  (4 sequences of 131072 tokens, 64 heads, 76 partials a row: 27 us with a
-// warp each, cold.)
+// INT4 pools split over three CTAs an SM: few rows of many partials are merged by a
+// CTA each (plan_attention has the rule and what it measured).
 template <typename T>
 pkv_status launch_reduce_wide(pkv::Workspace ws, int S, int H_q, void* out, cudaStream_t st) {
   PKV_CUDA(launch_pdl(pkv::attn_reduce_wide_kernel<T, 128>, dim3((unsigned)(S * H_q)),

@@ -372,7 +372,7 @@ struct TcCfg {
 // Largest CTA index i whose range starts at or before chunk c.
 __host__ __device__ __forceinline__ int cta_of_chunk(long long c, long long T, int n) {
   const long long x = (c + 1) * (long long)n - 1;
-  // (a 64-bit division is ten times a 32-bit one; T > c, so it fits where x does)
+  // (a 64-bit division is ten times a 32-bit one; T is the last of the int chunk starts)
   if (x >> 32 == 0) return (int)((uint32_t)x / (uint32_t)T);
   return (int)(x / T);
 }

@@ -187,11 +187,13 @@ __device__ __noinline__ void beam_tile_slow(const T* base, int V, int first, int
 // to the last bit, wherever the row lies: rows alike tie.  What does not belong to the
 // row counts as -inf.  Four CTAs an SM
 // (three for float32): the blocks stay packed in registers and are unpacked as they are used.
-// Bound by HBM (V e bytes a row) from afar: 512 rows of 131072 bf16 values in 38 us, of a
-// whole call's 51 where a copy would take 19; what a warp issues for the bound (the N-th
+// Bound by HBM (V e bytes a row) from afar: 512 rows of 131072 bf16 values in 38.5 us, of a
+// whole call's 49 where a copy would take 19; what a warp issues for the bound (the N-th
 // largest of the threads' maxima: with one over the warps' eight, 57 values a tile
 // went through and the call took 85 us) and a CTA's chain of loads, exponents and
-// reductions are the rest.
+// reductions are the rest.  Equal values count once in the bound: a row with fewer than N
+// distinct large values (bf16 logits far from zero, many at the type's lowest value)
+// sends its tiles to beam_tile_slow, 2300 us for N = 32; -inf costs nothing.
 template <typename T, int NV>
 __global__ void __launch_bounds__(kBeamThreads, sizeof(T) == 2 ? 4 : 3)
 beam_tiles_kernel(const __grid_constant__ BeamParams p) {
@@ -337,8 +339,10 @@ beam_tiles_kernel(const __grid_constant__ BeamParams p) {
 }
 
 // One CTA a request: the sums of its beams' rows, then the best of all tiles'
-// candidates and the finished beams.  10.5 us of the call of 51 us above: chains of
-// loads and reductions over shared memory.
+// candidates and the finished beams.  10.5 us of the call of 49 us above: chains of
+// loads and reductions over shared memory.  The bound is the N-th of a warp's 32 lanes:
+// at N = 32 nearly all candidates pass it, more than the buffer holds with many beams, and
+// are taken one after the other (32 of 16 beams over 131072 tokens: the call takes 819 us).
 constexpr int kBeamPickBuffer = 1024;
 constexpr int kBeamAhead = 2;                // candidates a thread holds from the start
 

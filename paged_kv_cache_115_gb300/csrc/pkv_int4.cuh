@@ -8,7 +8,8 @@
 // offsets are fixed to the bit.  Rounding z down keeps every x - z >= 0 whatever
 // the row's distance from zero is next to its spread: the error stays below
 // 0.57 s (half a step, and 15 codes of a scale that is off by 2^-8 at most).  A
-// scale below 2^-126 has no float32 reciprocal: r = 0, the row reads as z.  A row
+// scale below 2^-126 has no float32 reciprocal: r = 0, the row reads as z (less
+// than 2^-122 off).  A row
 // with a NaN or an infinity (or whose offset or scale overflows) gets s = z = NaN
 // and reads as NaN, as it would in a bf16 pool.
 //

@@ -116,7 +116,8 @@ attn_reduce_kernel(Workspace ws, int S, int H_q, T* __restrict__ out) {
 
 // The same merge by a CTA a row, for few rows of many partials: warp w takes
 // partials w, w + 8, ..., its state joins the others' in shared memory.  4 sequences
-// of 131072 tokens: the call took 118 us so, 137 with a warp a row.
+// of 65536 tokens, 64 heads, 57 partials a row: the call takes 69.1 us so, 78.8 with a
+// warp a row.
 template <typename T, int D>
 __global__ void __launch_bounds__(kReduceWarps * 32)
 attn_reduce_wide_kernel(Workspace ws, int H_q, T* __restrict__ out) {
