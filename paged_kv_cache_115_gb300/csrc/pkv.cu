@@ -213,9 +213,10 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
     p.hpc = tc_hpc(H_kv, ct);
     p.groups = H_kv / p.hpc;
     // members of a shared-prefix group: the columns of two blocks; INT4 pools those of
-    // one with G <= 4, which leaves registers for twice the warps, and none above: two
-    // blocks took 1.2 to 1.9 times what reading every member's own took (G 5 and 8; 2, 3, 4,
-    // 8 and 16 beams, prompts of 512 to 131072 tokens).
+    // one with G <= 4, which leaves registers for twice the warps (0.42 to 0.88 of the time
+    // without groups where they lie inside requests, 1.0 to 1.16 where not), and none above:
+    // two blocks took 1.2 to 1.9 times what reading every member's own took (G 5 and 8; 2, 3,
+    // 4, 8 and 16 beams, prompts of 512 to 131072 tokens).
     const int share_m = !c.share_prefix ? 1 : (ct == 4 ? (G <= 4 ? 8 / G : 1) : 16 / G);
     // one CTA per SM (shared memory bound), or as many as a pool format takes
     const int total = sms * pkv::tc_ctas(ct, p.hpc);
@@ -262,7 +263,8 @@ pkv_status plan_attention(int S, int H_q, int H_kv, int D, int K, int max_len, i
 
 // Plan for a quantized pool: the tensor-core kernel when the shape allows it
 // (bf16 queries, head_dim 128, G <= 8, block_size 8 or a multiple of 16, 16-byte aligned
-// pools and scales, queries aligned for its loads), else the CUDA-core kernel (head_dim 64 / 128, G <= 16).
+// pools and scales, queries aligned for its loads), else the CUDA-core kernel (head_dim
+// 64 / 128, G <= 16).
 pkv_status plan_attention_quant(int S, int H_q, int H_kv, int D, int K, int max_len,
                                 int64_t num_blocks, pkv_dtype q_dt, const pkv_kv_quant* quant,
                                 const pkv_attention_config* cfg, bool aligned_ok,
